@@ -85,7 +85,9 @@ class TsOuts(ctypes.Structure):
 
 
 EXPORTS = ("ts_fused_reduce_norm", "ts_reducescatter_fused_norm", "ts_allgather_fused_norm", "ts_qk_norm_sharded",
-           "ts_rms_norm_sharded", "ts_status_string", "ts_last_error_detail")
+           "ts_rms_norm_sharded", "ts_nvfp4_quantize", "ts_nvfp4_dequantize", "ts_nvfp4_gemm", "ts_moe_rows",
+           "ts_moe_sort", "ts_moe_dispatch", "ts_nvfp4_grouped_gemm", "ts_moe_combine", "ts_moe_combine_grad",
+           "ts_stalled_waits", "ts_status_string", "ts_last_error_detail")
 
 TS_FLAG_PDL = 1
 TS_FLAG_PDL_EARLY_READ = 2
@@ -129,6 +131,21 @@ def library(path: str | None = None):
         lib.ts_rms_norm_sharded.argtypes = [ctypes.POINTER(vp), ctypes.c_int, i64, i64, i64, vp,
                                             ctypes.c_float, vp, i64, u32, vp]
         lib.ts_rms_norm_sharded.restype = ctypes.c_int
+        i32 = ctypes.c_int
+        for name, types in (
+                ("ts_nvfp4_quantize", [vp, i64, i64, i64, vp, vp, vp, vp, i32, u32, vp]),
+                ("ts_nvfp4_dequantize", [vp, vp, i32, i64, i64, vp, vp, vp, i64, u32, vp]),
+                ("ts_nvfp4_gemm", [vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, u32, vp]),
+                ("ts_moe_sort", [vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, u32, vp]),
+                ("ts_moe_dispatch", [vp, i64, i64, i64, vp, i64, i64, vp, vp, vp, vp, i32, u32, vp]),
+                ("ts_nvfp4_grouped_gemm", [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, u32, vp]),
+                ("ts_moe_combine", [vp, i64, i64, i64, vp, vp, i64, i64, vp, i64, u32, vp]),
+                ("ts_moe_combine_grad", [vp, i64, vp, i64, i64, i64, vp, vp, i64, i64, vp, i64, vp, u32, vp]),
+                ("ts_stalled_waits", [vp])):
+            getattr(lib, name).argtypes = types
+            getattr(lib, name).restype = ctypes.c_int
+        lib.ts_moe_rows.argtypes = [i64, i64, i64, i64]
+        lib.ts_moe_rows.restype = i64
         lib.ts_status_string.argtypes = [ctypes.c_int]
         lib.ts_status_string.restype = ctypes.c_char_p
         lib.ts_last_error_detail.argtypes = []

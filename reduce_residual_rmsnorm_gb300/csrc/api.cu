@@ -7,14 +7,25 @@
 
 #include <cuda_runtime.h>
 
+#include "api_util.h"
 #include "launch.h"
 #include "ts_fused_norm.h"
 
+using tsfn::aligned;
 using tsfn::Epilogue;
+using tsfn::fail;
+using tsfn::ok;
+using tsfn::overlap;
+using tsfn::Span;
+using tsfn::span;
+
+namespace tsfn {
 
 namespace {
 
 thread_local char g_detail[512];
+
+}  // namespace
 
 int fail(int status, const char *fmt, ...)
 {
@@ -31,7 +42,11 @@ int ok()
     return TS_OK;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+const char *last_detail() { return g_detail; }
+
+}  // namespace tsfn
+
+namespace {
 
 // 1/n when n (>= 1) is a power of two, which fp32 holds exactly; else 0.
 float pow2_reciprocal(int64_t n)
@@ -42,27 +57,6 @@ float pow2_reciprocal(int64_t n)
     for (int64_t m = n; m > 1; m >>= 1)
         r *= 0.5f;
     return r;
-}
-
-struct Span {
-    uintptr_t lo = 0, hi = 0;  // [lo, hi)
-    const char *name = "";
-};
-
-Span span(const void *p, int64_t bytes, const char *name)
-{
-    Span s;
-    s.lo = reinterpret_cast<uintptr_t>(p);
-    s.hi = s.lo + (uintptr_t)(bytes > 0 ? bytes : 0);
-    s.name = name;
-    return s;
-}
-
-bool overlap(const Span &a, const Span &b)
-{
-    if (a.lo == a.hi || b.lo == b.hi)
-        return false;
-    return a.lo < b.hi && b.lo < a.hi;
 }
 
 // Which outputs each pattern writes: 'R' required, 'o' optional, '-' absent.
@@ -85,7 +79,7 @@ const char *const kOutputNames[6] = {"allreduce_out", "residual_out", "norm_out"
 constexpr int64_t kMaxH = 16384;
 constexpr uint32_t kKnownFlags = TS_FLAG_PDL;                           // sharded and all-gather norms
 constexpr uint32_t kFusedFlags = TS_FLAG_PDL | TS_FLAG_PDL_EARLY_READ | TS_FLAG_PDL_INDEPENDENT;  // fused, RS
-constexpr int64_t kMaxRows = 0x7FFFFFFFLL;
+using tsfn::kMaxRows;
 
 }  // namespace
 
@@ -104,7 +98,7 @@ extern "C" const char *ts_status_string(int status)
     }
 }
 
-extern "C" const char *ts_last_error_detail(void) { return g_detail; }
+extern "C" const char *ts_last_error_detail(void) { return tsfn::last_detail(); }
 
 namespace {
 

@@ -1,0 +1,504 @@
+// NVFP4 matrix products on the fifth-generation tensor cores: out = alpha A B^T
+// for one matrix of weights, or for each expert's with its own rows.
+//
+//   out[m, n] = bf16(alpha * sum_k (a sf_a)[m, k] (b sf_b)[n, k])       fp32 sums
+//
+// tcgen05.mma kind::mxf4nvf4 multiplies 64 packed E2M1 values of K per
+// instruction with one E4M3 scale factor per 16, from shared memory into
+// tensor memory.  Its operands are named P (128 rows, the accumulator's lanes)
+// and Q (BN rows, the accumulator's columns) here; a call of few tokens puts
+// the weights on P and the tokens on Q (SWAP), so that a tile is no taller
+// than the tokens need, a larger one the tokens on P.
+//
+// One block per SM, persistent over the tiles.  Warp 0 copies (one thread):
+// codes by TMA under the 128-byte swizzle, 256 elements of K (128 bytes a row)
+// per stage, scale factors by bulk copies of the 512-byte tiles of their 128x4
+// layout, which is the layout tensor memory wants.  Warp 1 multiplies (one
+// thread): scale factors from shared to tensor memory, then the products.
+// Warps 2 to 5 write the finished accumulator (one of two, so that the next
+// tile's products run meanwhile).  Every wait has a limit, after which the
+// block records it, waits for its copies in flight and ends.
+#include <cuda.h>
+
+#include "device_util.cuh"
+#include "launch_nvfp4.h"
+#include "tcgen05.cuh"
+
+namespace tsfn {
+
+namespace {
+
+__device__ uint32_t g_stalled_waits;
+
+constexpr int kThreads = 192;
+constexpr int kP = 128;               // rows of P per tile
+constexpr int kSfTile = 512;          // bytes of a 128-row, 64-element tile of scale factors
+constexpr int kWaitLimit = 1 << 22;   // tries of a wait
+constexpr int kSmemLimit = 232448;    // bytes of shared memory of a block
+
+template <int BN>
+struct Shape {
+    static constexpr int kBands = BN > 128 ? BN / 128 : 1;  // 128-row bands of Q's scale factors
+    static constexpr int kCodes = kP * 128 + BN * 128;      // bytes of codes per stage
+    static constexpr int kSf = 4 * kSfTile * (1 + kBands);  // bytes of scale factors per stage
+    static constexpr int kFixed = 1024 /* alignment */ + 4 * 1032 /* experts' first tiles */;
+    static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
+    static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
+    static constexpr int kSfP = 2 * BN;       // tensor-memory column of P's scale factors
+    static constexpr int kSfQ = kSfP + 16;    // and of Q's
+    static constexpr int kColumns = 512;      // one block per SM: all of it
+    static_assert(kSfQ + 16 * kBands <= kColumns, "accumulators and scale factors fit tensor memory");
+};
+
+struct KernelArgs {
+    const uint8_t *p_sf;
+    const uint8_t *q_sf;
+    const float *alpha;
+    uint16_t *out;
+    int64_t ldo;
+    int64_t p_rows, q_rows;  // dense: rows of P and Q
+    int kblocks;             // ceil(K / 64)
+    int wgt_rows;            // grouped: N
+    int wgt_bands;           // grouped: 128-row bands of an expert's scale factors
+    int64_t tok_rows;        // grouped: rows of the sorted tokens
+    const int32_t *start;
+    const int32_t *count;
+    int experts;
+};
+
+// One tile: the first rows of P and Q in their tensor maps, their scale-factor
+// bands, and the part of the output it covers.
+struct Tile {
+    int32_t p_row, q_row;
+    int64_t p_band, q_band;
+    int q_bands;       // bands of Q inside its buffer
+    int q_sub;         // 32-row group of Q's tile inside its band
+    int64_t tok0;      // output rows tok0 .. tok0 + tok_n
+    int tok_n;
+    int64_t wgt0;      // output columns wgt0 .. wgt0 + wgt_n
+    int wgt_n;
+    int expert;
+};
+
+template <int BN, bool SWAP>
+__device__ __forceinline__ Tile dense_tile(const KernelArgs &a, int64_t id)
+{
+    // groups of 8 P tiles pass over Q together, so that blocks running at the
+    // same time share rows of both
+    const int64_t np = (a.p_rows + kP - 1) / kP, nq = (a.q_rows + BN - 1) / BN;
+    const int64_t group = id / (8 * nq);
+    const int64_t gp = np - group * 8 < 8 ? np - group * 8 : 8;
+    const int64_t in = id - group * 8 * nq;
+    const int64_t p = group * 8 + in % gp, q = in / gp;
+    Tile t;
+    t.p_row = (int32_t)(p * kP);
+    t.q_row = (int32_t)(q * BN);
+    t.p_band = p;
+    t.q_band = (q * BN) >> 7;
+    const int64_t bands = (a.q_rows + 127) >> 7;
+    t.q_bands = (int)(bands - t.q_band < Shape<BN>::kBands ? bands - t.q_band : Shape<BN>::kBands);
+    t.q_sub = (int)((q * BN) & 127) >> 5;
+    const int64_t p_n = a.p_rows - t.p_row < kP ? a.p_rows - t.p_row : kP;
+    const int64_t q_n = a.q_rows - t.q_row < BN ? a.q_rows - t.q_row : BN;
+    t.tok0 = SWAP ? t.q_row : t.p_row;
+    t.tok_n = (int)(SWAP ? q_n : p_n);
+    t.wgt0 = SWAP ? t.p_row : t.q_row;
+    t.wgt_n = (int)(SWAP ? p_n : q_n);
+    t.expert = 0;
+    return t;
+}
+
+// first[e]: tiles of tokens before expert e.  An expert's tiles go over its
+// tokens first, so that blocks running at the same time share its weights.
+template <int BN, bool SWAP>
+__device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t *first, int64_t id)
+{
+    constexpr int kTok = SWAP ? BN : kP, kWgt = SWAP ? kP : BN;
+    const int64_t nw = (a.wgt_rows + kWgt - 1) / kWgt;
+    int lo = 0, hi = a.experts;  // the expert e with first[e] * nw <= id < first[e + 1] * nw
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)first[mid] * nw <= id)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int nt = first[lo + 1] - first[lo];
+    const int64_t in = id - (int64_t)first[lo] * nw;
+    const int tok = (int)(in % nt);
+    const int w0 = (int)(in / nt) * kWgt;
+    const int count = __ldg(a.count + lo), start = __ldg(a.start + lo);
+    const int t0 = tok * kTok;
+    Tile t;
+    t.expert = lo;
+    t.tok0 = start + t0;
+    t.tok_n = count - t0 < kTok ? count - t0 : kTok;
+    t.wgt0 = w0;
+    t.wgt_n = a.wgt_rows - w0 < kWgt ? a.wgt_rows - w0 : kWgt;
+    const int32_t tok_row = start + t0, wgt_row = lo * a.wgt_rows + w0;
+    const int64_t tok_band = tok_row >> 7, wgt_band = (int64_t)lo * a.wgt_bands + (w0 >> 7);
+    t.p_row = SWAP ? wgt_row : tok_row;
+    t.q_row = SWAP ? tok_row : wgt_row;
+    t.p_band = SWAP ? wgt_band : tok_band;
+    t.q_band = SWAP ? tok_band : wgt_band;
+    const int left = SWAP ? 1 : a.wgt_bands - (w0 >> 7);
+    t.q_bands = left < Shape<BN>::kBands ? left : Shape<BN>::kBands;
+    t.q_sub = ((SWAP ? tok_row : w0) & 127) >> 5;
+    return t;
+}
+
+// False when the wait ran into its limit, here or elsewhere in the block.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *dead)
+{
+    for (int i = 0; i < kWaitLimit; ++i) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (*dead)
+            return false;
+    }
+    *dead = 1;
+    atomicAdd(&g_stalled_waits, 1u);
+    return false;
+}
+
+template <int BN, bool SWAP, bool GROUPED>
+__global__ void __launch_bounds__(kThreads, 1)
+    nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ KernelArgs a)
+{
+    using S = Shape<BN>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[2 * S::kStages + 5];
+    __shared__ uint32_t tmem_at;
+    __shared__ int dead_flag;
+    uint8_t *codes = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint8_t *sf = codes + S::kStages * S::kCodes;
+    int32_t *first = reinterpret_cast<int32_t *>(sf + S::kStages * S::kSf);
+    volatile int *dead = &dead_flag;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
+    const uint32_t acc_full = empty + 8 * S::kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, 4);
+        }
+        mbar_init(drained, 1);
+        mbar_fence_init();
+        dead_flag = 0;
+        tma_prefetch_map(&p_map);
+        tma_prefetch_map(&q_map);
+    }
+    if (warp == 1)
+        tmem_alloc(smem_u32(&tmem_at), S::kColumns);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_at;
+    pdl_wait();
+
+    int64_t tiles;
+    if constexpr (GROUPED) {
+        constexpr int kTok = SWAP ? BN : kP, kWgt = SWAP ? kP : BN;
+        for (int e = threadIdx.x; e < a.experts; e += kThreads) {
+            const int start = __ldg(a.start + e), count = __ldg(a.count + e);
+            const bool good = start >= 0 && (start & 127) == 0 && count > 0 && (int64_t)start + count <= a.tok_rows;
+            first[e + 1] = good ? (count + kTok - 1) / kTok : 0;
+        }
+        __syncthreads();
+        if (warp == 0) {  // inclusive scan
+            int32_t sum = 0;
+            for (int e0 = 0; e0 < a.experts; e0 += 32) {
+                int32_t v = e0 + lane < a.experts ? first[e0 + lane + 1] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t up = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o)
+                        v += up;
+                }
+                if (e0 + lane < a.experts)
+                    first[e0 + lane + 1] = sum + v;
+                sum += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (lane == 0)
+                first[0] = 0;
+        }
+        __syncthreads();
+        tiles = (int64_t)first[a.experts] * ((a.wgt_rows + kWgt - 1) / kWgt);
+    } else {
+        tiles = ((a.p_rows + kP - 1) / kP) * ((a.q_rows + BN - 1) / BN);
+    }
+    auto tile_of = [&](int64_t id) {
+        if constexpr (GROUPED)
+            return grouped_tile<BN, SWAP>(a, first, id);
+        else
+            return dense_tile<BN, SWAP>(a, id);
+    };
+    const int steps = (a.kblocks + 3) >> 2;
+
+    if (warp == 0 && lane == 0) {
+        // ---- copies ----
+        int s = 0;
+        uint32_t parity = 0;
+        int64_t fills = 0;
+        bool good = true;
+        for (int64_t id = blockIdx.x; good && id < tiles; id += gridDim.x) {
+            const Tile t = tile_of(id);
+            const uint8_t *psf = a.p_sf + t.p_band * a.kblocks * kSfTile;
+            const uint8_t *qsf = a.q_sf + t.q_band * a.kblocks * kSfTile;
+            for (int kt = 0; kt < steps; ++kt) {
+                good = wait_bar(empty + 8 * s, parity ^ 1, dead);
+                if (!good)
+                    break;
+                const int nkb = a.kblocks - 4 * kt < 4 ? a.kblocks - 4 * kt : 4;
+                const uint32_t bar = full + 8 * s;
+                mbar_expect_tx(bar, (uint32_t)(S::kCodes + nkb * kSfTile * (1 + t.q_bands)));
+                const uint32_t c = smem_u32(codes + s * S::kCodes), f = smem_u32(sf + s * S::kSf);
+                tma_load_2d(c, &p_map, kt * 128, t.p_row, bar);
+                tma_load_2d(c + kP * 128, &q_map, kt * 128, t.q_row, bar);
+                bulk_load(f, psf + (int64_t)kt * 4 * kSfTile, (uint32_t)(nkb * kSfTile), bar);
+                for (int b = 0; b < t.q_bands; ++b)
+                    bulk_load(f + (1 + b) * 4 * kSfTile, qsf + ((int64_t)b * a.kblocks + kt * 4) * kSfTile,
+                              (uint32_t)(nkb * kSfTile), bar);
+                ++fills;
+                if (++s == S::kStages) {
+                    s = 0;
+                    parity ^= 1;
+                }
+            }
+        }
+        pdl_launch_dependents();
+        if (!good) {  // the copies in flight land before the block's shared memory goes
+            for (int i = 0; i < S::kStages && i < fills; ++i) {
+                const int64_t fill = fills - 1 - i;
+                for (int n = 0; n < kWaitLimit && !mbar_try_wait(full + 8 * (uint32_t)(fill % S::kStages),
+                                                                 (uint32_t)(fill / S::kStages) & 1);
+                     ++n) {
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---- products ----
+        constexpr uint32_t idesc = idesc_nvfp4(BN);
+        int s = 0;
+        uint32_t parity = 0;
+        int64_t n = 0;
+        bool good = true;
+        for (int64_t id = blockIdx.x; good && id < tiles; id += gridDim.x, ++n) {
+            const int q_sub = SWAP ? tile_of(id).q_sub : 0;
+            const uint32_t acc = (uint32_t)n & 1;
+            good = wait_bar(acc_empty + 8 * acc, ((uint32_t)(n >> 1) & 1) ^ 1, dead);
+            if (!good)
+                break;
+            tmem_fence_after();
+            const uint32_t d = tmem + acc * BN;
+            for (int kt = 0; kt < steps; ++kt) {
+                good = wait_bar(full + 8 * s, parity, dead);
+                if (!good)
+                    break;
+                tmem_fence_after();
+                const int nkb = a.kblocks - 4 * kt < 4 ? a.kblocks - 4 * kt : 4;
+                const uint32_t c = smem_u32(codes + s * S::kCodes), f = smem_u32(sf + s * S::kSf);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    tmem_copy_sf(tmem + S::kSfP + 4 * kb, desc_sf_tile(f + kb * kSfTile));
+#pragma unroll
+                    for (int b = 0; b < S::kBands; ++b)
+                        tmem_copy_sf(tmem + S::kSfQ + 4 * (kb * S::kBands + b),
+                                     desc_sf_tile(f + ((1 + b) * 4 + kb) * kSfTile));
+                }
+                const uint64_t pd = desc_swizzled128(c), qd = desc_swizzled128(c + kP * 128);
+                for (int kb = 0; kb < nkb; ++kb)
+                    mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + S::kSfP + 4 * kb,
+                              tmem + S::kSfQ + 4 * kb * S::kBands + q_sub, kt > 0 || kb > 0);
+                mma_commit(empty + 8 * s);
+                if (++s == S::kStages) {
+                    s = 0;
+                    parity ^= 1;
+                }
+            }
+            if (good)
+                mma_commit(acc_full + 8 * acc);
+        }
+        if (!good) {
+            mma_commit(drained);
+            for (int i = 0; i < kWaitLimit && !mbar_try_wait(drained, 0); ++i) {
+            }
+        }
+    } else if (warp >= 2) {
+        // ---- output ----
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane;  // lane of the accumulator
+        int64_t n = 0;
+        for (int64_t id = blockIdx.x; id < tiles; id += gridDim.x, ++n) {
+            const Tile t = tile_of(id);
+            const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
+            const uint32_t acc = (uint32_t)n & 1;
+            if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead)))
+                break;
+            tmem_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < BN; c0 += 32) {
+                uint32_t v[32];
+                tmem_load32(tmem + acc * BN + ((uint32_t)quad << 21) + c0, v);
+                tmem_wait_loads();
+                if constexpr (SWAP) {
+                    // lane = output column, register = token
+                    if (row < t.wgt_n) {
+                        uint16_t *o = a.out + (t.tok0 + c0) * a.ldo + t.wgt0 + row;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c0 + i < t.tok_n)
+                                o[i * a.ldo] = (uint16_t)pack_bf16x2(__uint_as_float(v[i]) * alpha, 0.0f);
+                    }
+                } else {
+                    if (row < t.tok_n) {
+                        uint16_t *o = a.out + (t.tok0 + row) * a.ldo + t.wgt0 + c0;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            if (c0 + i < t.wgt_n) {
+                                float f[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    f[e] = __uint_as_float(v[i + e]) * alpha;
+                                st_v4(o + i, pack8(f));
+                            }
+                    }
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(acc_empty + 8 * acc);
+        }
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tmem_fence_after();
+        tmem_dealloc(tmem, S::kColumns);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, found once.
+EncodeFn encode_fn()
+{
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// Codes [rows, K/2] in boxes of 128 bytes by `box_rows` rows, 128-byte swizzle,
+// zeros outside.
+bool codes_map(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t K, int box_rows)
+{
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, bool SWAP, bool GROUPED>
+cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
+{
+    using S = Shape<BN>;
+    static std::atomic<bool> grown[kMaxCachedDevices];
+    int dev = 0;
+    const int sms = current_device_sms(&dev);
+    if (sms <= 0)
+        return cudaErrorInvalidDevice;
+    if (dev >= kMaxCachedDevices || !grown[dev].load(std::memory_order_relaxed)) {
+        const cudaError_t err = cudaFuncSetAttribute(nvfp4_gemm_kernel<BN, SWAP, GROUPED>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (err != cudaSuccess)
+            return err;
+        if (dev < kMaxCachedDevices)
+            grown[dev].store(true, std::memory_order_relaxed);
+    }
+    const int64_t wgt_rows = GROUPED ? g.experts * g.N : g.N;
+    CUtensorMap p_map, q_map;
+    if (!codes_map(&p_map, SWAP ? g.wgt : g.tok, SWAP ? wgt_rows : g.tok_rows, g.K, kP) ||
+        !codes_map(&q_map, SWAP ? g.tok : g.wgt, SWAP ? g.tok_rows : wgt_rows, g.K, BN))
+        return cudaErrorInvalidValue;
+    KernelArgs a{};
+    a.p_sf = SWAP ? g.wgt_sf : g.tok_sf;
+    a.q_sf = SWAP ? g.tok_sf : g.wgt_sf;
+    a.alpha = g.alpha;
+    a.out = g.out;
+    a.ldo = g.ldo;
+    a.p_rows = SWAP ? g.N : g.tok_rows;
+    a.q_rows = SWAP ? g.tok_rows : g.N;
+    a.kblocks = (int)((g.K + 63) / 64);
+    a.wgt_rows = (int)g.N;
+    a.wgt_bands = (int)((g.N + 127) / 128);
+    a.tok_rows = g.tok_rows;
+    a.start = g.start;
+    a.count = g.count;
+    a.experts = g.experts;
+    int64_t grid = sms;
+    if (!GROUPED) {
+        const int64_t tiles = ((a.p_rows + kP - 1) / kP) * ((a.q_rows + BN - 1) / BN);
+        grid = tiles < grid ? tiles : grid;
+    }
+    return launch_kernel(nvfp4_gemm_kernel<BN, SWAP, GROUPED>, dim3((unsigned)grid), dim3(kThreads), (size_t)S::kSmem,
+                         stream, pdl, p_map, q_map, a);
+}
+
+// A tile of 32 tokens only where it is the call's only one, so that its scale
+// factors begin a band; tiles of 64 begin at an even column of theirs.
+template <bool GROUPED>
+cudaError_t launch_by_tokens(const GemmArgs &g, int64_t tokens, bool pdl, cudaStream_t stream)
+{
+    if constexpr (!GROUPED) {
+        if (tokens <= 32)
+            return launch_tiles<32, true, false>(g, pdl, stream);
+    }
+    if (tokens <= 64) return launch_tiles<64, true, GROUPED>(g, pdl, stream);
+    if (tokens <= 128) return launch_tiles<128, true, GROUPED>(g, pdl, stream);
+    return launch_tiles<128, false, GROUPED>(g, pdl, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_nvfp4_gemm(const GemmArgs &g, bool pdl, cudaStream_t stream)
+{
+    if (g.experts > 0)  // an expert's share of the entries
+        return launch_by_tokens<true>(g, (g.entries + g.experts - 1) / g.experts, pdl, stream);
+    return launch_by_tokens<false>(g, g.tok_rows, pdl, stream);
+}
+
+cudaError_t read_stalled_waits(uint32_t *count)
+{
+    const cudaError_t err = cudaDeviceSynchronize();
+    if (err != cudaSuccess)
+        return err;
+    return cudaMemcpyFromSymbol(count, g_stalled_waits, sizeof(*count));
+}
+
+}  // namespace tsfn

@@ -1,0 +1,272 @@
+// Row-wise NVFP4: bf16 rows to codes and scale factors, the values read back,
+// and token rows put in expert order, as bf16 or as NVFP4.
+//
+// Quantiser, for each 16-column block (the arithmetic of the NVFP4 epilogue of
+// fused_rows.cu, on x itself; every step one fp32 rounding):
+//   sf = e4m3(g * (amax/6)),  code = e2m1(x * (g / value(sf))),  0 if value(sf) == 0
+//
+// All three are bound by memory.  Work unit of a warp: 128 chunks of 8 columns
+// of one row (up to 4 per lane, all loads issued before the first is used), or
+// several whole rows where a row is shorter.  A block of 16 columns is a pair
+// of lanes, so its maximum is one shuffle; lanes 8i gather four scale factors
+// into one 32-bit store.
+#include "device_util.cuh"
+#include "launch_nvfp4.h"
+#include "sf_layout.cuh"
+
+namespace tsfn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunks = 4;  // chunks of 8 columns per lane
+
+// The 8 E2M1 codes of one lane's chunk, and its block's scale factor.
+__device__ __forceinline__ uint32_t quantize_chunk(const uint4 &v, float g, uint32_t &sf)
+{
+    float n[8];
+    unpack8(v, n);
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        amax = fmaxf(amax, fabsf(n[e]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    sf = cvt_e4m3(__fmul_rn(g, div_const_rn(amax, 6.0f, kRcp6)));
+    const float d = e4m3_value(sf);
+    uint32_t codes = 0;
+    if (d != 0.0f) {
+        const float es = __fdiv_rn(g, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            n[e] = __fmul_rn(n[e], es);
+        codes = cvt_e2m1x8(n);
+    }
+    return codes;
+}
+
+// The scale factors of four blocks (8 lanes) in one word, on the first lane.
+__device__ __forceinline__ uint32_t gather_sf(uint32_t sf)
+{
+    const uint32_t s2 = __shfl_down_sync(0xffffffffu, sf, 2);
+    const uint32_t s4 = __shfl_down_sync(0xffffffffu, sf, 4);
+    const uint32_t s6 = __shfl_down_sync(0xffffffffu, sf, 6);
+    return sf | (s2 << 8) | (s4 << 16) | (s6 << 24);
+}
+
+// The scale factors at chunk c of a row: four at a time where a row's come in
+// fours, else a byte per block, and zeros in the padding columns.
+__device__ __forceinline__ void store_sf(const RowsArgs &a, int64_t row, int c, uint32_t word)
+{
+    uint8_t *p = a.sf + sf_row_base(a.sf_layout, a.sf_cols, row);
+    const int k = c >> 1;
+    const int stride = sf_tile_stride(a.sf_layout);
+    if ((a.K & 63) == 0) {
+        if ((c & 7) == 0)
+            *reinterpret_cast<uint32_t *>(p + (int64_t)(k >> 2) * stride) = word;
+    } else if ((c & 1) == 0) {
+        p[(int64_t)(k >> 2) * stride + (k & 3)] = (uint8_t)word;
+        if (k + 1 == (int)(a.K >> 4))
+            for (int kk = k + 1; kk < (int)a.sf_cols; ++kk)
+                p[(int64_t)(kk >> 2) * stride + (kk & 3)] = 0;
+    }
+}
+
+// Row t -> NVFP4 row t, or its k rows (SCATTER).
+template <bool SCATTER>
+__global__ void __launch_bounds__(kThreads) nvfp4_rows_kernel(const __grid_constant__ RowsArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const int l = lane & ((1 << a.tpr_log2) - 1);
+    const int64_t t = (((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) << (5 - a.tpr_log2)) + (lane >> a.tpr_log2);
+    const int nc = (int)(a.K >> 3);
+    const int c0 = (int)blockIdx.y * (32 * kChunks) + l;
+    pdl_wait();
+    bool live = t < a.T;
+    if (!SCATTER && live && a.row_src != nullptr)
+        live = __ldg(a.row_src + t) >= 0;
+    const uint16_t *row = a.x + t * a.ldx;
+    uint4 v[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = c0 + (i << a.tpr_log2);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (live && c < nc)
+            v[i] = ld_stream(row + (int64_t)c * 8);
+    }
+    const float g = __ldg(a.g);
+    pdl_launch_dependents();
+    uint32_t codes[kChunks], sf[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        codes[i] = quantize_chunk(v[i], g, sf[i]);
+        const uint32_t four = gather_sf(sf[i]);
+        if ((a.K & 63) == 0)
+            sf[i] = four;
+    }
+    if (live) {
+        const int k = SCATTER ? a.k : 1;
+        for (int j = 0; j < k; ++j) {
+            const int64_t r = SCATTER ? (int64_t)__ldg(a.row_of + t * a.k + j) : t;
+            if (SCATTER && (r < 0 || r >= a.rows))
+                continue;
+            uint8_t *out = a.codes + r * (a.K >> 1);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = c0 + (i << a.tpr_log2);
+                if (c < nc) {
+                    *reinterpret_cast<uint32_t *>(out + (int64_t)c * 4) = codes[i];
+                    store_sf(a, r, c, sf[i]);
+                }
+            }
+        }
+    } else if (!SCATTER && a.row_src == nullptr && t < a.sf_rows) {
+        // a padding row of a swizzled layout: zeros only
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = c0 + (i << a.tpr_log2);
+            if (c < nc)
+                store_sf(a, t, c, 0u);
+        }
+    }
+}
+
+// Row t -> its k rows, copied.
+__global__ void __launch_bounds__(kThreads) dispatch_rows_kernel(const __grid_constant__ RowsArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const int l = lane & ((1 << a.tpr_log2) - 1);
+    const int64_t t = (((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) << (5 - a.tpr_log2)) + (lane >> a.tpr_log2);
+    const int nc = (int)(a.K >> 3);
+    const int c0 = (int)blockIdx.y * (32 * kChunks) + l;
+    pdl_wait();
+    if (t >= a.T)
+        return;
+    const uint16_t *row = a.x + t * a.ldx;
+    uint4 v[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = c0 + (i << a.tpr_log2);
+        if (c < nc)
+            v[i] = ld_stream(row + (int64_t)c * 8);
+    }
+    pdl_launch_dependents();
+    for (int j = 0; j < a.k; ++j) {
+        const int64_t r = __ldg(a.row_of + t * a.k + j);
+        if (r < 0 || r >= a.rows)
+            continue;
+        uint16_t *out = a.out + r * a.K;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = c0 + (i << a.tpr_log2);
+            if (c < nc)
+                st_v4(out + (int64_t)c * 8, v[i]);
+        }
+    }
+}
+
+// Two E2M1 codes -> two fp32 values (the hardware conversion to f16, exact).
+__device__ __forceinline__ float2 e2m1x2_values(uint32_t byte)
+{
+    float2 f;
+    asm("{\n\t.reg .b8 b;\n\t.reg .b32 h;\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.u8.u32 b, %2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 h, b;\n\t"
+        "mov.b32 {lo, hi}, h;\n\t"
+        "cvt.f32.f16 %0, lo;\n\t"
+        "cvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(byte));
+    return f;
+}
+
+__global__ void __launch_bounds__(kThreads) nvfp4_values_kernel(const __grid_constant__ DequantArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const int l = lane & ((1 << a.tpr_log2) - 1);
+    const int64_t t = (((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) << (5 - a.tpr_log2)) + (lane >> a.tpr_log2);
+    const int nc = (int)(a.K >> 3);
+    const int c0 = (int)blockIdx.y * (32 * kChunks) + l;
+    pdl_wait();
+    if (t >= a.T || (a.row_src != nullptr && __ldg(a.row_src + t) < 0))
+        return;
+    const uint8_t *codes = a.codes + t * (a.K >> 1);
+    const uint8_t *sf = a.sf + sf_row_base(a.sf_layout, a.sf_cols, t);
+    const int stride = sf_tile_stride(a.sf_layout);
+    uint32_t w[kChunks], s[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = c0 + (i << a.tpr_log2);
+        if (c < nc) {
+            const int k = c >> 1;
+            w[i] = *reinterpret_cast<const uint32_t *>(codes + (int64_t)c * 4);
+            s[i] = sf[(int64_t)(k >> 2) * stride + (k & 3)];
+        }
+    }
+    const float g = __ldg(a.g);
+    pdl_launch_dependents();
+    uint16_t *out = a.out + t * a.ldo;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = c0 + (i << a.tpr_log2);
+        if (c < nc) {
+            const float d = __fdiv_rn(e4m3_value(s[i]), g);
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 p = e2m1x2_values((w[i] >> (8 * e)) & 0xFFu);
+                f[2 * e] = __fmul_rn(p.x, d);
+                f[2 * e + 1] = __fmul_rn(p.y, d);
+            }
+            st_v4(out + (int64_t)c * 8, pack8(f));
+        }
+    }
+}
+
+// Lanes per row: 32 with up to 4 chunks each, fewer where a row has fewer than
+// 128 chunks, so that a warp takes several rows; at least 8 (where there are 8
+// chunks) for the gathered scale-factor stores.
+int lanes_log2(int64_t K)
+{
+    const int64_t nc = K / 8;
+    int l = 0;
+    while (l < 5 && (1 << l) < nc && ((kChunks << l) < nc || l < 3))
+        ++l;
+    return l;
+}
+
+dim3 grid_of(int64_t rows, int64_t K, int tpr_log2)
+{
+    const int64_t per_cta = (int64_t)kWarps << (5 - tpr_log2);
+    const int64_t segs = tpr_log2 == 5 ? (K / 8 + 32 * kChunks - 1) / (32 * kChunks) : 1;
+    return dim3((unsigned)((rows + per_cta - 1) / per_cta), (unsigned)segs);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(const RowsArgs &a, bool pdl, cudaStream_t stream)
+{
+    RowsArgs b = a;
+    b.tpr_log2 = lanes_log2(a.K);
+    const int64_t rows = a.row_src == nullptr ? a.sf_rows : a.T;
+    return launch_kernel(nvfp4_rows_kernel<false>, grid_of(rows, a.K, b.tpr_log2), dim3(kThreads), 0, stream, pdl, b);
+}
+
+cudaError_t launch_dispatch(const RowsArgs &a, bool pdl, cudaStream_t stream)
+{
+    RowsArgs b = a;
+    b.tpr_log2 = lanes_log2(a.K);
+    const dim3 grid = grid_of(a.T, a.K, b.tpr_log2);
+    if (a.out != nullptr)
+        return launch_kernel(dispatch_rows_kernel, grid, dim3(kThreads), 0, stream, pdl, b);
+    return launch_kernel(nvfp4_rows_kernel<true>, grid, dim3(kThreads), 0, stream, pdl, b);
+}
+
+cudaError_t launch_dequantize(const DequantArgs &a, bool pdl, cudaStream_t stream)
+{
+    DequantArgs b = a;
+    b.tpr_log2 = lanes_log2(a.K);
+    return launch_kernel(nvfp4_values_kernel, grid_of(a.T, a.K, b.tpr_log2), dim3(kThreads), 0, stream, pdl, b);
+}
+
+}  // namespace tsfn

@@ -33,7 +33,7 @@ __device__ uint32_t g_stalled_waits;
 constexpr int kThreads = 192;
 constexpr int kP = 128;               // rows of P per tile
 constexpr int kSfTile = 512;          // bytes of a 128-row, 64-element tile of scale factors
-constexpr int kWaitLimit = 1 << 22;   // tries of a wait
+constexpr long long kWaitCycles = 4000000000LL;  // a wait's limit: about 2 s
 constexpr int kSmemLimit = 232448;    // bytes of shared memory of a block
 
 template <int BN>
@@ -147,18 +147,33 @@ __device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t 
     return t;
 }
 
-// False when the wait ran into its limit, here or elsewhere in the block.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *dead)
+// Wait with a limit, for what is in flight when a block gives up.
+__device__ __noinline__ void wait_last(uint32_t bar, uint32_t parity)
 {
-    for (int i = 0; i < kWaitLimit; ++i) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity) && clock64() - t0 < kWaitCycles) {
+    }
+}
+
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *dead)
+{
+    const long long t0 = clock64();
+    while (!*dead) {
         if (mbar_try_wait(bar, parity))
             return true;
-        if (*dead)
-            return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *dead = 1;
+            atomicAdd(&g_stalled_waits, 1u);
+        }
     }
-    *dead = 1;
-    atomicAdd(&g_stalled_waits, 1u);
     return false;
+}
+
+// The whole warp waits; false in every lane when a wait ran into its limit,
+// here or elsewhere in the block.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *dead)
+{
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_slow(bar, parity, dead));
 }
 
 template <int BN, bool SWAP, bool GROUPED>
@@ -171,12 +186,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint64_t bars[2 * S::kStages + 5];
     __shared__ uint32_t tmem_at;
     __shared__ int dead_flag;
-    uint8_t *codes = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    uint8_t *sf = codes + S::kStages * S::kCodes;
-    int32_t *first = reinterpret_cast<int32_t *>(sf + S::kStages * S::kSf);
+    const uint32_t pad = (1024 - (smem_u32(raw) & 1023)) & 1023;
+    const uint32_t codes = smem_u32(raw) + pad;
+    const uint32_t sf = codes + S::kStages * S::kCodes;
+    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + S::kStages * (S::kCodes + S::kSf));
     volatile int *dead = &dead_flag;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
     const uint32_t acc_full = empty + 8 * S::kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
 
@@ -242,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const int steps = (a.kblocks + 3) >> 2;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ---- copies ----
         int s = 0;
         uint32_t parity = 0;
@@ -253,19 +269,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t *psf = a.p_sf + t.p_band * a.kblocks * kSfTile;
             const uint8_t *qsf = a.q_sf + t.q_band * a.kblocks * kSfTile;
             for (int kt = 0; kt < steps; ++kt) {
-                good = wait_bar(empty + 8 * s, parity ^ 1, dead);
+                good = wait_warp(empty + 8 * s, parity ^ 1, dead);
                 if (!good)
                     break;
                 const int nkb = a.kblocks - 4 * kt < 4 ? a.kblocks - 4 * kt : 4;
                 const uint32_t bar = full + 8 * s;
-                mbar_expect_tx(bar, (uint32_t)(S::kCodes + nkb * kSfTile * (1 + t.q_bands)));
-                const uint32_t c = smem_u32(codes + s * S::kCodes), f = smem_u32(sf + s * S::kSf);
-                tma_load_2d(c, &p_map, kt * 128, t.p_row, bar);
-                tma_load_2d(c + kP * 128, &q_map, kt * 128, t.q_row, bar);
-                bulk_load(f, psf + (int64_t)kt * 4 * kSfTile, (uint32_t)(nkb * kSfTile), bar);
-                for (int b = 0; b < t.q_bands; ++b)
-                    bulk_load(f + (1 + b) * 4 * kSfTile, qsf + ((int64_t)b * a.kblocks + kt * 4) * kSfTile,
-                              (uint32_t)(nkb * kSfTile), bar);
+                const uint32_t c = codes + s * S::kCodes, f = sf + s * S::kSf;
+                if (elect_one()) {
+                    mbar_expect_tx(bar, (uint32_t)(S::kCodes + nkb * kSfTile * (1 + t.q_bands)));
+                    tma_load_2d(c, &p_map, kt * 128, t.p_row, bar);
+                    tma_load_2d(c + kP * 128, &q_map, kt * 128, t.q_row, bar);
+                    bulk_load(f, psf + (int64_t)kt * 4 * kSfTile, (uint32_t)(nkb * kSfTile), bar);
+                    for (int b = 0; b < t.q_bands; ++b)
+                        bulk_load(f + (1 + b) * 4 * kSfTile, qsf + ((int64_t)b * a.kblocks + kt * 4) * kSfTile,
+                                  (uint32_t)(nkb * kSfTile), bar);
+                }
+                __syncwarp();
                 ++fills;
                 if (++s == S::kStages) {
                     s = 0;
@@ -277,13 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!good) {  // the copies in flight land before the block's shared memory goes
             for (int i = 0; i < S::kStages && i < fills; ++i) {
                 const int64_t fill = fills - 1 - i;
-                for (int n = 0; n < kWaitLimit && !mbar_try_wait(full + 8 * (uint32_t)(fill % S::kStages),
-                                                                 (uint32_t)(fill / S::kStages) & 1);
-                     ++n) {
-                }
+                wait_last(full + 8 * (uint32_t)(fill % S::kStages), (uint32_t)(fill / S::kStages) & 1);
             }
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ---- products ----
         constexpr uint32_t idesc = idesc_nvfp4(BN);
         int s = 0;
@@ -293,42 +309,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t id = blockIdx.x; good && id < tiles; id += gridDim.x, ++n) {
             const int q_sub = SWAP ? tile_of(id).q_sub : 0;
             const uint32_t acc = (uint32_t)n & 1;
-            good = wait_bar(acc_empty + 8 * acc, ((uint32_t)(n >> 1) & 1) ^ 1, dead);
+            good = wait_warp(acc_empty + 8 * acc, ((uint32_t)(n >> 1) & 1) ^ 1, dead);
             if (!good)
                 break;
-            tmem_fence_after();
             const uint32_t d = tmem + acc * BN;
             for (int kt = 0; kt < steps; ++kt) {
-                good = wait_bar(full + 8 * s, parity, dead);
+                good = wait_warp(full + 8 * s, parity, dead);
                 if (!good)
                     break;
                 tmem_fence_after();
                 const int nkb = a.kblocks - 4 * kt < 4 ? a.kblocks - 4 * kt : 4;
-                const uint32_t c = smem_u32(codes + s * S::kCodes), f = smem_u32(sf + s * S::kSf);
-                for (int kb = 0; kb < nkb; ++kb) {
-                    tmem_copy_sf(tmem + S::kSfP + 4 * kb, desc_sf_tile(f + kb * kSfTile));
+                if (elect_one()) {
+                    const uint32_t c = codes + s * S::kCodes, f = sf + s * S::kSf;
+                    const uint64_t fd = desc_sf_tile(f);
+                    const uint64_t pd = desc_swizzled128(c), qd = desc_swizzled128(c + kP * 128);
 #pragma unroll
-                    for (int b = 0; b < S::kBands; ++b)
-                        tmem_copy_sf(tmem + S::kSfQ + 4 * (kb * S::kBands + b),
-                                     desc_sf_tile(f + ((1 + b) * 4 + kb) * kSfTile));
+                    for (int kb = 0; kb < 4; ++kb)
+                        if (kb < nkb) {
+                            tmem_copy_sf(tmem + S::kSfP + 4 * kb, fd + kb * (kSfTile >> 4));
+#pragma unroll
+                            for (int b = 0; b < S::kBands; ++b)
+                                tmem_copy_sf(tmem + S::kSfQ + 4 * (kb * S::kBands + b),
+                                             fd + ((1 + b) * 4 + kb) * (kSfTile >> 4));
+                        }
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+                        if (kb < nkb)
+                            mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + S::kSfP + 4 * kb,
+                                      tmem + S::kSfQ + 4 * kb * S::kBands + q_sub, kt > 0 || kb > 0);
+                    mma_commit(empty + 8 * s);
+                    if (kt + 1 == steps)
+                        mma_commit(acc_full + 8 * acc);
                 }
-                const uint64_t pd = desc_swizzled128(c), qd = desc_swizzled128(c + kP * 128);
-                for (int kb = 0; kb < nkb; ++kb)
-                    mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + S::kSfP + 4 * kb,
-                              tmem + S::kSfQ + 4 * kb * S::kBands + q_sub, kt > 0 || kb > 0);
-                mma_commit(empty + 8 * s);
+                __syncwarp();
                 if (++s == S::kStages) {
                     s = 0;
                     parity ^= 1;
                 }
             }
-            if (good)
-                mma_commit(acc_full + 8 * acc);
         }
         if (!good) {
-            mma_commit(drained);
-            for (int i = 0; i < kWaitLimit && !mbar_try_wait(drained, 0); ++i) {
-            }
+            if (elect_one())
+                mma_commit(drained);
+            __syncwarp();
+            wait_last(drained, 0);
         }
     } else if (warp >= 2) {
         // ---- output ----
@@ -339,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Tile t = tile_of(id);
             const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
             const uint32_t acc = (uint32_t)n & 1;
-            if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead)))
+            if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
                 break;
             tmem_fence_after();
 #pragma unroll 1

@@ -238,9 +238,9 @@ def sf_shape(T: int, H: int, sf_layout: int = SFLayout.LINEAR) -> tuple[int, int
     """Shape of the NVFP4 scale-factor buffer for [T, H] values in ``sf_layout``
     (the swizzled layouts pad rows to 128 or 8 and columns to 4)."""
     layout = int(sf_layout)
-    if layout == SFLayout.LINEAR:
+    if layout == 2:  # LINEAR
         return T, H // 16
-    tile = 128 if layout == SFLayout.SWIZZLED_128x4 else 8
+    tile = 128 if layout == 0 else 8  # SWIZZLED_128x4, SWIZZLED_8x4
     return (T + tile - 1) // tile * tile, (H // 16 + 3) // 4 * 4
 
 

@@ -37,8 +37,11 @@ constexpr long long kWaitCycles = 4000000000LL;  // a wait's limit: about 2 s
 constexpr int kSmemLimit = 232448;    // bytes of shared memory of a block
 
 template <int BN>
+constexpr int kBandsOf = BN > 128 ? BN / 128 : 1;  // 128-row bands of Q's scale factors
+
+template <int BN>
 struct Shape {
-    static constexpr int kBands = BN > 128 ? BN / 128 : 1;  // 128-row bands of Q's scale factors
+    static constexpr int kBands = kBandsOf<BN>;
     static constexpr int kCodes = kP * 128 + BN * 128;      // bytes of codes per stage
     static constexpr int kSf = 4 * kSfTile * (1 + kBands);  // bytes of scale factors per stage
     static constexpr int kFixed = 1024 /* alignment */ + 4 * 1032 /* experts' first tiles */;
@@ -80,25 +83,25 @@ struct Tile {
     int expert;
 };
 
-template <int BN, bool SWAP>
+template <int PN, int BN, bool SWAP>
 __device__ __forceinline__ Tile dense_tile(const KernelArgs &a, int64_t id)
 {
     // groups of 8 P tiles pass over Q together, so that blocks running at the
     // same time share rows of both
-    const int64_t np = (a.p_rows + kP - 1) / kP, nq = (a.q_rows + BN - 1) / BN;
+    const int64_t np = (a.p_rows + PN - 1) / PN, nq = (a.q_rows + BN - 1) / BN;
     const int64_t group = id / (8 * nq);
     const int64_t gp = np - group * 8 < 8 ? np - group * 8 : 8;
     const int64_t in = id - group * 8 * nq;
     const int64_t p = group * 8 + in % gp, q = in / gp;
     Tile t;
-    t.p_row = (int32_t)(p * kP);
+    t.p_row = (int32_t)(p * PN);
     t.q_row = (int32_t)(q * BN);
-    t.p_band = p;
+    t.p_band = (p * PN) >> 7;
     t.q_band = (q * BN) >> 7;
     const int64_t bands = (a.q_rows + 127) >> 7;
-    t.q_bands = (int)(bands - t.q_band < Shape<BN>::kBands ? bands - t.q_band : Shape<BN>::kBands);
+    t.q_bands = (int)(bands - t.q_band < kBandsOf<BN> ? bands - t.q_band : kBandsOf<BN>);
     t.q_sub = (int)((q * BN) & 127) >> 5;
-    const int64_t p_n = a.p_rows - t.p_row < kP ? a.p_rows - t.p_row : kP;
+    const int64_t p_n = a.p_rows - t.p_row < PN ? a.p_rows - t.p_row : PN;
     const int64_t q_n = a.q_rows - t.q_row < BN ? a.q_rows - t.q_row : BN;
     t.tok0 = SWAP ? t.q_row : t.p_row;
     t.tok_n = (int)(SWAP ? q_n : p_n);
@@ -110,10 +113,10 @@ __device__ __forceinline__ Tile dense_tile(const KernelArgs &a, int64_t id)
 
 // first[e]: tiles of tokens before expert e.  An expert's tiles go over its
 // tokens first, so that blocks running at the same time share its weights.
-template <int BN, bool SWAP>
+template <int PN, int BN, bool SWAP>
 __device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t *first, int64_t id)
 {
-    constexpr int kTok = SWAP ? BN : kP, kWgt = SWAP ? kP : BN;
+    constexpr int kTok = SWAP ? BN : PN, kWgt = SWAP ? PN : BN;
     const int64_t nw = (a.wgt_rows + kWgt - 1) / kWgt;
     int lo = 0, hi = a.experts;  // the expert e with first[e] * nw <= id < first[e + 1] * nw
     while (hi - lo > 1) {
@@ -142,9 +145,56 @@ __device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t 
     t.p_band = SWAP ? wgt_band : tok_band;
     t.q_band = SWAP ? tok_band : wgt_band;
     const int left = SWAP ? 1 : a.wgt_bands - (w0 >> 7);
-    t.q_bands = left < Shape<BN>::kBands ? left : Shape<BN>::kBands;
+    t.q_bands = left < kBandsOf<BN> ? left : kBandsOf<BN>;
     t.q_sub = ((SWAP ? tok_row : w0) & 127) >> 5;
     return t;
+}
+
+// Tiles of the call.  Grouped: every thread of the block takes part and fills
+// first[0 .. experts].
+template <int PN, int BN, bool SWAP, bool GROUPED>
+__device__ __forceinline__ int64_t tile_count(const KernelArgs &a, int32_t *first)
+{
+    if constexpr (!GROUPED) {
+        return ((a.p_rows + PN - 1) / PN) * ((a.q_rows + BN - 1) / BN);
+    } else {
+        constexpr int kTok = SWAP ? BN : PN, kWgt = SWAP ? PN : BN;
+        const int lane = threadIdx.x & 31;
+        for (int e = threadIdx.x; e < a.experts; e += kThreads) {
+            const int start = __ldg(a.start + e), count = __ldg(a.count + e);
+            const bool good = start >= 0 && (start & 127) == 0 && count > 0 && (int64_t)start + count <= a.tok_rows;
+            first[e + 1] = good ? (count + kTok - 1) / kTok : 0;
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {  // inclusive scan
+            int32_t sum = 0;
+            for (int e0 = 0; e0 < a.experts; e0 += 32) {
+                int32_t v = e0 + lane < a.experts ? first[e0 + lane + 1] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t up = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o)
+                        v += up;
+                }
+                if (e0 + lane < a.experts)
+                    first[e0 + lane + 1] = sum + v;
+                sum += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (lane == 0)
+                first[0] = 0;
+        }
+        __syncthreads();
+        return (int64_t)first[a.experts] * ((a.wgt_rows + kWgt - 1) / kWgt);
+    }
+}
+
+template <int PN, int BN, bool SWAP, bool GROUPED>
+__device__ __forceinline__ Tile tile_at(const KernelArgs &a, const int32_t *first, int64_t id)
+{
+    if constexpr (GROUPED)
+        return grouped_tile<PN, BN, SWAP>(a, first, id);
+    else
+        return dense_tile<PN, BN, SWAP>(a, id);
 }
 
 // Wait with a limit, for what is in flight when a block gives up.
@@ -219,43 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_at;
     pdl_wait();
 
-    int64_t tiles;
-    if constexpr (GROUPED) {
-        constexpr int kTok = SWAP ? BN : kP, kWgt = SWAP ? kP : BN;
-        for (int e = threadIdx.x; e < a.experts; e += kThreads) {
-            const int start = __ldg(a.start + e), count = __ldg(a.count + e);
-            const bool good = start >= 0 && (start & 127) == 0 && count > 0 && (int64_t)start + count <= a.tok_rows;
-            first[e + 1] = good ? (count + kTok - 1) / kTok : 0;
-        }
-        __syncthreads();
-        if (warp == 0) {  // inclusive scan
-            int32_t sum = 0;
-            for (int e0 = 0; e0 < a.experts; e0 += 32) {
-                int32_t v = e0 + lane < a.experts ? first[e0 + lane + 1] : 0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int32_t up = __shfl_up_sync(0xffffffffu, v, o);
-                    if (lane >= o)
-                        v += up;
-                }
-                if (e0 + lane < a.experts)
-                    first[e0 + lane + 1] = sum + v;
-                sum += __shfl_sync(0xffffffffu, v, 31);
-            }
-            if (lane == 0)
-                first[0] = 0;
-        }
-        __syncthreads();
-        tiles = (int64_t)first[a.experts] * ((a.wgt_rows + kWgt - 1) / kWgt);
-    } else {
-        tiles = ((a.p_rows + kP - 1) / kP) * ((a.q_rows + BN - 1) / BN);
-    }
-    auto tile_of = [&](int64_t id) {
-        if constexpr (GROUPED)
-            return grouped_tile<BN, SWAP>(a, first, id);
-        else
-            return dense_tile<BN, SWAP>(a, id);
-    };
+    const int64_t tiles = tile_count<kP, BN, SWAP, GROUPED>(a, first);
+    auto tile_of = [&](int64_t id) { return tile_at<kP, BN, SWAP, GROUPED>(a, first, id); };
     const int steps = (a.kblocks + 3) >> 2;
 
     if (warp == 0) {
@@ -301,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ---- products ----
-        constexpr uint32_t idesc = idesc_nvfp4(BN);
+        constexpr uint32_t idesc = idesc_nvfp4(kP, BN);
         int s = 0;
         uint32_t parity = 0;
         int64_t n = 0;
@@ -411,6 +426,266 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// pair form: two blocks on one tile of 256 tokens by 256 weights
+// ---------------------------------------------------------------------------
+//
+// Each block of a cluster of two holds 128 tokens (P) and 128 of the weights'
+// rows (Q) in its shared memory; the first block's products (cta_group::2)
+// read both and write the accumulators of both, so that a block copies half of
+// what a 128 x 256 tile of its own would need.  The scale factors of Q's 256
+// rows are in both blocks.  Both blocks' copies complete on the first block's
+// barrier; its commits free the stages and publish the accumulators in both.
+//
+// Two accumulators of 256 columns and 48 columns of scale factors do not fit
+// the 512 columns: the accumulators share 64, which the output warps read
+// first and then give back, so that the next tile's products run during the
+// rest.  The output goes through shared memory, 32 rows of 64 bytes a warp and
+// step, and out by TMA.
+
+constexpr int kPairN = 256;
+constexpr int kPairCodes = kP * 128 + (kPairN / 2) * 128;   // bytes per stage and block
+constexpr int kPairSf = 4 * kSfTile * (1 + kPairN / 128);
+constexpr int kPairStages = 5;
+constexpr int kPairOut = 4 * 2 * 32 * 64;                   // staging: warps x buffers x rows x bytes
+constexpr int kPairSmem = 1024 + kPairStages * (kPairCodes + kPairSf) + kPairOut + 4 * 1032;
+constexpr int kPairAcc1 = 192;                              // column of the second accumulator
+constexpr int kPairSfP = kPairAcc1 + kPairN;                // columns of the scale factors
+constexpr int kPairSfQ = kPairSfP + 16;
+static_assert(kPairSfQ + 32 <= 512, "accumulators and scale factors fit tensor memory");
+static_assert(kPairSmem + 256 <= kSmemLimit, "stages and staging fit shared memory");
+
+template <bool GROUPED>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    nvfp4_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ CUtensorMap psf_map, const __grid_constant__ CUtensorMap qsf_map,
+                      const __grid_constant__ CUtensorMap out_map, const __grid_constant__ KernelArgs a)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[2 * kPairStages + 4];
+    __shared__ uint32_t tmem_at;
+    __shared__ int dead_flag;
+    const uint32_t pad = (1024 - (smem_u32(raw) & 1023)) & 1023;
+    const uint32_t codes = smem_u32(raw) + pad;
+    const uint32_t stage_out = codes + kPairStages * kPairCodes;
+    const uint32_t sf = stage_out + kPairOut;
+    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + kPairStages * (kPairCodes + kPairSf) + kPairOut);
+    volatile int *dead = &dead_flag;
+
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kPairStages;
+    const uint32_t acc_full = empty + 8 * kPairStages, acc_free = acc_full + 16, drained = acc_free + 8;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_full + 8, 1);
+        mbar_init(acc_free, 8);  // the output warps of both blocks
+        mbar_init(drained, 1);
+        mbar_fence_init();
+        dead_flag = 0;
+        tma_prefetch_map(&p_map);
+        tma_prefetch_map(&q_map);
+        tma_prefetch_map(&psf_map);
+        tma_prefetch_map(&qsf_map);
+        tma_prefetch_map(&out_map);
+    }
+    if (warp == 1)
+        pair_tmem_alloc(smem_u32(&tmem_at), 512);
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_at;
+    pdl_wait();
+
+    const int64_t tiles = tile_count<2 * kP, kPairN, false, GROUPED>(a, first);
+    auto tile_of = [&](int64_t id) { return tile_at<2 * kP, kPairN, false, GROUPED>(a, first, id); };
+    const int steps = (a.kblocks + 3) >> 2;
+    const int64_t id0 = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+    if (warp == 0) {
+        // ---- copies ----
+        int s = 0;
+        uint32_t parity = 0;
+        int64_t fills = 0;
+        bool good = true;
+        const uint32_t full0 = map_rank(full, 0);
+        for (int64_t id = id0; good && id < tiles; id += stride) {
+            const Tile t = tile_of(id);
+            const int32_t p_row = t.p_row + (int32_t)rank * kP, q_row = t.q_row + (int32_t)rank * (kPairN / 2);
+            const int32_t p_band = (int32_t)t.p_band + (int32_t)rank, q_band = (int32_t)t.q_band;
+            for (int kt = 0; kt < steps; ++kt) {
+                good = wait_warp(empty + 8 * s, parity ^ 1, dead);
+                if (!good)
+                    break;
+                const uint32_t bar = full0 + 8 * s;
+                const uint32_t c = codes + s * kPairCodes, f = sf + s * kPairSf;
+                if (elect_one()) {
+                    if (rank == 0)
+                        mbar_expect_tx(full + 8 * s, 2 * (kPairCodes + kPairSf));
+                    pair_load_2d(c, &p_map, kt * 128, p_row, bar);
+                    pair_load_2d(c + kP * 128, &q_map, kt * 128, q_row, bar);
+                    pair_load_2d(f, &psf_map, kt * 256, p_band, bar);
+                    pair_load_2d(f + 4 * kSfTile, &qsf_map, kt * 256, q_band, bar);
+                    pair_load_2d(f + 8 * kSfTile, &qsf_map, kt * 256, q_band + 1, bar);
+                }
+                __syncwarp();
+                ++fills;
+                if (++s == kPairStages) {
+                    s = 0;
+                    parity ^= 1;
+                }
+            }
+        }
+        pdl_launch_dependents();
+        if (!good && rank == 0) {  // both blocks' copies in flight land before the pair ends
+            for (int i = 0; i < kPairStages && i < fills; ++i) {
+                const int64_t fill = fills - 1 - i;
+                wait_last(full + 8 * (uint32_t)(fill % kPairStages), (uint32_t)(fill / kPairStages) & 1);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- products, by the first block for both ----
+        constexpr uint32_t idesc = idesc_nvfp4(2 * kP, kPairN);
+        int s = 0;
+        uint32_t parity = 0;
+        int64_t n = 0;
+        bool good = true;
+        for (int64_t id = id0; rank == 0 && good && id < tiles; id += stride, ++n) {
+            // the last tile's shared columns are read (before the first: at once)
+            good = wait_warp(acc_free, ((uint32_t)n & 1) ^ 1, dead);
+            if (!good)
+                break;
+            const uint32_t d = tmem + ((uint32_t)n & 1) * kPairAcc1;
+            for (int kt = 0; kt < steps; ++kt) {
+                good = wait_warp(full + 8 * s, parity, dead);
+                if (!good)
+                    break;
+                tmem_fence_after();
+                const int nkb = a.kblocks - 4 * kt < 4 ? a.kblocks - 4 * kt : 4;
+                if (elect_one()) {
+                    const uint32_t c = codes + s * kPairCodes;
+                    const uint64_t fd = desc_sf_tile(sf + s * kPairSf);
+                    const uint64_t pd = desc_swizzled128(c), qd = desc_swizzled128(c + kP * 128);
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+                        if (kb < nkb) {
+                            pair_copy_sf(tmem + kPairSfP + 4 * kb, fd + kb * (kSfTile >> 4));
+                            pair_copy_sf(tmem + kPairSfQ + 8 * kb, fd + (4 + kb) * (kSfTile >> 4));
+                            pair_copy_sf(tmem + kPairSfQ + 8 * kb + 4, fd + (8 + kb) * (kSfTile >> 4));
+                        }
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+                        if (kb < nkb)
+                            pair_mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + kPairSfP + 4 * kb,
+                                           tmem + kPairSfQ + 8 * kb, kt > 0 || kb > 0);
+                    pair_commit(empty + 8 * s);
+                    if (kt + 1 == steps)
+                        pair_commit(acc_full + 8 * ((uint32_t)n & 1));
+                }
+                __syncwarp();
+                if (++s == kPairStages) {
+                    s = 0;
+                    parity ^= 1;
+                }
+            }
+        }
+        if (!good) {
+            if (elect_one())
+                pair_commit(drained);
+            __syncwarp();
+            wait_last(drained, 0);
+        }
+    } else {
+        // ---- output ----
+        const int quad = warp & 3;
+        const uint32_t stage = stage_out + quad * (2 * 32 * 64);
+        const uint32_t free0 = map_rank(acc_free, 0);
+        int64_t n = 0;
+        uint32_t buf = 0;
+        for (int64_t id = id0; id < tiles; id += stride, ++n) {
+            const Tile t = tile_of(id);
+            const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
+            const uint32_t acc = (uint32_t)n & 1;
+            if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
+                break;
+            tmem_fence_after();
+            const int row0 = (int)rank * kP + quad * 32;  // of the warp's rows in the tile
+            const uint32_t src = tmem + acc * kPairAcc1 + ((uint32_t)quad << 21);
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const int c0 = ((i + (acc ? 0 : 6)) & 7) * 32;
+                uint32_t v[32];
+                tmem_load32(src + c0, v);
+                tmem_wait_loads();
+                if (i == 1) {  // the columns that the accumulators share are read
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(free0);
+                }
+                if (row0 >= t.tok_n || c0 >= t.wgt_n)
+                    continue;
+                const uint32_t to = stage + buf * (32 * 64);
+                if (lane == 0)
+                    bulk_wait_read<1>();
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        f[e] = __uint_as_float(v[8 * j + e]) * alpha;
+                    const uint4 w = pack8(f);
+                    // the 64-byte swizzle: 16-byte piece j of row l lies at j ^ (l / 2 % 4)
+                    const uint32_t at = to + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                                 : "memory");
+                }
+                const int rows = t.tok_n - row0;  // of the warp's 32 that the expert has
+                if (!GROUPED || rows >= 32) {
+                    fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&out_map, to, (int32_t)(t.wgt0 + c0), (int32_t)(t.tok0 + row0));
+                        bulk_commit();
+                    }
+                    buf ^= 1;
+                } else {
+                    __syncwarp();
+                    // 4 lanes per row, 16 bytes each
+#pragma unroll
+                    for (int r0 = 0; r0 < 32; r0 += 8) {
+                        const int r = r0 + (lane >> 2), j = lane & 3;
+                        uint4 w;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(to + r * 64 + ((j ^ ((r >> 1) & 3)) << 4)));
+                        if (r < rows && c0 + 8 * j < t.wgt_n)
+                            *reinterpret_cast<uint4 *>(a.out + (t.tok0 + row0 + r) * a.ldo + t.wgt0 + c0 + 8 * j) = w;
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0)
+            bulk_wait_read<0>();
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither block ends while the other's products or arrivals may reach it
+    if (warp == 1) {
+        tmem_fence_after();
+        pair_tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 
@@ -448,6 +723,67 @@ bool codes_map(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t K, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale factors in the 128x4 layout as [bands, kblocks * 512] bytes in boxes of
+// four tiles (2048 bytes, as 256 words of 8), zeros outside.
+bool sf_map(CUtensorMap *map, const uint8_t *sf, int64_t bands, int64_t kblocks)
+{
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)(kblocks * kSfTile / 8), (cuuint64_t)bands};
+    const cuuint64_t strides[1] = {(cuuint64_t)(kblocks * kSfTile)};
+    const cuuint32_t box[2] = {4 * kSfTile / 8, 1}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<uint8_t *>(sf), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The output [rows, N] in boxes of 32 rows by 32 columns, 64-byte swizzle.
+bool out_tile_map(CUtensorMap *map, uint16_t *out, int64_t rows, int64_t N, int64_t ldo)
+{
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ldo * 2)};
+    const cuuint32_t box[2] = {32, 32}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+KernelArgs kernel_args(const GemmArgs &g, bool swap)
+{
+    KernelArgs a{};
+    a.p_sf = swap ? g.wgt_sf : g.tok_sf;
+    a.q_sf = swap ? g.tok_sf : g.wgt_sf;
+    a.alpha = g.alpha;
+    a.out = g.out;
+    a.ldo = g.ldo;
+    a.p_rows = swap ? g.N : g.tok_rows;
+    a.q_rows = swap ? g.tok_rows : g.N;
+    a.kblocks = (int)((g.K + 63) / 64);
+    a.wgt_rows = (int)g.N;
+    a.wgt_bands = (int)((g.N + 127) / 128);
+    a.tok_rows = g.tok_rows;
+    a.start = g.start;
+    a.count = g.count;
+    a.experts = g.experts;
+    return a;
+}
+
+// Opt in to `bytes` of shared memory, once per kernel and device.
+template <typename Kernel>
+cudaError_t grow_smem(Kernel kernel, int bytes, std::atomic<bool> (&grown)[kMaxCachedDevices], int dev)
+{
+    if (dev < kMaxCachedDevices && grown[dev].load(std::memory_order_relaxed))
+        return cudaSuccess;
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess && dev < kMaxCachedDevices)
+        grown[dev].store(true, std::memory_order_relaxed);
+    return err;
+}
+
 template <int BN, bool SWAP, bool GROUPED>
 cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
 {
@@ -457,34 +793,15 @@ cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
     const int sms = current_device_sms(&dev);
     if (sms <= 0)
         return cudaErrorInvalidDevice;
-    if (dev >= kMaxCachedDevices || !grown[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t err = cudaFuncSetAttribute(nvfp4_gemm_kernel<BN, SWAP, GROUPED>,
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (err != cudaSuccess)
-            return err;
-        if (dev < kMaxCachedDevices)
-            grown[dev].store(true, std::memory_order_relaxed);
-    }
+    const cudaError_t err = grow_smem(nvfp4_gemm_kernel<BN, SWAP, GROUPED>, S::kSmem, grown, dev);
+    if (err != cudaSuccess)
+        return err;
     const int64_t wgt_rows = GROUPED ? g.experts * g.N : g.N;
     CUtensorMap p_map, q_map;
     if (!codes_map(&p_map, SWAP ? g.wgt : g.tok, SWAP ? wgt_rows : g.tok_rows, g.K, kP) ||
         !codes_map(&q_map, SWAP ? g.tok : g.wgt, SWAP ? g.tok_rows : wgt_rows, g.K, BN))
         return cudaErrorInvalidValue;
-    KernelArgs a{};
-    a.p_sf = SWAP ? g.wgt_sf : g.tok_sf;
-    a.q_sf = SWAP ? g.tok_sf : g.wgt_sf;
-    a.alpha = g.alpha;
-    a.out = g.out;
-    a.ldo = g.ldo;
-    a.p_rows = SWAP ? g.N : g.tok_rows;
-    a.q_rows = SWAP ? g.tok_rows : g.N;
-    a.kblocks = (int)((g.K + 63) / 64);
-    a.wgt_rows = (int)g.N;
-    a.wgt_bands = (int)((g.N + 127) / 128);
-    a.tok_rows = g.tok_rows;
-    a.start = g.start;
-    a.count = g.count;
-    a.experts = g.experts;
+    const KernelArgs a = kernel_args(g, SWAP);
     int64_t grid = sms;
     if (!GROUPED) {
         const int64_t tiles = ((a.p_rows + kP - 1) / kP) * ((a.q_rows + BN - 1) / BN);
@@ -492,6 +809,34 @@ cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
     }
     return launch_kernel(nvfp4_gemm_kernel<BN, SWAP, GROUPED>, dim3((unsigned)grid), dim3(kThreads), (size_t)S::kSmem,
                          stream, pdl, p_map, q_map, a);
+}
+
+template <bool GROUPED>
+cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
+{
+    static std::atomic<bool> grown[kMaxCachedDevices];
+    int dev = 0;
+    const int sms = current_device_sms(&dev);
+    if (sms < 2)
+        return cudaErrorInvalidDevice;
+    const cudaError_t err = grow_smem(nvfp4_pair_kernel<GROUPED>, kPairSmem, grown, dev);
+    if (err != cudaSuccess)
+        return err;
+    const KernelArgs a = kernel_args(g, false);
+    const int64_t experts = GROUPED ? g.experts : 1;
+    CUtensorMap p_map, q_map, psf_map, qsf_map, out_map;
+    if (!codes_map(&p_map, g.tok, g.tok_rows, g.K, kP) || !codes_map(&q_map, g.wgt, experts * g.N, g.K, kPairN / 2) ||
+        !sf_map(&psf_map, g.tok_sf, (g.tok_rows + 127) / 128, a.kblocks) ||
+        !sf_map(&qsf_map, g.wgt_sf, experts * a.wgt_bands, a.kblocks) ||
+        !out_tile_map(&out_map, g.out, g.tok_rows, g.N, g.ldo))
+        return cudaErrorInvalidValue;
+    int64_t pairs = sms / 2;
+    if (!GROUPED) {
+        const int64_t tiles = ((a.p_rows + 2 * kP - 1) / (2 * kP)) * ((a.q_rows + kPairN - 1) / kPairN);
+        pairs = tiles < pairs ? tiles : pairs;
+    }
+    return launch_kernel(nvfp4_pair_kernel<GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)kPairSmem,
+                         stream, pdl, p_map, q_map, psf_map, qsf_map, out_map, a);
 }
 
 // A tile of 32 tokens only where it is the call's only one, so that its scale
@@ -505,7 +850,7 @@ cudaError_t launch_by_tokens(const GemmArgs &g, int64_t tokens, bool pdl, cudaSt
     }
     if (tokens <= 64) return launch_tiles<64, true, GROUPED>(g, pdl, stream);
     if (tokens <= 128) return launch_tiles<128, true, GROUPED>(g, pdl, stream);
-    return launch_tiles<128, false, GROUPED>(g, pdl, stream);
+    return launch_pairs<GROUPED>(g, pdl, stream);
 }
 
 }  // namespace

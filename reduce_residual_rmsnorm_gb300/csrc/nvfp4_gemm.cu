@@ -160,7 +160,7 @@ __device__ __forceinline__ int64_t tile_count(const KernelArgs &a, int32_t *firs
     } else {
         constexpr int kTok = SWAP ? BN : PN, kWgt = SWAP ? PN : BN;
         const int lane = threadIdx.x & 31;
-        for (int e = threadIdx.x; e < a.experts; e += kThreads) {
+        for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
             const int start = __ldg(a.start + e), count = __ldg(a.count + e);
             const bool good = start >= 0 && (start & 127) == 0 && count > 0 && (int64_t)start + count <= a.tok_rows;
             first[e + 1] = good ? (count + kTok - 1) / kTok : 0;
@@ -446,7 +446,8 @@ constexpr int kPairN = 256;
 constexpr int kPairCodes = kP * 128 + (kPairN / 2) * 128;   // bytes per stage and block
 constexpr int kPairSf = 4 * kSfTile * (1 + kPairN / 128);
 constexpr int kPairStages = 5;
-constexpr int kPairOut = 4 * 2 * 32 * 64;                   // staging: warps x buffers x rows x bytes
+constexpr int kPairThreads = 320;
+constexpr int kPairOut = 8 * 32 * 64;                       // staging: warps x rows x bytes
 constexpr int kPairSmem = 1024 + kPairStages * (kPairCodes + kPairSf) + kPairOut + 4 * 1032;
 constexpr int kPairAcc1 = 192;                              // column of the second accumulator
 constexpr int kPairSfP = kPairAcc1 + kPairN;                // columns of the scale factors
@@ -455,7 +456,7 @@ static_assert(kPairSfQ + 32 <= 512, "accumulators and scale factors fit tensor m
 static_assert(kPairSmem + 256 <= kSmemLimit, "stages and staging fit shared memory");
 
 template <bool GROUPED>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     nvfp4_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap psf_map, const __grid_constant__ CUtensorMap qsf_map,
                       const __grid_constant__ CUtensorMap out_map, const __grid_constant__ KernelArgs a)
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_full + 8, 1);
-        mbar_init(acc_free, 8);  // the output warps of both blocks
+        mbar_init(acc_free, 16);  // the output warps of both blocks
         mbar_init(drained, 1);
         mbar_fence_init();
         dead_flag = 0;
@@ -601,12 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             wait_last(drained, 0);
         }
     } else {
-        // ---- output ----
-        const int quad = warp & 3;
-        const uint32_t stage = stage_out + quad * (2 * 32 * 64);
+        // ---- output: two warps for each 32 lanes, every other 32 columns ----
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t stage = stage_out + (warp - 2) * (32 * 64);
         const uint32_t free0 = map_rank(acc_free, 0);
         int64_t n = 0;
-        uint32_t buf = 0;
         for (int64_t id = id0; id < tiles; id += stride, ++n) {
             const Tile t = tile_of(id);
             const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
@@ -615,61 +615,55 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 break;
             tmem_fence_after();
             const int row0 = (int)rank * kP + quad * 32;  // of the warp's rows in the tile
+            const int rows = t.tok_n - row0;              // of its 32 that are the call's (the expert's)
             const uint32_t src = tmem + acc * kPairAcc1 + ((uint32_t)quad << 21);
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-                const int c0 = ((i + (acc ? 0 : 6)) & 7) * 32;
-                uint32_t v[32];
-                tmem_load32(src + c0, v);
-                tmem_wait_loads();
-                if (i == 1) {  // the columns that the accumulators share are read
-                    tmem_fence_before();
-                    __syncwarp();
+            // columns 192.. of the first accumulator are columns 0.. of the second
+            const int c_first = acc ? 0 : 6;
+            uint32_t v[2][32];
+            tmem_load32(src + ((half + c_first) & 7) * 32, v[0]);
+            tmem_wait_loads();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(free0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c0 = ((2 * i + half + c_first) & 7) * 32;
+                if (i < 3)
+                    tmem_load32(src + ((2 * i + 2 + half + c_first) & 7) * 32, v[(i + 1) & 1]);
+                if (rows > 0 && c0 < t.wgt_n) {
                     if (lane == 0)
-                        mbar_arrive_cluster(free0);
-                }
-                if (row0 >= t.tok_n || c0 >= t.wgt_n)
-                    continue;
-                const uint32_t to = stage + buf * (32 * 64);
-                if (lane == 0)
-                    bulk_wait_read<1>();
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f[e] = __uint_as_float(v[8 * j + e]) * alpha;
-                    const uint4 w = pack8(f);
-                    // the 64-byte swizzle: 16-byte piece j of row l lies at j ^ (l / 2 % 4)
-                    const uint32_t at = to + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                                 : "memory");
-                }
-                const int rows = t.tok_n - row0;  // of the warp's 32 that the expert has
-                if (!GROUPED || rows >= 32) {
-                    fence_async_proxy();
+                        bulk_wait_read<0>();
                     __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&out_map, to, (int32_t)(t.wgt0 + c0), (int32_t)(t.tok0 + row0));
-                        bulk_commit();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = __uint_as_float(v[i & 1][8 * j + e]) * alpha;
+                        // the 64-byte swizzle: 16-byte piece j of row l lies at j ^ (l / 2 % 4)
+                        st_shared(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pack8(f));
                     }
-                    buf ^= 1;
-                } else {
-                    __syncwarp();
-                    // 4 lanes per row, 16 bytes each
+                    if (!GROUPED || rows >= 32) {
+                        fence_async_proxy();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&out_map, stage, (int32_t)(t.wgt0 + c0), (int32_t)(t.tok0 + row0));
+                            bulk_commit();
+                        }
+                    } else {
+                        // not all of the rows are this expert's: 4 lanes per row, 16 bytes each
+                        __syncwarp();
 #pragma unroll
-                    for (int r0 = 0; r0 < 32; r0 += 8) {
-                        const int r = r0 + (lane >> 2), j = lane & 3;
-                        uint4 w;
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                     : "r"(to + r * 64 + ((j ^ ((r >> 1) & 3)) << 4)));
-                        if (r < rows && c0 + 8 * j < t.wgt_n)
-                            *reinterpret_cast<uint4 *>(a.out + (t.tok0 + row0 + r) * a.ldo + t.wgt0 + c0 + 8 * j) = w;
+                        for (int r0 = 0; r0 < 32; r0 += 8) {
+                            const int r = r0 + (lane >> 2), j = lane & 3;
+                            const uint4 w = ld_shared(stage + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+                            if (r < rows && c0 + 8 * j < t.wgt_n)
+                                *reinterpret_cast<uint4 *>(a.out + (t.tok0 + row0 + r) * a.ldo + t.wgt0 + c0 + 8 * j) = w;
+                        }
                     }
-                    __syncwarp();
                 }
+                tmem_wait_loads();
             }
         }
         if (lane == 0)
@@ -835,7 +829,7 @@ cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
         const int64_t tiles = ((a.p_rows + 2 * kP - 1) / (2 * kP)) * ((a.q_rows + kPairN - 1) / kPairN);
         pairs = tiles < pairs ? tiles : pairs;
     }
-    return launch_kernel(nvfp4_pair_kernel<GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)kPairSmem,
+    return launch_kernel(nvfp4_pair_kernel<GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), (size_t)kPairSmem,
                          stream, pdl, p_map, q_map, psf_map, qsf_map, out_map, a);
 }
 

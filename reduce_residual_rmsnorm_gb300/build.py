@@ -3,7 +3,9 @@
 Each ``csrc/*.cu`` translation unit is compiled in parallel, then linked into
 one shared object with the CUDA runtime linked statically, so the library
 loads on any machine with a CUDA driver.  No fast-math: IEEE division and
-square root, denormals kept (the quantisers depend on them).
+square root, denormals kept (the quantisers depend on them).  Beside it
+``_python_calls.so`` (g++ against the installed PyTorch) marshals the calls of
+``_nvfp4_moe``.
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libts_fused_norm.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+CALLS_SRC = os.path.join(CSRC, "python_calls.cpp")
+CALLS_PATH = os.path.join(PKG, "_python_calls.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,14 +46,14 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -63,6 +68,38 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if not force and up_to_date():
             return LIB_PATH
         return _build_locked(verbose, extra_flags)
+
+
+def _compile_calls() -> str:
+    """The object file of python_calls.cpp."""
+    import torch
+
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD_DIR, "python_calls.cpp.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
+           "-isystem", os.path.join(top, "include"),
+           "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-c", CALLS_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN", "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {CALLS_PATH} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def _build_locked(verbose: bool, extra_flags: list[str] | None) -> str:
@@ -80,13 +117,16 @@ def _build_locked(verbose: bool, extra_flags: list[str] | None) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(compile_one, sources()))
+        calls_obj = calls.result()
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_calls(calls_obj)
     return LIB_PATH
 
 

@@ -72,6 +72,7 @@ struct SortArgs {
     int32_t *row_src;
     int32_t *start;
     int32_t *count;
+    int warps;         // warps of a block that have entries
     int64_t per_warp;  // entries of one warp, a multiple of 32
 };
 

@@ -15,67 +15,83 @@ namespace {
 // sort
 // ---------------------------------------------------------------------------
 //
-// A counting sort in one cluster, each warp taking consecutive entries so that
-// the order is stable without atomics.  Pass 1 counts each warp's entries per
-// expert (the lanes with the same expert find each other with match.any; the
-// first adds their number).  A thread per expert then turns the counts into
-// offsets: over the warps of the block, over the blocks of the cluster (their
-// totals read through distributed shared memory) and, by a block scan of the
-// counts rounded up to `align`, over the experts.  Pass 2 reads the ids again
-// (from L2) and an entry's row is its warp's offset plus its rank among the
-// lanes with the same expert.
+// A counting sort in one cluster of 8 blocks, each warp taking consecutive
+// entries so that the order is stable.  Pass 1 counts each warp's entries per
+// expert in shared memory.  A thread per expert turns the counts into offsets:
+// over the warps of the block, over the blocks of the cluster (their totals read
+// through distributed shared memory) and, by a block scan of the counts rounded
+// up to `align`, over the experts.  Pass 2: an entry's row is its warp's offset
+// plus its rank among the lanes with the same expert (match.any).  What bounds
+// it is latency: ids are loaded 8 steps ahead, and kept in registers between
+// the passes where a warp has no more than 256.  16 x 8 entries over 64 experts
+// take 2.8 us (3.3 with starts at multiples of 128, whose row_src has 8 K
+// entries), 8192 x 8 entries 11.2 us.  One block instead of the cluster measured
+// 2.5 and 3.5 us on the first two, 6.1 against 3.4 at 2048 entries and 64
+// against 11.2 at 65536.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortCluster = 8;
+constexpr int kSortSteps = 8;  // steps of 32 entries whose ids are loaded together
 
 __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_constant__ SortArgs a)
 {
     extern __shared__ int32_t smem[];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nthr = blockDim.x, nw = nthr >> 5;
-    const int E = a.E;
-    int32_t *hist = smem;           // [nw][E] counts, then each warp's next row
-    int32_t *total = hist + nw * E; // [E] this block's counts
-    int32_t *used = total + E;      // [E] the row behind an expert's last entry
-    int32_t *next = used + E;       // [E] the next expert's first row
-    int32_t *carry = next + E;      // [32] the warps' sums
+    const int nthr = blockDim.x;
+    const int E = a.E, nw = a.warps;  // warps with entries
+    int32_t *hist = smem;             // [nw][E] counts, then each warp's next row after the expert's base
+    int32_t *total = hist + nw * E;   // [E] this block's counts
+    int32_t *base = total + E;        // [E] the expert's first row of this block
+    int32_t *used = base + E;         // [E] the row behind an expert's last entry
+    int32_t *next = used + E;         // [E] the next expert's first row
+    int32_t *carry = next + E;        // [32] the warps' sums
 
     for (int i = tid; i < nw * E; i += nthr)
         hist[i] = 0;
     __syncthreads();
     pdl_wait();
 
-    const int rank = (int)cluster.block_rank();
+    constexpr int blocks = kSortCluster;
+    const int rank = (int)blockIdx.x;  // the grid is one cluster
     const int64_t begin = ((int64_t)rank * nw + warp) * a.per_warp;
-    const int64_t end = begin + a.per_warp < a.n ? begin + a.per_warp : a.n;
+    const int64_t stop = begin + a.per_warp < a.n ? begin + a.per_warp : a.n;
+    const int64_t end = warp < nw ? stop : begin;
     int32_t *mine = hist + warp * E;
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int id = i < end ? __ldg(a.ids + i) : -1;
-        const bool held = id >= 0 && id < E;
-        const unsigned same = __match_any_sync(0xffffffffu, held ? id : -1);
-        if (held && lane == __ffs(same) - 1)
-            mine[id] += __popc(same);
-        __syncwarp();
+    int id[kSortSteps];
+    auto load = [&](int64_t i0) {
+#pragma unroll
+        for (int u = 0; u < kSortSteps; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            const int v = i < end ? __ldg(a.ids + i) : -1;
+            id[u] = v >= 0 && v < E ? v : -1;
+        }
+    };
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortSteps) {
+        load(i0);
+#pragma unroll
+        for (int u = 0; u < kSortSteps; ++u)
+            if (id[u] >= 0)
+                atomicAdd(mine + id[u], 1);
     }
     __syncthreads();
-    for (int e = tid; e < E; e += nthr) {  // counts -> offsets inside the block
+    if (tid < E) {  // counts -> offsets inside the block
         int32_t sum = 0;
+#pragma unroll 4
         for (int w = 0; w < nw; ++w) {
-            const int32_t c = hist[w * E + e];
-            hist[w * E + e] = sum;
+            const int32_t c = hist[w * E + tid];
+            hist[w * E + tid] = sum;
             sum += c;
         }
-        total[e] = sum;
+        total[tid] = sum;
     }
     cluster.sync();
 
     // a thread per expert: its count in the whole call and in the blocks before
     // this one, and its first row by a scan of the rounded counts
-    const int blocks = (int)cluster.num_blocks();
     int32_t before = 0, all = 0;
     if (tid < E) {
+#pragma unroll
         for (int b = 0; b < blocks; ++b) {
             const int32_t c = *cluster.map_shared_rank(total + tid, b);
             before += b < rank ? c : 0;
@@ -99,8 +115,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
     if (tid < E) {
         used[tid] = start + all;
         next[tid] = start + padded;
-        for (int w = 0; w < nw; ++w)
-            hist[w * E + tid] += start + before;
+        base[tid] = start + before;
         if (rank == 0) {
             a.start[tid] = start;
             a.count[tid] = all;
@@ -109,33 +124,39 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
         }
     }
     __syncthreads();
+    pdl_launch_dependents();
+
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortSteps) {
+        if (a.per_warp > 32 * kSortSteps)
+            load(i0);
+#pragma unroll
+        for (int u = 0; u < kSortSteps; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            if (i - lane >= end)
+                break;
+            const bool held = id[u] >= 0;
+            const unsigned same = __match_any_sync(0xffffffffu, id[u]);
+            int32_t row = -1;
+            if (held)
+                row = base[id[u]] + mine[id[u]] + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (held && lane == __ffs(same) - 1)
+                mine[id[u]] += __popc(same);
+            __syncwarp();
+            if (i < end) {
+                a.row_of[i] = row;
+                if (held)
+                    a.row_src[row] = (int32_t)i;
+            }
+        }
+    }
     // rows without an entry: behind each expert's last one, and behind the last expert
-    const int threads = blocks * nthr;
-    for (int e = rank * nw + warp; e < E; e += blocks * nw)
+    const int threads = blocks * nthr, warps = threads >> 5;
+    for (int e = rank * (nthr >> 5) + warp; e < E; e += warps)
         for (int32_t r = used[e] + lane; r < next[e]; r += 32)
             a.row_src[r] = -1;
     for (int64_t r = next[E - 1] + (int64_t)rank * nthr + tid; r < a.rows; r += threads)
         a.row_src[r] = -1;
-    pdl_launch_dependents();
-
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int id = i < end ? __ldg(a.ids + i) : -1;
-        const bool held = id >= 0 && id < E;
-        const unsigned same = __match_any_sync(0xffffffffu, held ? id : -1);
-        int32_t row = -1;
-        if (held)
-            row = mine[id] + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-        if (held && lane == __ffs(same) - 1)
-            mine[id] += __popc(same);
-        __syncwarp();
-        if (i < end) {
-            a.row_of[i] = row;
-            if (held)
-                a.row_src[row] = (int32_t)i;
-        }
-    }
     cluster.sync();  // a block's counts stay readable until every block is done
 }
 
@@ -261,15 +282,17 @@ __global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const __
 cudaError_t launch_sort(const SortArgs &a, bool pdl, cudaStream_t stream)
 {
     SortArgs b = a;
-    // a block for up to 8192 entries (8 steps of a warp), else a cluster
-    const int blocks = a.n > 8192 ? kSortCluster : 1;
-    const int64_t want = (a.n + 31) / 32;
-    int warps = blocks > 1 || want >= 32 ? 32 : (want < 1 ? 1 : (int)want);
-    const int least = (a.E + 31) / 32;  // a thread per expert
-    warps = warps < least ? least : warps;
-    const int64_t all = (int64_t)blocks * warps;
+    constexpr int blocks = kSortCluster;
+    const int64_t steps = (a.n + 32 * blocks - 1) / (32 * blocks);  // of 32 entries, per block
+    b.warps = steps < 1 ? 1 : (steps < 32 ? (int)steps : 32);
+    const int64_t all = (int64_t)blocks * b.warps;
     b.per_warp = ((a.n + all - 1) / all + 31) / 32 * 32;
-    const size_t smem = (size_t)((warps + 3) * a.E + 32) * sizeof(int32_t);
+    // a thread per expert, and enough to fill row_src with few stores each
+    const int64_t fill = a.rows / (8 * blocks) < 1024 ? (a.rows / (8 * blocks) + 31) / 32 * 32 : 1024;
+    int nthr = b.warps * 32;
+    nthr = nthr < (a.E + 31) / 32 * 32 ? (a.E + 31) / 32 * 32 : nthr;
+    nthr = nthr < fill ? (int)fill : nthr;
+    const size_t smem = (size_t)((b.warps + 4) * a.E + 32) * sizeof(int32_t);
     static std::atomic<bool> grown[kMaxCachedDevices];
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -277,27 +300,13 @@ cudaError_t launch_sort(const SortArgs &a, bool pdl, cudaStream_t stream)
         return err;
     if (dev >= kMaxCachedDevices || !grown[dev].load(std::memory_order_relaxed)) {
         err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (35 * 1024 + 32) * (int)sizeof(int32_t));
+                                   (36 * 1024 + 32) * (int)sizeof(int32_t));
         if (err != cudaSuccess)
             return err;
         if (dev < kMaxCachedDevices)
             grown[dev].store(true, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3((unsigned)(warps * 32));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)blocks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, moe_sort_kernel, b);
+    return launch_clusters(moe_sort_kernel, dim3(blocks), dim3((unsigned)nthr), smem, stream, pdl, blocks, b);
 }
 
 cudaError_t launch_combine(const CombineArgs &a, bool pdl, cudaStream_t stream)

@@ -39,12 +39,14 @@ constexpr int kSmemLimit = 232448;    // bytes of shared memory of a block
 template <int BN>
 constexpr int kBandsOf = BN > 128 ? BN / 128 : 1;  // 128-row bands of Q's scale factors
 
-template <int BN>
+// SPLIT: room for the partial sums of a tile whose K is split over a cluster.
+template <int BN, bool SPLIT>
 struct Shape {
     static constexpr int kBands = kBandsOf<BN>;
     static constexpr int kCodes = kP * 128 + BN * 128;      // bytes of codes per stage
     static constexpr int kSf = 4 * kSfTile * (1 + kBands);  // bytes of scale factors per stage
-    static constexpr int kFixed = 1024 /* alignment */ + 4 * 1032 /* experts' first tiles */;
+    static constexpr int kPartials = SPLIT ? BN * kP * 4 : 0;
+    static constexpr int kFixed = 1024 /* alignment */ + 4 * 1032 /* experts' first tiles */ + kPartials;
     static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
     static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
     static constexpr int kSfP = 2 * BN;       // tensor-memory column of P's scale factors
@@ -61,6 +63,7 @@ struct KernelArgs {
     int64_t ldo;
     int64_t p_rows, q_rows;  // dense: rows of P and Q
     int kblocks;             // ceil(K / 64)
+    int split_log2;          // dense, few tokens: 2^split_log2 blocks of a cluster share a tile's K
     int wgt_rows;            // grouped: N
     int wgt_bands;           // grouped: 128-row bands of an expert's scale factors
     int64_t tok_rows;        // grouped: rows of the sorted tokens
@@ -226,25 +229,36 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_slow(bar, parity, dead));
 }
 
-template <int BN, bool SWAP, bool GROUPED>
+// As wait_warp; what other blocks of the cluster wrote before they arrived is visible.
+__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int *dead)
+{
+    const bool good = wait_warp(bar, parity, dead);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return good;
+}
+
+template <int BN, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1)
     nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ KernelArgs a)
 {
-    using S = Shape<BN>;
+    using S = Shape<BN, !GROUPED>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * S::kStages + 5];
+    __shared__ uint64_t bars[2 * S::kStages + 6];
     __shared__ uint32_t tmem_at;
     __shared__ int dead_flag;
     const uint32_t pad = (1024 - (smem_u32(raw) & 1023)) & 1023;
     const uint32_t codes = smem_u32(raw) + pad;
     const uint32_t sf = codes + S::kStages * S::kCodes;
-    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + S::kStages * (S::kCodes + S::kSf));
+    const uint32_t sums = sf + S::kStages * S::kSf;  // the cluster's partial sums of this block's share
+    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + S::kStages * (S::kCodes + S::kSf) + S::kPartials);
     volatile int *dead = &dead_flag;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
     const uint32_t acc_full = empty + 8 * S::kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+    const uint32_t partial = drained + 8;  // the cluster's partial sums are here
+    const int lg = GROUPED ? 0 : a.split_log2, split = 1 << lg, rank = GROUPED ? 0 : (int)cluster_rank();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -256,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(acc_empty + 8 * i, 4);
         }
         mbar_init(drained, 1);
+        mbar_init(partial, 4 * split);
         mbar_fence_init();
         dead_flag = 0;
         tma_prefetch_map(&p_map);
@@ -265,13 +280,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&tmem_at), S::kColumns);
     tmem_fence_before();
     __syncthreads();
+    if (split > 1)
+        cluster_sync();  // the barriers of every block are ready
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
     pdl_wait();
 
-    const int64_t tiles = tile_count<kP, BN, SWAP, GROUPED>(a, first);
-    auto tile_of = [&](int64_t id) { return tile_at<kP, BN, SWAP, GROUPED>(a, first, id); };
-    const int steps = (a.kblocks + 3) >> 2;
+    const int64_t tiles = tile_count<kP, BN, true, GROUPED>(a, first);
+    auto tile_of = [&](int64_t id) { return tile_at<kP, BN, true, GROUPED>(a, first, id); };
+    // this block's steps of 256 elements of K, and its tiles
+    const int all_steps = (a.kblocks + 3) >> 2;
+    const int kt0 = (all_steps * rank) >> lg, kt1 = (all_steps * (rank + 1)) >> lg;
+    const int64_t id0 = blockIdx.x >> lg, stride = gridDim.x >> lg;
 
     if (warp == 0) {
         // ---- copies ----
@@ -279,11 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0;
         int64_t fills = 0;
         bool good = true;
-        for (int64_t id = blockIdx.x; good && id < tiles; id += gridDim.x) {
+        for (int64_t id = id0; good && id < tiles; id += stride) {
             const Tile t = tile_of(id);
             const uint8_t *psf = a.p_sf + t.p_band * a.kblocks * kSfTile;
             const uint8_t *qsf = a.q_sf + t.q_band * a.kblocks * kSfTile;
-            for (int kt = 0; kt < steps; ++kt) {
+            for (int kt = kt0; kt < kt1; ++kt) {
                 good = wait_warp(empty + 8 * s, parity ^ 1, dead);
                 if (!good)
                     break;
@@ -321,14 +341,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0;
         int64_t n = 0;
         bool good = true;
-        for (int64_t id = blockIdx.x; good && id < tiles; id += gridDim.x, ++n) {
-            const int q_sub = SWAP ? tile_of(id).q_sub : 0;
+        for (int64_t id = id0; good && id < tiles; id += stride, ++n) {
+            const int q_sub = GROUPED ? tile_of(id).q_sub : 0;
             const uint32_t acc = (uint32_t)n & 1;
             good = wait_warp(acc_empty + 8 * acc, ((uint32_t)(n >> 1) & 1) ^ 1, dead);
             if (!good)
                 break;
             const uint32_t d = tmem + acc * BN;
-            for (int kt = 0; kt < steps; ++kt) {
+            for (int kt = kt0; kt < kt1; ++kt) {
                 good = wait_warp(full + 8 * s, parity, dead);
                 if (!good)
                     break;
@@ -351,9 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kb = 0; kb < 4; ++kb)
                         if (kb < nkb)
                             mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + S::kSfP + 4 * kb,
-                                      tmem + S::kSfQ + 4 * kb * S::kBands + q_sub, kt > 0 || kb > 0);
+                                      tmem + S::kSfQ + 4 * kb * S::kBands + q_sub, kt > kt0 || kb > 0);
                     mma_commit(empty + 8 * s);
-                    if (kt + 1 == steps)
+                    if (kt + 1 == kt1)
                         mma_commit(acc_full + 8 * acc);
                 }
                 __syncwarp();
@@ -373,8 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- output ----
         const int quad = warp & 3;
         const int row = quad * 32 + lane;  // lane of the accumulator
+        // byte offset of block r's partial sums of four tokens, the i-th of a block's share: [split][BN / 4 / split][128][4]
+        auto sum_at = [&](int r, int i) { return 16 * ((((r * (BN / 4)) >> lg) + i) * kP + row); };
         int64_t n = 0;
-        for (int64_t id = blockIdx.x; id < tiles; id += gridDim.x, ++n) {
+        for (int64_t id = id0; id < tiles; id += stride, ++n) {
             const Tile t = tile_of(id);
             const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
             const uint32_t acc = (uint32_t)n & 1;
@@ -383,32 +405,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < BN; c0 += 32) {
+                if (c0 >= t.tok_n)
+                    break;
                 uint32_t v[32];
                 tmem_load32(tmem + acc * BN + ((uint32_t)quad << 21) + c0, v);
                 tmem_wait_loads();
-                if constexpr (SWAP) {
-                    // lane = output column, register = token
-                    if (row < t.wgt_n) {
-                        uint16_t *o = a.out + (t.tok0 + c0) * a.ldo + t.wgt0 + row;
+                // lane = output column, register = token
+                if (split > 1) {
+                    // four tokens' partial sums to the block that sums them up
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c0 + i < t.tok_n)
-                                o[i * a.ldo] = (uint16_t)pack_bf16x2(__uint_as_float(v[i]) * alpha, 0.0f);
+                    for (int j = 0; j < 8; ++j) {
+                        const int four = (c0 >> 2) + j;
+                        if (4 * four < t.tok_n)
+                            st_cluster(map_rank(sums + sum_at(rank, four >> lg), four & (split - 1)),
+                                       make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
                     }
-                } else {
-                    if (row < t.tok_n) {
-                        uint16_t *o = a.out + (t.tok0 + row) * a.ldo + t.wgt0 + c0;
+                } else if (row < t.wgt_n) {
+                    uint16_t *o = a.out + (t.tok0 + c0) * a.ldo + t.wgt0 + row;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            if (c0 + i < t.wgt_n) {
-                                float f[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    f[e] = __uint_as_float(v[i + e]) * alpha;
-                                st_v4(o + i, pack8(f));
-                            }
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        if (c0 + i < t.tok_n)
+                            o[i * a.ldo] = (uint16_t)pack_bf16x2(__uint_as_float(v[i]) * alpha, 0.0f);
                 }
+            }
+            if (split > 1) {  // the only tile of the cluster
+                const int fours = (t.tok_n + 3) >> 2;
+                __syncwarp();
+                if (lane < split && lane < fours)
+                    mbar_arrive_cluster(map_rank(partial, lane));
+                if (rank >= fours || !wait_warp_cluster(partial, 0, dead))
+                    break;
+                for (int four = rank; four < fours; four += split) {
+                    float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int r = 0; r < split; ++r) {  // in the blocks' order
+                        const uint4 w = ld_shared(sums + sum_at(r, four >> lg));
+                        f[0] += __uint_as_float(w.x);
+                        f[1] += __uint_as_float(w.y);
+                        f[2] += __uint_as_float(w.z);
+                        f[3] += __uint_as_float(w.w);
+                    }
+                    // two neighbouring columns in one word: even lanes the first two tokens, odd lanes the others
+                    const bool odd = lane & 1;
+                    const float p0 = __shfl_xor_sync(0xffffffffu, odd ? f[0] : f[2], 1);
+                    const float p1 = __shfl_xor_sync(0xffffffffu, odd ? f[1] : f[3], 1);
+                    const int tok = 4 * four + (odd ? 2 : 0);
+                    uint16_t *o = a.out + (t.tok0 + tok) * a.ldo + t.wgt0 + (row & ~1);
+                    if (row < t.wgt_n && tok < t.tok_n)
+                        *reinterpret_cast<uint32_t *>(o) =
+                            odd ? pack_bf16x2(p0 * alpha, f[2] * alpha) : pack_bf16x2(f[0] * alpha, p0 * alpha);
+                    if (row < t.wgt_n && tok + 1 < t.tok_n)
+                        *reinterpret_cast<uint32_t *>(o + a.ldo) =
+                            odd ? pack_bf16x2(p1 * alpha, f[3] * alpha) : pack_bf16x2(f[1] * alpha, p1 * alpha);
+                }
+                break;
             }
             tmem_fence_before();
             __syncwarp();
@@ -442,49 +491,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rest.  The output goes through shared memory, 32 rows of 64 bytes a warp and
 // step, and out by TMA.
 
-constexpr int kPairN = 256;
-constexpr int kPairCodes = kP * 128 + (kPairN / 2) * 128;   // bytes per stage and block
-constexpr int kPairSf = 4 * kSfTile * (1 + kPairN / 128);
-constexpr int kPairStages = 5;
 constexpr int kPairThreads = 320;
-constexpr int kPairOut = 8 * 32 * 64;                       // staging: warps x rows x bytes
-constexpr int kPairSmem = 1024 + kPairStages * (kPairCodes + kPairSf) + kPairOut + 4 * 1032;
-constexpr int kPairAcc1 = 192;                              // column of the second accumulator
-constexpr int kPairSfP = kPairAcc1 + kPairN;                // columns of the scale factors
-constexpr int kPairSfQ = kPairSfP + 16;
-static_assert(kPairSfQ + 32 <= 512, "accumulators and scale factors fit tensor memory");
-static_assert(kPairSmem + 256 <= kSmemLimit, "stages and staging fit shared memory");
 
-template <bool GROUPED>
+template <int BN>
+struct PairShape {
+    static constexpr bool kShared = BN == 256;                   // the accumulators share columns
+    static constexpr int kBands = BN / 128;
+    static constexpr int kCodes = kP * 128 + (BN / 2) * 128;     // bytes per stage and block
+    static constexpr int kSf = 4 * kSfTile * (1 + kBands);
+    static constexpr int kOut = 8 * 32 * 64;                     // staging: warps x rows x bytes
+    static constexpr int kFixed = 1024 + kOut + 4 * 1032;
+    static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
+    static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
+    static constexpr int kAcc1 = kShared ? BN - 64 : BN;         // column of the second accumulator
+    static constexpr int kSfP = kAcc1 + BN;                      // columns of the scale factors
+    static constexpr int kSfQ = kSfP + 16;
+    static constexpr int kChunks = BN / 32;                      // 32-column pieces of the output
+    static_assert(kSfQ + 16 * kBands <= 512, "accumulators and scale factors fit tensor memory");
+};
+
+template <int BN, bool GROUPED>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     nvfp4_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap psf_map, const __grid_constant__ CUtensorMap qsf_map,
                       const __grid_constant__ CUtensorMap out_map, const __grid_constant__ KernelArgs a)
 {
+    using S = PairShape<BN>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * kPairStages + 4];
+    __shared__ uint64_t bars[2 * S::kStages + 5];
     __shared__ uint32_t tmem_at;
     __shared__ int dead_flag;
     const uint32_t pad = (1024 - (smem_u32(raw) & 1023)) & 1023;
     const uint32_t codes = smem_u32(raw) + pad;
-    const uint32_t stage_out = codes + kPairStages * kPairCodes;
-    const uint32_t sf = stage_out + kPairOut;
-    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + kPairStages * (kPairCodes + kPairSf) + kPairOut);
+    const uint32_t stage_out = codes + S::kStages * S::kCodes;
+    const uint32_t sf = stage_out + S::kOut;
+    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + S::kStages * (S::kCodes + S::kSf) + S::kOut);
     volatile int *dead = &dead_flag;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kPairStages;
-    const uint32_t acc_full = empty + 8 * kPairStages, acc_free = acc_full + 16, drained = acc_free + 8;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
+    const uint32_t acc_full = empty + 8 * S::kStages, acc_free = acc_full + 16, drained = acc_free + 16;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairStages; ++s) {
+        for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_full + 8, 1);
-        mbar_init(acc_free, 16);  // the output warps of both blocks
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_free + 8 * i, 16);  // the output warps of both blocks
+        }
         mbar_init(drained, 1);
         mbar_fence_init();
         dead_flag = 0;
@@ -503,8 +560,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = tmem_at;
     pdl_wait();
 
-    const int64_t tiles = tile_count<2 * kP, kPairN, false, GROUPED>(a, first);
-    auto tile_of = [&](int64_t id) { return tile_at<2 * kP, kPairN, false, GROUPED>(a, first, id); };
+    const int64_t tiles = tile_count<2 * kP, BN, false, GROUPED>(a, first);
+    auto tile_of = [&](int64_t id) { return tile_at<2 * kP, BN, false, GROUPED>(a, first, id); };
     const int steps = (a.kblocks + 3) >> 2;
     const int64_t id0 = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
@@ -517,26 +574,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t full0 = map_rank(full, 0);
         for (int64_t id = id0; good && id < tiles; id += stride) {
             const Tile t = tile_of(id);
-            const int32_t p_row = t.p_row + (int32_t)rank * kP, q_row = t.q_row + (int32_t)rank * (kPairN / 2);
+            const int32_t p_row = t.p_row + (int32_t)rank * kP, q_row = t.q_row + (int32_t)rank * (BN / 2);
             const int32_t p_band = (int32_t)t.p_band + (int32_t)rank, q_band = (int32_t)t.q_band;
             for (int kt = 0; kt < steps; ++kt) {
                 good = wait_warp(empty + 8 * s, parity ^ 1, dead);
                 if (!good)
                     break;
                 const uint32_t bar = full0 + 8 * s;
-                const uint32_t c = codes + s * kPairCodes, f = sf + s * kPairSf;
+                const uint32_t c = codes + s * S::kCodes, f = sf + s * S::kSf;
                 if (elect_one()) {
                     if (rank == 0)
-                        mbar_expect_tx(full + 8 * s, 2 * (kPairCodes + kPairSf));
+                        mbar_expect_tx(full + 8 * s, 2 * (S::kCodes + S::kSf));
                     pair_load_2d(c, &p_map, kt * 128, p_row, bar);
                     pair_load_2d(c + kP * 128, &q_map, kt * 128, q_row, bar);
                     pair_load_2d(f, &psf_map, kt * 256, p_band, bar);
-                    pair_load_2d(f + 4 * kSfTile, &qsf_map, kt * 256, q_band, bar);
-                    pair_load_2d(f + 8 * kSfTile, &qsf_map, kt * 256, q_band + 1, bar);
+#pragma unroll
+                    for (int b = 0; b < S::kBands; ++b)
+                        pair_load_2d(f + 4 * (1 + b) * kSfTile, &qsf_map, kt * 256, q_band + b, bar);
                 }
                 __syncwarp();
                 ++fills;
-                if (++s == kPairStages) {
+                if (++s == S::kStages) {
                     s = 0;
                     parity ^= 1;
                 }
@@ -544,24 +602,26 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
         pdl_launch_dependents();
         if (!good && rank == 0) {  // both blocks' copies in flight land before the pair ends
-            for (int i = 0; i < kPairStages && i < fills; ++i) {
+            for (int i = 0; i < S::kStages && i < fills; ++i) {
                 const int64_t fill = fills - 1 - i;
-                wait_last(full + 8 * (uint32_t)(fill % kPairStages), (uint32_t)(fill / kPairStages) & 1);
+                wait_last(full + 8 * (uint32_t)(fill % S::kStages), (uint32_t)(fill / S::kStages) & 1);
             }
         }
     } else if (warp == 1) {
         // ---- products, by the first block for both ----
-        constexpr uint32_t idesc = idesc_nvfp4(2 * kP, kPairN);
+        constexpr uint32_t idesc = idesc_nvfp4(2 * kP, BN);
         int s = 0;
         uint32_t parity = 0;
         int64_t n = 0;
         bool good = true;
         for (int64_t id = id0; rank == 0 && good && id < tiles; id += stride, ++n) {
-            // the last tile's shared columns are read (before the first: at once)
-            good = wait_warp(acc_free, ((uint32_t)n & 1) ^ 1, dead);
+            // the tile before has given the shared columns back, or the one before
+            // that its accumulator (without one: at once)
+            good = S::kShared ? wait_warp(acc_free, ((uint32_t)n & 1) ^ 1, dead)
+                              : wait_warp(acc_free + 8 * ((uint32_t)n & 1), ((uint32_t)(n >> 1) & 1) ^ 1, dead);
             if (!good)
                 break;
-            const uint32_t d = tmem + ((uint32_t)n & 1) * kPairAcc1;
+            const uint32_t d = tmem + ((uint32_t)n & 1) * S::kAcc1;
             for (int kt = 0; kt < steps; ++kt) {
                 good = wait_warp(full + 8 * s, parity, dead);
                 if (!good)
@@ -569,27 +629,29 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 tmem_fence_after();
                 const int nkb = a.kblocks - 4 * kt < 4 ? a.kblocks - 4 * kt : 4;
                 if (elect_one()) {
-                    const uint32_t c = codes + s * kPairCodes;
-                    const uint64_t fd = desc_sf_tile(sf + s * kPairSf);
+                    const uint32_t c = codes + s * S::kCodes;
+                    const uint64_t fd = desc_sf_tile(sf + s * S::kSf);
                     const uint64_t pd = desc_swizzled128(c), qd = desc_swizzled128(c + kP * 128);
 #pragma unroll
                     for (int kb = 0; kb < 4; ++kb)
                         if (kb < nkb) {
-                            pair_copy_sf(tmem + kPairSfP + 4 * kb, fd + kb * (kSfTile >> 4));
-                            pair_copy_sf(tmem + kPairSfQ + 8 * kb, fd + (4 + kb) * (kSfTile >> 4));
-                            pair_copy_sf(tmem + kPairSfQ + 8 * kb + 4, fd + (8 + kb) * (kSfTile >> 4));
+                            pair_copy_sf(tmem + S::kSfP + 4 * kb, fd + kb * (kSfTile >> 4));
+#pragma unroll
+                            for (int b = 0; b < S::kBands; ++b)
+                                pair_copy_sf(tmem + S::kSfQ + 4 * (S::kBands * kb + b),
+                                             fd + (4 * (1 + b) + kb) * (kSfTile >> 4));
                         }
 #pragma unroll
                     for (int kb = 0; kb < 4; ++kb)
                         if (kb < nkb)
-                            pair_mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + kPairSfP + 4 * kb,
-                                           tmem + kPairSfQ + 8 * kb, kt > 0 || kb > 0);
+                            pair_mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + S::kSfP + 4 * kb,
+                                           tmem + S::kSfQ + 4 * S::kBands * kb, kt > 0 || kb > 0);
                     pair_commit(empty + 8 * s);
                     if (kt + 1 == steps)
                         pair_commit(acc_full + 8 * ((uint32_t)n & 1));
                 }
                 __syncwarp();
-                if (++s == kPairStages) {
+                if (++s == S::kStages) {
                     s = 0;
                     parity ^= 1;
                 }
@@ -616,21 +678,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             tmem_fence_after();
             const int row0 = (int)rank * kP + quad * 32;  // of the warp's rows in the tile
             const int rows = t.tok_n - row0;              // of its 32 that are the call's (the expert's)
-            const uint32_t src = tmem + acc * kPairAcc1 + ((uint32_t)quad << 21);
-            // columns 192.. of the first accumulator are columns 0.. of the second
-            const int c_first = acc ? 0 : 6;
+            const uint32_t src = tmem + acc * S::kAcc1 + ((uint32_t)quad << 21);
+            // 32-column pieces, this warp's first one among the shared: the last two of
+            // the first accumulator, the first two of the second
+            const int first_piece = half + (S::kShared && acc == 0 ? S::kChunks - 2 : 0);
+            auto column = [&](int i) { return ((2 * i + first_piece) & (S::kChunks - 1)) * 32; };
             uint32_t v[2][32];
-            tmem_load32(src + ((half + c_first) & 7) * 32, v[0]);
+            tmem_load32(src + column(0), v[0]);
             tmem_wait_loads();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(free0);
+            if (S::kShared) {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(free0);
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c0 = ((2 * i + half + c_first) & 7) * 32;
-                if (i < 3)
-                    tmem_load32(src + ((2 * i + 2 + half + c_first) & 7) * 32, v[(i + 1) & 1]);
+            for (int i = 0; i < S::kChunks / 2; ++i) {
+                const int c0 = column(i);
+                if (i + 1 < S::kChunks / 2)
+                    tmem_load32(src + column(i + 1), v[(i + 1) & 1]);
                 if (rows > 0 && c0 < t.wgt_n) {
                     if (lane == 0)
                         bulk_wait_read<0>();
@@ -664,6 +730,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
                 tmem_wait_loads();
+            }
+            if (!S::kShared) {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(free0 + 8 * acc);
             }
         }
         if (lane == 0)
@@ -778,34 +850,36 @@ cudaError_t grow_smem(Kernel kernel, int bytes, std::atomic<bool> (&grown)[kMaxC
     return err;
 }
 
-template <int BN, bool SWAP, bool GROUPED>
+template <int BN, bool GROUPED>
 cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
 {
-    using S = Shape<BN>;
+    using S = Shape<BN, !GROUPED>;
     static std::atomic<bool> grown[kMaxCachedDevices];
     int dev = 0;
     const int sms = current_device_sms(&dev);
     if (sms <= 0)
         return cudaErrorInvalidDevice;
-    const cudaError_t err = grow_smem(nvfp4_gemm_kernel<BN, SWAP, GROUPED>, S::kSmem, grown, dev);
+    const cudaError_t err = grow_smem(nvfp4_gemm_kernel<BN, GROUPED>, S::kSmem, grown, dev);
     if (err != cudaSuccess)
         return err;
-    const int64_t wgt_rows = GROUPED ? g.experts * g.N : g.N;
     CUtensorMap p_map, q_map;
-    if (!codes_map(&p_map, SWAP ? g.wgt : g.tok, SWAP ? wgt_rows : g.tok_rows, g.K, kP) ||
-        !codes_map(&q_map, SWAP ? g.tok : g.wgt, SWAP ? g.tok_rows : wgt_rows, g.K, BN))
+    if (!codes_map(&p_map, g.wgt, GROUPED ? g.experts * g.N : g.N, g.K, kP) ||
+        !codes_map(&q_map, g.tok, g.tok_rows, g.K, BN))
         return cudaErrorInvalidValue;
-    const KernelArgs a = kernel_args(g, SWAP);
+    KernelArgs a = kernel_args(g, true);
     int64_t grid = sms;
     if (!GROUPED) {
         const int64_t tiles = ((a.p_rows + kP - 1) / kP) * ((a.q_rows + BN - 1) / BN);
+        const int steps = (a.kblocks + 3) / 4;
+        while (a.split_log2 < 2 && (tiles << (a.split_log2 + 1)) <= sms && (2 << a.split_log2) <= steps)
+            ++a.split_log2;
         grid = tiles < grid ? tiles : grid;
     }
-    return launch_kernel(nvfp4_gemm_kernel<BN, SWAP, GROUPED>, dim3((unsigned)grid), dim3(kThreads), (size_t)S::kSmem,
-                         stream, pdl, p_map, q_map, a);
+    return launch_clusters(nvfp4_gemm_kernel<BN, GROUPED>, dim3((unsigned)(grid << a.split_log2)), dim3(kThreads),
+                           (size_t)S::kSmem, stream, pdl, 1u << a.split_log2, p_map, q_map, a);
 }
 
-template <bool GROUPED>
+template <int BN, bool GROUPED>
 cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
 {
     static std::atomic<bool> grown[kMaxCachedDevices];
@@ -813,23 +887,23 @@ cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
     const int sms = current_device_sms(&dev);
     if (sms < 2)
         return cudaErrorInvalidDevice;
-    const cudaError_t err = grow_smem(nvfp4_pair_kernel<GROUPED>, kPairSmem, grown, dev);
+    const cudaError_t err = grow_smem(nvfp4_pair_kernel<BN, GROUPED>, PairShape<BN>::kSmem, grown, dev);
     if (err != cudaSuccess)
         return err;
     const KernelArgs a = kernel_args(g, false);
     const int64_t experts = GROUPED ? g.experts : 1;
     CUtensorMap p_map, q_map, psf_map, qsf_map, out_map;
-    if (!codes_map(&p_map, g.tok, g.tok_rows, g.K, kP) || !codes_map(&q_map, g.wgt, experts * g.N, g.K, kPairN / 2) ||
+    if (!codes_map(&p_map, g.tok, g.tok_rows, g.K, kP) || !codes_map(&q_map, g.wgt, experts * g.N, g.K, BN / 2) ||
         !sf_map(&psf_map, g.tok_sf, (g.tok_rows + 127) / 128, a.kblocks) ||
         !sf_map(&qsf_map, g.wgt_sf, experts * a.wgt_bands, a.kblocks) ||
         !out_tile_map(&out_map, g.out, g.tok_rows, g.N, g.ldo))
         return cudaErrorInvalidValue;
     int64_t pairs = sms / 2;
     if (!GROUPED) {
-        const int64_t tiles = ((a.p_rows + 2 * kP - 1) / (2 * kP)) * ((a.q_rows + kPairN - 1) / kPairN);
+        const int64_t tiles = ((a.p_rows + 2 * kP - 1) / (2 * kP)) * ((a.q_rows + BN - 1) / BN);
         pairs = tiles < pairs ? tiles : pairs;
     }
-    return launch_kernel(nvfp4_pair_kernel<GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), (size_t)kPairSmem,
+    return launch_kernel(nvfp4_pair_kernel<BN, GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), (size_t)PairShape<BN>::kSmem,
                          stream, pdl, p_map, q_map, psf_map, qsf_map, out_map, a);
 }
 
@@ -840,11 +914,22 @@ cudaError_t launch_by_tokens(const GemmArgs &g, int64_t tokens, bool pdl, cudaSt
 {
     if constexpr (!GROUPED) {
         if (tokens <= 32)
-            return launch_tiles<32, true, false>(g, pdl, stream);
+            return launch_tiles<32, false>(g, pdl, stream);
     }
-    if (tokens <= 64) return launch_tiles<64, true, GROUPED>(g, pdl, stream);
-    if (tokens <= 128) return launch_tiles<128, true, GROUPED>(g, pdl, stream);
-    return launch_pairs<GROUPED>(g, pdl, stream);
+    if (tokens <= 64) return launch_tiles<64, GROUPED>(g, pdl, stream);
+    if (tokens <= 128) return launch_tiles<128, GROUPED>(g, pdl, stream);
+    if constexpr (!GROUPED) {
+        const int sms = current_device_sms();
+        const int64_t np = (g.tok_rows + 2 * kP - 1) / (2 * kP), pairs = sms > 1 ? sms / 2 : 1;
+        const int64_t w256 = (np * ((g.N + 255) / 256) + pairs - 1) / pairs;
+        const int64_t w128 = (np * ((g.N + 127) / 128) + pairs - 1) / pairs;
+        // half as wide tiles where they take no more waves of pairs: N=7168 K=7168
+        // M=256 9.4 us against 11.6, N=2112 M=1024 9.6 against 11.6; with two waves
+        // to one they lose (M=512 14.7 against 12.8), with three to two they are even
+        if (w128 <= w256)
+            return launch_pairs<128, false>(g, pdl, stream);
+    }
+    return launch_pairs<256, GROUPED>(g, pdl, stream);
 }
 
 }  // namespace

@@ -214,6 +214,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// 16 bytes into the shared memory of a block of the cluster (an address of map_rank).
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
 // As tma_load_2d into this block, completing on a barrier of either block of the pair.
 __device__ __forceinline__ void pair_load_2d(uint32_t dst, const void *map, int32_t x, int32_t y, uint32_t bar)
 {

@@ -54,45 +54,56 @@ __device__ __forceinline__ uint32_t gather_sf(uint32_t sf)
     return sf | (s2 << 8) | (s4 << 16) | (s6 << 24);
 }
 
-// The scale factors at chunk c of a row: four at a time where a row's come in
-// fours, else a byte per block, and zeros in the padding columns.
-__device__ __forceinline__ void store_sf(const RowsArgs &a, int64_t row, int c, uint32_t word)
+// Stores the scale factors of a row's chunks c0 + 2^lg * i: four at a time where
+// a row's come in fours, else a byte per block, and zeros in the padding columns.
+__device__ __forceinline__ void store_sf(const RowsArgs &a, int64_t row, int c0, int lg, const uint32_t (&sf)[kChunks])
 {
-    uint8_t *p = a.sf + sf_row_base(a.sf_layout, a.sf_cols, row);
-    const int k = c >> 1;
+    const int nc = (int)(a.K >> 3);
     const int stride = sf_tile_stride(a.sf_layout);
+    uint8_t *p = a.sf + sf_row_base(a.sf_layout, a.sf_cols, row);
     if ((a.K & 63) == 0) {
-        if ((c & 7) == 0)
-            *reinterpret_cast<uint32_t *>(p + (int64_t)(k >> 2) * stride) = word;
-    } else if ((c & 1) == 0) {
-        p[(int64_t)(k >> 2) * stride + (k & 3)] = (uint8_t)word;
-        if (k + 1 == (int)(a.K >> 4))
-            for (int kk = k + 1; kk < (int)a.sf_cols; ++kk)
-                p[(int64_t)(kk >> 2) * stride + (kk & 3)] = 0;
+        if ((c0 & 7) == 0) {  // (2^lg >= 8 here)
+            p += (int64_t)(c0 >> 3) * stride;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+                if (c0 + (i << lg) < nc)
+                    *reinterpret_cast<uint32_t *>(p + (int64_t)(i << lg >> 3) * stride) = sf[i];
+        }
+    } else if ((c0 & 1) == 0) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int k = (c0 + (i << lg)) >> 1, n = nc >> 1;
+            if (k < n)
+                p[(int64_t)(k >> 2) * stride + (k & 3)] = (uint8_t)sf[i];
+            if (k + 1 == n)
+                for (int kk = n; kk < (int)a.sf_cols; ++kk)
+                    p[(int64_t)(kk >> 2) * stride + (kk & 3)] = 0;
+        }
     }
 }
 
-// Row t -> NVFP4 row t, or its k rows (SCATTER).
-template <bool SCATTER>
-__global__ void __launch_bounds__(kThreads) nvfp4_rows_kernel(const __grid_constant__ RowsArgs a)
+// Row t -> NVFP4 row t, or its k rows (SCATTER).  WIDE: a warp per 128 chunks of
+// a row.  Four blocks per SM, which the latency of a warp's one round of loads
+// needs.
+template <bool SCATTER, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 4) nvfp4_rows_kernel(const __grid_constant__ RowsArgs a)
 {
+    const int lg = WIDE ? 5 : a.tpr_log2;
     const int lane = threadIdx.x & 31;
-    const int l = lane & ((1 << a.tpr_log2) - 1);
-    const int64_t t = (((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) << (5 - a.tpr_log2)) + (lane >> a.tpr_log2);
+    const int64_t t = (((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) << (5 - lg)) + (lane >> lg);
     const int nc = (int)(a.K >> 3);
-    const int c0 = (int)blockIdx.y * (32 * kChunks) + l;
+    const int c0 = (int)blockIdx.y * (32 * kChunks) + (lane & ((1 << lg) - 1));
     pdl_wait();
     bool live = t < a.T;
     if (!SCATTER && live && a.row_src != nullptr)
         live = __ldg(a.row_src + t) >= 0;
-    const uint16_t *row = a.x + t * a.ldx;
+    const uint16_t *row = a.x + t * a.ldx + (int64_t)c0 * 8;
     uint4 v[kChunks];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-        const int c = c0 + (i << a.tpr_log2);
         v[i] = make_uint4(0, 0, 0, 0);
-        if (live && c < nc)
-            v[i] = ld_stream(row + (int64_t)c * 8);
+        if (live && c0 + (i << lg) < nc)
+            v[i] = ld_stream(row + (int64_t)(i << lg) * 8);
     }
     const float g = __ldg(a.g);
     pdl_launch_dependents();
@@ -106,28 +117,24 @@ __global__ void __launch_bounds__(kThreads) nvfp4_rows_kernel(const __grid_const
     }
     if (live) {
         const int k = SCATTER ? a.k : 1;
+        const int32_t *row_of = SCATTER ? a.row_of + t * a.k : nullptr;
+        int64_t r = SCATTER ? (int64_t)__ldg(row_of) : t;
         for (int j = 0; j < k; ++j) {
-            const int64_t r = SCATTER ? (int64_t)__ldg(a.row_of + t * a.k + j) : t;
-            if (SCATTER && (r < 0 || r >= a.rows))
-                continue;
-            uint8_t *out = a.codes + r * (a.K >> 1);
+            const int64_t r_next = SCATTER && j + 1 < k ? (int64_t)__ldg(row_of + j + 1) : 0;
+            if (!SCATTER || (r >= 0 && r < a.rows)) {
+                uint8_t *out = a.codes + r * (a.K >> 1) + (int64_t)c0 * 4;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int c = c0 + (i << a.tpr_log2);
-                if (c < nc) {
-                    *reinterpret_cast<uint32_t *>(out + (int64_t)c * 4) = codes[i];
-                    store_sf(a, r, c, sf[i]);
-                }
+                for (int i = 0; i < kChunks; ++i)
+                    if (c0 + (i << lg) < nc)
+                        *reinterpret_cast<uint32_t *>(out + (int64_t)(i << lg) * 4) = codes[i];
+                store_sf(a, r, c0, lg, sf);
             }
+            r = r_next;
         }
     } else if (!SCATTER && a.row_src == nullptr && t < a.sf_rows) {
         // a padding row of a swizzled layout: zeros only
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int c = c0 + (i << a.tpr_log2);
-            if (c < nc)
-                store_sf(a, t, c, 0u);
-        }
+        const uint32_t none[kChunks] = {};
+        store_sf(a, t, c0, lg, none);
     }
 }
 
@@ -249,7 +256,10 @@ cudaError_t launch_quantize(const RowsArgs &a, bool pdl, cudaStream_t stream)
     RowsArgs b = a;
     b.tpr_log2 = lanes_log2(a.K);
     const int64_t rows = a.row_src == nullptr ? a.sf_rows : a.T;
-    return launch_kernel(nvfp4_rows_kernel<false>, grid_of(rows, a.K, b.tpr_log2), dim3(kThreads), 0, stream, pdl, b);
+    const dim3 grid = grid_of(rows, a.K, b.tpr_log2);
+    if (b.tpr_log2 == 5)
+        return launch_kernel(nvfp4_rows_kernel<false, true>, grid, dim3(kThreads), 0, stream, pdl, b);
+    return launch_kernel(nvfp4_rows_kernel<false, false>, grid, dim3(kThreads), 0, stream, pdl, b);
 }
 
 cudaError_t launch_dispatch(const RowsArgs &a, bool pdl, cudaStream_t stream)
@@ -259,7 +269,9 @@ cudaError_t launch_dispatch(const RowsArgs &a, bool pdl, cudaStream_t stream)
     const dim3 grid = grid_of(a.T, a.K, b.tpr_log2);
     if (a.out != nullptr)
         return launch_kernel(dispatch_rows_kernel, grid, dim3(kThreads), 0, stream, pdl, b);
-    return launch_kernel(nvfp4_rows_kernel<true>, grid, dim3(kThreads), 0, stream, pdl, b);
+    if (b.tpr_log2 == 5)
+        return launch_kernel(nvfp4_rows_kernel<true, true>, grid, dim3(kThreads), 0, stream, pdl, b);
+    return launch_kernel(nvfp4_rows_kernel<true, false>, grid, dim3(kThreads), 0, stream, pdl, b);
 }
 
 cudaError_t launch_dequantize(const DequantArgs &a, bool pdl, cudaStream_t stream)

@@ -5,11 +5,11 @@
 // fused_rows.cu, on x itself; every step one fp32 rounding):
 //   sf = e4m3(g * (amax/6)),  code = e2m1(x * (g / value(sf))),  0 if value(sf) == 0
 //
-// All three are bound by memory.  Work unit of a warp: 128 chunks of 8 columns
-// of one row (up to 4 per lane, all loads issued before the first is used), or
-// several whole rows where a row is shorter.  A block of 16 columns is a pair
-// of lanes, so its maximum is one shuffle; lanes 8i gather four scale factors
-// into one 32-bit store.
+// All three are bound by memory.  Work unit of a warp: 1024 columns of one row,
+// or several whole rows where a row is shorter, all loads issued before the
+// first is used.  The quantiser gives a lane whole blocks (two, 32 lanes apart),
+// so that a block's scale is computed once; four lanes gather their scale
+// factors into one 32-bit store.  The others give a lane chunks of 8 columns.
 #include "device_util.cuh"
 #include "launch_nvfp4.h"
 #include "sf_layout.cuh"
@@ -21,98 +21,100 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunks = 4;  // chunks of 8 columns per lane
+constexpr int kBlocks = 2;  // blocks of 16 columns per lane
 
-// The 8 E2M1 codes of one lane's chunk, and its block's scale factor.
-__device__ __forceinline__ uint32_t quantize_chunk(const uint4 &v, float g, uint32_t &sf)
+// The 16 E2M1 codes of a block, and its scale factor.
+__device__ __forceinline__ uint2 quantize_block(const uint4 (&v)[2], float g, uint32_t &sf)
 {
-    float n[8];
-    unpack8(v, n);
+    float n[2][8];
+    unpack8(v[0], n[0]);
+    unpack8(v[1], n[1]);
     float amax = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        amax = fmaxf(amax, fabsf(n[e]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, fmaxf(fabsf(n[0][e]), fabsf(n[1][e])));
     sf = cvt_e4m3(__fmul_rn(g, div_const_rn(amax, 6.0f, kRcp6)));
     const float d = e4m3_value(sf);
-    uint32_t codes = 0;
-    if (d != 0.0f) {
-        const float es = __fdiv_rn(g, d);
+    if (d == 0.0f)
+        return make_uint2(0, 0);
+    const float es = __fdiv_rn(g, d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            n[e] = __fmul_rn(n[e], es);
-        codes = cvt_e2m1x8(n);
+    for (int e = 0; e < 8; ++e) {
+        n[0][e] = __fmul_rn(n[0][e], es);
+        n[1][e] = __fmul_rn(n[1][e], es);
     }
-    return codes;
+    return make_uint2(cvt_e2m1x8(n[0]), cvt_e2m1x8(n[1]));
 }
 
-// The scale factors of four blocks (8 lanes) in one word, on the first lane.
+// The scale factors of four lanes' blocks in one word, on the first lane.
 __device__ __forceinline__ uint32_t gather_sf(uint32_t sf)
 {
-    const uint32_t s2 = __shfl_down_sync(0xffffffffu, sf, 2);
-    const uint32_t s4 = __shfl_down_sync(0xffffffffu, sf, 4);
-    const uint32_t s6 = __shfl_down_sync(0xffffffffu, sf, 6);
-    return sf | (s2 << 8) | (s4 << 16) | (s6 << 24);
+    const uint32_t two = sf | (__shfl_down_sync(0xffffffffu, sf, 1) << 8);
+    return two | (__shfl_down_sync(0xffffffffu, two, 2) << 16);
 }
 
-// Stores the scale factors of a row's chunks c0 + 2^lg * i: four at a time where
-// a row's come in fours, else a byte per block, and zeros in the padding columns.
-__device__ __forceinline__ void store_sf(const RowsArgs &a, int64_t row, int c0, int lg, const uint32_t (&sf)[kChunks])
+// Stores the scale factors of a row's blocks b0 + 2^lg * i: four at a time where
+// a row's come in fours, else one by one, and zeros in the padding columns.
+__device__ __forceinline__ void store_sf(const RowsArgs &a, int64_t row, int b0, int lg, const uint32_t (&sf)[kBlocks])
 {
-    const int nc = (int)(a.K >> 3);
+    const int nb = (int)(a.K >> 4);
     const int stride = sf_tile_stride(a.sf_layout);
     uint8_t *p = a.sf + sf_row_base(a.sf_layout, a.sf_cols, row);
-    if ((a.K & 63) == 0) {
-        if ((c0 & 7) == 0) {  // (2^lg >= 8 here)
-            p += (int64_t)(c0 >> 3) * stride;
+    if ((nb & 3) == 0) {
+        if ((b0 & 3) == 0) {  // (2^lg >= 4 here)
+            p += (int64_t)(b0 >> 2) * stride;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i)
-                if (c0 + (i << lg) < nc)
-                    *reinterpret_cast<uint32_t *>(p + (int64_t)(i << lg >> 3) * stride) = sf[i];
+            for (int i = 0; i < kBlocks; ++i)
+                if (b0 + (i << lg) < nb)
+                    *reinterpret_cast<uint32_t *>(p + (int64_t)(i << lg >> 2) * stride) = sf[i];
         }
-    } else if ((c0 & 1) == 0) {
+    } else {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int k = (c0 + (i << lg)) >> 1, n = nc >> 1;
-            if (k < n)
+        for (int i = 0; i < kBlocks; ++i) {
+            const int k = b0 + (i << lg);
+            if (k < nb)
                 p[(int64_t)(k >> 2) * stride + (k & 3)] = (uint8_t)sf[i];
-            if (k + 1 == n)
-                for (int kk = n; kk < (int)a.sf_cols; ++kk)
+            if (k + 1 == nb)
+                for (int kk = nb; kk < (int)a.sf_cols; ++kk)
                     p[(int64_t)(kk >> 2) * stride + (kk & 3)] = 0;
         }
     }
 }
 
-// Row t -> NVFP4 row t, or its k rows (SCATTER).  WIDE: a warp per 128 chunks of
+// Row t -> NVFP4 row t, or its k rows (SCATTER).  WIDE: a warp per 1024 columns of
 // a row.  Four blocks per SM, which the latency of a warp's one round of loads
-// needs.
+// needs (dispatch of 4096 x 8 rows of 7168: 44 us, two blocks 62).
 template <bool SCATTER, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 4) nvfp4_rows_kernel(const __grid_constant__ RowsArgs a)
 {
     const int lg = WIDE ? 5 : a.tpr_log2;
     const int lane = threadIdx.x & 31;
     const int64_t t = (((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) << (5 - lg)) + (lane >> lg);
-    const int nc = (int)(a.K >> 3);
-    const int c0 = (int)blockIdx.y * (32 * kChunks) + (lane & ((1 << lg) - 1));
+    const int nb = (int)(a.K >> 4);
+    const int b0 = (int)blockIdx.y * (32 * kBlocks) + (lane & ((1 << lg) - 1));
     pdl_wait();
     bool live = t < a.T;
     if (!SCATTER && live && a.row_src != nullptr)
         live = __ldg(a.row_src + t) >= 0;
-    const uint16_t *row = a.x + t * a.ldx + (int64_t)c0 * 8;
-    uint4 v[kChunks];
+    const uint16_t *row = a.x + t * a.ldx + (int64_t)b0 * 16;
+    uint4 v[kBlocks][2];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (live && c0 + (i << lg) < nc)
-            v[i] = ld_stream(row + (int64_t)(i << lg) * 8);
+    for (int i = 0; i < kBlocks; ++i) {
+        v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+        if (live && b0 + (i << lg) < nb) {
+            v[i][0] = ld_stream(row + (int64_t)(i << lg) * 16);
+            v[i][1] = ld_stream(row + (int64_t)(i << lg) * 16 + 8);
+        }
     }
     const float g = __ldg(a.g);
     pdl_launch_dependents();
-    uint32_t codes[kChunks], sf[kChunks];
+    uint2 codes[kBlocks];
+    uint32_t sf[kBlocks];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        codes[i] = quantize_chunk(v[i], g, sf[i]);
+    for (int i = 0; i < kBlocks; ++i) {
+        codes[i] = quantize_block(v[i], g, sf[i]);
         const uint32_t four = gather_sf(sf[i]);
-        if ((a.K & 63) == 0)
+        if ((nb & 3) == 0)
             sf[i] = four;
     }
     if (live) {
@@ -122,19 +124,19 @@ __global__ void __launch_bounds__(kThreads, 4) nvfp4_rows_kernel(const __grid_co
         for (int j = 0; j < k; ++j) {
             const int64_t r_next = SCATTER && j + 1 < k ? (int64_t)__ldg(row_of + j + 1) : 0;
             if (!SCATTER || (r >= 0 && r < a.rows)) {
-                uint8_t *out = a.codes + r * (a.K >> 1) + (int64_t)c0 * 4;
+                uint8_t *out = a.codes + r * (a.K >> 1) + (int64_t)b0 * 8;
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i)
-                    if (c0 + (i << lg) < nc)
-                        *reinterpret_cast<uint32_t *>(out + (int64_t)(i << lg) * 4) = codes[i];
-                store_sf(a, r, c0, lg, sf);
+                for (int i = 0; i < kBlocks; ++i)
+                    if (b0 + (i << lg) < nb)
+                        *reinterpret_cast<uint2 *>(out + (int64_t)(i << lg) * 8) = codes[i];
+                store_sf(a, r, b0, lg, sf);
             }
             r = r_next;
         }
     } else if (!SCATTER && a.row_src == nullptr && t < a.sf_rows) {
         // a padding row of a swizzled layout: zeros only
-        const uint32_t none[kChunks] = {};
-        store_sf(a, t, c0, lg, none);
+        const uint32_t none[kBlocks] = {};
+        store_sf(a, t, b0, lg, none);
     }
 }
 
@@ -230,23 +232,22 @@ __global__ void __launch_bounds__(kThreads) nvfp4_values_kernel(const __grid_con
     }
 }
 
-// Lanes per row: 32 with up to 4 chunks each, fewer where a row has fewer than
-// 128 chunks, so that a warp takes several rows; at least 8 (where there are 8
-// chunks) for the gathered scale-factor stores.
-int lanes_log2(int64_t K)
+// Lanes per row of `units` chunks or blocks: 32 with up to `each` of them, fewer
+// (but at least 4 where there are 4) where a row has less, so that a warp takes
+// several rows.
+int lanes_log2(int64_t units, int each)
 {
-    const int64_t nc = K / 8;
     int l = 0;
-    while (l < 5 && (1 << l) < nc && ((kChunks << l) < nc || l < 3))
+    while (l < 5 && (1 << l) < units && ((each << l) < units || l < 2))
         ++l;
     return l;
 }
 
+// Rows along x, 1024 columns of a row along y.
 dim3 grid_of(int64_t rows, int64_t K, int tpr_log2)
 {
     const int64_t per_cta = (int64_t)kWarps << (5 - tpr_log2);
-    const int64_t segs = tpr_log2 == 5 ? (K / 8 + 32 * kChunks - 1) / (32 * kChunks) : 1;
-    return dim3((unsigned)((rows + per_cta - 1) / per_cta), (unsigned)segs);
+    return dim3((unsigned)((rows + per_cta - 1) / per_cta), (unsigned)((K + 1023) / 1024));
 }
 
 }  // namespace
@@ -254,7 +255,7 @@ dim3 grid_of(int64_t rows, int64_t K, int tpr_log2)
 cudaError_t launch_quantize(const RowsArgs &a, bool pdl, cudaStream_t stream)
 {
     RowsArgs b = a;
-    b.tpr_log2 = lanes_log2(a.K);
+    b.tpr_log2 = lanes_log2(a.K / 16, kBlocks);
     const int64_t rows = a.row_src == nullptr ? a.sf_rows : a.T;
     const dim3 grid = grid_of(rows, a.K, b.tpr_log2);
     if (b.tpr_log2 == 5)
@@ -265,7 +266,7 @@ cudaError_t launch_quantize(const RowsArgs &a, bool pdl, cudaStream_t stream)
 cudaError_t launch_dispatch(const RowsArgs &a, bool pdl, cudaStream_t stream)
 {
     RowsArgs b = a;
-    b.tpr_log2 = lanes_log2(a.K);
+    b.tpr_log2 = a.out != nullptr ? lanes_log2(a.K / 8, kChunks) : lanes_log2(a.K / 16, kBlocks);
     const dim3 grid = grid_of(a.T, a.K, b.tpr_log2);
     if (a.out != nullptr)
         return launch_kernel(dispatch_rows_kernel, grid, dim3(kThreads), 0, stream, pdl, b);
@@ -277,7 +278,7 @@ cudaError_t launch_dispatch(const RowsArgs &a, bool pdl, cudaStream_t stream)
 cudaError_t launch_dequantize(const DequantArgs &a, bool pdl, cudaStream_t stream)
 {
     DequantArgs b = a;
-    b.tpr_log2 = lanes_log2(a.K);
+    b.tpr_log2 = lanes_log2(a.K / 8, kChunks);
     return launch_kernel(nvfp4_values_kernel, grid_of(a.T, a.K, b.tpr_log2), dim3(kThreads), 0, stream, pdl, b);
 }
 

@@ -82,10 +82,15 @@ __device__ __forceinline__ void store_sf(const RowsArgs &a, int64_t row, int b0,
 }
 
 // Row t -> NVFP4 row t, or its k rows (SCATTER).  WIDE: a warp per 1024 columns of
-// a row.  Four blocks per SM, which the latency of a warp's one round of loads
-// needs (dispatch of 4096 x 8 rows of 7168: 44 us, two blocks 62).
+// a row.  As many blocks per SM as the registers allow, which the latency of a
+// warp's one round of loads needs (16384 x 5120 in the 128x4 layout: 30.9 us with
+// 5, 33.1 with 4; the copy floor is 31.7, some of the output stays in L2).
+// A dispatch of 4096 x 8 rows of 7168 takes 38.7 us, 28.8 without the scale
+// factors: a row's lie 512 bytes apart, so every 4 of them are a line of their
+// own for the store unit.  Its codes go out with the streaming hint (43.6 us
+// without): they are eight times the tokens and displace them.
 template <bool SCATTER, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 4) nvfp4_rows_kernel(const __grid_constant__ RowsArgs a)
+__global__ void __launch_bounds__(kThreads, SCATTER ? 4 : 5) nvfp4_rows_kernel(const __grid_constant__ RowsArgs a)
 {
     const int lg = WIDE ? 5 : a.tpr_log2;
     const int lane = threadIdx.x & 31;
@@ -127,8 +132,12 @@ __global__ void __launch_bounds__(kThreads, 4) nvfp4_rows_kernel(const __grid_co
                 uint8_t *out = a.codes + r * (a.K >> 1) + (int64_t)b0 * 8;
 #pragma unroll
                 for (int i = 0; i < kBlocks; ++i)
-                    if (b0 + (i << lg) < nb)
-                        *reinterpret_cast<uint2 *>(out + (int64_t)(i << lg) * 8) = codes[i];
+                    if (b0 + (i << lg) < nb) {
+                        if (SCATTER)
+                            st_v2(out + (int64_t)(i << lg) * 8, codes[i]);
+                        else
+                            *reinterpret_cast<uint2 *>(out + (int64_t)(i << lg) * 8) = codes[i];
+                    }
                 store_sf(a, r, b0, lg, sf);
             }
             r = r_next;

@@ -95,7 +95,7 @@ def _link_calls(obj: str) -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = CALLS_PATH + ".tmp%d" % os.getpid()
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN", "-L", lib,
-           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of {CALLS_PATH} failed:\n{r.stdout}\n{r.stderr}")

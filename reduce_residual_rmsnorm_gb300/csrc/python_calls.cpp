@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -164,7 +165,7 @@ public:
     static at::Tensor fresh(const Dims &d, at::ScalarType type, const at::Tensor &like)
     {
         if (like.is_cuda())
-            return at::empty(d.ref(), like.options().dtype(type).requires_grad(false));
+            return at::detail::empty_cuda(d.ref(), type, like.device(), std::nullopt);
         return at::empty(d.ref(), at::TensorOptions().dtype(type).pinned_memory(true));
     }
 

@@ -869,10 +869,14 @@ cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
     KernelArgs a = kernel_args(g, true);
     int64_t grid = sms;
     if (!GROUPED) {
+        // K over 2 or 4 blocks where all tiles still run at once.  (Of clusters of 4
+        // a GB300 runs 36 at a time on its 152 SMs, of 8 only 15.)
         const int64_t tiles = ((a.p_rows + kP - 1) / kP) * ((a.q_rows + BN - 1) / BN);
         const int steps = (a.kblocks + 3) / 4;
-        while (a.split_log2 < 2 && (tiles << (a.split_log2 + 1)) <= sms && (2 << a.split_log2) <= steps)
-            ++a.split_log2;
+        if (4 * tiles <= sms - sms / 16 && steps >= 4)
+            a.split_log2 = 2;
+        else if (2 * tiles <= sms && steps >= 2)
+            a.split_log2 = 1;
         grid = tiles < grid ? tiles : grid;
     }
     return launch_clusters(nvfp4_gemm_kernel<BN, GROUPED>, dim3((unsigned)(grid << a.split_log2)), dim3(kThreads),

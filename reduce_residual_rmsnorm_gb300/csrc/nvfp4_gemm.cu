@@ -147,7 +147,7 @@ __device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t 
     t.q_row = SWAP ? tok_row : wgt_row;
     t.p_band = SWAP ? wgt_band : tok_band;
     t.q_band = SWAP ? tok_band : wgt_band;
-    const int left = SWAP ? 1 : a.wgt_bands - (w0 >> 7);
+    const int left = SWAP ? (t.tok_n + 127) >> 7 : a.wgt_bands - (w0 >> 7);
     t.q_bands = left < kBandsOf<BN> ? left : kBandsOf<BN>;
     t.q_sub = ((SWAP ? tok_row : w0) & 127) >> 5;
     return t;
@@ -560,8 +560,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = tmem_at;
     pdl_wait();
 
-    const int64_t tiles = tile_count<2 * kP, BN, false, GROUPED>(a, first);
-    auto tile_of = [&](int64_t id) { return tile_at<2 * kP, BN, false, GROUPED>(a, first, id); };
+    const int64_t tiles = tile_count<2 * kP, BN, GROUPED, GROUPED>(a, first);
+    auto tile_of = [&](int64_t id) { return tile_at<2 * kP, BN, GROUPED, GROUPED>(a, first, id); };
+    // columns of the products of a tile: all, or the expert's tokens rounded up
+    auto columns = [](const Tile &t) { return GROUPED ? (t.tok_n + 31) & ~31 : BN; };
     const int steps = (a.kblocks + 3) >> 2;
     const int64_t id0 = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
@@ -574,7 +576,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t full0 = map_rank(full, 0);
         for (int64_t id = id0; good && id < tiles; id += stride) {
             const Tile t = tile_of(id);
-            const int32_t p_row = t.p_row + (int32_t)rank * kP, q_row = t.q_row + (int32_t)rank * (BN / 2);
+            const int32_t p_row = t.p_row + (int32_t)rank * kP, q_row = t.q_row + (int32_t)rank * (columns(t) / 2);
+            const int q_bands = GROUPED ? t.q_bands : S::kBands;
             const int32_t p_band = (int32_t)t.p_band + (int32_t)rank, q_band = (int32_t)t.q_band;
             for (int kt = 0; kt < steps; ++kt) {
                 good = wait_warp(empty + 8 * s, parity ^ 1, dead);
@@ -584,13 +587,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t c = codes + s * S::kCodes, f = sf + s * S::kSf;
                 if (elect_one()) {
                     if (rank == 0)
-                        mbar_expect_tx(full + 8 * s, 2 * (S::kCodes + S::kSf));
+                        mbar_expect_tx(full + 8 * s, 2u * (uint32_t)(S::kCodes + 4 * kSfTile * (1 + q_bands)));
                     pair_load_2d(c, &p_map, kt * 128, p_row, bar);
                     pair_load_2d(c + kP * 128, &q_map, kt * 128, q_row, bar);
                     pair_load_2d(f, &psf_map, kt * 256, p_band, bar);
 #pragma unroll
                     for (int b = 0; b < S::kBands; ++b)
-                        pair_load_2d(f + 4 * (1 + b) * kSfTile, &qsf_map, kt * 256, q_band + b, bar);
+                        if (b < q_bands)
+                            pair_load_2d(f + 4 * (1 + b) * kSfTile, &qsf_map, kt * 256, q_band + b, bar);
                 }
                 __syncwarp();
                 ++fills;
@@ -609,12 +613,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp == 1) {
         // ---- products, by the first block for both ----
-        constexpr uint32_t idesc = idesc_nvfp4(2 * kP, BN);
         int s = 0;
         uint32_t parity = 0;
         int64_t n = 0;
         bool good = true;
         for (int64_t id = id0; rank == 0 && good && id < tiles; id += stride, ++n) {
+            const uint32_t idesc = idesc_nvfp4(2 * kP, (uint32_t)(GROUPED ? columns(tile_of(id)) : BN));
             // the tile before has given the shared columns back, or the one before
             // that its accumulator (without one: at once)
             good = S::kShared ? wait_warp(acc_free, ((uint32_t)n & 1) ^ 1, dead)
@@ -676,8 +680,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
                 break;
             tmem_fence_after();
-            const int row0 = (int)rank * kP + quad * 32;  // of the warp's rows in the tile
-            const int rows = t.tok_n - row0;              // of its 32 that are the call's (the expert's)
+            const int row0 = (int)rank * kP + quad * 32;  // of the warp's lanes in the tile
+            const int lanes = (GROUPED ? t.wgt_n : t.tok_n) - row0, cols = GROUPED ? t.tok_n : t.wgt_n;
             const uint32_t src = tmem + acc * S::kAcc1 + ((uint32_t)quad << 21);
             // 32-column pieces, this warp's first one among the shared: the last two of
             // the first accumulator, the first two of the second
@@ -697,35 +701,53 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 const int c0 = column(i);
                 if (i + 1 < S::kChunks / 2)
                     tmem_load32(src + column(i + 1), v[(i + 1) & 1]);
-                if (rows > 0 && c0 < t.wgt_n) {
+                if (lanes > 0 && c0 < cols) {
                     if (lane == 0)
                         bulk_wait_read<0>();
                     __syncwarp();
+                    // 32 rows of 64 bytes under the 64-byte swizzle: 16-byte piece j of
+                    // row r lies at j ^ (r / 2 % 4)
+                    const int rows = GROUPED ? cols - c0 : lanes;  // that are the call's (the expert's)
+                    if constexpr (GROUPED) {
+                        // lane = output column, register = row: neighbouring lanes exchange, an
+                        // even lane takes both columns of the first of two rows, an odd one of the second
+                        const bool odd = lane & 1;
+                        const int at = lane >> 1;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float f[8];
+                        for (int r = 0; r < 32; r += 2) {
+                            const uint32_t mine = v[i & 1][r], other = v[i & 1][r + 1];
+                            const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? mine : other, 1)) * alpha;
+                            const float kept = __uint_as_float(odd ? other : mine) * alpha;
+                            st_shared32(stage + (r + odd) * 64 + (((at >> 2) ^ ((r >> 1) & 3)) << 4) + (at & 3) * 4,
+                                        odd ? pack_bf16x2(got, kept) : pack_bf16x2(kept, got));
+                        }
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            f[e] = __uint_as_float(v[i & 1][8 * j + e]) * alpha;
-                        // the 64-byte swizzle: 16-byte piece j of row l lies at j ^ (l / 2 % 4)
-                        st_shared(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pack8(f));
+                        for (int j = 0; j < 4; ++j) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                f[e] = __uint_as_float(v[i & 1][8 * j + e]) * alpha;
+                            st_shared(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pack8(f));
+                        }
                     }
+                    const int64_t row = t.tok0 + (GROUPED ? c0 : row0), col = t.wgt0 + (GROUPED ? row0 : c0);
                     if (!GROUPED || rows >= 32) {
                         fence_async_proxy();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_2d(&out_map, stage, (int32_t)(t.wgt0 + c0), (int32_t)(t.tok0 + row0));
+                            tma_store_2d(&out_map, stage, (int32_t)col, (int32_t)row);
                             bulk_commit();
                         }
                     } else {
-                        // not all of the rows are this expert's: 4 lanes per row, 16 bytes each
+                        // rows of the next expert follow: 4 lanes per row, 16 bytes each
                         __syncwarp();
 #pragma unroll
                         for (int r0 = 0; r0 < 32; r0 += 8) {
                             const int r = r0 + (lane >> 2), j = lane & 3;
                             const uint4 w = ld_shared(stage + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
-                            if (r < rows && c0 + 8 * j < t.wgt_n)
-                                *reinterpret_cast<uint4 *>(a.out + (t.tok0 + row0 + r) * a.ldo + t.wgt0 + c0 + 8 * j) = w;
+                            if (r < rows && 8 * j < lanes)
+                                *reinterpret_cast<uint4 *>(a.out + (row + r) * a.ldo + col + 8 * j) = w;
                         }
                     }
                 }
@@ -894,12 +916,13 @@ cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
     const cudaError_t err = grow_smem(nvfp4_pair_kernel<BN, GROUPED>, PairShape<BN>::kSmem, grown, dev);
     if (err != cudaSuccess)
         return err;
-    const KernelArgs a = kernel_args(g, false);
+    const KernelArgs a = kernel_args(g, GROUPED);
     const int64_t experts = GROUPED ? g.experts : 1;
-    CUtensorMap p_map, q_map, psf_map, qsf_map, out_map;
-    if (!codes_map(&p_map, g.tok, g.tok_rows, g.K, kP) || !codes_map(&q_map, g.wgt, experts * g.N, g.K, BN / 2) ||
-        !sf_map(&psf_map, g.tok_sf, (g.tok_rows + 127) / 128, a.kblocks) ||
-        !sf_map(&qsf_map, g.wgt_sf, experts * a.wgt_bands, a.kblocks) ||
+    CUtensorMap tok_map, wgt_map, tok_sf_map, wgt_sf_map, out_map;
+    if (!codes_map(&tok_map, g.tok, g.tok_rows, g.K, GROUPED ? BN / 2 : kP) ||
+        !codes_map(&wgt_map, g.wgt, experts * g.N, g.K, GROUPED ? kP : BN / 2) ||
+        !sf_map(&tok_sf_map, g.tok_sf, (g.tok_rows + 127) / 128, a.kblocks) ||
+        !sf_map(&wgt_sf_map, g.wgt_sf, experts * a.wgt_bands, a.kblocks) ||
         !out_tile_map(&out_map, g.out, g.tok_rows, g.N, g.ldo))
         return cudaErrorInvalidValue;
     int64_t pairs = sms / 2;
@@ -908,7 +931,8 @@ cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
         pairs = tiles < pairs ? tiles : pairs;
     }
     return launch_kernel(nvfp4_pair_kernel<BN, GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), (size_t)PairShape<BN>::kSmem,
-                         stream, pdl, p_map, q_map, psf_map, qsf_map, out_map, a);
+                         stream, pdl, GROUPED ? wgt_map : tok_map, GROUPED ? tok_map : wgt_map,
+                         GROUPED ? wgt_sf_map : tok_sf_map, GROUPED ? tok_sf_map : wgt_sf_map, out_map, a);
 }
 
 // A tile of 32 tokens only where it is the call's only one, so that its scale
@@ -920,8 +944,13 @@ cudaError_t launch_by_tokens(const GemmArgs &g, int64_t tokens, bool pdl, cudaSt
         if (tokens <= 32)
             return launch_tiles<32, false>(g, pdl, stream);
     }
-    if (tokens <= 64) return launch_tiles<64, GROUPED>(g, pdl, stream);
-    if (tokens <= 128) return launch_tiles<128, GROUPED>(g, pdl, stream);
+    // Grouped, 64 experts, N=4096 K=7168: with 16 tokens an expert 64 columns take
+    // 164 us, 128 columns 167, pairs 183; with 32 172, 167, 184; with 64 205, 180, 187
+    // (16 experts, N=K=2048: 14.1, 13.8, 12.0); with 96 264, 198, 194.
+    if (tokens <= (GROUPED ? 16 : 64))
+        return launch_tiles<64, GROUPED>(g, pdl, stream);
+    if (tokens <= (GROUPED ? 63 : 128))
+        return launch_tiles<128, GROUPED>(g, pdl, stream);
     if constexpr (!GROUPED) {
         const int sms = current_device_sms();
         const int64_t np = (g.tok_rows + 2 * kP - 1) / (2 * kP), pairs = sms > 1 ? sms / 2 : 1;

@@ -270,7 +270,8 @@ def _grouped(dev, counts, N, K, tokens_hint=None, starts=None):
 @pytest.mark.parametrize("hint", (None, 1, 100000), ids=("by-count", "few", "many"))
 @pytest.mark.parametrize("counts,N,K", [
     ([1], 8, 32), ([0, 0, 0], 128, 64), ([3, 0, 1, 7], 136, 160), ([128, 127, 129, 0, 1], 264, 96),
-    ([33, 64, 65, 100, 0, 2], 384, 512), ([300, 0, 513, 5], 200, 288)], ids=str)
+    ([33, 64, 65, 100, 0, 2], 384, 512), ([300, 0, 513, 5], 200, 288), ([255, 256, 257, 31, 32, 224, 225], 520, 320),
+    ([1000, 161, 0, 448], 1032, 1024)], ids=str)
 def test_grouped(dev, counts, N, K, hint):
     _grouped(dev, counts, N, K, hint)
 

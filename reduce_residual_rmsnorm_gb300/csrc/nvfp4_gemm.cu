@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(free0);
+                    mbar_arrive_cluster_relaxed(free0);
             }
 #pragma unroll
             for (int i = 0; i < S::kChunks / 2; ++i) {
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(free0 + 8 * acc);
+                    mbar_arrive_cluster_relaxed(free0 + 8 * acc);
             }
         }
         if (lane == 0)

@@ -226,6 +226,14 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint4 v)
                  : "memory");
 }
 
+// As above without ordering this thread's memory accesses, for what only tensor
+// memory is to be ordered by (tcgen05.wait and the fence before).  The release
+// of the other form took over 1000 cycles behind outstanding stores.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // As tma_load_2d into this block, completing on a barrier of either block of the pair.
 __device__ __forceinline__ void pair_load_2d(uint32_t dst, const void *map, int32_t x, int32_t y, uint32_t bar)
 {

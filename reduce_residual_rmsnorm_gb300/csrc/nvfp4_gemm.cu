@@ -5,19 +5,25 @@
 //
 // tcgen05.mma kind::mxf4nvf4 multiplies 64 packed E2M1 values of K per
 // instruction with one E4M3 scale factor per 16, from shared memory into
-// tensor memory.  Its operands are named P (128 rows, the accumulator's lanes)
-// and Q (BN rows, the accumulator's columns) here; a call of few tokens puts
-// the weights on P and the tokens on Q (SWAP), so that a tile is no taller
-// than the tokens need, a larger one the tokens on P.
+// tensor memory.  Its operands are named P (128 rows a block, the accumulator's
+// lanes) and Q (the accumulator's columns) here.  Which matrix is which:
+//   - up to 128 tokens, and up to 63 an expert: weights on P, tokens on Q, so that
+//     a tile is no wider than the tokens need (nvfp4_gemm_kernel).  Bound by the
+//     weights' bytes, and where those are few by latency: K of a tile is then
+//     split over a cluster.
+//   - more tokens: pairs of blocks (nvfp4_pair_kernel) with tokens on P, and in
+//     the grouped form weights on P and an expert's tokens on Q, whose number of
+//     columns follows them.  Bound by the tensor cores: 7.3 PFLOP/s at 8192 x
+//     7168 x 7168, 86 % of a tile's cycles, and the power limit in long runs.
 //
-// One block per SM, persistent over the tiles.  Warp 0 copies (one thread):
-// codes by TMA under the 128-byte swizzle, 256 elements of K (128 bytes a row)
-// per stage, scale factors by bulk copies of the 512-byte tiles of their 128x4
-// layout, which is the layout tensor memory wants.  Warp 1 multiplies (one
-// thread): scale factors from shared to tensor memory, then the products.
-// Warps 2 to 5 write the finished accumulator (one of two, so that the next
-// tile's products run meanwhile).  Every wait has a limit, after which the
-// block records it, waits for its copies in flight and ends.
+// One block per SM, persistent over the tiles.  Warp 0 copies: codes by TMA
+// under the 128-byte swizzle, 256 elements of K (128 bytes a row) per stage,
+// scale factors in the 512-byte tiles of their 128x4 layout, which is the
+// layout tensor memory wants.  Warp 1 multiplies: scale factors from shared to
+// tensor memory, then the products.  The other warps write the finished
+// accumulator, one of two, while the next tile's products run.  Every wait has
+// a limit, after which the block records it, waits for its copies in flight
+// and ends.
 #include <cuda.h>
 
 #include "device_util.cuh"
@@ -35,6 +41,7 @@ constexpr int kP = 128;               // rows of P per tile
 constexpr int kSfTile = 512;          // bytes of a 128-row, 64-element tile of scale factors
 constexpr long long kWaitCycles = 4000000000LL;  // a wait's limit: about 2 s
 constexpr int kSmemLimit = 232448;    // bytes of shared memory of a block
+constexpr int kSlack = 1024 + 4 * 1032;  // alignment, and the experts' first tiles
 
 template <int BN>
 constexpr int kBandsOf = BN > 128 ? BN / 128 : 1;  // 128-row bands of Q's scale factors
@@ -46,7 +53,7 @@ struct Shape {
     static constexpr int kCodes = kP * 128 + BN * 128;      // bytes of codes per stage
     static constexpr int kSf = 4 * kSfTile * (1 + kBands);  // bytes of scale factors per stage
     static constexpr int kPartials = SPLIT ? BN * kP * 4 : 0;
-    static constexpr int kFixed = 1024 /* alignment */ + 4 * 1032 /* experts' first tiles */ + kPartials;
+    static constexpr int kFixed = kSlack + kPartials;
     static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
     static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
     static constexpr int kSfP = 2 * BN;       // tensor-memory column of P's scale factors
@@ -475,21 +482,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// pair form: two blocks on one tile of 256 tokens by 256 weights
+// pair form: two blocks on one tile of 256 rows of P by BN of Q
 // ---------------------------------------------------------------------------
 //
-// Each block of a cluster of two holds 128 tokens (P) and 128 of the weights'
-// rows (Q) in its shared memory; the first block's products (cta_group::2)
-// read both and write the accumulators of both, so that a block copies half of
-// what a 128 x 256 tile of its own would need.  The scale factors of Q's 256
-// rows are in both blocks.  Both blocks' copies complete on the first block's
-// barrier; its commits free the stages and publish the accumulators in both.
+// Each block of a cluster of two holds 128 rows of P and half of Q's in its
+// shared memory; the first block's products (cta_group::2) read both and write
+// the accumulators of both, so that a block copies half of what a 128 x 256
+// tile of its own would need (8192 x 7168 x 7168: 183 us with tiles of 128 x 128
+// for each block, 123 so).  The scale factors of Q's rows are in both blocks.
+// Both blocks' copies complete on the first block's barrier; its commits free
+// the stages and publish the accumulators in both.
 //
 // Two accumulators of 256 columns and 48 columns of scale factors do not fit
 // the 512 columns: the accumulators share 64, which the output warps read
 // first and then give back, so that the next tile's products run during the
 // rest.  The output goes through shared memory, 32 rows of 64 bytes a warp and
 // step, and out by TMA.
+//
+// Of the 16.7 K cycles that a tile takes at K = 7168 (14.3 K of them products),
+// the products wait 1.0 K for the shared columns, 0.4 K for the first stage and
+// 180 a stage for the copies.  Tried without gain: a second staging buffer
+// (K = 512 4 % faster, K = 7168 1 % slower), 128-byte rows of output (1 % slower),
+// Q's scale factors multicast to the pair (none), the next tile found ahead
+// (none; 7 % slower grouped).
 
 constexpr int kPairThreads = 320;
 
@@ -500,7 +515,7 @@ struct PairShape {
     static constexpr int kCodes = kP * 128 + (BN / 2) * 128;     // bytes per stage and block
     static constexpr int kSf = 4 * kSfTile * (1 + kBands);
     static constexpr int kOut = 8 * 32 * 64;                     // staging: warps x rows x bytes
-    static constexpr int kFixed = 1024 + kOut + 4 * 1032;
+    static constexpr int kFixed = kSlack + kOut;
     static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
     static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
     static constexpr int kAcc1 = kShared ? BN - 64 : BN;         // column of the second accumulator
@@ -891,8 +906,10 @@ cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
     KernelArgs a = kernel_args(g, true);
     int64_t grid = sms;
     if (!GROUPED) {
-        // K over 2 or 4 blocks where all tiles still run at once.  (Of clusters of 4
-        // a GB300 runs 36 at a time on its 152 SMs, of 8 only 15.)
+        // K over 2 or 4 blocks where all tiles still run at once: M=1 4096 x 4096
+        // 6.0 us alone, 4.4 over 2, 4.2 over 4; M=16 N=2112 K=7168 8.7, 5.9, 4.4;
+        // M=128 N=512 K=7168 11.4, 9.6, 6.8.  (Of clusters of 4 a GB300 runs 36 at
+        // a time on its 152 SMs, of 8 only 15.)
         const int64_t tiles = ((a.p_rows + kP - 1) / kP) * ((a.q_rows + BN - 1) / BN);
         const int steps = (a.kblocks + 3) / 4;
         if (4 * tiles <= sms - sms / 16 && steps >= 4)
@@ -930,8 +947,8 @@ cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
         const int64_t tiles = ((a.p_rows + 2 * kP - 1) / (2 * kP)) * ((a.q_rows + BN - 1) / BN);
         pairs = tiles < pairs ? tiles : pairs;
     }
-    return launch_kernel(nvfp4_pair_kernel<BN, GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), (size_t)PairShape<BN>::kSmem,
-                         stream, pdl, GROUPED ? wgt_map : tok_map, GROUPED ? tok_map : wgt_map,
+    return launch_kernel(nvfp4_pair_kernel<BN, GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kPairThreads),
+                         (size_t)PairShape<BN>::kSmem, stream, pdl, GROUPED ? wgt_map : tok_map, GROUPED ? tok_map : wgt_map,
                          GROUPED ? wgt_sf_map : tok_sf_map, GROUPED ? tok_sf_map : wgt_sf_map, out_map, a);
 }
 
@@ -946,7 +963,8 @@ cudaError_t launch_by_tokens(const GemmArgs &g, int64_t tokens, bool pdl, cudaSt
     }
     // Grouped, 64 experts, N=4096 K=7168: with 16 tokens an expert 64 columns take
     // 164 us, 128 columns 167, pairs 183; with 32 172, 167, 184; with 64 205, 180, 187
-    // (16 experts, N=K=2048: 14.1, 13.8, 12.0); with 96 264, 198, 194.
+    // (16 experts, N=K=2048: 14.1, 13.8, 12.0); with 96 264, 198, 194.  (The pairs
+    // have become up to 7 % faster since.)
     if (tokens <= (GROUPED ? 16 : 64))
         return launch_tiles<64, GROUPED>(g, pdl, stream);
     if (tokens <= (GROUPED ? 63 : 128))

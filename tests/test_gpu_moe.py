@@ -219,6 +219,51 @@ def test_bad_indices_are_skipped(dev):
     assert (dw[(bad < 0) | (bad >= 7)] == 0).all()
 
 
+def test_rows_past_32_bit_offsets(dev):
+    """Rows more than 2^31 elements behind the first are moved, summed and differentiated."""
+    n, H, T = 34000, 65536, 2
+    row_of = torch.tensor([[n - 1, 0], [n - 3, n - 2]], dtype=torch.int32, device=dev)
+    rows = pkg.MoERows(row_of, torch.empty(n, dtype=torch.int32, device=dev), None, None)
+    x, w = torch.randn(T, H).bfloat16().to(dev), torch.ones(T, 2, device=dev)
+    y = torch.empty(n, H, dtype=torch.bfloat16, device=dev)
+    pkg.ts_moe_dispatch(x, rows, out=y)
+    for t in range(T):
+        for j in range(2):
+            assert torch.equal(y[int(row_of[t, j])], x[t])
+    assert torch.equal(pkg.ts_moe_combine(y, rows, w), (2 * x.float()).bfloat16())
+    dy = torch.empty_like(y)
+    _, dw = pkg.ts_moe_combine_grad(x, y, rows, w, dy=dy)
+    assert torch.equal(dy[n - 1], x[0]) and torch.equal(dy[n - 2], x[1])
+    dots = x.double().square().sum(1, keepdim=True)
+    assert ((dw.double() - dots).abs() <= (H / 256 + 16) * 2.0 ** -24 * dots).all()
+    g = torch.tensor([100.0], device=dev)
+    codes, sf = pkg.ts_moe_dispatch(x, rows, g, sf_layout=2)
+    q, s = pkg.ts_nvfp4_quantize(x, g)
+    assert torch.equal(codes[n - 1], q[0]) and torch.equal(sf[n - 2], s[1])
+
+
+def test_pinned_host_buffers_and_another_stream(dev):
+    T, k, E, H = 19, 3, 7, 136
+    ids = _ids(T, k, E, 3)
+    x, w = torch.randn(T, H).bfloat16(), torch.rand(T, k)
+    rows = pkg.ts_moe_sort(torch.from_numpy(ids).to(dev), E)
+    out = pkg.ts_moe_dispatch(x.to(dev), rows, out=torch.zeros(rows.row_src.numel(), H, dtype=torch.bfloat16, device=dev))
+    want = pkg.ts_moe_combine(out, rows, w.to(dev))
+    wdy, wdw = pkg.ts_moe_combine_grad(x.to(dev), out, rows, w.to(dev), dy=torch.zeros_like(out))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    xh, wh = x.pin_memory(), w.pin_memory()
+    hrows = pkg.ts_moe_sort(torch.from_numpy(ids).pin_memory(), E, stream=s)
+    hout = torch.zeros(hrows.row_src.numel(), H, dtype=torch.bfloat16).pin_memory()
+    pkg.ts_moe_dispatch(xh, hrows, out=hout, stream=s.cuda_stream)
+    got = pkg.ts_moe_combine(hout, hrows, wh, stream=s)
+    hdy = torch.zeros_like(hout).pin_memory()
+    _, hdw = pkg.ts_moe_combine_grad(xh, hout, hrows, wh, dy=hdy, stream=s)
+    s.synchronize()
+    for a, b in zip((*rows, out, want, wdy, wdw), (*hrows, hout, got, hdy, hdw)):
+        assert b.is_pinned() and torch.equal(a.cpu(), b)
+
+
 # ---------------------------------------------------------------------------
 # the layer
 # ---------------------------------------------------------------------------

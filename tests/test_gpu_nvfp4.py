@@ -139,6 +139,34 @@ def test_rows_without_an_entry_are_left(dev):
     assert (out[::3] == 7.0).all() and not (out[1::3] == 7.0).all()
 
 
+def test_strided_rows_and_pinned_host_buffers(dev):
+    """Rows of a wider matrix, and buffers in page-locked host memory, give the bits of contiguous device rows."""
+    wide = _x(21, 400, 4)
+    x, g = wide[:, 16:16 + 240], torch.tensor([37.0])
+    q, s = pkg.ts_nvfp4_quantize(x.contiguous().to(dev), g.to(dev), sf_layout=1)
+    q2, s2 = pkg.ts_nvfp4_quantize(wide.to(dev)[:, 16:16 + 240], g.to(dev), sf_layout=1)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    q3, s3 = pkg.ts_nvfp4_quantize(wide.pin_memory()[:, 16:16 + 240], g.pin_memory(), sf_layout=1)
+    v3 = pkg.ts_nvfp4_dequantize(q3, s3, g.pin_memory(), sf_layout=1)
+    torch.cuda.synchronize()
+    assert q3.is_pinned() and torch.equal(q.cpu(), q3) and torch.equal(s.cpu(), s3)
+    assert torch.equal(pkg.ts_nvfp4_dequantize(q, s, g.to(dev), sf_layout=1).cpu(), v3)
+
+
+def test_rows_past_32_bit_offsets(dev):
+    """More than 2^31 elements in and out: the last rows are those of a small call."""
+    T, K = 33000, 65536
+    x = torch.empty(T, K, dtype=torch.bfloat16, device=dev)
+    tail = _x(3, K, 9).to(dev)
+    x[-3:] = tail
+    g = torch.tensor([5.0], device=dev)
+    q, s = pkg.ts_nvfp4_quantize(x, g)
+    q1, s1 = pkg.ts_nvfp4_quantize(tail, g)
+    assert torch.equal(q[-3:], q1) and torch.equal(s[-3:], s1)
+    pkg.ts_nvfp4_dequantize(q, s, g, out=x)
+    assert torch.equal(x[-3:], pkg.ts_nvfp4_dequantize(q1, s1, g))
+
+
 # ---------------------------------------------------------------------------
 # the product
 # ---------------------------------------------------------------------------
@@ -178,6 +206,42 @@ def test_gemm_random(dev, M, N, K):
     want, mag = want * alpha.double(), mag * alpha.double()
     got = pkg.ts_nvfp4_gemm(ta, tas, tb, tbs, alpha, launch_with_pdl=True).double()
     assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * mag).all()
+
+
+@pytest.mark.parametrize("M", (90, 1500))
+def test_gemm_out_past_32_bit_offsets(dev, M):
+    """An output whose last rows lie more than 2^31 elements behind the first."""
+    N, K, ldo = 72, 64, (1 << 31) // 80 if M == 90 else (1 << 31) // 1400
+    ldo = ldo // 8 * 8
+    a, asf, ta, tas = ref.random_nvfp4(M, K, 3, dev, ref.EXACT_SF)
+    b, bsf, tb, tbs = ref.random_nvfp4(N, K, 4, dev, ref.EXACT_SF)
+    out = torch.empty(M, ldo, dtype=torch.bfloat16, device=dev)[:, :N]
+    assert (M - 1) * out.stride(0) > 1 << 31
+    pkg.ts_nvfp4_gemm(ta, tas, tb, tbs, torch.ones(1, device=dev), out=out)
+    want, _ = _want(a, asf, b, bsf, dev)
+    assert torch.equal(out, want.float().bfloat16())
+
+
+def test_gemm_reads_no_scale_factor_of_other_rows(dev):
+    """NaN scale factors in the padding rows, and rows of NaN scale factors, stay in their own rows and columns."""
+    for M, N in ((5, 24), (70, 136), (300, 264)):
+        a, asf, ta, tas = ref.random_nvfp4(M, 160, 1, dev, ref.EXACT_SF)
+        b, bsf, tb, tbs = ref.random_nvfp4(N, 160, 2, dev, ref.EXACT_SF)
+        asf[M // 2], bsf[3] = 127, 127
+        live = np.zeros((ref.up(M, 128), 12), bool)
+        at, _ = ref.sf_places(ref.up(M, 128), 12, 0)
+        buf = np.full(at.size, 127, np.uint8)
+        at_live, _ = ref.sf_places(M, 12, 0)
+        buf[at_live[:, 10:]] = 0  # the padding columns are zero by definition
+        buf[at_live[:, :10]] = asf
+        tas = torch.from_numpy(buf.reshape(live.shape)).to(dev)
+        tbs = torch.from_numpy(ref.lay_out(bsf, 0)).to(dev)
+        got = pkg.ts_nvfp4_gemm(ta, tas, tb, tbs, torch.ones(1, device=dev))
+        want, _ = _want(a, np.where(asf == 127, 0, asf), b, np.where(bsf == 127, 0, bsf), dev)
+        want = want.float().bfloat16()
+        bad = torch.zeros(M, N, dtype=torch.bool, device=dev)
+        bad[M // 2], bad[:, 3] = True, True
+        assert got[bad].isnan().all() and torch.equal(got[~bad], want[~bad])
 
 
 def test_gemm_no_rows(dev):

@@ -786,6 +786,9 @@ SWEEP_TOKENS = (1, 16, 64, 256, 1024, 4096, 16384)
 # the other entry points in the same table: all-gather pattern 2 over R=8 slices
 # of 1536 | 512 | 64 rows, and the MiniMax QK norm on R=8 shards of q 1024 | k 128
 SWEEP_OTHER = ("allgather-fp8", "qk")
+# and the NVFP4 product with a 7168 x 7168 matrix, and the steps of a layer of 64 experts of 4096 x 7168, 8 a token
+SWEEP_NVFP4 = dict(N=7168, K=7168)
+SWEEP_MOE = dict(k=8, E=64, N=4096, H=7168)
 
 
 def sweep_t(reps: int = 40) -> None:
@@ -876,6 +879,69 @@ def sweep_t(reps: int = 40) -> None:
                                               qi["k_weight"], EPS, qo, ko, launch_with_pdl=True, stream=stream),
                qk_bytes(qs.R, T, qs.q_shard, qs.k_shard), entry="qk", R=qs.R, T=T)
         del qi, qo, ko
+    sweep_nvfp4_moe(report, dev, stream)
+
+
+def fp4_bytes(rows, cols):
+    """Codes and scale factors of NVFP4 values."""
+    return rows * cols * 9 // 16
+
+
+def sweep_nvfp4_moe(report, dev, stream) -> None:
+    """The rows of ``sweep_t`` for the NVFP4 and expert-routing entry points."""
+    import torch
+
+    import reduce_residual_rmsnorm_gb300 as pkg
+
+    kw = dict(launch_with_pdl=True, stream=stream)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(0)
+    one = torch.ones(1, device=dev)
+
+    def fp4(*shape):
+        """Random codes and scale factors of [.., rows, cols] values."""
+        codes = torch.randint(0, 256, (*shape[:-1], shape[-1] // 2), generator=gen, device=dev, dtype=torch.uint8)
+        sf = torch.randint(40, 70, (*shape[:-2], *pkg.sf_shape(shape[-2], shape[-1], 0)), generator=gen, device=dev,
+                           dtype=torch.uint8)
+        return codes, sf
+
+    N, K = SWEEP_NVFP4["N"], SWEEP_NVFP4["K"]
+    b, bs = fp4(N, K)
+    for T in SWEEP_TOKENS:
+        x = torch.randn((T, K), generator=gen, device=dev).to(torch.bfloat16)
+        q, s = pkg.ts_nvfp4_quantize(x, one, sf_layout=0)
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        report(lambda: pkg.ts_nvfp4_quantize(x, one, quant_out=q, scale_out=s, sf_layout=0, **kw),  # noqa: B023
+               2 * T * K + fp4_bytes(T, K), entry="nvfp4-quantize", T=T, K=K)
+        report(lambda: pkg.ts_nvfp4_gemm(q, s, b, bs, one, out=out, **kw),  # noqa: B023
+               fp4_bytes(T + N, K) + 2 * T * N, entry="nvfp4-gemm", T=T, N=N, K=K, flops=2 * T * N * K)
+        del x, q, s, out
+    k, E, N, H = (SWEEP_MOE[n] for n in ("k", "E", "N", "H"))
+    b, bs = fp4(E, N, H)
+    alpha = torch.ones(E, device=dev)
+    for T in SWEEP_TOKENS[:-1]:
+        ids = torch.rand((T, E), generator=gen, device=dev).topk(k, dim=1)[1].int().contiguous()
+        rows = pkg.ts_moe_sort(ids, E, row_align=128)
+        n, touched = T * k, int((rows.expert_count > 0).sum())
+        x = torch.randn((T, H), generator=gen, device=dev).to(torch.bfloat16)
+        w = torch.rand((T, k), generator=gen, device=dev)
+        q, s = pkg.ts_moe_dispatch(x, rows, one)
+        y = pkg.ts_nvfp4_grouped_gemm(q, s, b, bs, alpha, rows)
+        z = torch.empty((rows.row_src.numel(), H), dtype=torch.bfloat16, device=dev)
+        pkg.ts_moe_dispatch(x, rows, out=z)
+        dz, dw, out = torch.empty_like(z), torch.empty_like(w), torch.empty_like(x)
+        key = dict(T=T, k=k, E=E, H=H)
+        report(lambda: pkg.ts_moe_sort(ids, E, row_align=128, rows=rows, **kw),  # noqa: B023
+               8 * n + 4 * rows.row_src.numel() + 8 * E, entry="moe-sort", **key)
+        report(lambda: pkg.ts_moe_dispatch(x, rows, one, quant_out=q, scale_out=s, **kw),  # noqa: B023
+               2 * T * H + fp4_bytes(n, H) + 4 * n, entry="moe-dispatch-nvfp4", **key)
+        report(lambda: pkg.ts_nvfp4_grouped_gemm(q, s, b, bs, alpha, rows, out=y, **kw),  # noqa: B023
+               fp4_bytes(n + touched * N, H) + 2 * n * N, entry="nvfp4-grouped-gemm", N=N, flops=2 * n * N * H, **key)
+        report(lambda: pkg.ts_moe_combine(z, rows, w, out=out, **kw),  # noqa: B023
+               2 * (n + T) * H + 8 * n, entry="moe-combine", **key)
+        report(lambda: pkg.ts_moe_combine_grad(x, z, rows, w, dy=dz, dweights=dw, **kw),  # noqa: B023
+               2 * (2 * n + T) * H + 12 * n, entry="moe-combine-grad", **key)
+        del ids, rows, x, w, q, s, y, z, dz, dw, out
 
 
 def c_abi_call_cost():

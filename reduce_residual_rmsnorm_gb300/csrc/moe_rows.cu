@@ -212,41 +212,44 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const __grid_constant_
     st_v4(a.out + t * a.ldo + (int64_t)c * 8, pack8(acc));
 }
 
-// One block per token: dout's chunk is read once for up to 8 slots, whose rows
-// of y are read and whose rows of dy are written with it; the dot products are
-// summed over the block in a fixed order.
+// One block per token: dout's chunk is read once for up to SLOTS slots, whose
+// rows of y are read and whose rows of dy are written with it; the dot products
+// are summed over the block in an order that H alone fixes.  Bound by memory:
+// 4096 x 8 rows of 7168 in 156.5 us, 94 % of the copy rate.  Blocks of up to 512
+// threads measured 173.7 us there, 4.8 against 4.7 at 16 tokens.
 constexpr int kGradThreads = 256;
 
-__global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const __grid_constant__ CombineArgs a)
+template <int SLOTS>
+__global__ void __launch_bounds__(kGradThreads, SLOTS > 4 ? 2 : 3) moe_combine_grad_kernel(const __grid_constant__ CombineArgs a)
 {
-    __shared__ float part[kGradThreads / 32][kSlots];
+    __shared__ float part[kGradThreads / 32][SLOTS];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nc = (int)(a.H >> 3);
     pdl_wait();
     const uint16_t *drow = a.dout + t * a.ldd;
-    for (int j0 = 0; j0 < a.k; j0 += kSlots) {
-        int64_t r[kSlots];
-        float w[kSlots], dot[kSlots];
+    for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+        int64_t r[SLOTS];
+        float w[SLOTS], dot[SLOTS];
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
+        for (int j = 0; j < SLOTS; ++j) {
             r[j] = j0 + j < a.k ? (int64_t)__ldg(a.row_of + t * a.k + j0 + j) : -1;
             if (!row_ok(r[j], a.rows))
                 r[j] = -1;
             w[j] = r[j] >= 0 ? __ldg(a.weights + t * a.k + j0 + j) : 0.0f;
             dot[j] = 0.0f;
         }
-        for (int c = tid; c < nc; c += kGradThreads) {
-            uint4 y[kSlots];
+        for (int c = tid; c < nc; c += blockDim.x) {
+            uint4 y[SLOTS];
             const uint4 dv = ld_keep(drow + (int64_t)c * 8);
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j)
+            for (int j = 0; j < SLOTS; ++j)
                 if (r[j] >= 0)
                     y[j] = ld_stream(a.y + r[j] * a.ldy + (int64_t)c * 8);
             float d[8];
             unpack8(dv, d);
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j)
+            for (int j = 0; j < SLOTS; ++j)
                 if (r[j] >= 0) {
                     float f[8], o[8];
                     unpack8(y[j], f);
@@ -259,16 +262,15 @@ __global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const __
                 }
         }
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
+        for (int j = 0; j < SLOTS; ++j) {
             dot[j] = warp_sum(dot[j]);
             if (lane == 0)
                 part[warp][j] = dot[j];
         }
         __syncthreads();
-        if (tid < kSlots && j0 + tid < a.k) {
+        if (tid < SLOTS && j0 + tid < a.k) {
             float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kGradThreads / 32; ++i)
+            for (int i = 0; i < (int)(blockDim.x >> 5); ++i)
                 s += part[i][tid];
             a.dweights[t * a.k + j0 + tid] = s;
         }
@@ -320,7 +322,13 @@ cudaError_t launch_combine(const CombineArgs &a, bool pdl, cudaStream_t stream)
 
 cudaError_t launch_combine_grad(const CombineArgs &a, bool pdl, cudaStream_t stream)
 {
-    return launch_kernel(moe_combine_grad_kernel, dim3((unsigned)a.T), dim3(kGradThreads), 0, stream, pdl, a);
+    // no more threads than chunks and no more slots in registers than the call
+    // has: 4096 x 2 rows of 1024 in 7.1 us, 20.5 with 256 threads and 8 slots
+    const int nc = (int)(a.H / 8);
+    const dim3 grid((unsigned)a.T), block((unsigned)(nc < kGradThreads ? (nc + 31) / 32 * 32 : kGradThreads));
+    if (a.k <= 4)
+        return launch_kernel(moe_combine_grad_kernel<4>, grid, block, 0, stream, pdl, a);
+    return launch_kernel(moe_combine_grad_kernel<kSlots>, grid, block, 0, stream, pdl, a);
 }
 
 }  // namespace tsfn

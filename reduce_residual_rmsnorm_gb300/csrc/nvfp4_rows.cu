@@ -12,7 +12,6 @@
 // factors into one 32-bit store.  The others give a lane chunks of 8 columns.
 #include "device_util.cuh"
 #include "launch_nvfp4.h"
-#include "sf_layout.cuh"
 
 namespace tsfn {
 
@@ -21,6 +20,24 @@ namespace {
 constexpr int kThreads = 256;  // at most
 constexpr int kChunks = 4;  // chunks of 8 columns per lane
 constexpr int kBlocks = 2;  // blocks of 16 columns per lane
+
+// Where row m's scale factors begin and how far a group of 4 lies from the next,
+// for rows of sf_cols of them in one of the three layouts (those of
+// sf_layout.cuh, whose functions take the fused call's arguments).
+__device__ __forceinline__ int64_t sf_row_base(int layout, int64_t sf_cols, int64_t m)
+{
+    const int64_t groups = sf_cols >> 2;
+    if (layout == kSfSwizzled128x4)  // 512-byte tiles: row 32*i + j of a tile at byte 16*j + 4*i
+        return (m >> 7) * groups * 512 + (m & 31) * 16 + ((m & 127) >> 5) * 4;
+    if (layout == kSfSwizzled8x4)  // 32-byte tiles, row-major inside
+        return (m >> 3) * groups * 32 + (m & 7) * 4;
+    return m * sf_cols;
+}
+
+__device__ __forceinline__ int sf_group_stride(int layout)
+{
+    return layout == kSfSwizzled128x4 ? 512 : (layout == kSfSwizzled8x4 ? 32 : 4);
+}
 
 // The 16 E2M1 codes of a block, and its scale factor.
 __device__ __forceinline__ uint2 quantize_block(const uint4 (&v)[2], float g, uint32_t &sf)
@@ -57,7 +74,7 @@ __device__ __forceinline__ uint32_t gather_sf(uint32_t sf)
 __device__ __forceinline__ void store_sf(const RowsArgs &a, int64_t row, int b0, int lg, const uint32_t (&sf)[kBlocks])
 {
     const int nb = (int)(a.K >> 4);
-    const int stride = sf_tile_stride(a.sf_layout);
+    const int stride = sf_group_stride(a.sf_layout);
     uint8_t *p = a.sf + sf_row_base(a.sf_layout, a.sf_cols, row);
     if ((nb & 3) == 0) {
         if ((b0 & 3) == 0) {  // (2^lg >= 4 here)
@@ -209,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) nvfp4_values_kernel(const __grid_con
         return;
     const uint8_t *codes = a.codes + t * (a.K >> 1);
     const uint8_t *sf = a.sf + sf_row_base(a.sf_layout, a.sf_cols, t);
-    const int stride = sf_tile_stride(a.sf_layout);
+    const int stride = sf_group_stride(a.sf_layout);
     uint32_t w[kChunks], s[kChunks];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {

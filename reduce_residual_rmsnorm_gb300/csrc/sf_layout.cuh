@@ -15,29 +15,20 @@
 
 namespace tsfn {
 
-__device__ __forceinline__ int sf_tile_stride(int layout)
+__device__ __forceinline__ int sf_tile_stride(const FusedArgs &a)
 {
-    return layout == kSfLinear ? 4 : (layout == kSfSwizzled8x4 ? 32 : 512);
+    return a.sf_layout == kSfLinear ? 4 : (a.sf_layout == kSfSwizzled8x4 ? 32 : 512);
 }
-
-// sf_cols: the 16-column blocks of a row, padded to a multiple of 4 where the
-// layout is swizzled.
-__device__ __forceinline__ int64_t sf_row_base(int layout, int64_t sf_cols, int64_t m)
-{
-    if (layout == kSfLinear)
-        return m * sf_cols;
-    const int64_t tiles_per_band = sf_cols >> 2;
-    if (layout == kSfSwizzled8x4)  // 32-byte tiles, row-major inside: row m%8 at byte 4*(m%8)
-        return (m >> 3) * tiles_per_band * 32 + (m & 7) * 4;
-    // 512-byte tiles; inside a tile row m%128 = 32*i + j sits at byte 16*j + 4*i
-    return (m >> 7) * tiles_per_band * 512 + (m & 31) * 16 + ((m & 127) >> 5) * 4;
-}
-
-__device__ __forceinline__ int sf_tile_stride(const FusedArgs &a) { return sf_tile_stride(a.sf_layout); }
 
 __device__ __forceinline__ int64_t sf_row_base(const FusedArgs &a, int64_t m)
 {
-    return sf_row_base(a.sf_layout, a.sf_cols, m);
+    if (a.sf_layout == kSfLinear)
+        return m * (a.H >> 4);
+    const int64_t tiles_per_band = a.sf_cols >> 2;
+    if (a.sf_layout == kSfSwizzled8x4)  // 32-byte tiles, row-major inside: row m%8 at byte 4*(m%8)
+        return (m >> 3) * tiles_per_band * 32 + (m & 7) * 4;
+    // 512-byte tiles; inside a tile row m%128 = 32*i + j sits at byte 16*j + 4*i
+    return (m >> 7) * tiles_per_band * 512 + (m & 31) * 16 + ((m & 127) >> 5) * 4;
 }
 
 __device__ __forceinline__ int64_t sf_offset(const FusedArgs &a, int64_t m, int64_t k)

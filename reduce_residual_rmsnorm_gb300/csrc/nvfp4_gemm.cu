@@ -16,7 +16,7 @@
 //     columns follows them.  Bound by the tensor cores: 7.3 PFLOP/s at 8192 x
 //     7168 x 7168, 86 % of a tile's cycles, and the power limit in long runs.
 //
-// One block per SM, persistent over the tiles.  Warp 0 copies: codes by TMA
+// One block per SM, persistent over the tiles.  One warp copies (two where tokens are few): codes by TMA
 // under the 128-byte swizzle, 256 elements of K (128 bytes a row) per stage,
 // scale factors in the 512-byte tiles of their 128x4 layout, which is the
 // layout tensor memory wants.  Warp 1 multiplies: scale factors from shared to
@@ -36,7 +36,7 @@ namespace {
 
 __device__ uint32_t g_stalled_waits;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kP = 128;               // rows of P per tile
 constexpr int kSfTile = 512;          // bytes of a 128-row, 64-element tile of scale factors
 constexpr long long kWaitCycles = 4000000000LL;  // a wait's limit: about 2 s
@@ -93,26 +93,30 @@ struct Tile {
     int expert;
 };
 
+// (Tiles are fewer than 2^31, since the output fits the GPU: 32-bit divisions.)
 template <int PN, int BN, bool SWAP>
-__device__ __forceinline__ Tile dense_tile(const KernelArgs &a, int64_t id)
+__device__ __forceinline__ Tile dense_tile(const KernelArgs &a, uint32_t id)
 {
-    // groups of 8 P tiles pass over Q together, so that blocks running at the
-    // same time share rows of both
-    const int64_t np = (a.p_rows + PN - 1) / PN, nq = (a.q_rows + BN - 1) / BN;
-    const int64_t group = id / (8 * nq);
-    const int64_t gp = np - group * 8 < 8 ? np - group * 8 : 8;
-    const int64_t in = id - group * 8 * nq;
-    const int64_t p = group * 8 + in % gp, q = in / gp;
+    uint32_t p = id, q = 0;
+    if constexpr (!SWAP) {
+        // groups of 8 P tiles pass over Q together, so that blocks running at the
+        // same time share rows of both
+        const uint32_t np = (uint32_t)((a.p_rows + PN - 1) / PN), nq = (uint32_t)((a.q_rows + BN - 1) / BN);
+        const uint32_t group = id / (8 * nq);
+        const uint32_t gp = np - group * 8 < 8 ? np - group * 8 : 8;
+        const uint32_t in = id - group * 8 * nq;
+        q = in / gp;
+        p = group * 8 + in - q * gp;
+    }  // else the tokens are one tile of Q
     Tile t;
     t.p_row = (int32_t)(p * PN);
     t.q_row = (int32_t)(q * BN);
-    t.p_band = (p * PN) >> 7;
-    t.q_band = (q * BN) >> 7;
-    const int64_t bands = (a.q_rows + 127) >> 7;
-    t.q_bands = (int)(bands - t.q_band < kBandsOf<BN> ? bands - t.q_band : kBandsOf<BN>);
-    t.q_sub = (int)((q * BN) & 127) >> 5;
+    t.p_band = t.p_row >> 7;
+    t.q_band = t.q_row >> 7;
     const int64_t p_n = a.p_rows - t.p_row < PN ? a.p_rows - t.p_row : PN;
     const int64_t q_n = a.q_rows - t.q_row < BN ? a.q_rows - t.q_row : BN;
+    t.q_bands = (int)(q_n + 127) >> 7;
+    t.q_sub = 0;
     t.tok0 = SWAP ? t.q_row : t.p_row;
     t.tok_n = (int)(SWAP ? q_n : p_n);
     t.wgt0 = SWAP ? t.p_row : t.q_row;
@@ -204,7 +208,7 @@ __device__ __forceinline__ Tile tile_at(const KernelArgs &a, const int32_t *firs
     if constexpr (GROUPED)
         return grouped_tile<PN, BN, SWAP>(a, first, id);
     else
-        return dense_tile<PN, BN, SWAP>(a, id);
+        return dense_tile<PN, BN, SWAP>(a, (uint32_t)id);
 }
 
 // Wait with a limit, for what is in flight when a block gives up.
@@ -215,11 +219,18 @@ __device__ __noinline__ void wait_last(uint32_t bar, uint32_t parity)
     }
 }
 
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
+{
+    return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+}
+
+template <bool CLUSTER>
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *dead)
 {
     const long long t0 = clock64();
     while (!*dead) {
-        if (mbar_try_wait(bar, parity))
+        if (try_wait<CLUSTER>(bar, parity))
             return true;
         if (clock64() - t0 > kWaitCycles) {
             *dead = 1;
@@ -230,18 +241,11 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 }
 
 // The whole warp waits; false in every lane when a wait ran into its limit,
-// here or elsewhere in the block.
+// here or elsewhere in the block.  CLUSTER: for what another block sent.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *dead)
 {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_slow(bar, parity, dead));
-}
-
-// As wait_warp; what other blocks of the cluster wrote before they arrived is visible.
-__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int *dead)
-{
-    const bool good = wait_warp(bar, parity, dead);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return good;
+    return __all_sync(0xffffffffu, try_wait<CLUSTER>(bar, parity) || wait_slow<CLUSTER>(bar, parity, dead));
 }
 
 template <int BN, bool GROUPED>
@@ -267,6 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t partial = drained + 8;  // the cluster's partial sums are here
     const int lg = GROUPED ? 0 : a.split_log2, split = 1 << lg, rank = GROUPED ? 0 : (int)cluster_rank();
 
+    // four-token groups of the partial sums that this block sums up
+    const int fours = ((int)a.q_rows + 3) >> 2, my_fours = rank < fours ? (fours - rank + split - 1) >> lg : 0;
+
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full + 8 * s, 1);
@@ -277,8 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(acc_empty + 8 * i, 4);
         }
         mbar_init(drained, 1);
-        mbar_init(partial, 4 * split);
+        mbar_init(partial, 1);
         mbar_fence_init();
+        if (split > 1)
+            mbar_expect_tx(partial, (uint32_t)(split * my_fours * kP * 16));
         dead_flag = 0;
         tma_prefetch_map(&p_map);
         tma_prefetch_map(&q_map);
@@ -291,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();  // the barriers of every block are ready
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
-    pdl_wait();
+    if (GROUPED)  // (else the warps that touch global memory wait, with their tile found)
+        pdl_wait();
 
     const int64_t tiles = tile_count<kP, BN, true, GROUPED>(a, first);
     auto tile_of = [&](int64_t id) { return tile_at<kP, BN, true, GROUPED>(a, first, id); };
@@ -300,31 +310,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kt0 = (all_steps * rank) >> lg, kt1 = (all_steps * (rank + 1)) >> lg;
     const int64_t id0 = blockIdx.x >> lg, stride = gridDim.x >> lg;
 
-    if (warp == 0) {
-        // ---- copies ----
+    if (warp == 0 || warp == 6) {
+        // ---- copies: warp 0 P, warp 6 Q; an issue takes about 100 cycles ----
+        const bool of_p = warp == 0;
+        const CUtensorMap *map = of_p ? &p_map : &q_map;
         int s = 0;
         uint32_t parity = 0;
         int64_t fills = 0;
         bool good = true;
         for (int64_t id = id0; good && id < tiles; id += stride) {
             const Tile t = tile_of(id);
-            const uint8_t *psf = a.p_sf + t.p_band * a.kblocks * kSfTile;
-            const uint8_t *qsf = a.q_sf + t.q_band * a.kblocks * kSfTile;
+            const uint8_t *from = of_p ? a.p_sf + t.p_band * a.kblocks * kSfTile : a.q_sf + t.q_band * a.kblocks * kSfTile;
+            const int32_t row = of_p ? t.p_row : t.q_row;
+            if (!GROUPED && fills == 0)
+                pdl_wait();
             for (int kt = kt0; kt < kt1; ++kt) {
                 good = wait_warp(empty + 8 * s, parity ^ 1, dead);
                 if (!good)
                     break;
                 const int nkb = a.kblocks - 4 * kt < 4 ? a.kblocks - 4 * kt : 4;
                 const uint32_t bar = full + 8 * s;
-                const uint32_t c = codes + s * S::kCodes, f = sf + s * S::kSf;
+                const uint32_t c = codes + s * S::kCodes + (of_p ? 0 : kP * 128);
+                const uint32_t f = sf + s * S::kSf + (of_p ? 0 : 4 * kSfTile);
                 if (elect_one()) {
-                    mbar_expect_tx(bar, (uint32_t)(S::kCodes + nkb * kSfTile * (1 + t.q_bands)));
-                    tma_load_2d(c, &p_map, kt * 128, t.p_row, bar);
-                    tma_load_2d(c + kP * 128, &q_map, kt * 128, t.q_row, bar);
-                    bulk_load(f, psf + (int64_t)kt * 4 * kSfTile, (uint32_t)(nkb * kSfTile), bar);
-                    for (int b = 0; b < t.q_bands; ++b)
-                        bulk_load(f + (1 + b) * 4 * kSfTile, qsf + ((int64_t)b * a.kblocks + kt * 4) * kSfTile,
-                                  (uint32_t)(nkb * kSfTile), bar);
+                    if (of_p)  // (Q's bytes may be there before they are expected)
+                        mbar_expect_tx(bar, (uint32_t)(S::kCodes + 2 * nkb * kSfTile));
+                    tma_load_2d(c, map, kt * 128, row, bar);
+                    bulk_load(f, from + (int64_t)kt * 4 * kSfTile, (uint32_t)(nkb * kSfTile), bar);
                 }
                 __syncwarp();
                 ++fills;
@@ -396,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             wait_last(drained, 0);
         }
-    } else if (warp >= 2) {
+    } else {
         // ---- output ----
         const int quad = warp & 3;
         const int row = quad * 32 + lane;  // lane of the accumulator
@@ -405,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t n = 0;
         for (int64_t id = id0; id < tiles; id += stride, ++n) {
             const Tile t = tile_of(id);
+            if (!GROUPED && n == 0)
+                pdl_wait();
             const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
             const uint32_t acc = (uint32_t)n & 1;
             if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
@@ -423,9 +437,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int four = (c0 >> 2) + j;
+                        const uint32_t to = four & (split - 1);
                         if (4 * four < t.tok_n)
-                            st_cluster(map_rank(sums + sum_at(rank, four >> lg), four & (split - 1)),
-                                       make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                            st_async_cluster(map_rank(sums + sum_at(rank, four >> lg), to),
+                                             make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]),
+                                             map_rank(partial, to));
                     }
                 } else if (row < t.wgt_n) {
                     uint16_t *o = a.out + (t.tok0 + c0) * a.ldo + t.wgt0 + row;
@@ -436,11 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (split > 1) {  // the only tile of the cluster
-                const int fours = (t.tok_n + 3) >> 2;
-                __syncwarp();
-                if (lane < split && lane < fours)
-                    mbar_arrive_cluster(map_rank(partial, lane));
-                if (rank >= fours || !wait_warp_cluster(partial, 0, dead))
+                if (my_fours == 0 || !wait_warp<true>(partial, 0, dead))
                     break;
                 for (int four = rank; four < fours; four += split) {
                     float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -473,12 +485,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
+    if (split > 1)
+        cluster_arrive();
     tmem_fence_before();
     __syncthreads();
     if (warp == 1) {
         tmem_fence_after();
         tmem_dealloc(tmem, S::kColumns);
     }
+    if (split > 1)
+        cluster_wait();  // no block ends while another may still send it sums
 }
 
 // ---------------------------------------------------------------------------
@@ -573,7 +589,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
-    pdl_wait();
+    if (GROUPED)  // (else the warps that touch global memory wait, with their tile found)
+        pdl_wait();
 
     const int64_t tiles = tile_count<2 * kP, BN, GROUPED, GROUPED>(a, first);
     auto tile_of = [&](int64_t id) { return tile_at<2 * kP, BN, GROUPED, GROUPED>(a, first, id); };
@@ -594,6 +611,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             const int32_t p_row = t.p_row + (int32_t)rank * kP, q_row = t.q_row + (int32_t)rank * (columns(t) / 2);
             const int q_bands = GROUPED ? t.q_bands : S::kBands;
             const int32_t p_band = (int32_t)t.p_band + (int32_t)rank, q_band = (int32_t)t.q_band;
+            if (!GROUPED && fills == 0)
+                pdl_wait();
             for (int kt = 0; kt < steps; ++kt) {
                 good = wait_warp(empty + 8 * s, parity ^ 1, dead);
                 if (!good)
@@ -690,6 +709,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         int64_t n = 0;
         for (int64_t id = id0; id < tiles; id += stride, ++n) {
             const Tile t = tile_of(id);
+            if (!GROUPED && n == 0)
+                pdl_wait();
             const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
             const uint32_t acc = (uint32_t)n & 1;
             if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))

@@ -60,6 +60,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 
+// As mbar_try_wait; what other blocks of the cluster sent is visible after it.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+
 // ---------------------------------------------------------------------------
 // copies into shared memory
 // ---------------------------------------------------------------------------
@@ -209,29 +222,30 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
     return r;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// 16 bytes into the shared memory of a block of the cluster (an address of map_rank).
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint4 v)
-{
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
-// As above without ordering this thread's memory accesses, for what only tensor
-// memory is to be ordered by (tcgen05.wait and the fence before).  The release
-// of the other form took over 1000 cycles behind outstanding stores.
+// Arrive on a barrier of the cluster (an address of map_rank) without ordering
+// this thread's memory accesses, for what only tensor memory is to be ordered by
+// (tcgen05.wait and the fence before).  A releasing arrival took over 1000 cycles
+// behind outstanding stores.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 16 bytes into the shared memory of a block of the cluster, counted on a barrier
+// of that block when they are there (both addresses of map_rank).
+__device__ __forceinline__ void st_async_cluster(uint32_t addr, uint4 v, uint32_t bar)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+                 : "memory");
 }
 
 // As tma_load_2d into this block, completing on a barrier of either block of the pair.

@@ -7,7 +7,7 @@
 // instruction with one E4M3 scale factor per 16, from shared memory into
 // tensor memory.  Its operands are named P (128 rows a block, the accumulator's
 // lanes) and Q (the accumulator's columns) here.  Which matrix is which:
-//   - up to 128 tokens, and up to 63 an expert: weights on P, tokens on Q, so that
+//   - up to 64 tokens (128 with a long K), and up to 63 an expert: weights on P, tokens on Q, so that
 //     a tile is no wider than the tokens need (nvfp4_gemm_kernel).  Bound by the
 //     weights' bytes, and where those are few by latency: K of a tile is then
 //     split over a cluster.
@@ -908,6 +908,22 @@ cudaError_t grow_smem(Kernel kernel, int bytes, std::atomic<bool> (&grown)[kMaxC
     return err;
 }
 
+// Blocks (as a power of two) that share the K of a tile of few tokens: 4 or 2
+// where all tiles still run at once (of clusters of 4 a GB300 runs 36 at a time
+// on its 152 SMs, of 8 only 15) and K is long enough to pay for the exchange,
+// which takes about 0.5 us for a group of 4 tokens and grows with the groups.
+// us alone, over 2, over 4:
+//   M=1   N=4096 K=1024 2.8 2.7 2.9, K=4096 5.6 3.9 3.8;  N=7168 K=1024 2.8 3.0, K=2048 3.8 3.7
+//   M=32  N=4096 K=1024 2.9 3.4 3.5, K=2048 3.9 4.0 3.7, K=4096 5.8 4.9 4.3;  N=7168 K=2048 3.9 4.4
+//   M=64  N=2112 K=2048 5.0 5.2 4.0;  N=4096 K=4096 7.0 6.2 5.2
+int split_log2_of(int64_t tiles, int steps, int64_t tokens, int sms)
+{
+    const bool one_group = tokens <= 4;
+    if (4 * tiles <= sms - sms / 16 && steps >= (one_group ? 4 : 8))
+        return 2;
+    return 2 * tiles <= sms && steps >= (one_group ? 8 : 12) ? 1 : 0;
+}
+
 template <int BN, bool GROUPED>
 cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
 {
@@ -927,16 +943,8 @@ cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
     KernelArgs a = kernel_args(g, true);
     int64_t grid = sms;
     if (!GROUPED) {
-        // K over 2 or 4 blocks where all tiles still run at once: M=1 4096 x 4096
-        // 6.0 us alone, 4.4 over 2, 4.2 over 4; M=16 N=2112 K=7168 8.7, 5.9, 4.4;
-        // M=128 N=512 K=7168 11.4, 9.6, 6.8.  (Of clusters of 4 a GB300 runs 36 at
-        // a time on its 152 SMs, of 8 only 15.)
-        const int64_t tiles = ((a.p_rows + kP - 1) / kP) * ((a.q_rows + BN - 1) / BN);
-        const int steps = (a.kblocks + 3) / 4;
-        if (4 * tiles <= sms - sms / 16 && steps >= 4)
-            a.split_log2 = 2;
-        else if (2 * tiles <= sms && steps >= 2)
-            a.split_log2 = 1;
+        const int64_t tiles = (g.N + kP - 1) / kP;
+        a.split_log2 = split_log2_of(tiles, (a.kblocks + 3) / 4, g.tok_rows, sms);
         grid = tiles < grid ? tiles : grid;
     }
     return launch_clusters(nvfp4_gemm_kernel<BN, GROUPED>, dim3((unsigned)(grid << a.split_log2)), dim3(kThreads),
@@ -988,10 +996,16 @@ cudaError_t launch_by_tokens(const GemmArgs &g, int64_t tokens, bool pdl, cudaSt
     // have become up to 7 % faster since.)
     if (tokens <= (GROUPED ? 16 : 64))
         return launch_tiles<64, GROUPED>(g, pdl, stream);
-    if (tokens <= (GROUPED ? 63 : 128))
+    if (GROUPED && tokens <= 63)
         return launch_tiles<128, GROUPED>(g, pdl, stream);
     if constexpr (!GROUPED) {
         const int sms = current_device_sms();
+        // up to 128 tokens still as one tile's columns where few tiles walk a long K: M=128
+        // N=2112 K=7168 7.0 us against 8.1 in pairs, but K=2048 5.7 against 4.4; M=65 N=7168
+        // K=7168 8.8 against 8.6
+        const int steps = (int)((g.K + 255) / 256);
+        if (tokens <= 128 && steps >= 20 && split_log2_of((g.N + kP - 1) / kP, steps, tokens, sms) == 2)
+            return launch_tiles<128, false>(g, pdl, stream);
         const int64_t np = (g.tok_rows + 2 * kP - 1) / (2 * kP), pairs = sms > 1 ? sms / 2 : 1;
         const int64_t w256 = (np * ((g.N + 255) / 256) + pairs - 1) / pairs;
         const int64_t w128 = (np * ((g.N + 127) / 128) + pairs - 1) / pairs;

@@ -179,7 +179,8 @@ def _want(a, asf, b, bsf, dev):
 
 GEMM = [(1, 8, 32), (1, 128, 64), (2, 16, 96), (5, 136, 160), (31, 72, 256), (32, 264, 288), (33, 128, 512),
         (64, 200, 64), (65, 520, 1056), (100, 256, 320), (128, 384, 2048), (129, 128, 256), (130, 8, 32),
-        (200, 136, 1120), (257, 264, 512), (385, 640, 96), (1000, 1032, 544), (7, 4096, 4096)]
+        (200, 136, 1120), (257, 264, 512), (385, 640, 96), (1000, 1032, 544), (7, 4096, 4096), (4, 264, 1024), (9, 512, 2080),
+        (40, 200, 2048), (61, 8192, 3104), (70, 1032, 5152), (128, 264, 6400), (97, 72, 1056)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)

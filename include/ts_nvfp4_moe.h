@@ -22,6 +22,7 @@
  *   - Results are deterministic.  The row-wise operators give a row the same
  *     bits in every call; the two products sum K in an order that depends on
  *     the call's sizes, so there a row's last bits may change with M.
+ *   - Row strides (ldx, ldo, ...) are in elements, at most 2^30.
  *   - Index arrays that the kernels read (row_of, row_src, expert_start,
  *     expert_count) are device data that the host cannot check: an entry that
  *     points outside the buffers it refers to is skipped, never followed.
@@ -42,7 +43,8 @@ extern "C" {
  *   code = e2m1(x * (g / value(sf)))               0 for the block if value(sf) == 0
  *
  * every step in fp32 with one rounding, ties to even, saturating (the
- * arithmetic of patterns 3 and 5, on x itself).
+ * arithmetic of patterns 3 and 5, on x itself).  An infinite x saturates its
+ * block's scale factor; a NaN leaves its block's codes unspecified.
  *
  *   x             bf16 [T, K], row stride ldx (elements, >= K, multiple of 8).
  *   scale_factor  fp32[1], device-accessible: g.

@@ -77,8 +77,8 @@ int check_cols(const char *name, int64_t cols, int64_t multiple)
 
 int check_stride(const char *name, int64_t ld, int64_t cols)
 {
-    if (ld < cols || ld % 8 != 0 || ld > (1LL << 40))
-        return fail(TS_ERR_SHAPE, "%s = %lld must be a multiple of 8 and at least %lld", name, (long long)ld,
+    if (ld < cols || ld % 8 != 0 || ld > (1LL << 30))  // (rows of 2^31 stay within 64 bits of bytes)
+        return fail(TS_ERR_SHAPE, "%s = %lld must be a multiple of 8 in %lld..2^30", name, (long long)ld,
                     (long long)cols);
     return TS_OK;
 }

@@ -63,6 +63,18 @@ public:
     {
         if (n != want)
             raise(PyExc_TypeError, "%zd arguments, %zd are wanted", n, want);
+        PyObject *stream = args[n - 1];
+        if (stream != Py_None) {  // a torch.cuda.Stream or a raw handle
+            PyObject *raw = PyObject_HasAttrString(stream, "cuda_stream") ? PyObject_GetAttrString(stream, "cuda_stream")
+                                                                          : PyNumber_Index(stream);
+            if (raw == nullptr)
+                throw Raised{};
+            stream_ = static_cast<cudaStream_t>(PyLong_AsVoidPtr(raw));
+            Py_DECREF(raw);
+            if (PyErr_Occurred())
+                throw Raised{};
+            given_ = true;
+        }
     }
 
     bool none(int i) const { return args_[i] == Py_None; }
@@ -161,11 +173,19 @@ public:
         return none(i) ? nullptr : static_cast<const int32_t *>(flat(i, name, kI32, want).data_ptr());
     }
 
-    // A new contiguous tensor where `like` lives.
-    static at::Tensor fresh(const Dims &d, at::ScalarType type, const at::Tensor &like)
+    // A new contiguous tensor where `like` lives, from the memory of the stream
+    // that writes it: another stream's free memory may still be in use there.
+    at::Tensor fresh(const Dims &d, at::ScalarType type, const at::Tensor &like) const
     {
-        if (like.is_cuda())
+        if (like.is_cuda()) {
+            if (!given_)
+                return at::detail::empty_cuda(d.ref(), type, like.device(), std::nullopt);
+            const c10::DeviceIndex device = like.device().index();
+            const c10::cuda::CUDAStreamGuard guard(stream_ == nullptr
+                                                       ? c10::cuda::getDefaultCUDAStream(device)
+                                                       : c10::cuda::getStreamFromExternal(stream_, device));
             return at::detail::empty_cuda(d.ref(), type, like.device(), std::nullopt);
+        }
         return at::empty(d.ref(), at::TensorOptions().dtype(type).pinned_memory(true));
     }
 
@@ -196,20 +216,7 @@ public:
             throw Raised{};
         const int now = c10::cuda::current_device();
         const int device = device_ < 0 ? now : device_;
-        void *stream = nullptr;
-        if (args_[n_ - 1] == Py_None) {
-            stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-        } else {
-            PyObject *raw = PyObject_HasAttrString(args_[n_ - 1], "cuda_stream")
-                                ? PyObject_GetAttrString(args_[n_ - 1], "cuda_stream")
-                                : PyNumber_Index(args_[n_ - 1]);
-            if (raw == nullptr)
-                throw Raised{};
-            stream = PyLong_AsVoidPtr(raw);
-            Py_DECREF(raw);
-            if (PyErr_Occurred())
-                throw Raised{};
-        }
+        void *stream = given_ ? stream_ : c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
         const uint32_t flags = pdl ? TS_FLAG_PDL : 0u;
         int status;
         if (device == now) {
@@ -237,6 +244,8 @@ private:
     PyObject *const *args_;
     Py_ssize_t n_;
     int device_ = -1;
+    cudaStream_t stream_ = nullptr;
+    bool given_ = false;
 };
 
 Dims sf_dims(int64_t T, int64_t K, int64_t layout)
@@ -328,7 +337,7 @@ PyObject *sort(PyObject *const *args, Py_ssize_t n)
     if (E < 0 || E > (1 << 20))
         raise(PyExc_ValueError, "num_experts out of range");
     const at::Tensor of = c.output(3, "rows.row_of", kI32, dims(T, k), ids);
-    const at::Tensor src = fresh ? Call::fresh(dims(rows), kI32, ids) : c.flat(4, "rows.row_src", kI32);
+    const at::Tensor src = fresh ? c.fresh(dims(rows), kI32, ids) : c.flat(4, "rows.row_src", kI32);
     const at::Tensor start = c.output(5, "rows.expert_start", kI32, dims(E + 1), ids);
     const at::Tensor count = c.output(6, "rows.expert_count", kI32, dims(E), ids);
     c.run([&](uint32_t flags, void *stream) {

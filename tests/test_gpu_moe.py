@@ -264,6 +264,69 @@ def test_pinned_host_buffers_and_another_stream(dev):
         assert b.is_pinned() and torch.equal(a.cpu(), b)
 
 
+def test_outputs_belong_to_the_given_stream(dev):
+    """A new output comes from the memory of the stream that writes it, not from what the current stream has just freed
+    with work still queued on it."""
+    T, k, E, H = 64, 2, 4, 4096
+    rows = _rows(dev, T, k, E, stray=False)
+    x = torch.randn(T, H).bfloat16().to(dev)
+    y = torch.zeros(rows.row_src.numel(), H, dtype=torch.bfloat16, device=dev)
+    pkg.ts_moe_dispatch(x, rows, out=y)
+    want = pkg.ts_moe_combine(y, rows).clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        for _ in range(20):
+            junk = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+            torch.cuda._sleep(2_000_000)
+            junk.fill_(-1.0)  # queued behind the sleep
+            del junk
+            got = pkg.ts_moe_combine(y, rows, stream=stream)
+            s.synchronize()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+
+
+def test_refusals_of_tensors(dev):
+    """What the binding refuses (types, shapes, places) and what the library does (sizes), before any launch."""
+    f, ids = torch.ones(1, device=dev), torch.zeros(3, 2, dtype=torch.int32, device=dev)
+    x = torch.zeros(3, 64, dtype=torch.bfloat16, device=dev)
+    q, s = pkg.ts_nvfp4_quantize(x, f, sf_layout=0)
+    rows = pkg.ts_moe_sort(ids, 4)
+    y, w = torch.zeros(6, 64, dtype=torch.bfloat16, device=dev), torch.ones(3, 2, device=dev)
+    for err, call in (
+            (TypeError, lambda: pkg.ts_nvfp4_quantize(x.half(), f)), (TypeError, lambda: pkg.ts_nvfp4_quantize(x.float(), f)),
+            (TypeError, lambda: pkg.ts_nvfp4_quantize(x, 1.0)), (TypeError, lambda: pkg.ts_nvfp4_quantize(x.cpu(), f)),
+            (ValueError, lambda: pkg.ts_nvfp4_quantize(x.t(), f)), (ValueError, lambda: pkg.ts_nvfp4_quantize(x[0], f)),
+            (ValueError, lambda: pkg.ts_nvfp4_quantize(x, torch.ones(2, device=dev))),
+            (ValueError, lambda: pkg.ts_nvfp4_quantize(x, f, row_src=ids)),
+            (ValueError, lambda: pkg.ts_nvfp4_quantize(x, f, quant_out=q.new_empty(3, 33))),
+            (ValueError, lambda: pkg.ts_nvfp4_quantize(x, f, scale_out=s, sf_layout=1)),
+            (TypeError, lambda: pkg.ts_nvfp4_quantize(x, f, stream="s")),
+            (pkg.TsError, lambda: pkg.ts_nvfp4_quantize(x[:, :40], f)), (pkg.TsError, lambda: pkg.ts_nvfp4_quantize(x, f, sf_layout=5)),
+            (pkg.TsError, lambda: pkg.ts_nvfp4_quantize(x[:, 1:49], f)),
+            (ValueError, lambda: pkg.ts_nvfp4_dequantize(q, s, f)), (ValueError, lambda: pkg.ts_nvfp4_dequantize(q[0], s, f)),
+            (ValueError, lambda: pkg.ts_nvfp4_gemm(q, s, q[:, :16].contiguous(), s, f)),
+            (ValueError, lambda: pkg.ts_nvfp4_gemm(q, s[:64], q, s, f)), (TypeError, lambda: pkg.ts_nvfp4_gemm(q.cpu().pin_memory(), s, q, s, f)),
+            (pkg.TsError, lambda: pkg.ts_nvfp4_gemm(q, s, q, s, f)),  # N = 3
+            (ValueError, lambda: pkg.ts_nvfp4_gemm(q, s, q, s, f, out=x)),
+            (TypeError, lambda: pkg.ts_moe_sort(ids.long(), 4)), (ValueError, lambda: pkg.ts_moe_sort(ids[0], 4)),
+            (ValueError, lambda: pkg.ts_moe_sort(ids, 0)), (ValueError, lambda: pkg.ts_moe_sort(ids, 2000)),
+            (pkg.TsError, lambda: pkg.ts_moe_sort(ids, 4, row_align=128, rows=rows)),
+            (ValueError, lambda: pkg.ts_moe_sort(ids, 5, rows=rows)),
+            (ValueError, lambda: pkg.ts_moe_dispatch(x[:2], rows)), (ValueError, lambda: pkg.ts_moe_dispatch(x, rows, out=y[:5])),
+            (ValueError, lambda: pkg.ts_moe_dispatch(x, rows, f, out=y)), (ValueError, lambda: pkg.ts_moe_dispatch(x, rows, quant_out=q)),
+            (pkg.TsError, lambda: pkg.ts_moe_dispatch(y[3:6], rows, out=y)),  # overlap
+            (ValueError, lambda: pkg.ts_moe_combine(y, rows, w[:2])), (TypeError, lambda: pkg.ts_moe_combine(y, rows, w.double())),
+            (ValueError, lambda: pkg.ts_moe_combine_grad(x[:2], y, rows, w)),
+            (ValueError, lambda: pkg.ts_moe_combine_grad(x, y, rows, w, dy=y[:4])),
+            (pkg.TsError, lambda: pkg.ts_moe_combine_grad(x, y, rows, w, dy=y)),
+            (ValueError, lambda: pkg.ts_nvfp4_grouped_gemm(q, s, q, s, f, rows))):
+        with pytest.raises(err) as e:
+            call()
+        assert str(e.value)
+
+
 # ---------------------------------------------------------------------------
 # the layer
 # ---------------------------------------------------------------------------

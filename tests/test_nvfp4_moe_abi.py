@@ -66,7 +66,7 @@ REFUSED = [
                                                                (C, "H", "ldy"))],
     (G, dict(K=65568), UNSUPPORTED), (X, dict(K=65568), UNSUPPORTED),
     *[(n, {ld: v}, SHAPE) for n, ld in ((Q, "ldx"), (D, "ldo"), (G, "ldo"), (P, "ldx"), (X, "ldo"), (C, "ldy"), (C, "ldo"),
-                                        (R, "ldd"), (R, "ldy"), (R, "lddy")) for v in (64, 100, -104)],
+                                        (R, "ldd"), (R, "ldy"), (R, "lddy")) for v in (64, 100, -104, (1 << 30) + 8)],
     (Q, dict(sf_layout=3), BAD_PATTERN), (D, dict(sf_layout=-1), BAD_PATTERN),
     (P, dict(out=None, scale_factor=_at(3), quant_out=_at(4), scale_out=_at(5), sf_layout=7), BAD_PATTERN),
     *[(n, dict(k=v), SHAPE) for n in (S, P, C, R) for v in (0, 65, -1)],

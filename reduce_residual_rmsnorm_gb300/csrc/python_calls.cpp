@@ -189,6 +189,15 @@ public:
         return at::empty(d.ref(), at::TensorOptions().dtype(type).pinned_memory(true));
     }
 
+    // A contiguous tensor on part of another's storage.
+    static at::Tensor part_of(const at::Tensor &all, int64_t offset, const Dims &d)
+    {
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+        t.unsafeGetTensorImpl()->set_storage_offset(offset);
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(d.ref());
+        return t;
+    }
+
     // The output that is given, checked, or a new one.
     at::Tensor output(int i, const char *name, at::ScalarType type, const Dims &want, const at::Tensor &like)
     {
@@ -336,10 +345,22 @@ PyObject *sort(PyObject *const *args, Py_ssize_t n)
     }
     if (E < 0 || E > (1 << 20))
         raise(PyExc_ValueError, "num_experts out of range");
-    const at::Tensor of = c.output(3, "rows.row_of", kI32, dims(T, k), ids);
-    const at::Tensor src = fresh ? c.fresh(dims(rows), kI32, ids) : c.flat(4, "rows.row_src", kI32);
-    const at::Tensor start = c.output(5, "rows.expert_start", kI32, dims(E + 1), ids);
-    const at::Tensor count = c.output(6, "rows.expert_count", kI32, dims(E), ids);
+    at::Tensor of, src, start, count;
+    if (fresh) {  // parts of one allocation, each on a 256-byte boundary
+        const Dims d[4] = {dims(T, k), dims(rows), dims(E + 1), dims(E)};
+        int64_t at[5] = {0};
+        for (int i = 0; i < 4; ++i)
+            at[i + 1] = at[i] + (c10::multiply_integers(d[i].ref()) + 63) / 64 * 64;
+        const at::Tensor all = c.fresh(dims(at[4]), kI32, ids);
+        at::Tensor *const part[4] = {&of, &src, &start, &count};
+        for (int i = 0; i < 4; ++i)
+            *part[i] = Call::part_of(all, at[i], d[i]);
+    } else {
+        of = c.flat(3, "rows.row_of", kI32, dims(T, k));
+        src = c.flat(4, "rows.row_src", kI32);
+        start = c.flat(5, "rows.expert_start", kI32, dims(E + 1));
+        count = c.flat(6, "rows.expert_count", kI32, dims(E));
+    }
     c.run([&](uint32_t flags, void *stream) {
         return ts_moe_sort(ptr<int32_t>(ids), T, k, E, align, src.numel(), ptr<int32_t>(of), ptr<int32_t>(src),
                            ptr<int32_t>(start), ptr<int32_t>(count), flags, stream);

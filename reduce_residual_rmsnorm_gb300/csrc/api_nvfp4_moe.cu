@@ -249,8 +249,8 @@ extern "C" int ts_nvfp4_grouped_gemm(const void *a, const void *a_scale, const v
     TS_TRY(check_product(N, K, ldo));
     if (E < 1 || E > kMaxExperts)
         return fail(TS_ERR_SHAPE, "E = %lld outside 1..%lld", (long long)E, (long long)kMaxExperts);
-    if (E * N > kMaxRows)
-        return fail(TS_ERR_SHAPE, "E * N = %lld above %lld", (long long)(E * N), (long long)kMaxRows);
+    if (E * N > kMaxRows - 511)  // (32-bit row coordinates, to the end of the last tile)
+        return fail(TS_ERR_SHAPE, "E * N = %lld above %lld", (long long)(E * N), (long long)(kMaxRows - 511));
     if (rows % 128 != 0)
         return fail(TS_ERR_SHAPE, "rows = %lld must be a multiple of 128", (long long)rows);
     if (entries < 0)

@@ -7,14 +7,15 @@
 // instruction with one E4M3 scale factor per 16, from shared memory into
 // tensor memory.  Its operands are named P (128 rows a block, the accumulator's
 // lanes) and Q (the accumulator's columns) here.  Which matrix is which:
-//   - up to 64 tokens (128 with a long K), and up to 63 an expert: weights on P, tokens on Q, so that
-//     a tile is no wider than the tokens need (nvfp4_gemm_kernel).  Bound by the
-//     weights' bytes, and where those are few by latency: K of a tile is then
-//     split over a cluster.
-//   - more tokens: pairs of blocks (nvfp4_pair_kernel) with tokens on P, and in
-//     the grouped form weights on P and an expert's tokens on Q, whose number of
-//     columns follows them.  Bound by the tensor cores: 7.5 PFLOP/s at 8192 x
-//     7168 x 7168, 86 % of a tile's cycles, and the power limit in long runs.
+//   - up to 64 tokens (128 with a long K): weights on P, tokens on Q, so that a
+//     tile is no wider than the tokens need (nvfp4_few_kernel).  Bound by the
+//     weights' bytes, and where those are few by latency.
+//   - more tokens: pairs of blocks (nvfp4_pair_kernel) with tokens on P and weights
+//     on Q.  Bound by the tensor cores: 7.5 PFLOP/s at 8192 x 7168 x 7168, 86 % of
+//     a tile's cycles, and by the power limit in long runs.
+//   - experts: pairs with weights on P and an expert's tokens on Q, whose number of
+//     columns follows them.  Bound by the experts' bytes (within 4 to 9 % of them up
+//     to 64 tokens an expert), then as above.
 //
 // One block per SM, persistent over the tiles.  One warp copies (two where tokens are few): codes by TMA
 // under the 128-byte swizzle, 256 elements of K (128 bytes a row) per stage,
@@ -41,26 +42,6 @@ constexpr int kP = 128;               // rows of P per tile
 constexpr int kSfTile = 512;          // bytes of a 128-row, 64-element tile of scale factors
 constexpr long long kWaitCycles = 4000000000LL;  // a wait's limit: about 2 s
 constexpr int kSmemLimit = 232448;    // bytes of shared memory of a block
-constexpr int kSlack = 1024 + 4 * 1032;  // alignment, and the experts' first tiles
-
-template <int BN>
-constexpr int kBandsOf = BN > 128 ? BN / 128 : 1;  // 128-row bands of Q's scale factors
-
-// SPLIT: room for the partial sums of a tile whose K is split over a cluster.
-template <int BN, bool SPLIT>
-struct Shape {
-    static constexpr int kBands = kBandsOf<BN>;
-    static constexpr int kCodes = kP * 128 + BN * 128;      // bytes of codes per stage
-    static constexpr int kSf = 4 * kSfTile * (1 + kBands);  // bytes of scale factors per stage
-    static constexpr int kPartials = SPLIT ? BN * kP * 4 : 0;
-    static constexpr int kFixed = kSlack + kPartials;
-    static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
-    static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
-    static constexpr int kSfP = 2 * BN;       // tensor-memory column of P's scale factors
-    static constexpr int kSfQ = kSfP + 16;    // and of Q's
-    static constexpr int kColumns = 512;      // one block per SM: all of it
-    static_assert(kSfQ + 16 * kBands <= kColumns, "accumulators and scale factors fit tensor memory");
-};
 
 struct KernelArgs {
     const uint8_t *p_sf;
@@ -80,137 +61,137 @@ struct KernelArgs {
 };
 
 // One tile: the first rows of P and Q in their tensor maps, their scale-factor
-// bands, and the part of the output it covers.
+// bands of 128 rows, and the part of the output it covers.
 struct Tile {
     int32_t p_row, q_row;
-    int64_t p_band, q_band;
-    int q_bands;       // bands of Q inside its buffer
-    int q_sub;         // 32-row group of Q's tile inside its band
-    int64_t tok0;      // output rows tok0 .. tok0 + tok_n
+    int32_t p_band, q_band;
+    int q_bands;   // of the tile's rows of Q
+    int64_t tok0;  // output rows tok0 .. tok0 + tok_n
     int tok_n;
-    int64_t wgt0;      // output columns wgt0 .. wgt0 + wgt_n
+    int64_t wgt0;  // output columns wgt0 .. wgt0 + wgt_n
     int wgt_n;
     int expert;
 };
 
-// (Tiles are fewer than 2^31, since the output fits the GPU: 32-bit divisions.)
-template <int PN, int BN, bool SWAP>
-__device__ __forceinline__ Tile dense_tile(const KernelArgs &a, uint32_t id)
+// Few tokens: weights on P, all tokens one tile of Q.
+__device__ __forceinline__ Tile few_tile(const KernelArgs &a, int32_t id)
 {
-    uint32_t p = id, q = 0;
-    if constexpr (!SWAP) {
-        // groups of 6 P tiles pass over Q together, so that pairs running at the same
-        // time share rows of both (8192 x 7168 x 7168 112.5 us, 16384 x 5120 x 5120 116.6;
-        // groups of 4 112.8 and 121.1, of 8 114.1 and 119.8, of 16 115.4 and 121.4)
-        constexpr uint32_t kGroup = 6;
-        const uint32_t np = (uint32_t)((a.p_rows + PN - 1) / PN), nq = (uint32_t)((a.q_rows + BN - 1) / BN);
-        const uint32_t group = id / (kGroup * nq);
-        const uint32_t gp = np - group * kGroup < kGroup ? np - group * kGroup : kGroup;
-        const uint32_t in = id - group * kGroup * nq;
-        q = in / gp;
-        p = group * kGroup + in - q * gp;
-    }  // else the tokens are one tile of Q
     Tile t;
-    t.p_row = (int32_t)(p * PN);
-    t.q_row = (int32_t)(q * BN);
-    t.p_band = t.p_row >> 7;
-    t.q_band = t.q_row >> 7;
-    const int64_t p_n = a.p_rows - t.p_row < PN ? a.p_rows - t.p_row : PN;
-    const int64_t q_n = a.q_rows - t.q_row < BN ? a.q_rows - t.q_row : BN;
-    t.q_bands = (int)(q_n + 127) >> 7;
-    t.q_sub = 0;
-    t.tok0 = SWAP ? t.q_row : t.p_row;
-    t.tok_n = (int)(SWAP ? q_n : p_n);
-    t.wgt0 = SWAP ? t.p_row : t.q_row;
-    t.wgt_n = (int)(SWAP ? p_n : q_n);
+    t.p_row = id * kP;
+    t.q_row = 0;
+    t.p_band = id;
+    t.q_band = 0;
+    t.q_bands = 1;
+    t.tok0 = 0;
+    t.tok_n = (int)a.q_rows;
+    t.wgt0 = t.p_row;
+    t.wgt_n = (int)(a.p_rows - t.p_row < kP ? a.p_rows - t.p_row : kP);
     t.expert = 0;
     return t;
 }
 
-// first[e]: tiles of tokens before expert e.  An expert's tiles go over its
-// tokens first, so that blocks running at the same time share its weights.
-template <int PN, int BN, bool SWAP>
-__device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t *first, int64_t id)
+// Pairs: tokens on P, weights on Q.  Groups of 6 P tiles pass over Q together, so
+// that pairs running at the same time share rows of both (8192 x 7168 x 7168 112.5
+// us, 16384 x 5120 x 5120 116.6; groups of 4 112.8 and 121.1, of 8 114.1 and 119.8,
+// of 16 115.4 and 121.4).  (Tiles are fewer than 2^31, since the output fits the
+// GPU: 32-bit divisions.)
+template <int BN>
+__device__ __forceinline__ Tile dense_tile(const KernelArgs &a, uint32_t id)
 {
-    constexpr int kTok = SWAP ? BN : PN, kWgt = SWAP ? PN : BN;
-    const int64_t nw = (a.wgt_rows + kWgt - 1) / kWgt;
-    int lo = 0, hi = a.experts;  // the expert e with first[e] * nw <= id < first[e + 1] * nw
+    constexpr uint32_t kGroup = 6;
+    const uint32_t np = (uint32_t)((a.p_rows + 2 * kP - 1) / (2 * kP)), nq = (uint32_t)((a.q_rows + BN - 1) / BN);
+    const uint32_t group = id / (kGroup * nq);
+    const uint32_t gp = np - group * kGroup < kGroup ? np - group * kGroup : kGroup;
+    const uint32_t in = id - group * kGroup * nq;
+    const uint32_t q = in / gp, p = group * kGroup + in - q * gp;
+    Tile t;
+    t.p_row = (int32_t)(p * 2 * kP);
+    t.q_row = (int32_t)(q * BN);
+    t.p_band = t.p_row >> 7;
+    t.q_band = t.q_row >> 7;
+    t.q_bands = BN / 128;
+    t.tok0 = t.p_row;
+    t.tok_n = (int)(a.p_rows - t.p_row < 2 * kP ? a.p_rows - t.p_row : 2 * kP);
+    t.wgt0 = t.q_row;
+    t.wgt_n = (int)(a.q_rows - t.q_row < BN ? a.q_rows - t.q_row : BN);
+    t.expert = 0;
+    return t;
+}
+
+// Pairs, grouped: weights on P, an expert's tokens on Q.  first[e]: tiles of tokens
+// before expert e.  An expert's tiles go over its tokens first, so that pairs
+// running at the same time share its weights.
+template <int BN>
+__device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t *first, uint32_t id)
+{
+    const uint32_t nw = ((uint32_t)a.wgt_rows + 2 * kP - 1) / (2 * kP), before = id / nw;
+    int lo = 0, hi = a.experts;  // the expert e with first[e] <= before < first[e + 1]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((int64_t)first[mid] * nw <= id)
+        if ((uint32_t)first[mid] <= before)
             lo = mid;
         else
             hi = mid;
     }
-    const int nt = first[lo + 1] - first[lo];
-    const int64_t in = id - (int64_t)first[lo] * nw;
-    const int tok = (int)(in % nt);
-    const int w0 = (int)(in / nt) * kWgt;
+    const uint32_t nt = (uint32_t)(first[lo + 1] - first[lo]);
+    const uint32_t in = id - (uint32_t)first[lo] * nw;
+    const uint32_t w = in / nt;
+    const int t0 = (int)(in - w * nt) * BN, w0 = (int)w * 2 * kP;
     const int count = __ldg(a.count + lo), start = __ldg(a.start + lo);
-    const int t0 = tok * kTok;
     Tile t;
     t.expert = lo;
     t.tok0 = start + t0;
-    t.tok_n = count - t0 < kTok ? count - t0 : kTok;
+    t.tok_n = count - t0 < BN ? count - t0 : BN;
     t.wgt0 = w0;
-    t.wgt_n = a.wgt_rows - w0 < kWgt ? a.wgt_rows - w0 : kWgt;
-    const int32_t tok_row = start + t0, wgt_row = lo * a.wgt_rows + w0;
-    const int64_t tok_band = tok_row >> 7, wgt_band = (int64_t)lo * a.wgt_bands + (w0 >> 7);
-    t.p_row = SWAP ? wgt_row : tok_row;
-    t.q_row = SWAP ? tok_row : wgt_row;
-    t.p_band = SWAP ? wgt_band : tok_band;
-    t.q_band = SWAP ? tok_band : wgt_band;
-    const int left = SWAP ? (t.tok_n + 127) >> 7 : a.wgt_bands - (w0 >> 7);
-    t.q_bands = left < kBandsOf<BN> ? left : kBandsOf<BN>;
-    t.q_sub = ((SWAP ? tok_row : w0) & 127) >> 5;
+    t.wgt_n = a.wgt_rows - w0 < 2 * kP ? a.wgt_rows - w0 : 2 * kP;
+    t.p_row = lo * a.wgt_rows + w0;
+    t.q_row = start + t0;
+    t.p_band = lo * a.wgt_bands + (w0 >> 7);
+    t.q_band = t.q_row >> 7;
+    t.q_bands = (t.tok_n + 127) >> 7;
     return t;
 }
 
-// Tiles of the call.  Grouped: every thread of the block takes part and fills
-// first[0 .. experts].
-template <int PN, int BN, bool SWAP, bool GROUPED>
-__device__ __forceinline__ int64_t tile_count(const KernelArgs &a, int32_t *first)
-{
-    if constexpr (!GROUPED) {
-        return ((a.p_rows + PN - 1) / PN) * ((a.q_rows + BN - 1) / BN);
-    } else {
-        constexpr int kTok = SWAP ? BN : PN, kWgt = SWAP ? PN : BN;
-        const int lane = threadIdx.x & 31;
-        for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-            const int start = __ldg(a.start + e), count = __ldg(a.count + e);
-            const bool good = start >= 0 && (start & 127) == 0 && count > 0 && (int64_t)start + count <= a.tok_rows;
-            first[e + 1] = good ? (count + kTok - 1) / kTok : 0;
-        }
-        __syncthreads();
-        if (threadIdx.x < 32) {  // inclusive scan
-            int32_t sum = 0;
-            for (int e0 = 0; e0 < a.experts; e0 += 32) {
-                int32_t v = e0 + lane < a.experts ? first[e0 + lane + 1] : 0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int32_t up = __shfl_up_sync(0xffffffffu, v, o);
-                    if (lane >= o)
-                        v += up;
-                }
-                if (e0 + lane < a.experts)
-                    first[e0 + lane + 1] = sum + v;
-                sum += __shfl_sync(0xffffffffu, v, 31);
-            }
-            if (lane == 0)
-                first[0] = 0;
-        }
-        __syncthreads();
-        return (int64_t)first[a.experts] * ((a.wgt_rows + kWgt - 1) / kWgt);
-    }
-}
-
-template <int PN, int BN, bool SWAP, bool GROUPED>
-__device__ __forceinline__ Tile tile_at(const KernelArgs &a, const int32_t *first, int64_t id)
+template <int BN, bool GROUPED>
+__device__ __forceinline__ Tile pair_tile(const KernelArgs &a, const int32_t *first, int64_t id)
 {
     if constexpr (GROUPED)
-        return grouped_tile<PN, BN, SWAP>(a, first, id);
+        return grouped_tile<BN>(a, first, (uint32_t)id);
     else
-        return dense_tile<PN, BN, SWAP>(a, (uint32_t)id);
+        return dense_tile<BN>(a, (uint32_t)id);
+}
+
+// Tiles of a grouped call; every thread of the block takes part and fills
+// first[0 .. experts].
+template <int BN>
+__device__ __forceinline__ int64_t grouped_tiles(const KernelArgs &a, int32_t *first)
+{
+    const int lane = threadIdx.x & 31;
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+        const int start = __ldg(a.start + e), count = __ldg(a.count + e);
+        const bool good = start >= 0 && (start & 127) == 0 && count > 0 && (int64_t)start + count <= a.tok_rows;
+        first[e + 1] = good ? (count + BN - 1) / BN : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {  // inclusive scan
+        int32_t sum = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 32) {
+            int32_t v = e0 + lane < a.experts ? first[e0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t up = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o)
+                    v += up;
+            }
+            if (e0 + lane < a.experts)
+                first[e0 + lane + 1] = sum + v;
+            sum += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0)
+            first[0] = 0;
+    }
+    __syncthreads();
+    return (int64_t)first[a.experts] * ((a.wgt_rows + 2 * kP - 1) / (2 * kP));
 }
 
 // Wait with a limit, for what is in flight when a block gives up.
@@ -250,12 +231,40 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, try_wait<CLUSTER>(bar, parity) || wait_slow<CLUSTER>(bar, parity, dead));
 }
 
-template <int BN, bool GROUPED>
+// ---------------------------------------------------------------------------
+// few tokens
+// ---------------------------------------------------------------------------
+//
+// A tile is 128 rows of the weights and all tokens, so that a row of weights is
+// read once.  Where few tiles leave SMs idle, 2 or 4 blocks of a cluster share a
+// tile's K and each sums up a share of the tokens from all of them, in their
+// order.  Latency counts here: two warps copy, since an issue takes about 100
+// cycles; the partial sums travel by stores that the receiving barrier counts,
+// with no fence; and a tile is found before the dependency wait.  1 x 4096 x 4096
+// takes 3.8 us (1.4 of bytes): about 0.5 us from the wait to the first copy's
+// issue, 0.8 to its arrival, 0.9 for the four steps, 0.3 to the accumulator, 0.4
+// to the exchanged sums.
+
+template <int BN>
+struct Shape {
+    static constexpr int kCodes = kP * 128 + BN * 128;  // bytes of codes per stage
+    static constexpr int kSf = 8 * kSfTile;             // bytes of scale factors per stage
+    static constexpr int kPartials = BN * kP * 4;
+    static constexpr int kFixed = 1024 + kPartials;     // and alignment
+    static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
+    static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
+    static constexpr int kSfP = 2 * BN;       // tensor-memory column of P's scale factors
+    static constexpr int kSfQ = kSfP + 16;    // and of Q's
+    static constexpr int kColumns = 512;      // one block per SM: all of it
+    static_assert(kSfQ + 16 <= kColumns, "accumulators and scale factors fit tensor memory");
+};
+
+template <int BN>
 __global__ void __launch_bounds__(kThreads, 1)
-    nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+    nvfp4_few_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ KernelArgs a)
 {
-    using S = Shape<BN, !GROUPED>;
+    using S = Shape<BN>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * S::kStages + 6];
     __shared__ uint32_t tmem_at;
@@ -264,14 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t codes = smem_u32(raw) + pad;
     const uint32_t sf = codes + S::kStages * S::kCodes;
     const uint32_t sums = sf + S::kStages * S::kSf;  // the cluster's partial sums of this block's share
-    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + S::kStages * (S::kCodes + S::kSf) + S::kPartials);
     volatile int *dead = &dead_flag;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
     const uint32_t acc_full = empty + 8 * S::kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
     const uint32_t partial = drained + 8;  // the cluster's partial sums are here
-    const int lg = GROUPED ? 0 : a.split_log2, split = 1 << lg, rank = GROUPED ? 0 : (int)cluster_rank();
+    const int lg = a.split_log2, split = 1 << lg, rank = (int)cluster_rank();
 
     // four-token groups of the partial sums that this block sums up
     const int fours = ((int)a.q_rows + 3) >> 2, my_fours = rank < fours ? (fours - rank + split - 1) >> lg : 0;
@@ -302,15 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();  // the barriers of every block are ready
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
-    if (GROUPED)  // (else the warps that touch global memory wait, with their tile found)
-        pdl_wait();
-
-    const int64_t tiles = tile_count<kP, BN, true, GROUPED>(a, first);
-    auto tile_of = [&](int64_t id) { return tile_at<kP, BN, true, GROUPED>(a, first, id); };
+    // (the warps that touch global memory wait for the kernel before, with their tile found)
+    const int32_t tiles = (int32_t)((a.p_rows + kP - 1) / kP);
     // this block's steps of 256 elements of K, and its tiles
     const int all_steps = (a.kblocks + 3) >> 2;
     const int kt0 = (all_steps * rank) >> lg, kt1 = (all_steps * (rank + 1)) >> lg;
-    const int64_t id0 = blockIdx.x >> lg, stride = gridDim.x >> lg;
+    const int32_t id0 = (int32_t)blockIdx.x >> lg, stride = (int32_t)gridDim.x >> lg;
 
     if (warp == 0 || warp == 6) {
         // ---- copies: warp 0 P, warp 6 Q; an issue takes about 100 cycles ----
@@ -320,11 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0;
         int64_t fills = 0;
         bool good = true;
-        for (int64_t id = id0; good && id < tiles; id += stride) {
-            const Tile t = tile_of(id);
-            const uint8_t *from = of_p ? a.p_sf + t.p_band * a.kblocks * kSfTile : a.q_sf + t.q_band * a.kblocks * kSfTile;
+        for (int32_t id = id0; good && id < tiles; id += stride) {
+            const Tile t = few_tile(a, id);
+            const uint8_t *from = of_p ? a.p_sf + (int64_t)t.p_band * a.kblocks * kSfTile : a.q_sf;
             const int32_t row = of_p ? t.p_row : t.q_row;
-            if (!GROUPED && fills == 0)
+            if (fills == 0)
                 pdl_wait();
             for (int kt = kt0; kt < kt1; ++kt) {
                 good = wait_warp(empty + 8 * s, parity ^ 1, dead);
@@ -362,8 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0;
         int64_t n = 0;
         bool good = true;
-        for (int64_t id = id0; good && id < tiles; id += stride, ++n) {
-            const int q_sub = GROUPED ? tile_of(id).q_sub : 0;
+        for (int32_t id = id0; good && id < tiles; id += stride, ++n) {
             const uint32_t acc = (uint32_t)n & 1;
             good = wait_warp(acc_empty + 8 * acc, ((uint32_t)(n >> 1) & 1) ^ 1, dead);
             if (!good)
@@ -383,16 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kb = 0; kb < 4; ++kb)
                         if (kb < nkb) {
                             tmem_copy_sf(tmem + S::kSfP + 4 * kb, fd + kb * (kSfTile >> 4));
-#pragma unroll
-                            for (int b = 0; b < S::kBands; ++b)
-                                tmem_copy_sf(tmem + S::kSfQ + 4 * (kb * S::kBands + b),
-                                             fd + ((1 + b) * 4 + kb) * (kSfTile >> 4));
+                            tmem_copy_sf(tmem + S::kSfQ + 4 * kb, fd + (4 + kb) * (kSfTile >> 4));
                         }
 #pragma unroll
                     for (int kb = 0; kb < 4; ++kb)
                         if (kb < nkb)
                             mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + S::kSfP + 4 * kb,
-                                      tmem + S::kSfQ + 4 * kb * S::kBands + q_sub, kt > kt0 || kb > 0);
+                                      tmem + S::kSfQ + 4 * kb, kt > kt0 || kb > 0);
                     mma_commit(empty + 8 * s);
                     if (kt + 1 == kt1)
                         mma_commit(acc_full + 8 * acc);
@@ -417,11 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // byte offset of block r's partial sums of four tokens, the i-th of a block's share: [split][BN / 4 / split][128][4]
         auto sum_at = [&](int r, int i) { return 16 * ((((r * (BN / 4)) >> lg) + i) * kP + row); };
         int64_t n = 0;
-        for (int64_t id = id0; id < tiles; id += stride, ++n) {
-            const Tile t = tile_of(id);
-            if (!GROUPED && n == 0)
+        for (int32_t id = id0; id < tiles; id += stride, ++n) {
+            const Tile t = few_tile(a, id);
+            if (n == 0)
                 pdl_wait();
-            const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
+            const float alpha = __ldg(a.alpha);
             const uint32_t acc = (uint32_t)n & 1;
             if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
                 break;
@@ -533,7 +534,7 @@ struct PairShape {
     static constexpr int kCodes = kP * 128 + (BN / 2) * 128;     // bytes per stage and block
     static constexpr int kSf = 4 * kSfTile * (1 + kBands);
     static constexpr int kOut = 8 * 32 * 64;                     // staging: warps x rows x bytes
-    static constexpr int kFixed = kSlack + kOut;
+    static constexpr int kFixed = 1024 + kOut + 4 * 1032;       // and alignment, the experts' first tiles
     static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
     static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
     static constexpr int kAcc1 = kShared ? BN - 64 : BN;         // column of the second accumulator
@@ -591,11 +592,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
-    if (GROUPED)  // (else the warps that touch global memory wait, with their tile found)
+    int64_t tiles;
+    if constexpr (GROUPED) {
         pdl_wait();
-
-    const int64_t tiles = tile_count<2 * kP, BN, GROUPED, GROUPED>(a, first);
-    auto tile_of = [&](int64_t id) { return tile_at<2 * kP, BN, GROUPED, GROUPED>(a, first, id); };
+        tiles = grouped_tiles<BN>(a, first);
+    } else {  // (the warps that touch global memory wait, with their tile found)
+        tiles = ((a.p_rows + 2 * kP - 1) / (2 * kP)) * ((a.q_rows + BN - 1) / BN);
+    }
+    auto tile_of = [&](int64_t id) { return pair_tile<BN, GROUPED>(a, first, id); };
     // columns of the products of a tile: all, or the expert's tokens rounded up
     auto columns = [](const Tile &t) { return GROUPED ? (t.tok_n + 31) & ~31 : BN; };
     const int steps = (a.kblocks + 3) >> 2;
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             const Tile t = tile_of(id);
             const int32_t p_row = t.p_row + (int32_t)rank * kP, q_row = t.q_row + (int32_t)rank * (columns(t) / 2);
             const int q_bands = GROUPED ? t.q_bands : S::kBands;
-            const int32_t p_band = (int32_t)t.p_band + (int32_t)rank, q_band = (int32_t)t.q_band;
+            const int32_t p_band = t.p_band + (int32_t)rank, q_band = t.q_band;
             if (!GROUPED && fills == 0)
                 pdl_wait();
             for (int kt = 0; kt < steps; ++kt) {
@@ -926,30 +930,25 @@ int split_log2_of(int64_t tiles, int steps, int64_t tokens, int sms)
     return 2 * tiles <= sms && steps >= (one_group ? 8 : 12) ? 1 : 0;
 }
 
-template <int BN, bool GROUPED>
-cudaError_t launch_tiles(const GemmArgs &g, bool pdl, cudaStream_t stream)
+template <int BN>
+cudaError_t launch_few(const GemmArgs &g, bool pdl, cudaStream_t stream)
 {
-    using S = Shape<BN, !GROUPED>;
+    using S = Shape<BN>;
     static std::atomic<bool> grown[kMaxCachedDevices];
     int dev = 0;
     const int sms = current_device_sms(&dev);
     if (sms <= 0)
         return cudaErrorInvalidDevice;
-    const cudaError_t err = grow_smem(nvfp4_gemm_kernel<BN, GROUPED>, S::kSmem, grown, dev);
+    const cudaError_t err = grow_smem(nvfp4_few_kernel<BN>, S::kSmem, grown, dev);
     if (err != cudaSuccess)
         return err;
     CUtensorMap p_map, q_map;
-    if (!codes_map(&p_map, g.wgt, GROUPED ? g.experts * g.N : g.N, g.K, kP) ||
-        !codes_map(&q_map, g.tok, g.tok_rows, g.K, BN))
+    if (!codes_map(&p_map, g.wgt, g.N, g.K, kP) || !codes_map(&q_map, g.tok, g.tok_rows, g.K, BN))
         return cudaErrorInvalidValue;
     KernelArgs a = kernel_args(g, true);
-    int64_t grid = sms;
-    if (!GROUPED) {
-        const int64_t tiles = (g.N + kP - 1) / kP;
-        a.split_log2 = split_log2_of(tiles, (a.kblocks + 3) / 4, g.tok_rows, sms);
-        grid = tiles < grid ? tiles : grid;
-    }
-    return launch_clusters(nvfp4_gemm_kernel<BN, GROUPED>, dim3((unsigned)(grid << a.split_log2)), dim3(kThreads),
+    const int64_t tiles = (g.N + kP - 1) / kP, grid = tiles < sms ? tiles : sms;
+    a.split_log2 = split_log2_of(tiles, (a.kblocks + 3) / 4, g.tok_rows, sms);
+    return launch_clusters(nvfp4_few_kernel<BN>, dim3((unsigned)(grid << a.split_log2)), dim3(kThreads),
                            (size_t)S::kSmem, stream, pdl, 1u << a.split_log2, p_map, q_map, a);
 }
 
@@ -983,50 +982,39 @@ cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
                          GROUPED ? wgt_sf_map : tok_sf_map, GROUPED ? tok_sf_map : wgt_sf_map, out_map, a);
 }
 
-// A tile of 32 tokens only where it is the call's only one, so that its scale
-// factors begin a band; tiles of 64 begin at an even column of theirs.
-template <bool GROUPED>
-cudaError_t launch_by_tokens(const GemmArgs &g, int64_t tokens, bool pdl, cudaStream_t stream)
-{
-    if constexpr (!GROUPED) {
-        if (tokens <= 32)
-            return launch_tiles<32, false>(g, pdl, stream);
-    }
-    // Grouped, 64 experts, N=4096 K=7168: with 16 tokens an expert 64 columns take
-    // 164 us, 128 columns 167, pairs 183; with 32 172, 167, 184; with 64 205, 180, 187
-    // (16 experts, N=K=2048: 14.1, 13.8, 12.0); with 96 264, 198, 194.  (The pairs
-    // have become up to 7 % faster since.)
-    if (tokens <= (GROUPED ? 16 : 64))
-        return launch_tiles<64, GROUPED>(g, pdl, stream);
-    if (GROUPED && tokens <= 63)
-        return launch_tiles<128, GROUPED>(g, pdl, stream);
-    if constexpr (!GROUPED) {
-        const int sms = current_device_sms();
-        // up to 128 tokens still as one tile's columns where few tiles walk a long K: M=128
-        // N=2112 K=7168 7.0 us against 8.1 in pairs, but K=2048 5.7 against 4.4; M=65 N=7168
-        // K=7168 8.8 against 8.6
-        const int steps = (int)((g.K + 255) / 256);
-        if (tokens <= 128 && steps >= 20 && split_log2_of((g.N + kP - 1) / kP, steps, tokens, sms) == 2)
-            return launch_tiles<128, false>(g, pdl, stream);
-        const int64_t np = (g.tok_rows + 2 * kP - 1) / (2 * kP), pairs = sms > 1 ? sms / 2 : 1;
-        const int64_t w256 = (np * ((g.N + 255) / 256) + pairs - 1) / pairs;
-        const int64_t w128 = (np * ((g.N + 127) / 128) + pairs - 1) / pairs;
-        // half as wide tiles where they take no more waves of pairs: N=7168 K=7168
-        // M=256 9.4 us against 11.6, N=2112 M=1024 9.6 against 11.6; with two waves
-        // to one they lose (M=512 14.7 against 12.8), with three to two they are even
-        if (w128 <= w256)
-            return launch_pairs<128, false>(g, pdl, stream);
-    }
-    return launch_pairs<256, GROUPED>(g, pdl, stream);
-}
-
 }  // namespace
 
 cudaError_t launch_nvfp4_gemm(const GemmArgs &g, bool pdl, cudaStream_t stream)
 {
-    if (g.experts > 0)  // an expert's share of the entries
-        return launch_by_tokens<true>(g, (g.entries + g.experts - 1) / g.experts, pdl, stream);
-    return launch_by_tokens<false>(g, g.tok_rows, pdl, stream);
+    if (g.experts > 0) {
+        // Tiles of 128 or 256 tokens, by an expert's share of the entries.  64 experts of
+        // 4096 x 7168, us with tiles of 128 and of 256: 2 tokens an expert 126 and 132, 32
+        // 162 and 172, 64 171 and 175, 96 182 and 182, 128 194 and 191, 256 280 and 231.
+        // (Tiles of 64 tokens of one block each: 128 with 2 tokens, 210 with 64.)
+        if (g.entries <= 96 * (int64_t)g.experts)
+            return launch_pairs<128, true>(g, pdl, stream);
+        return launch_pairs<256, true>(g, pdl, stream);
+    }
+    if (g.tok_rows <= 32)
+        return launch_few<32>(g, pdl, stream);
+    if (g.tok_rows <= 64)
+        return launch_few<64>(g, pdl, stream);
+    const int sms = current_device_sms();
+    // up to 128 tokens still as one tile's columns where few tiles walk a long K: M=128
+    // N=2112 K=7168 7.0 us against 8.1 in pairs, but K=2048 5.7 against 4.4; M=65 N=7168
+    // K=7168 8.8 against 8.6
+    const int steps = (int)((g.K + 255) / 256);
+    if (g.tok_rows <= 128 && steps >= 20 && split_log2_of((g.N + kP - 1) / kP, steps, g.tok_rows, sms) == 2)
+        return launch_few<128>(g, pdl, stream);
+    // half as wide tiles where they take no more waves of pairs: N=7168 K=7168
+    // M=256 9.4 us against 11.6, N=2112 M=1024 9.6 against 11.6; with two waves
+    // to one they lose (M=512 14.7 against 12.8), with three to two they are even
+    const int64_t np = (g.tok_rows + 2 * kP - 1) / (2 * kP), pairs = sms > 1 ? sms / 2 : 1;
+    const int64_t w256 = (np * ((g.N + 255) / 256) + pairs - 1) / pairs;
+    const int64_t w128 = (np * ((g.N + 127) / 128) + pairs - 1) / pairs;
+    if (w128 <= w256)
+        return launch_pairs<128, false>(g, pdl, stream);
+    return launch_pairs<256, false>(g, pdl, stream);
 }
 
 cudaError_t read_stalled_waits(uint32_t *count)

@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (split > 1)
-        cluster_arrive();
+        cluster_arrive_relaxed();
     tmem_fence_before();
     __syncthreads();
     if (warp == 1) {

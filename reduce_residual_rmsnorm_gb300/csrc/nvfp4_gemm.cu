@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_before();
     __syncthreads();
     if (split > 1)
-        cluster_sync();  // the barriers of every block are ready
+        cluster_sync_relaxed();  // the barriers of every block are ready
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
     // (the warps that touch global memory wait for the kernel before, with their tile found)
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         pair_tmem_alloc(smem_u32(&tmem_at), 512);
     tmem_fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_sync_relaxed();
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
     int64_t tiles;

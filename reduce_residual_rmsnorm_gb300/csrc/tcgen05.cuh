@@ -231,6 +231,14 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// As cluster_sync, for the start: of what was written before, only the barriers made
+// before mbar_fence_init are there for the other blocks.
+__device__ __forceinline__ void cluster_sync_relaxed()
+{
+    cluster_arrive_relaxed();
+    cluster_wait();
+}
+
 // Arrive on a barrier of the cluster (an address of map_rank) without ordering
 // this thread's memory accesses, for what only tensor memory is to be ordered by
 // (tcgen05.wait and the fence before).  A releasing arrival took over 1000 cycles

@@ -119,8 +119,10 @@ __device__ __forceinline__ Tile dense_tile(const KernelArgs &a, uint32_t id)
 }
 
 // Pairs, grouped: weights on P, an expert's tokens on Q.  first[e]: tiles of tokens
-// before expert e.  An expert's tiles go over its tokens first, so that pairs
-// running at the same time share its weights.
+// before expert e.  Groups of 8 tiles of an expert's tokens pass over its weights
+// together, so that pairs running at the same time share rows of both (32768 tokens
+// of one expert of 4096 x 7168: 326 us over all tokens first, 268 in groups; in
+// groups of 4 as fast, of 16 271).
 template <int BN>
 __device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t *first, uint32_t id)
 {
@@ -133,10 +135,13 @@ __device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t 
         else
             hi = mid;
     }
-    const uint32_t nt = (uint32_t)(first[lo + 1] - first[lo]);
-    const uint32_t in = id - (uint32_t)first[lo] * nw;
-    const uint32_t w = in / nt;
-    const int t0 = (int)(in - w * nt) * BN, w0 = (int)w * 2 * kP;
+    constexpr uint32_t kGroup = 8;
+    const uint32_t nt = (uint32_t)(first[lo + 1] - first[lo]), from = id - (uint32_t)first[lo] * nw;
+    const uint32_t group = from / (kGroup * nw);
+    const uint32_t gt = nt - group * kGroup < kGroup ? nt - group * kGroup : kGroup;
+    const uint32_t in = from - group * kGroup * nw;
+    const uint32_t w = in / gt;
+    const int t0 = (int)(group * kGroup + in - w * gt) * BN, w0 = (int)w * 2 * kP;
     const int count = __ldg(a.count + lo), start = __ldg(a.start + lo);
     Tile t;
     t.expert = lo;

@@ -341,6 +341,13 @@ def test_grouped(dev, counts, N, K, hint):
     _grouped(dev, counts, N, K, hint)
 
 
+@pytest.mark.parametrize("hint", (1, 100000), ids=("few", "many"))
+@pytest.mark.parametrize("counts,N", [([5000], 520), ([1, 2049, 1025, 4097, 2048], 776)], ids=str)
+def test_grouped_many_tokens(dev, counts, N, hint):
+    """More tiles of tokens than pass over the weights together."""
+    _grouped(dev, counts, N, 96, hint)
+
+
 def test_grouped_many_experts(dev):
     r = np.random.RandomState(0)
     _grouped(dev, [int(v) for v in r.randint(0, 4, 300)], 72, 64)

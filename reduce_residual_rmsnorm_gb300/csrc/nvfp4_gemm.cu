@@ -167,7 +167,8 @@ __device__ __forceinline__ Tile pair_tile(const KernelArgs &a, const int32_t *fi
 }
 
 // Tiles of a grouped call; every thread of the block takes part and fills
-// first[0 .. experts].
+// first[0 .. experts].  No more than experts with rows of their own can have: where
+// they share rows the numbers stay in 32 bits, and the last experts' tiles fall away.
 template <int BN>
 __device__ __forceinline__ int64_t grouped_tiles(const KernelArgs &a, int32_t *first)
 {
@@ -179,6 +180,7 @@ __device__ __forceinline__ int64_t grouped_tiles(const KernelArgs &a, int32_t *f
     }
     __syncthreads();
     if (threadIdx.x < 32) {  // inclusive scan
+        const int32_t most = (int32_t)(a.tok_rows / BN) + a.experts;
         int32_t sum = 0;
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
             int32_t v = e0 + lane < a.experts ? first[e0 + lane + 1] : 0;
@@ -188,9 +190,10 @@ __device__ __forceinline__ int64_t grouped_tiles(const KernelArgs &a, int32_t *f
                 if (lane >= o)
                     v += up;
             }
+            v = sum + v < most ? sum + v : most;
             if (e0 + lane < a.experts)
-                first[e0 + lane + 1] = sum + v;
-            sum += __shfl_sync(0xffffffffu, v, 31);
+                first[e0 + lane + 1] = v;
+            sum = __shfl_sync(0xffffffffu, v, 31);
         }
         if (lane == 0)
             first[0] = 0;

@@ -153,10 +153,8 @@ public:
         if (t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1))
             raise(PyExc_ValueError, "%s must be 2-D with unit column stride", name);
         *ld = t.stride(0);
-        if (t.size(0) <= 1) {  // a single row has no stride that matters; torch may report any
-            const int64_t least = (t.size(1) + 7) / 8 * 8;
-            *ld = *ld > least ? *ld : least;
-        }
+        if (t.size(0) <= 1)  // a single row has no stride that matters; torch may report any
+            *ld = (t.size(1) + 7) / 8 * 8;
         return t;
     }
 

@@ -341,6 +341,19 @@ def test_grouped(dev, counts, N, K, hint):
     _grouped(dev, counts, N, K, hint)
 
 
+def test_one_row_of_any_stride(dev):
+    """A single row of a wider buffer, whose stride is no multiple of 8."""
+    g = torch.ones(1, device=dev)
+    x = torch.randn(1, 77, device=dev).bfloat16()
+    q, s = pkg.ts_nvfp4_quantize(x[:, :64], g, sf_layout=pkg.SFLayout.SWIZZLED_128x4)
+    want_q, want_s = pkg.ts_nvfp4_quantize(x[:, :64].contiguous(), g, sf_layout=pkg.SFLayout.SWIZZLED_128x4)
+    assert torch.equal(q, want_q) and torch.equal(s, want_s)
+    wide = torch.zeros(1, 77, dtype=torch.bfloat16, device=dev)
+    pkg.ts_nvfp4_gemm(q, s, q.expand(8, -1).contiguous(), s, g, out=wide[:, :8])
+    assert torch.equal(wide[:, :1], pkg.ts_nvfp4_gemm(q, s, q.expand(8, -1).contiguous(), s, g)[:, :1])
+    assert not wide[:, 8:].any()
+
+
 @pytest.mark.parametrize("hint", (1, 100000), ids=("few", "many"))
 @pytest.mark.parametrize("counts,N", [([5000], 520), ([1, 2049, 1025, 4097, 2048], 776)], ids=str)
 def test_grouped_many_tokens(dev, counts, N, hint):
@@ -351,6 +364,23 @@ def test_grouped_many_tokens(dev, counts, N, hint):
 def test_grouped_many_experts(dev):
     r = np.random.RandomState(0)
     _grouped(dev, [int(v) for v in r.randint(0, 4, 300)], 72, 64)
+
+
+def test_grouped_shared_rows(dev):
+    """Experts that share rows, more of them than rows have tiles, stay inside the buffers."""
+    E, rows, N, K = 300, 1024, 64, 64
+    a, asf, ta, tas = ref.random_nvfp4(rows, K, 5, dev, ref.EXACT_SF)
+    b, bsf, tb, tbs = ref.random_nvfp4(N, K, 6, dev, ref.EXACT_SF)
+    i32 = lambda v: torch.full((v[0],), v[1], dtype=torch.int32, device=dev)  # noqa: E731
+    for hint in (1, 100000):
+        r = pkg.MoERows(torch.empty(hint, 1, dtype=torch.int32, device=dev), i32((rows, 0)), i32((E + 1, 0)), i32((E, rows)))
+        out = Guarded((rows, N), torch.bfloat16, dev)
+        pkg.ts_nvfp4_grouped_gemm(ta, tas, tb.expand(E, -1, -1).contiguous(), tbs.expand(E, -1, -1).contiguous(),
+                                  torch.ones(E, device=dev), r, out=out.t)
+        torch.cuda.synchronize()
+        assert out.intact()
+        assert torch.equal(out.t, _want(a, asf, b, bsf, dev)[0].float().bfloat16())
+    assert pkg.ts_stalled_waits() == 0
 
 
 def test_grouped_skips_bad_starts(dev):

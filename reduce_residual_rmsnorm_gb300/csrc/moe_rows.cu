@@ -15,24 +15,26 @@ namespace {
 // sort
 // ---------------------------------------------------------------------------
 //
-// A counting sort in one cluster of 8 blocks, each warp taking consecutive
+// A counting sort in one cluster of 8 or 16 blocks, each warp taking consecutive
 // entries so that the order is stable.  Pass 1 counts each warp's entries per
 // expert in shared memory.  A thread per expert turns the counts into offsets:
 // over the warps of the block, over the blocks of the cluster (their totals read
 // through distributed shared memory) and, by a block scan of the counts rounded
 // up to `align`, over the experts.  Pass 2: an entry's row is its warp's offset
-// plus its rank among the lanes with the same expert (match.any).  What bounds
-// it is latency: ids are loaded 8 steps ahead, and kept in registers between
-// the passes where a warp has no more than 256.  16 x 8 entries over 64 experts
-// take 2.8 us (3.3 with starts at multiples of 128, whose row_src has 8 K
-// entries), 8192 x 8 entries 11.2 us.  One block instead of the cluster measured
-// 2.5 and 3.5 us on the first two, 6.1 against 3.4 at 2048 entries and 64
-// against 11.2 at 65536.
+// plus its rank among the lanes with the same expert, found by a vote on each bit
+// of the id (match.any goes over the distinct ids one by one: 41.2 us against 28.6
+// at 32768 x 8 entries over 256 experts).  What bounds it is latency, and with
+// many entries the scattered stores of a few SMs: ids are loaded 8 steps ahead,
+// and kept in registers between the passes where a warp has no more than 256.
+// us over 8 and 16 blocks: 256 x 8 entries over 64 experts 3.3 3.35, 1024 x 8 5.2 4.0,
+// 8192 x 8 8.9 6.8, 32768 x 8 26.6 16.5; 16 x 8 entries take 2.8 (3.2 with starts at
+// multiples of 128, whose row_src has 8 K entries).  One block instead of the
+// cluster measured 2.5 and 3.5 us on the last two, 64 at 8192 x 8.
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortCluster = 8;
 constexpr int kSortSteps = 8;  // steps of 32 entries whose ids are loaded together
 
+template <int BLOCKS>
 __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_constant__ SortArgs a)
 {
     extern __shared__ int32_t smem[];
@@ -52,7 +54,6 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
     __syncthreads();
     pdl_wait();
 
-    constexpr int blocks = kSortCluster;
     const int rank = (int)blockIdx.x;  // the grid is one cluster
     const int64_t begin = ((int64_t)rank * nw + warp) * a.per_warp;
     const int64_t stop = begin + a.per_warp < a.n ? begin + a.per_warp : a.n;
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
     int32_t before = 0, all = 0;
     if (tid < E) {
 #pragma unroll
-        for (int b = 0; b < blocks; ++b) {
+        for (int b = 0; b < BLOCKS; ++b) {
             const int32_t c = *cluster.map_shared_rank(total + tid, b);
             before += b < rank ? c : 0;
             all += c;
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
     __syncthreads();
     pdl_launch_dependents();
 
+    const int bits = 32 - __clz(E - 1);
     for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortSteps) {
         if (a.per_warp > 32 * kSortSteps)
             load(i0);
@@ -135,7 +137,12 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
             if (i - lane >= end)
                 break;
             const bool held = id[u] >= 0;
-            const unsigned same = __match_any_sync(0xffffffffu, id[u]);
+            unsigned same = __ballot_sync(0xffffffffu, held);  // and has the same bits
+            for (int b = 0; b < bits; ++b) {
+                const bool on = (id[u] >> b) & 1;
+                const unsigned with = __ballot_sync(0xffffffffu, on);
+                same &= on ? with : ~with;
+            }
             int32_t row = -1;
             if (held)
                 row = base[id[u]] + mine[id[u]] + __popc(same & ((1u << lane) - 1));
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
         }
     }
     // rows without an entry: behind each expert's last one, and behind the last expert
-    const int threads = blocks * nthr, warps = threads >> 5;
+    const int threads = BLOCKS * nthr, warps = threads >> 5;
     for (int e = rank * (nthr >> 5) + warp; e < E; e += warps)
         for (int32_t r = used[e] + lane; r < next[e]; r += 32)
             a.row_src[r] = -1;
@@ -281,16 +288,18 @@ __global__ void __launch_bounds__(kGradThreads, SLOTS > 4 ? 2 : 3) moe_combine_g
 
 }  // namespace
 
-cudaError_t launch_sort(const SortArgs &a, bool pdl, cudaStream_t stream)
+namespace {
+
+template <int BLOCKS>
+cudaError_t launch_sort_over(const SortArgs &a, bool pdl, cudaStream_t stream)
 {
     SortArgs b = a;
-    constexpr int blocks = kSortCluster;
-    const int64_t steps = (a.n + 32 * blocks - 1) / (32 * blocks);  // of 32 entries, per block
+    const int64_t steps = (a.n + 32 * BLOCKS - 1) / (32 * BLOCKS);  // of 32 entries, per block
     b.warps = steps < 1 ? 1 : (steps < 32 ? (int)steps : 32);
-    const int64_t all = (int64_t)blocks * b.warps;
+    const int64_t all = (int64_t)BLOCKS * b.warps;
     b.per_warp = ((a.n + all - 1) / all + 31) / 32 * 32;
     // a thread per expert, and enough to fill row_src with few stores each
-    const int64_t fill = a.rows / (8 * blocks) < 1024 ? (a.rows / (8 * blocks) + 31) / 32 * 32 : 1024;
+    const int64_t fill = a.rows / (8 * BLOCKS) < 1024 ? (a.rows / (8 * BLOCKS) + 31) / 32 * 32 : 1024;
     int nthr = b.warps * 32;
     nthr = nthr < (a.E + 31) / 32 * 32 ? (a.E + 31) / 32 * 32 : nthr;
     nthr = nthr < fill ? (int)fill : nthr;
@@ -301,14 +310,23 @@ cudaError_t launch_sort(const SortArgs &a, bool pdl, cudaStream_t stream)
     if (err != cudaSuccess)
         return err;
     if (dev >= kMaxCachedDevices || !grown[dev].load(std::memory_order_relaxed)) {
-        err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        err = cudaFuncSetAttribute(moe_sort_kernel<BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (36 * 1024 + 32) * (int)sizeof(int32_t));
+        if (err == cudaSuccess && BLOCKS > 8)
+            err = cudaFuncSetAttribute(moe_sort_kernel<BLOCKS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (err != cudaSuccess)
             return err;
         if (dev < kMaxCachedDevices)
             grown[dev].store(true, std::memory_order_relaxed);
     }
-    return launch_clusters(moe_sort_kernel, dim3(blocks), dim3((unsigned)nthr), smem, stream, pdl, blocks, b);
+    return launch_clusters(moe_sort_kernel<BLOCKS>, dim3(BLOCKS), dim3((unsigned)nthr), smem, stream, pdl, BLOCKS, b);
+}
+
+}  // namespace
+
+cudaError_t launch_sort(const SortArgs &a, bool pdl, cudaStream_t stream)
+{
+    return a.n <= 4096 ? launch_sort_over<8>(a, pdl, stream) : launch_sort_over<16>(a, pdl, stream);
 }
 
 cudaError_t launch_combine(const CombineArgs &a, bool pdl, cudaStream_t stream)

@@ -54,6 +54,12 @@ def test_sort(dev, T, k, E, align):
         assert np.array_equal(host(got), want), name
 
 
+@pytest.mark.parametrize("T,k,E,align", [(512, 8, 1024, 128), (513, 8, 1, 1), (2049, 2, 2, 128), (16384, 8, 17, 128), (40000, 5, 1024, 256)])
+def test_sort_around_its_forms(dev, T, k, E, align):
+    """Entries up to and beyond what 8 blocks take, and beyond what the registers hold."""
+    test_sort(dev, T, k, E, align)
+
+
 @pytest.mark.parametrize("ids", ([[0] * 40] * 300, [[-1] * 4] * 9, [[7] * 2] * 5000), ids=("one", "none", "last"))
 def test_sort_one_sided(dev, ids):
     ids = np.array(ids, np.int32)

@@ -14,17 +14,16 @@
 //     on Q.  Bound by the tensor cores: 7.5 PFLOP/s at 8192 x 7168 x 7168, 86 % of
 //     a tile's cycles, and by the power limit in long runs.
 //   - experts: pairs with weights on P and an expert's tokens on Q, whose number of
-//     columns follows them.  Bound by the experts' bytes (within 4 to 9 % of them up
+//     columns follows them.  Bound by the experts' bytes (within 3 to 11 % of them up
 //     to 64 tokens an expert), then as above.
 //
-// One block per SM, persistent over the tiles.  One warp copies (two where tokens are few): codes by TMA
-// under the 128-byte swizzle, 256 elements of K (128 bytes a row) per stage,
-// scale factors in the 512-byte tiles of their 128x4 layout, which is the
-// layout tensor memory wants.  Warp 1 multiplies: scale factors from shared to
-// tensor memory, then the products.  The other warps write the finished
-// accumulator, one of two, while the next tile's products run.  Every wait has
-// a limit, after which the block records it, waits for its copies in flight
-// and ends.
+// One block per SM, persistent over the tiles.  One warp copies (two where tokens
+// are few): codes by TMA under the 128-byte swizzle, 256 elements of K (128 bytes a
+// row) per stage, scale factors in the 512-byte tiles of their 128x4 layout, which
+// is the layout tensor memory wants.  Warp 1 multiplies: scale factors from shared
+// to tensor memory, then the products.  The other warps write the finished
+// accumulator, one of two, while the next tile's products run.  Every wait has a
+// limit, after which the block records it, waits for its copies in flight and ends.
 #include <cuda.h>
 
 #include "device_util.cuh"
@@ -248,10 +247,11 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 // tile's K and each sums up a share of the tokens from all of them, in their
 // order.  Latency counts here: two warps copy, since an issue takes about 100
 // cycles; the partial sums travel by stores that the receiving barrier counts,
-// with no fence; and a tile is found before the dependency wait.  1 x 4096 x 4096
-// takes 3.8 us (1.4 of bytes): about 0.5 us from the wait to the first copy's
-// issue, 0.8 to its arrival, 0.9 for the four steps, 0.3 to the accumulator, 0.4
-// to the exchanged sums.
+// with no fence; the cluster's last arrival orders nothing (3.8 us below with one
+// that waits for the outputs); and a tile is found before the dependency wait.
+// 1 x 4096 x 4096 takes 3.4 us (1.4 of bytes): about 0.2 us from the wait to the
+// first copy's issue, 0.9 to its arrival, 0.9 for the four steps, 0.2 to the
+// accumulator, 0.3 to the exchanged sums.
 
 template <int BN>
 struct Shape {
@@ -530,8 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the products wait 1.0 K for the shared columns, 0.4 K for the first stage and
 // 180 a stage for the copies.  Tried without gain: a second staging buffer
 // (K = 512 4 % faster, K = 7168 1 % slower), 128-byte rows of output (1 % slower),
-// Q's scale factors multicast to the pair (none), the next tile found ahead
-// (none; 7 % slower grouped).
+// Q's scale factors multicast to the pair or both bands of them in one copy (none),
+// the next tile found ahead (none; 7 % slower grouped), an expert's weights fetched
+// to L2 ahead of the copies (1 to 18 % slower).
 
 constexpr int kPairThreads = 320;
 

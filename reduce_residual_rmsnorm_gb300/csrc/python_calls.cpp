@@ -4,7 +4,7 @@
 //
 // A decoded token's operator runs for 2 to 6 us on the GPU, and the same
 // marshalling through ctypes took 9 to 18 us of the calling thread on the
-// node's CPU; here it takes 3 to 6.  The documented functions are those of
+// node's CPU; here it takes 2 to 5.  The documented functions are those of
 // _nvfp4_moe.py, which pass their arguments on by position.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

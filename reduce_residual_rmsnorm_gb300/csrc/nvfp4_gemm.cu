@@ -526,6 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rest.  The output goes through shared memory, 32 rows of 64 bytes a warp and
 // step, and out by TMA.
 //
+// SPLIT: two pairs of a cluster of four share the K of their one tile, since a
+// block's copies alone, 28 KB a step, take 310 cycles of its 360; each gives the
+// other half of its sums (256 x 2112 x 7168: 6.4 us, 8.05 in one pair).
+//
 // Of the 16.7 K cycles that a tile takes at K = 7168 (14.3 K of them products),
 // the products wait 1.0 K for the shared columns, 0.4 K for the first stage and
 // 180 a stage for the copies.  Tried without gain: a second staging buffer
@@ -536,14 +540,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kPairThreads = 320;
 
-template <int BN>
+template <int BN, bool SPLIT = false>
 struct PairShape {
     static constexpr bool kShared = BN == 256;                   // the accumulators share columns
     static constexpr int kBands = BN / 128;
     static constexpr int kCodes = kP * 128 + (BN / 2) * 128;     // bytes per stage and block
     static constexpr int kSf = 4 * kSfTile * (1 + kBands);
     static constexpr int kOut = 8 * 32 * 64;                     // staging: warps x rows x bytes
-    static constexpr int kFixed = 1024 + kOut + 4 * 1032;       // and alignment, the experts' first tiles
+    static constexpr int kSums = SPLIT ? 8 * 32 * 128 : 0;       // the other pair's sums: warps x rows x bytes
+    static constexpr int kFixed = 1024 + kOut + kSums + 4 * 1032;  // and alignment, the experts' first tiles
     static constexpr int kStages = (kSmemLimit - kFixed - 256) / (kCodes + kSf);
     static constexpr int kSmem = kFixed + kStages * (kCodes + kSf);
     static constexpr int kAcc1 = kShared ? BN - 64 : BN;         // column of the second accumulator
@@ -551,30 +556,34 @@ struct PairShape {
     static constexpr int kSfQ = kSfP + 16;
     static constexpr int kChunks = BN / 32;                      // 32-column pieces of the output
     static_assert(kSfQ + 16 * kBands <= 512, "accumulators and scale factors fit tensor memory");
+    static_assert(!SPLIT || BN == 128, "a warp has two pieces of the output and gives one away");
 };
 
-template <int BN, bool GROUPED>
-__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+template <int BN, bool GROUPED, bool SPLIT>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 2, 1, 1)
     nvfp4_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap psf_map, const __grid_constant__ CUtensorMap qsf_map,
                       const __grid_constant__ CUtensorMap out_map, const __grid_constant__ KernelArgs a)
 {
-    using S = PairShape<BN>;
+    using S = PairShape<BN, SPLIT>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[2 * S::kStages + 5];
+    __shared__ uint64_t bars[2 * S::kStages + 6];
     __shared__ uint32_t tmem_at;
     __shared__ int dead_flag;
     const uint32_t pad = (1024 - (smem_u32(raw) & 1023)) & 1023;
     const uint32_t codes = smem_u32(raw) + pad;
     const uint32_t stage_out = codes + S::kStages * S::kCodes;
     const uint32_t sf = stage_out + S::kOut;
-    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + S::kStages * (S::kCodes + S::kSf) + S::kOut);
+    const uint32_t sums = sf + S::kStages * S::kSf;
+    int32_t *first = reinterpret_cast<int32_t *>(raw + pad + S::kStages * (S::kCodes + S::kSf) + S::kOut + S::kSums);
     volatile int *dead = &dead_flag;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t in_cluster = cluster_rank(), rank = in_cluster & 1, lead = in_cluster & 2;
+    const uint32_t both = 3u << lead;  // the pair's blocks
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
-    const uint32_t acc_full = empty + 8 * S::kStages, acc_free = acc_full + 16, drained = acc_free + 16;
+    const uint32_t acc_full = empty + 8 * S::kStages, acc_free = acc_full + 16, drained = acc_free + 16,
+                   partial = drained + 8;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -586,7 +595,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             mbar_init(acc_free + 8 * i, 16);  // the output warps of both blocks
         }
         mbar_init(drained, 1);
+        mbar_init(partial, 1);
         mbar_fence_init();
+        if (SPLIT)
+            mbar_expect_tx(partial, S::kSums);
         dead_flag = 0;
         tma_prefetch_map(&p_map);
         tma_prefetch_map(&q_map);
@@ -611,8 +623,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     auto tile_of = [&](int64_t id) { return pair_tile<BN, GROUPED>(a, first, id); };
     // columns of the products of a tile: all, or the expert's tokens rounded up
     auto columns = [](const Tile &t) { return GROUPED ? (t.tok_n + 31) & ~31 : BN; };
-    const int steps = (a.kblocks + 3) >> 2;
-    const int64_t id0 = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    // this pair's steps of 256 elements of K, and its tiles
+    const int all_steps = (a.kblocks + 3) >> 2;
+    const int kt0 = SPLIT && lead ? all_steps >> 1 : 0, kt1 = SPLIT && !lead ? all_steps >> 1 : all_steps;
+    const int64_t id0 = blockIdx.x >> (SPLIT ? 2 : 1), stride = gridDim.x >> (SPLIT ? 2 : 1);
 
     if (warp == 0) {
         // ---- copies ----
@@ -620,7 +634,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t parity = 0;
         int64_t fills = 0;
         bool good = true;
-        const uint32_t full0 = map_rank(full, 0);
+        const uint32_t full0 = map_rank(full, lead);
         for (int64_t id = id0; good && id < tiles; id += stride) {
             const Tile t = tile_of(id);
             const int32_t p_row = t.p_row + (int32_t)rank * kP, q_row = t.q_row + (int32_t)rank * (columns(t) / 2);
@@ -628,7 +642,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             const int32_t p_band = t.p_band + (int32_t)rank, q_band = t.q_band;
             if (!GROUPED && fills == 0)
                 pdl_wait();
-            for (int kt = 0; kt < steps; ++kt) {
+            for (int kt = kt0; kt < kt1; ++kt) {
                 good = wait_warp(empty + 8 * s, parity ^ 1, dead);
                 if (!good)
                     break;
@@ -675,7 +689,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             if (!good)
                 break;
             const uint32_t d = tmem + ((uint32_t)n & 1) * S::kAcc1;
-            for (int kt = 0; kt < steps; ++kt) {
+            for (int kt = kt0; kt < kt1; ++kt) {
                 good = wait_warp(full + 8 * s, parity, dead);
                 if (!good)
                     break;
@@ -698,10 +712,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                     for (int kb = 0; kb < 4; ++kb)
                         if (kb < nkb)
                             pair_mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + S::kSfP + 4 * kb,
-                                           tmem + S::kSfQ + 4 * S::kBands * kb, kt > 0 || kb > 0);
-                    pair_commit(empty + 8 * s);
-                    if (kt + 1 == steps)
-                        pair_commit(acc_full + 8 * ((uint32_t)n & 1));
+                                           tmem + S::kSfQ + 4 * S::kBands * kb, kt > kt0 || kb > 0);
+                    pair_commit(empty + 8 * s, both);
+                    if (kt + 1 == kt1)
+                        pair_commit(acc_full + 8 * ((uint32_t)n & 1), both);
                 }
                 __syncwarp();
                 if (++s == S::kStages) {
@@ -712,7 +726,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
         if (!good) {
             if (elect_one())
-                pair_commit(drained);
+                pair_commit(drained, both);
             __syncwarp();
             wait_last(drained, 0);
         }
@@ -720,7 +734,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         // ---- output: two warps for each 32 lanes, every other 32 columns ----
         const int quad = warp & 3, half = (warp - 2) >> 2;
         const uint32_t stage = stage_out + (warp - 2) * (32 * 64);
-        const uint32_t free0 = map_rank(acc_free, 0);
+        const uint32_t free0 = map_rank(acc_free, lead);
         int64_t n = 0;
         for (int64_t id = id0; id < tiles; id += stride, ++n) {
             const Tile t = tile_of(id);
@@ -740,7 +754,35 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             auto column = [&](int i) { return ((2 * i + first_piece) & (S::kChunks - 1)) * 32; };
             uint32_t v[2][32];
             tmem_load32(src + column(0), v[0]);
+            if (SPLIT)
+                tmem_load32(src + column(1), v[1]);
             tmem_wait_loads();
+            if (SPLIT) {
+                // (the cluster's only tile) each pair gives one of a warp's two pieces to
+                // the other and adds the other's sums to the one it keeps
+                const uint32_t to = in_cluster ^ 2, at = sums + ((warp - 2) * 256 + lane) * 16;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint4 w;
+                    w.x = lead ? v[0][4 * j] : v[1][4 * j];
+                    w.y = lead ? v[0][4 * j + 1] : v[1][4 * j + 1];
+                    w.z = lead ? v[0][4 * j + 2] : v[1][4 * j + 2];
+                    w.w = lead ? v[0][4 * j + 3] : v[1][4 * j + 3];
+                    st_async_cluster(map_rank(at + j * 512, to), w, map_rank(partial, to));
+                }
+                if (!wait_warp<true>(partial, 0, dead))
+                    break;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 w = ld_shared(at + j * 512);
+                    const uint32_t got[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t kept = lead ? v[1][4 * j + e] : v[0][4 * j + e];
+                        v[0][4 * j + e] = __float_as_uint(__uint_as_float(kept) + __uint_as_float(got[e]));
+                    }
+                }
+            }
             if (S::kShared) {
                 tmem_fence_before();
                 __syncwarp();
@@ -748,9 +790,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                     mbar_arrive_cluster_relaxed(free0);
             }
 #pragma unroll
-            for (int i = 0; i < S::kChunks / 2; ++i) {
-                const int c0 = column(i);
-                if (i + 1 < S::kChunks / 2)
+            for (int i = 0; i < (SPLIT ? 1 : S::kChunks / 2); ++i) {
+                const int c0 = column(SPLIT ? (int)(lead >> 1) : i);
+                if (!SPLIT && i + 1 < S::kChunks / 2)
                     tmem_load32(src + column(i + 1), v[(i + 1) & 1]);
                 if (lanes > 0 && c0 < cols) {
                     if (lane == 0)
@@ -961,7 +1003,7 @@ cudaError_t launch_few(const GemmArgs &g, bool pdl, cudaStream_t stream)
                            (size_t)S::kSmem, stream, pdl, 1u << a.split_log2, p_map, q_map, a);
 }
 
-template <int BN, bool GROUPED>
+template <int BN, bool GROUPED, bool SPLIT = false>
 cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
 {
     static std::atomic<bool> grown[kMaxCachedDevices];
@@ -969,7 +1011,7 @@ cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
     const int sms = current_device_sms(&dev);
     if (sms < 2)
         return cudaErrorInvalidDevice;
-    const cudaError_t err = grow_smem(nvfp4_pair_kernel<BN, GROUPED>, PairShape<BN>::kSmem, grown, dev);
+    const cudaError_t err = grow_smem(nvfp4_pair_kernel<BN, GROUPED, SPLIT>, PairShape<BN, SPLIT>::kSmem, grown, dev);
     if (err != cudaSuccess)
         return err;
     const KernelArgs a = kernel_args(g, GROUPED);
@@ -986,8 +1028,8 @@ cudaError_t launch_pairs(const GemmArgs &g, bool pdl, cudaStream_t stream)
         const int64_t tiles = ((a.p_rows + 2 * kP - 1) / (2 * kP)) * ((a.q_rows + BN - 1) / BN);
         pairs = tiles < pairs ? tiles : pairs;
     }
-    return launch_kernel(nvfp4_pair_kernel<BN, GROUPED>, dim3((unsigned)(2 * pairs)), dim3(kPairThreads),
-                         (size_t)PairShape<BN>::kSmem, stream, pdl, GROUPED ? wgt_map : tok_map, GROUPED ? tok_map : wgt_map,
+    return launch_kernel(nvfp4_pair_kernel<BN, GROUPED, SPLIT>, dim3((unsigned)((SPLIT ? 4 : 2) * pairs)), dim3(kPairThreads),
+                         (size_t)PairShape<BN, SPLIT>::kSmem, stream, pdl, GROUPED ? wgt_map : tok_map, GROUPED ? tok_map : wgt_map,
                          GROUPED ? wgt_sf_map : tok_sf_map, GROUPED ? tok_sf_map : wgt_sf_map, out_map, a);
 }
 
@@ -1009,18 +1051,26 @@ cudaError_t launch_nvfp4_gemm(const GemmArgs &g, bool pdl, cudaStream_t stream)
     if (g.tok_rows <= 64)
         return launch_few<64>(g, pdl, stream);
     const int sms = current_device_sms();
-    // up to 128 tokens still as one tile's columns where few tiles walk a long K: M=128
-    // N=2112 K=7168 7.0 us against 8.1 in pairs, but K=2048 5.7 against 4.4; M=65 N=7168
-    // K=7168 8.8 against 8.6
     const int steps = (int)((g.K + 255) / 256);
-    if (g.tok_rows <= 128 && steps >= 20 && split_log2_of((g.N + kP - 1) / kP, steps, g.tok_rows, sms) == 2)
+    const int64_t np = (g.tok_rows + 2 * kP - 1) / (2 * kP), pairs = sms > 1 ? sms / 2 : 1;
+    const int64_t t128 = np * ((g.N + 127) / 128), t256 = np * ((g.N + 255) / 256);
+    const bool two_calls = 8 * t128 <= sms;  // over two pairs each, the next call's blocks fit beside this one's
+    // up to 128 tokens still as one tile's columns where few tiles walk a long K (us so and
+    // in pairs: M=65 N=2112 K=2048 5.7 4.4, K=7168 5.5 6.2, M=104 6.4 6.3, M=128 6.9 6.4;
+    // N=4096 K=7168 M=128 7.3 7.3; M=128 N=2112 K=16384 9.4 9.8)
+    if (g.tok_rows <= (two_calls && steps < 40 ? 96 : 128) && steps >= 20 &&
+        split_log2_of((g.N + kP - 1) / kP, steps, g.tok_rows, sms) == 2)
         return launch_few<128>(g, pdl, stream);
+    // a tile's K over two pairs where it is long enough to pay for the exchange, of
+    // which the next call hides a part (us in one pair and over two: 17 tiles, M=256
+    // N=2112, K=2048 4.4 4.5, K=4096 5.8 5.25, K=7168 8.05 6.4; 32 tiles, N=4096, K=4096
+    // 5.8 6.05, K=7168 8.1 7.2)
+    if (4 * t128 <= sms - sms / 16 && steps >= (two_calls ? 12 : 20))
+        return launch_pairs<128, false, true>(g, pdl, stream);
     // half as wide tiles where they take no more waves of pairs: N=7168 K=7168
     // M=256 9.4 us against 11.6, N=2112 M=1024 9.6 against 11.6; with two waves
     // to one they lose (M=512 14.7 against 12.8), with three to two they are even
-    const int64_t np = (g.tok_rows + 2 * kP - 1) / (2 * kP), pairs = sms > 1 ? sms / 2 : 1;
-    const int64_t w256 = (np * ((g.N + 255) / 256) + pairs - 1) / pairs;
-    const int64_t w128 = (np * ((g.N + 127) / 128) + pairs - 1) / pairs;
+    const int64_t w256 = (t256 + pairs - 1) / pairs, w128 = (t128 + pairs - 1) / pairs;
     if (w128 <= w256)
         return launch_pairs<128, false>(g, pdl, stream);
     return launch_pairs<256, false>(g, pdl, stream);

@@ -315,10 +315,10 @@ __device__ __forceinline__ void pair_mma_nvfp4(uint32_t d, uint64_t a, uint64_t 
 }
 
 // As mma_commit, on the barrier at this address in both blocks.
-__device__ __forceinline__ void pair_commit(uint32_t bar)
+__device__ __forceinline__ void pair_commit(uint32_t bar, uint32_t blocks = 3)
 {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(bar), "h"((uint16_t)3)
+                 ::"r"(bar), "h"((uint16_t)blocks)
                  : "memory");
 }
 

@@ -209,6 +209,43 @@ def test_gemm_random(dev, M, N, K):
     assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * mag).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(97, 8, 5152), (128, 2112, 5152), (129, 520, 2848), (256, 1000, 3104), (257, 2112, 5408),
+                                   (300, 136, 4096), (512, 2048, 5152), (700, 264, 2912), (1000, 1032, 5152)])
+def test_gemm_exact_over_two_pairs(dev, M, N, K):
+    """Few tiles with a long K, of odd and even steps."""
+    test_gemm_exact(dev, M, N, K)
+
+
+def test_gemm_over_two_pairs_replayed(dev):
+    """The same call twice in a graph, on two streams, gives the bits of the direct call."""
+    sets = []
+    for i in range(2):
+        _, _, ta, tas = ref.random_nvfp4(300, 4128, 10 + i, dev)
+        _, _, tb, tbs = ref.random_nvfp4(1032, 4128, 20 + i, dev)
+        sets.append((ta, tas, tb, tbs, torch.ones(1, device=dev)))
+    direct = [pkg.ts_nvfp4_gemm(*s) for s in sets]
+    outs = [[torch.empty_like(d) for d in direct] for _ in range(2)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main), torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        for stream, to in zip((main, side), outs):
+            for _ in range(4):
+                for s, o in zip(sets, to):
+                    pkg.ts_nvfp4_gemm(*s, out=o, launch_with_pdl=True, stream=stream)
+        main.wait_stream(side)
+    for _ in range(3):
+        for o in outs[0] + outs[1]:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for to in outs:
+            for o, d in zip(to, direct):
+                assert torch.equal(o, d)
+    assert pkg.ts_stalled_waits() == 0
+
+
 @pytest.mark.parametrize("M", (90, 1500))
 def test_gemm_out_past_32_bit_offsets(dev, M):
     """An output whose last rows lie more than 2^31 elements behind the first."""

@@ -108,7 +108,7 @@ __device__ __forceinline__ Tile dense_tile(const KernelArgs &a, uint32_t id)
     t.q_row = (int32_t)(q * BN);
     t.p_band = t.p_row >> 7;
     t.q_band = t.q_row >> 7;
-    t.q_bands = BN / 128;
+    t.q_bands = (BN + 127) / 128;
     t.tok0 = t.p_row;
     t.tok_n = (int)(a.p_rows - t.p_row < 2 * kP ? a.p_rows - t.p_row : 2 * kP);
     t.wgt0 = t.q_row;
@@ -520,6 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Both blocks' copies complete on the first block's barrier; its commits free
 // the stages and publish the accumulators in both.
 //
+// A tile is as wide, BN = 128, 192 or 256, as its call's waves of tiles are cheapest.
+//
 // Two accumulators of 256 columns and 48 columns of scale factors do not fit
 // the 512 columns: the accumulators share 64, which the output warps read
 // first and then give back, so that the next tile's products run during the
@@ -543,7 +545,7 @@ constexpr int kPairThreads = 320;
 template <int BN, bool SPLIT = false>
 struct PairShape {
     static constexpr bool kShared = BN == 256;                   // the accumulators share columns
-    static constexpr int kBands = BN / 128;
+    static constexpr int kBands = (BN + 127) / 128;
     static constexpr int kCodes = kP * 128 + (BN / 2) * 128;     // bytes per stage and block
     static constexpr int kSf = 4 * kSfTile * (1 + kBands);
     static constexpr int kOut = 8 * 32 * 64;                     // staging: warps x rows x bytes
@@ -689,6 +691,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
             if (!good)
                 break;
             const uint32_t d = tmem + ((uint32_t)n & 1) * S::kAcc1;
+            // (tiles of 192 rows of Q begin in the middle of every other band)
+            const uint32_t sf_q = tmem + S::kSfQ + (BN == 192 ? (uint32_t)(tile_of(id).q_row & 127) >> 5 : 0);
             for (int kt = kt0; kt < kt1; ++kt) {
                 good = wait_warp(full + 8 * s, parity, dead);
                 if (!good)
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
                     for (int kb = 0; kb < 4; ++kb)
                         if (kb < nkb)
                             pair_mma_nvfp4(d, pd + 2 * kb, qd + 2 * kb, idesc, tmem + S::kSfP + 4 * kb,
-                                           tmem + S::kSfQ + 4 * S::kBands * kb, kt > kt0 || kb > 0);
+                                           sf_q + 4 * S::kBands * kb, kt > kt0 || kb > 0);
                     pair_commit(empty + 8 * s, both);
                     if (kt + 1 == kt1)
                         pair_commit(acc_full + 8 * ((uint32_t)n & 1), both);
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
             // 32-column pieces, this warp's first one among the shared: the last two of
             // the first accumulator, the first two of the second
             const int first_piece = half + (S::kShared && acc == 0 ? S::kChunks - 2 : 0);
-            auto column = [&](int i) { return ((2 * i + first_piece) & (S::kChunks - 1)) * 32; };
+            auto column = [&](int i) { return (S::kShared ? (2 * i + first_piece) & (S::kChunks - 1) : 2 * i + first_piece) * 32; };
             uint32_t v[2][32];
             tmem_load32(src + column(0), v[0]);
             if (SPLIT)
@@ -1053,7 +1057,7 @@ cudaError_t launch_nvfp4_gemm(const GemmArgs &g, bool pdl, cudaStream_t stream)
     const int sms = current_device_sms();
     const int steps = (int)((g.K + 255) / 256);
     const int64_t np = (g.tok_rows + 2 * kP - 1) / (2 * kP), pairs = sms > 1 ? sms / 2 : 1;
-    const int64_t t128 = np * ((g.N + 127) / 128), t256 = np * ((g.N + 255) / 256);
+    const int64_t t128 = np * ((g.N + 127) / 128);
     const bool two_calls = 8 * t128 <= sms;  // over two pairs each, the next call's blocks fit beside this one's
     // up to 128 tokens still as one tile's columns where few tiles walk a long K (us so and
     // in pairs: M=65 N=2112 K=2048 5.7 4.4, K=7168 5.5 6.2, M=104 6.4 6.3, M=128 6.9 6.4;
@@ -1067,12 +1071,17 @@ cudaError_t launch_nvfp4_gemm(const GemmArgs &g, bool pdl, cudaStream_t stream)
     // 5.8 6.05, K=7168 8.1 7.2)
     if (4 * t128 <= sms - sms / 16 && steps >= (two_calls ? 12 : 20))
         return launch_pairs<128, false, true>(g, pdl, stream);
-    // half as wide tiles where they take no more waves of pairs: N=7168 K=7168
-    // M=256 9.4 us against 11.6, N=2112 M=1024 9.6 against 11.6; with two waves
-    // to one they lose (M=512 14.7 against 12.8), with three to two they are even
-    const int64_t w256 = (t256 + pairs - 1) / pairs, w128 = (t128 + pairs - 1) / pairs;
-    if (w128 <= w256)
+    // the width whose waves of pairs take least: a wave with tiles of 128 rows of weights
+    // 0.65 and of 192 0.83 of the time with 256 (K=7168: 5.7, 7.3 and 8.8 us).  us with 128,
+    // 192, 256: N=7168 K=7168 M=512 14.1 10.8 12.1, M=1024 20.3 17.7 20.3, M=2048 36.9 32.0
+    // 29.6; N=5120 K=5120 M=768 11.6 13.2 9.8, M=1024 15.4 13.1 15.9; N=2112 K=7168 M=1024
+    // 9.0 10.4 11.1
+    auto waves = [&](int64_t width) { return (np * ((g.N + width - 1) / width) + pairs - 1) / pairs; };
+    const int64_t c128 = 65 * waves(128), c192 = 83 * waves(192), c256 = 100 * waves(256);
+    if (c128 < c192 && c128 < c256)
         return launch_pairs<128, false>(g, pdl, stream);
+    if (c192 < c256)
+        return launch_pairs<192, false>(g, pdl, stream);
     return launch_pairs<256, false>(g, pdl, stream);
 }
 

@@ -216,6 +216,12 @@ def test_gemm_exact_over_two_pairs(dev, M, N, K):
     test_gemm_exact(dev, M, N, K)
 
 
+@pytest.mark.parametrize("M,N,K", [(257, 7200, 544), (512, 7168, 96), (1024, 5000, 160), (1500, 7168, 288), (2048, 5120, 1056)])
+def test_gemm_exact_in_tiles_of_192(dev, M, N, K):
+    """Tiles that begin in the middle of 128 rows of scale factors, the last one whole and not."""
+    test_gemm_exact(dev, M, N, K)
+
+
 def test_gemm_over_two_pairs_replayed(dev):
     """The same call twice in a graph, on two streams, gives the bits of the direct call."""
     sets = []

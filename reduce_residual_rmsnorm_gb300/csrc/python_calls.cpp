@@ -196,6 +196,17 @@ public:
         return t;
     }
 
+    // NVFP4 codes and scale factors, given or new; small new ones share an allocation,
+    // which takes 0.7 us of the thread.
+    std::pair<at::Tensor, at::Tensor> nvfp4_outputs(int i, const Dims &q, const Dims &s, const at::Tensor &like)
+    {
+        const int64_t at = (c10::multiply_integers(q.ref()) + 255) / 256 * 256, all = at + c10::multiply_integers(s.ref());
+        if (!none(i) || !none(i + 1) || all > 65536)
+            return {output(i, "quant_out", kU8, q, like), output(i + 1, "scale_out", kU8, s, like)};
+        const at::Tensor both = fresh(dims(all), kU8, like);
+        return {part_of(both, 0, q), part_of(both, at, s)};
+    }
+
     // The output that is given, checked, or a new one.
     at::Tensor output(int i, const char *name, at::ScalarType type, const Dims &want, const at::Tensor &like)
     {
@@ -278,10 +289,10 @@ PyObject *quantize(PyObject *const *args, Py_ssize_t n)
     const int64_t T = x.size(0), K = x.size(1), layout = c.integer(5);
     const float *g = c.one(1, "scale_factor");
     const int32_t *src = c.optional_i32(2, "row_src", dims(T));
-    const at::Tensor q = c.output(3, "quant_out", kU8, dims(T, K / 2), x);
-    const at::Tensor s = c.output(4, "scale_out", kU8, sf_dims(T, K, layout), x);
+    const auto [q, s] = c.nvfp4_outputs(3, dims(T, K / 2), sf_dims(T, K, layout), x);
+    void *const qp = ptr(q), *const sp = ptr(s);
     c.run([&](uint32_t flags, void *stream) {
-        return ts_nvfp4_quantize(ptr(x), T, K, ldx, g, src, ptr(q), ptr(s), (int)layout, flags, stream);
+        return ts_nvfp4_quantize(ptr(x), T, K, ldx, g, src, qp, sp, (int)layout, flags, stream);
     });
     return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(s));
 }
@@ -398,11 +409,11 @@ PyObject *dispatch(PyObject *const *args, Py_ssize_t n)
     if (!c.none(4))
         raise(PyExc_ValueError, "out and scale_factor exclude each other");
     const float *g = c.one(3, "scale_factor");
-    const at::Tensor q = c.output(5, "quant_out", kU8, dims(rows, H / 2), x);
-    const at::Tensor s = c.output(6, "scale_out", kU8, sf_dims(rows, H, layout), x);
+    const auto [q, s] = c.nvfp4_outputs(5, dims(rows, H / 2), sf_dims(rows, H, layout), x);
+    void *const qp = ptr(q), *const sp = ptr(s);
     c.run([&](uint32_t flags, void *stream) {
-        return ts_moe_dispatch(ptr(x), T, H, ldx, ptr<int32_t>(of), of.size(1), rows, nullptr, g, ptr(q), ptr(s), (int)layout,
-                               flags, stream);
+        return ts_moe_dispatch(ptr(x), T, H, ldx, ptr<int32_t>(of), of.size(1), rows, nullptr, g, qp, sp, (int)layout, flags,
+                               stream);
     });
     return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(s));
 }

@@ -504,8 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_fence_after();
         tmem_dealloc(tmem, S::kColumns);
     }
-    if (split > 1)
+    if (split > 1) {
         cluster_wait();  // no block ends while another may still send it sums
+        if (*dead)       // (one that gave up has not seen them arrive)
+            wait_last(partial, 0);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -863,7 +866,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
-    cluster_sync();  // neither block ends while the other's products or arrivals may reach it
+    cluster_sync();  // no block ends while another's products, arrivals or sums may reach it
+    if (SPLIT && *dead)
+        wait_last(partial, 0);
     if (warp == 1) {
         tmem_fence_after();
         pair_tmem_dealloc(tmem, 512);

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync_relaxed();  // the barriers of every block are ready
     tmem_fence_after();
     const uint32_t tmem = tmem_at;
-    // (the warps that touch global memory wait for the kernel before, with their tile found)
+    // (each warp waits for the kernel before on its own, before its first wait with a limit)
     const int32_t tiles = (int32_t)((a.p_rows + kP - 1) / kP);
     // this block's steps of 256 elements of K, and its tiles
     const int all_steps = (a.kblocks + 3) >> 2;
@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0;
         int64_t n = 0;
         bool good = true;
+        pdl_wait();  // (the limit of a wait is for this kernel's work, not for the kernel before)
         for (int32_t id = id0; good && id < tiles; id += stride, ++n) {
             const uint32_t acc = (uint32_t)n & 1;
             good = wait_warp(acc_empty + 8 * acc, ((uint32_t)(n >> 1) & 1) ^ 1, dead);
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
     if constexpr (GROUPED) {
         pdl_wait();
         tiles = grouped_tiles<BN>(a, first);
-    } else {  // (the warps that touch global memory wait, with their tile found)
+    } else {  // (each warp waits on its own, before its first wait with a limit)
         tiles = ((a.p_rows + 2 * kP - 1) / (2 * kP)) * ((a.q_rows + BN - 1) / BN);
     }
     auto tile_of = [&](int64_t id) { return pair_tile<BN, GROUPED>(a, first, id); };
@@ -685,6 +686,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
         uint32_t parity = 0;
         int64_t n = 0;
         bool good = true;
+        if (!GROUPED)
+            pdl_wait();  // (the limit of a wait is for this kernel's work, not for the kernel before)
         for (int64_t id = id0; rank == 0 && good && id < tiles; id += stride, ++n) {
             const uint32_t idesc = idesc_nvfp4(2 * kP, (uint32_t)(GROUPED ? columns(tile_of(id)) : BN));
             // the tile before has given the shared columns back, or the one before

@@ -91,6 +91,27 @@ public:
         return x;
     }
 
+    // A scale-factor layout.  Refused here: the shapes of outputs follow it, and
+    // a wider integer must not become another layout on its way to the library.
+    int layout(int i) const
+    {
+        const int64_t v = integer(i);
+        if (v == TS_SF_SWIZZLED_128x4 || v == TS_SF_SWIZZLED_8x4 || v == TS_SF_LINEAR)
+            return (int)v;
+        const std::string detail = "sf_layout " + std::to_string(v) + " is not a QuantizationSFLayout code";
+        PyObject *module = PyImport_ImportModule("reduce_residual_rmsnorm_gb300._binding");
+        PyObject *type = module == nullptr ? nullptr : PyObject_GetAttrString(module, "TsError");
+        PyObject *error = type == nullptr ? nullptr
+                                          : PyObject_CallFunction(type, "iss", TS_ERR_BAD_PATTERN,
+                                                                  ts_status_string(TS_ERR_BAD_PATTERN), detail.c_str());
+        if (error != nullptr)
+            PyErr_SetObject(type, error);
+        Py_XDECREF(error);
+        Py_XDECREF(type);
+        Py_XDECREF(module);
+        throw Raised{};
+    }
+
     // A tensor that the kernels can address, of a type.
     const at::Tensor &tensor(int i, const char *name, at::ScalarType type)
     {
@@ -266,7 +287,7 @@ private:
     bool given_ = false;
 };
 
-Dims sf_dims(int64_t T, int64_t K, int64_t layout)
+Dims sf_dims(int64_t T, int64_t K, int layout)
 {
     if (layout == TS_SF_LINEAR)
         return dims(T, K / 16);
@@ -284,15 +305,16 @@ T *ptr(const at::Tensor &t)
 PyObject *quantize(PyObject *const *args, Py_ssize_t n)
 {
     Call c(args, n, 8);
+    const int layout = c.layout(5);
     int64_t ldx;
     const at::Tensor &x = c.matrix(0, "x", &ldx);
-    const int64_t T = x.size(0), K = x.size(1), layout = c.integer(5);
+    const int64_t T = x.size(0), K = x.size(1);
     const float *g = c.one(1, "scale_factor");
     const int32_t *src = c.optional_i32(2, "row_src", dims(T));
     const auto [q, s] = c.nvfp4_outputs(3, dims(T, K / 2), sf_dims(T, K, layout), x);
     void *const qp = ptr(q), *const sp = ptr(s);
     c.run([&](uint32_t flags, void *stream) {
-        return ts_nvfp4_quantize(ptr(x), T, K, ldx, g, src, qp, sp, (int)layout, flags, stream);
+        return ts_nvfp4_quantize(ptr(x), T, K, ldx, g, src, qp, sp, layout, flags, stream);
     });
     return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(s));
 }
@@ -301,17 +323,18 @@ PyObject *quantize(PyObject *const *args, Py_ssize_t n)
 PyObject *dequantize(PyObject *const *args, Py_ssize_t n)
 {
     Call c(args, n, 8);
+    const int layout = c.layout(3);
     const at::Tensor &q = c.flat(0, "quant", kU8);
     if (q.dim() != 2)
         raise(PyExc_ValueError, "quant must be [T, K/2]");
-    const int64_t T = q.size(0), K = 2 * q.size(1), layout = c.integer(3);
+    const int64_t T = q.size(0), K = 2 * q.size(1);
     const at::Tensor &s = c.flat(1, "scale", kU8, sf_dims(T, K, layout));
     const float *g = c.one(2, "scale_factor");
     const int32_t *src = c.optional_i32(4, "row_src", dims(T));
     int64_t ldo;
     const at::Tensor out = c.matrix_output(5, "out", T, K, q, &ldo);
     c.run([&](uint32_t flags, void *stream) {
-        return ts_nvfp4_dequantize(ptr(q), ptr(s), (int)layout, T, K, g, src, ptr(out), ldo, flags, stream);
+        return ts_nvfp4_dequantize(ptr(q), ptr(s), layout, T, K, g, src, ptr(out), ldo, flags, stream);
     });
     return THPVariable_Wrap(out);
 }
@@ -390,19 +413,21 @@ const at::Tensor &row_of(Call &c, int i)
 PyObject *dispatch(PyObject *const *args, Py_ssize_t n)
 {
     Call c(args, n, 10);
+    const bool fp4 = !c.none(3);
+    const int layout = fp4 ? c.layout(7) : TS_SF_LINEAR;  // (the bf16 form has none)
     int64_t ldx;
     const at::Tensor &x = c.matrix(0, "x", &ldx);
-    const int64_t T = x.size(0), H = x.size(1), rows = c.integer(2), layout = c.integer(7);
+    const int64_t T = x.size(0), H = x.size(1), rows = c.integer(2);
     const at::Tensor &of = row_of(c, 1);
     if (of.size(0) != T)
         raise(PyExc_ValueError, "rows.row_of must be [T, k]");
-    if (c.none(3)) {
+    if (!fp4) {
         if (!c.none(5) || !c.none(6))
             raise(PyExc_ValueError, "quant_out and scale_out need scale_factor");
         const at::Tensor out = c.output(4, "out", kBF16, dims(rows, H), x);
         c.run([&](uint32_t flags, void *stream) {
             return ts_moe_dispatch(ptr(x), T, H, ldx, ptr<int32_t>(of), of.size(1), rows, ptr(out), nullptr, nullptr, nullptr,
-                                   (int)layout, flags, stream);
+                                   layout, flags, stream);
         });
         return THPVariable_Wrap(out);
     }
@@ -412,7 +437,7 @@ PyObject *dispatch(PyObject *const *args, Py_ssize_t n)
     const auto [q, s] = c.nvfp4_outputs(5, dims(rows, H / 2), sf_dims(rows, H, layout), x);
     void *const qp = ptr(q), *const sp = ptr(s);
     c.run([&](uint32_t flags, void *stream) {
-        return ts_moe_dispatch(ptr(x), T, H, ldx, ptr<int32_t>(of), of.size(1), rows, nullptr, g, qp, sp, (int)layout, flags,
+        return ts_moe_dispatch(ptr(x), T, H, ldx, ptr<int32_t>(of), of.size(1), rows, nullptr, g, qp, sp, layout, flags,
                                stream);
     });
     return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(s));

@@ -23,7 +23,8 @@
 // is the layout tensor memory wants.  Warp 1 multiplies: scale factors from shared
 // to tensor memory, then the products.  The other warps write the finished
 // accumulator, one of two, while the next tile's products run.  Every wait has a
-// limit, after which the block records it, waits for its copies in flight and ends.
+// limit, after which the block records it and ends, once the copies, products and
+// sums that its cluster has in flight have arrived.
 #include <cuda.h>
 
 #include "device_util.cuh"
@@ -39,7 +40,10 @@ __device__ uint32_t g_stalled_waits;
 constexpr int kThreads = 224;
 constexpr int kP = 128;               // rows of P per tile
 constexpr int kSfTile = 512;          // bytes of a 128-row, 64-element tile of scale factors
-constexpr long long kWaitCycles = 4000000000LL;  // a wait's limit: about 2 s
+#ifndef TSFN_WAIT_CYCLES
+#define TSFN_WAIT_CYCLES 4000000000LL
+#endif
+constexpr long long kWaitCycles = TSFN_WAIT_CYCLES;  // a wait's limit: about 2 s
 constexpr int kSmemLimit = 232448;    // bytes of shared memory of a block
 
 struct KernelArgs {
@@ -201,11 +205,46 @@ __device__ __forceinline__ int64_t grouped_tiles(const KernelArgs &a, int32_t *f
     return (int64_t)first[a.experts] * ((a.wgt_rows + 2 * kP - 1) / (2 * kP));
 }
 
+#ifdef TSFN_RUN_OUT
+// For the tests of the give-up path, which are built with it: the waits that begin
+// this many cycles after their block's start run out at once.
+__device__ long long g_run_out = 1LL << 62;
+
+__device__ __forceinline__ long long &block_start()
+{
+    __shared__ long long start;
+    return start;
+}
+
+__device__ __forceinline__ bool run_out(volatile int *dead)
+{
+    const bool out = __shfl_sync(0xffffffffu, (int)(clock64() - block_start() >= g_run_out), 0) != 0;
+    if (out && (threadIdx.x & 31) == 0) {
+        *dead = 1;
+        atomicAdd(&g_stalled_waits, 1u);
+    }
+    return out;
+}
+#endif
+
 // Wait with a limit, for what is in flight when a block gives up.
 __device__ __noinline__ void wait_last(uint32_t bar, uint32_t parity)
 {
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity) && clock64() - t0 < kWaitCycles) {
+    }
+}
+
+// The same for the copies of the last fills of the stages, with one limit for all
+// (a fill that another warp or block left undone does not complete; what came of it
+// has arrived by then).
+__device__ __noinline__ void wait_fills(uint32_t full, uint32_t fills, uint32_t stages)
+{
+    const long long t0 = clock64();
+    for (uint32_t i = 0; i < stages && i < fills; ++i) {
+        const uint32_t fill = fills - 1 - i;
+        while (!mbar_try_wait(full + 8 * (fill % stages), (fill / stages) & 1) && clock64() - t0 < kWaitCycles) {
+        }
     }
 }
 
@@ -235,6 +274,10 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *dead)
 {
+#ifdef TSFN_RUN_OUT
+    if (run_out(dead))
+        return false;
+#endif
     return __all_sync(0xffffffffu, try_wait<CLUSTER>(bar, parity) || wait_slow<CLUSTER>(bar, parity, dead));
 }
 
@@ -276,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * S::kStages + 6];
     __shared__ uint32_t tmem_at;
+    __shared__ uint32_t fills_made[2];  // by the two copying warps
     __shared__ int dead_flag;
     const uint32_t pad = (1024 - (smem_u32(raw) & 1023)) & 1023;
     const uint32_t codes = smem_u32(raw) + pad;
@@ -307,6 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (split > 1)
             mbar_expect_tx(partial, (uint32_t)(split * my_fours * kP * 16));
         dead_flag = 0;
+#ifdef TSFN_RUN_OUT
+        block_start() = clock64();
+#endif
         tma_prefetch_map(&p_map);
         tma_prefetch_map(&q_map);
     }
@@ -331,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap *map = of_p ? &p_map : &q_map;
         int s = 0;
         uint32_t parity = 0;
-        int64_t fills = 0;
+        uint32_t fills = 0;
         bool good = true;
         for (int32_t id = id0; good && id < tiles; id += stride) {
             const Tile t = few_tile(a, id);
@@ -362,12 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         pdl_launch_dependents();
-        if (!good) {  // the copies in flight land before the block's shared memory goes
-            for (int i = 0; i < S::kStages && i < fills; ++i) {
-                const int64_t fill = fills - 1 - i;
-                wait_last(full + 8 * (uint32_t)(fill % S::kStages), (uint32_t)(fill / S::kStages) & 1);
-            }
-        }
+        if (lane == 0)
+            fills_made[of_p ? 0 : 1] = fills;
     } else if (warp == 1) {
         // ---- products ----
         constexpr uint32_t idesc = idesc_nvfp4(kP, BN);
@@ -413,12 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     parity ^= 1;
                 }
             }
-        }
-        if (!good) {
-            if (elect_one())
-                mma_commit(drained);
-            __syncwarp();
-            wait_last(drained, 0);
         }
     } else {
         // ---- output ----
@@ -501,6 +538,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_arrive_relaxed();
     tmem_fence_before();
     __syncthreads();
+    if (*dead) {  // some warp gave up: the copies and products of every warp end before the block's memory goes
+        if (warp == 0 || warp == 6) {
+            wait_fills(full, fills_made[warp == 0 ? 0 : 1], S::kStages);
+        } else if (warp == 1) {
+            if (elect_one())
+                mma_commit(drained);
+            __syncwarp();
+            wait_last(drained, 0);
+        }
+        __syncwarp();
+    }
     if (warp == 1) {
         tmem_fence_after();
         tmem_dealloc(tmem, S::kColumns);
@@ -575,6 +623,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * S::kStages + 6];
     __shared__ uint32_t tmem_at;
+    __shared__ uint32_t fills_made;
     __shared__ int dead_flag;
     const uint32_t pad = (1024 - (smem_u32(raw) & 1023)) & 1023;
     const uint32_t codes = smem_u32(raw) + pad;
@@ -606,6 +655,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
         if (SPLIT)
             mbar_expect_tx(partial, S::kSums);
         dead_flag = 0;
+#ifdef TSFN_RUN_OUT
+        block_start() = clock64();
+#endif
         tma_prefetch_map(&p_map);
         tma_prefetch_map(&q_map);
         tma_prefetch_map(&psf_map);
@@ -638,7 +690,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
         // ---- copies ----
         int s = 0;
         uint32_t parity = 0;
-        int64_t fills = 0;
+        uint32_t fills = 0;
         bool good = true;
         const uint32_t full0 = map_rank(full, lead);
         for (int64_t id = id0; good && id < tiles; id += stride) {
@@ -674,12 +726,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
             }
         }
         pdl_launch_dependents();
-        if (!good && rank == 0) {  // both blocks' copies in flight land before the pair ends
-            for (int i = 0; i < S::kStages && i < fills; ++i) {
-                const int64_t fill = fills - 1 - i;
-                wait_last(full + 8 * (uint32_t)(fill % S::kStages), (uint32_t)(fill / S::kStages) & 1);
-            }
-        }
+        if (lane == 0)
+            fills_made = fills;
     } else if (warp == 1) {
         // ---- products, by the first block for both ----
         int s = 0;
@@ -733,12 +781,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
                     parity ^= 1;
                 }
             }
-        }
-        if (!good) {
-            if (elect_one())
-                pair_commit(drained, both);
-            __syncwarp();
-            wait_last(drained, 0);
         }
     } else {
         // ---- output: two warps for each 32 lanes, every other 32 columns ----
@@ -869,9 +911,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
+    if (*dead && threadIdx.x < (SPLIT ? 4 : 2))  // a block that gave up tells the cluster
+        st_cluster32(map_rank(smem_u32(&dead_flag), threadIdx.x), 1);
+    __syncwarp();
     cluster_sync();  // no block ends while another's products, arrivals or sums may reach it
-    if (SPLIT && *dead)
-        wait_last(partial, 0);
+    if (*dead) {  // in every block of the cluster: what is in flight ends before any block's memory goes
+        if (warp == 0 && rank == 0) {  // both blocks' copies complete here
+            const uint32_t mine = fills_made, other = ld_cluster32(map_rank(smem_u32(&fills_made), lead | 1));
+            wait_fills(full, mine > other ? mine : other, S::kStages);
+        } else if (warp == 1) {
+            if (rank == 0 && elect_one())
+                pair_commit(drained, both);
+            __syncwarp();
+            wait_last(drained, 0);
+        }
+        if (SPLIT)
+            wait_last(partial, 0);
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == 1) {
         tmem_fence_after();
         pair_tmem_dealloc(tmem, 512);

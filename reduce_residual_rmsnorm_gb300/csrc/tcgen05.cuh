@@ -248,6 +248,19 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// A word of the shared memory of a block of the cluster (an address of map_rank).
+__device__ __forceinline__ void st_cluster32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_cluster32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // 16 bytes into the shared memory of a block of the cluster, counted on a barrier
 // of that block when they are there (both addresses of map_rank).
 __device__ __forceinline__ void st_async_cluster(uint32_t addr, uint4 v, uint32_t bar)

@@ -1,6 +1,9 @@
 // Internal interface between the checks of the NVFP4 and expert-routing entry
 // points (api_nvfp4_moe.cu) and their launchers.  Sizes are validated; the
-// contents of the index arrays are not, and the kernels check them.
+// contents of the index arrays are not, and the kernels check them.  Any input may
+// be the output of the kernel before, which still runs when a dependent launch
+// begins: the kernels read none of them through the non-coherent path (ld.global.nc),
+// whose loads may also be moved ahead of the wait for that kernel.
 #pragma once
 
 #include <cstdint>

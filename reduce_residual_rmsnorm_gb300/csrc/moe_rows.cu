@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
 #pragma unroll
         for (int u = 0; u < kSortSteps; ++u) {
             const int64_t i = i0 + 32 * u + lane;
-            const int v = i < end ? __ldg(a.ids + i) : -1;
+            const int v = i < end ? a.ids[i] : -1;
             id[u] = v >= 0 && v < E ? v : -1;
         }
     };
@@ -173,6 +173,14 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const __grid_
 
 constexpr int kSlots = 8;  // slots whose rows are in flight together
 
+// For data that is read again, once for each group of slots.
+__device__ __forceinline__ uint4 ld_cached(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ bool row_ok(int64_t r, int64_t rows) { return r >= 0 && r < rows; }
 
 // One thread per chunk of 8 columns of an output row.
@@ -189,19 +197,22 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const __grid_constant_
         acc[e] = 0.0f;
     const int32_t *row_of = a.row_of + t * a.k;
     for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+        int32_t r[kSlots];
         uint4 v[kSlots];
         float w[kSlots];
         bool on[kSlots];
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
-            const bool slot = j0 + j < a.k;
-            const int64_t r = slot ? (int64_t)__ldg(row_of + j0 + j) : -1;
-            on[j] = row_ok(r, a.rows);
+            r[j] = j0 + j < a.k ? row_of[j0 + j] : -1;
+            on[j] = row_ok(r[j], a.rows);
+        }
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
             w[j] = 1.0f;
             if (on[j]) {
-                v[j] = ld_stream(a.y + r * a.ldy + (int64_t)c * 8);
+                v[j] = ld_stream(a.y + r[j] * a.ldy + (int64_t)c * 8);
                 if (a.weights != nullptr)
-                    w[j] = __ldg(a.weights + t * a.k + j0 + j);
+                    w[j] = a.weights[t * a.k + j0 + j];
             }
         }
         if (j0 + kSlots >= a.k)
@@ -240,15 +251,15 @@ __global__ void __launch_bounds__(kGradThreads, SLOTS > 4 ? 2 : 3) moe_combine_g
         float w[SLOTS], dot[SLOTS];
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
-            r[j] = j0 + j < a.k ? (int64_t)__ldg(a.row_of + t * a.k + j0 + j) : -1;
+            r[j] = j0 + j < a.k ? (int64_t)a.row_of[t * a.k + j0 + j] : -1;
             if (!row_ok(r[j], a.rows))
                 r[j] = -1;
-            w[j] = r[j] >= 0 ? __ldg(a.weights + t * a.k + j0 + j) : 0.0f;
+            w[j] = r[j] >= 0 ? a.weights[t * a.k + j0 + j] : 0.0f;
             dot[j] = 0.0f;
         }
         for (int c = tid; c < nc; c += blockDim.x) {
             uint4 y[SLOTS];
-            const uint4 dv = ld_keep(drow + (int64_t)c * 8);
+            const uint4 dv = ld_cached(drow + (int64_t)c * 8);
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j)
                 if (r[j] >= 0)

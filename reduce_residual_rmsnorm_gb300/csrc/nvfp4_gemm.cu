@@ -145,7 +145,7 @@ __device__ __forceinline__ Tile grouped_tile(const KernelArgs &a, const int32_t 
     const uint32_t in = from - group * kGroup * nw;
     const uint32_t w = in / gt;
     const int t0 = (int)(group * kGroup + in - w * gt) * BN, w0 = (int)w * 2 * kP;
-    const int count = __ldg(a.count + lo), start = __ldg(a.start + lo);
+    const int count = a.count[lo], start = a.start[lo];
     Tile t;
     t.expert = lo;
     t.tok0 = start + t0;
@@ -177,7 +177,7 @@ __device__ __forceinline__ int64_t grouped_tiles(const KernelArgs &a, int32_t *f
 {
     const int lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-        const int start = __ldg(a.start + e), count = __ldg(a.count + e);
+        const int start = a.start[e], count = a.count[e];
         const bool good = start >= 0 && (start & 127) == 0 && count > 0 && (int64_t)start + count <= a.tok_rows;
         first[e + 1] = good ? (count + BN - 1) / BN : 0;
     }
@@ -464,11 +464,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // byte offset of block r's partial sums of four tokens, the i-th of a block's share: [split][BN / 4 / split][128][4]
         auto sum_at = [&](int r, int i) { return 16 * ((((r * (BN / 4)) >> lg) + i) * kP + row); };
         int64_t n = 0;
+        float alpha = 0.0f;
         for (int32_t id = id0; id < tiles; id += stride, ++n) {
             const Tile t = few_tile(a, id);
-            if (n == 0)
+            if (n == 0) {
                 pdl_wait();
-            const float alpha = __ldg(a.alpha);
+                alpha = *a.alpha;
+            }
             const uint32_t acc = (uint32_t)n & 1;
             if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
                 break;
@@ -788,11 +790,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
         const uint32_t stage = stage_out + (warp - 2) * (32 * 64);
         const uint32_t free0 = map_rank(acc_free, lead);
         int64_t n = 0;
+        float alpha = 0.0f;
         for (int64_t id = id0; id < tiles; id += stride, ++n) {
             const Tile t = tile_of(id);
-            if (!GROUPED && n == 0)
+            if (!GROUPED && n == 0) {
                 pdl_wait();
-            const float alpha = __ldg(a.alpha + (GROUPED ? t.expert : 0));
+                alpha = *a.alpha;
+            }
+            if (GROUPED)
+                alpha = a.alpha[t.expert];
             const uint32_t acc = (uint32_t)n & 1;
             if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
                 break;

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, SCATTER ? 4 : 5) nvfp4_rows_kernel(c
     pdl_wait();
     bool live = t < a.T;
     if (!SCATTER && live && a.row_src != nullptr)
-        live = __ldg(a.row_src + t) >= 0;
+        live = a.row_src[t] >= 0;
     const uint16_t *row = a.x + t * a.ldx + (int64_t)b0 * 16;
     uint4 v[kBlocks][2];
 #pragma unroll
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, SCATTER ? 4 : 5) nvfp4_rows_kernel(c
             v[i][1] = ld_stream(row + (int64_t)(i << lg) * 16 + 8);
         }
     }
-    const float g = __ldg(a.g);
+    const float g = *a.g;
     pdl_launch_dependents();
     uint2 codes[kBlocks];
     uint32_t sf[kBlocks];
@@ -141,9 +141,9 @@ __global__ void __launch_bounds__(kThreads, SCATTER ? 4 : 5) nvfp4_rows_kernel(c
     if (live) {
         const int k = SCATTER ? a.k : 1;
         const int32_t *row_of = SCATTER ? a.row_of + t * a.k : nullptr;
-        int64_t r = SCATTER ? (int64_t)__ldg(row_of) : t;
+        int64_t r = SCATTER ? (int64_t)*row_of : t;
         for (int j = 0; j < k; ++j) {
-            const int64_t r_next = SCATTER && j + 1 < k ? (int64_t)__ldg(row_of + j + 1) : 0;
+            const int64_t r_next = SCATTER && j + 1 < k ? (int64_t)row_of[j + 1] : 0;
             if (!SCATTER || (r >= 0 && r < a.rows)) {
                 uint8_t *out = a.codes + r * (a.K >> 1) + (int64_t)b0 * 8;
 #pragma unroll
@@ -165,7 +165,9 @@ __global__ void __launch_bounds__(kThreads, SCATTER ? 4 : 5) nvfp4_rows_kernel(c
     }
 }
 
-// Row t -> its k rows, copied.
+// Row t -> its k rows, copied.  Where a warp has one token, its lanes look up the rows
+// of 32 slots in one load and pass them round (16 x 8 rows of 7168 1.9 us; one load
+// after the other, which the stores hold up, 2.1).
 __global__ void __launch_bounds__(kThreads) dispatch_rows_kernel(const __grid_constant__ RowsArgs a)
 {
     const int lane = threadIdx.x & 31;
@@ -185,8 +187,18 @@ __global__ void __launch_bounds__(kThreads) dispatch_rows_kernel(const __grid_co
             v[i] = ld_stream(row + (int64_t)c * 8);
     }
     pdl_launch_dependents();
+    const int32_t *row_of = a.row_of + t * a.k;
+    const bool wide = a.tpr_log2 == 5;
+    int32_t mine = 0;
+#pragma unroll 8
     for (int j = 0; j < a.k; ++j) {
-        const int64_t r = __ldg(a.row_of + t * a.k + j);
+        int32_t r;
+        if (wide) {
+            if ((j & 31) == 0)
+                mine = j + lane < a.k ? row_of[j + lane] : -1;
+            r = __shfl_sync(0xffffffffu, mine, j & 31);
+        } else
+            r = row_of[j];
         if (r < 0 || r >= a.rows)
             continue;
         uint16_t *out = a.out + r * a.K;
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) nvfp4_values_kernel(const __grid_con
     const int nc = (int)(a.K >> 3);
     const int c0 = (int)blockIdx.y * (32 * kChunks) + l;
     pdl_wait();
-    if (t >= a.T || (a.row_src != nullptr && __ldg(a.row_src + t) < 0))
+    if (t >= a.T || (a.row_src != nullptr && a.row_src[t] < 0))
         return;
     const uint8_t *codes = a.codes + t * (a.K >> 1);
     const uint8_t *sf = a.sf + sf_row_base(a.sf_layout, a.sf_cols, t);
@@ -237,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) nvfp4_values_kernel(const __grid_con
             s[i] = sf[(int64_t)(k >> 2) * stride + (k & 3)];
         }
     }
-    const float g = __ldg(a.g);
+    const float g = *a.g;
     pdl_launch_dependents();
     uint16_t *out = a.out + t * a.ldo;
 #pragma unroll

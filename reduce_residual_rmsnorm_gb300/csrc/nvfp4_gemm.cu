@@ -216,16 +216,22 @@ __device__ __forceinline__ long long &block_start()
     return start;
 }
 
-__device__ __forceinline__ bool run_out(volatile int *dead)
+__device__ __forceinline__ bool run_out()
 {
-    const bool out = __shfl_sync(0xffffffffu, (int)(clock64() - block_start() >= g_run_out), 0) != 0;
-    if (out && (threadIdx.x & 31) == 0) {
-        *dead = 1;
-        atomicAdd(&g_stalled_waits, 1u);
-    }
-    return out;
+    return __shfl_sync(0xffffffffu, (int)(clock64() - block_start() >= g_run_out), 0) != 0;
 }
 #endif
+
+// A wait ran into its limit: the block gives up, and the others of its pair or cluster
+// of pairs (PEERS of them with it), whose copies and products reach its memory.
+template <int PEERS>
+__device__ __noinline__ void give_up(volatile int *dead)
+{
+    *dead = 1;
+    for (uint32_t r = 0; PEERS > 1 && r < PEERS; ++r)
+        st_cluster32(map_rank(smem_u32((const void *)dead), r), 1);
+    atomicAdd(&g_stalled_waits, 1u);
+}
 
 // Wait with a limit, for what is in flight when a block gives up.
 __device__ __noinline__ void wait_last(uint32_t bar, uint32_t parity)
@@ -254,31 +260,33 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
     return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
 }
 
-template <bool CLUSTER>
+template <bool CLUSTER, int PEERS>
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *dead)
 {
     const long long t0 = clock64();
     while (!*dead) {
         if (try_wait<CLUSTER>(bar, parity))
             return true;
-        if (clock64() - t0 > kWaitCycles) {
-            *dead = 1;
-            atomicAdd(&g_stalled_waits, 1u);
-        }
+        if (clock64() - t0 > kWaitCycles)
+            give_up<PEERS>(dead);
     }
     return false;
 }
 
 // The whole warp waits; false in every lane when a wait ran into its limit,
 // here or elsewhere in the block.  CLUSTER: for what another block sent.
-template <bool CLUSTER = false>
+template <int PEERS, bool CLUSTER = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *dead)
 {
 #ifdef TSFN_RUN_OUT
-    if (run_out(dead))
+    if (run_out()) {
+        if ((threadIdx.x & 31) == 0)
+            give_up<PEERS>(dead);
+        __syncwarp();
         return false;
+    }
 #endif
-    return __all_sync(0xffffffffu, try_wait<CLUSTER>(bar, parity) || wait_slow<CLUSTER>(bar, parity, dead));
+    return __all_sync(0xffffffffu, try_wait<CLUSTER>(bar, parity) || wait_slow<CLUSTER, PEERS>(bar, parity, dead));
 }
 
 // ---------------------------------------------------------------------------
@@ -309,6 +317,21 @@ struct Shape {
     static constexpr int kColumns = 512;      // one block per SM: all of it
     static_assert(kSfQ + 16 <= kColumns, "accumulators and scale factors fit tensor memory");
 };
+
+// What a block that gave up has in flight ends: each copying warp's copies, and the
+// products.  (Out of line here and below: the kernels' ends stay short.)
+__device__ __noinline__ void few_drain(int warp, uint32_t full, uint32_t fills, uint32_t stages, uint32_t drained)
+{
+    if (warp == 0 || warp == 6) {
+        wait_fills(full, fills, stages);
+    } else if (warp == 1) {
+        if (elect_one())
+            mma_commit(drained);
+        __syncwarp();
+        wait_last(drained, 0);
+    }
+    __syncwarp();
+}
 
 template <int BN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -387,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fills == 0)
                 pdl_wait();
             for (int kt = kt0; kt < kt1; ++kt) {
-                good = wait_warp(empty + 8 * s, parity ^ 1, dead);
+                good = wait_warp<1>(empty + 8 * s, parity ^ 1, dead);
                 if (!good)
                     break;
                 const int nkb = a.kblocks - 4 * kt < 4 ? a.kblocks - 4 * kt : 4;
@@ -421,12 +444,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         pdl_wait();  // (the limit of a wait is for this kernel's work, not for the kernel before)
         for (int32_t id = id0; good && id < tiles; id += stride, ++n) {
             const uint32_t acc = (uint32_t)n & 1;
-            good = wait_warp(acc_empty + 8 * acc, ((uint32_t)(n >> 1) & 1) ^ 1, dead);
+            good = wait_warp<1>(acc_empty + 8 * acc, ((uint32_t)(n >> 1) & 1) ^ 1, dead);
             if (!good)
                 break;
             const uint32_t d = tmem + acc * BN;
             for (int kt = kt0; kt < kt1; ++kt) {
-                good = wait_warp(full + 8 * s, parity, dead);
+                good = wait_warp<1>(full + 8 * s, parity, dead);
                 if (!good)
                     break;
                 tmem_fence_after();
@@ -472,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 alpha = *a.alpha;
             }
             const uint32_t acc = (uint32_t)n & 1;
-            if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
+            if (!wait_warp<1>(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
                 break;
             tmem_fence_after();
 #pragma unroll 1
@@ -503,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (split > 1) {  // the only tile of the cluster
-                if (my_fours == 0 || !wait_warp<true>(partial, 0, dead))
+                if (my_fours == 0 || !wait_warp<1, true>(partial, 0, dead))
                     break;
                 for (int four = rank; four < fours; four += split) {
                     float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -540,24 +563,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_arrive_relaxed();
     tmem_fence_before();
     __syncthreads();
-    if (*dead) {  // some warp gave up: the copies and products of every warp end before the block's memory goes
-        if (warp == 0 || warp == 6) {
-            wait_fills(full, fills_made[warp == 0 ? 0 : 1], S::kStages);
-        } else if (warp == 1) {
-            if (elect_one())
-                mma_commit(drained);
-            __syncwarp();
-            wait_last(drained, 0);
-        }
-        __syncwarp();
-    }
+    const bool gave_up = *dead != 0;  // some warp of the block
+    if (gave_up)  // the copies and products of every warp end before the block's memory goes
+        few_drain(warp, full, fills_made[warp == 6], S::kStages, drained);
     if (warp == 1) {
         tmem_fence_after();
         tmem_dealloc(tmem, S::kColumns);
     }
     if (split > 1) {
         cluster_wait();  // no block ends while another may still send it sums
-        if (*dead)       // (one that gave up has not seen them arrive)
+        if (gave_up)     // (it has not seen them arrive)
             wait_last(partial, 0);
     }
 }
@@ -615,6 +630,24 @@ struct PairShape {
     static_assert(!SPLIT || BN == 128, "a warp has two pieces of the output and gives one away");
 };
 
+// What the blocks of a pair have in flight ends, when one of them gave up: the copies
+// of both, which complete in the first, and the products.
+__device__ __noinline__ void pair_drain(int warp, uint32_t in_cluster, uint32_t full, uint32_t fills_at, uint32_t stages,
+                                        uint32_t drained)
+{
+    const uint32_t rank = in_cluster & 1, lead = in_cluster & 2;
+    if (warp == 0 && rank == 0) {
+        const uint32_t mine = ld_cluster32(map_rank(fills_at, lead)), other = ld_cluster32(map_rank(fills_at, lead | 1));
+        wait_fills(full, mine > other ? mine : other, stages);
+    } else if (warp == 1) {
+        if (rank == 0 && elect_one())
+            pair_commit(drained, 3u << lead);
+        __syncwarp();
+        wait_last(drained, 0);
+    }
+    __syncwarp();
+}
+
 template <int BN, bool GROUPED, bool SPLIT>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 2, 1, 1)
     nvfp4_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
@@ -622,6 +655,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
                       const __grid_constant__ CUtensorMap out_map, const __grid_constant__ KernelArgs a)
 {
     using S = PairShape<BN, SPLIT>;
+    constexpr int kPeers = SPLIT ? 4 : 2;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * S::kStages + 6];
     __shared__ uint32_t tmem_at;
@@ -703,7 +737,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
             if (!GROUPED && fills == 0)
                 pdl_wait();
             for (int kt = kt0; kt < kt1; ++kt) {
-                good = wait_warp(empty + 8 * s, parity ^ 1, dead);
+                good = wait_warp<kPeers>(empty + 8 * s, parity ^ 1, dead);
                 if (!good)
                     break;
                 const uint32_t bar = full0 + 8 * s;
@@ -742,15 +776,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
             const uint32_t idesc = idesc_nvfp4(2 * kP, (uint32_t)(GROUPED ? columns(tile_of(id)) : BN));
             // the tile before has given the shared columns back, or the one before
             // that its accumulator (without one: at once)
-            good = S::kShared ? wait_warp(acc_free, ((uint32_t)n & 1) ^ 1, dead)
-                              : wait_warp(acc_free + 8 * ((uint32_t)n & 1), ((uint32_t)(n >> 1) & 1) ^ 1, dead);
+            good = S::kShared ? wait_warp<kPeers>(acc_free, ((uint32_t)n & 1) ^ 1, dead)
+                              : wait_warp<kPeers>(acc_free + 8 * ((uint32_t)n & 1), ((uint32_t)(n >> 1) & 1) ^ 1, dead);
             if (!good)
                 break;
             const uint32_t d = tmem + ((uint32_t)n & 1) * S::kAcc1;
             // (tiles of 192 rows of Q begin in the middle of every other band)
             const uint32_t sf_q = tmem + S::kSfQ + (BN == 192 ? (uint32_t)(tile_of(id).q_row & 127) >> 5 : 0);
             for (int kt = kt0; kt < kt1; ++kt) {
-                good = wait_warp(full + 8 * s, parity, dead);
+                good = wait_warp<kPeers>(full + 8 * s, parity, dead);
                 if (!good)
                     break;
                 tmem_fence_after();
@@ -800,7 +834,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
             if (GROUPED)
                 alpha = a.alpha[t.expert];
             const uint32_t acc = (uint32_t)n & 1;
-            if (!wait_warp(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
+            if (!wait_warp<kPeers>(acc_full + 8 * acc, (uint32_t)(n >> 1) & 1, dead))
                 break;
             tmem_fence_after();
             const int row0 = (int)rank * kP + quad * 32;  // of the warp's lanes in the tile
@@ -828,7 +862,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
                     w.w = lead ? v[0][4 * j + 3] : v[1][4 * j + 3];
                     st_async_cluster(map_rank(at + j * 512, to), w, map_rank(partial, to));
                 }
-                if (!wait_warp<true>(partial, 0, dead))
+                if (!wait_warp<kPeers, true>(partial, 0, dead))
                     break;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -917,20 +951,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(SPLIT ? 4 : 
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
-    if (*dead && threadIdx.x < (SPLIT ? 4 : 2))  // a block that gave up tells the cluster
-        st_cluster32(map_rank(smem_u32(&dead_flag), threadIdx.x), 1);
-    __syncwarp();
     cluster_sync();  // no block ends while another's products, arrivals or sums may reach it
     if (*dead) {  // in every block of the cluster: what is in flight ends before any block's memory goes
-        if (warp == 0 && rank == 0) {  // both blocks' copies complete here
-            const uint32_t mine = fills_made, other = ld_cluster32(map_rank(smem_u32(&fills_made), lead | 1));
-            wait_fills(full, mine > other ? mine : other, S::kStages);
-        } else if (warp == 1) {
-            if (rank == 0 && elect_one())
-                pair_commit(drained, both);
-            __syncwarp();
-            wait_last(drained, 0);
-        }
+        pair_drain(warp, in_cluster, full, smem_u32(&fills_made), S::kStages, drained);
         if (SPLIT)
             wait_last(partial, 0);
         __syncwarp();

@@ -33,6 +33,19 @@ struct Raised {};
     throw Raised{};
 }
 
+// The interpreter is left to other threads: a launch may wait for room in its queue,
+// an allocation for the device.
+class Unlocked {
+public:
+    Unlocked() : state_(PyEval_SaveThread()) {}
+    ~Unlocked() { PyEval_RestoreThread(state_); }
+    Unlocked(const Unlocked &) = delete;
+    Unlocked &operator=(const Unlocked &) = delete;
+
+private:
+    PyThreadState *state_;
+};
+
 // A shape to compare with or to say.
 struct Dims {
     int64_t d[3];
@@ -196,6 +209,7 @@ public:
     // that writes it: another stream's free memory may still be in use there.
     at::Tensor fresh(const Dims &d, at::ScalarType type, const at::Tensor &like) const
     {
+        const Unlocked unlocked;
         if (like.is_cuda()) {
             if (!given_)
                 return at::detail::empty_cuda(d.ref(), type, like.device(), std::nullopt);
@@ -258,11 +272,14 @@ public:
         void *stream = given_ ? stream_ : c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
         const uint32_t flags = pdl ? TS_FLAG_PDL : 0u;
         int status;
-        if (device == now) {
-            status = call(flags, stream);
-        } else {
-            const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
-            status = call(flags, stream);
+        {
+            const Unlocked unlocked;
+            if (device == now) {
+                status = call(flags, stream);
+            } else {
+                const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+                status = call(flags, stream);
+            }
         }
         if (status != TS_OK)
             failed(status);

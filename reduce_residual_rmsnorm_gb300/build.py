@@ -5,7 +5,8 @@ one shared object with the CUDA runtime linked statically, so the library
 loads on any machine with a CUDA driver.  No fast-math: IEEE division and
 square root, denormals kept (the quantisers depend on them).  Beside it
 ``_python_calls.so`` (g++ against the installed PyTorch) marshals the calls of
-``_nvfp4_moe``.
+``_nvfp4_moe``.  The library needs none of PyTorch: it is linked first, and
+alone where no PyTorch with CUDA is installed.
 """
 from __future__ import annotations
 
@@ -45,16 +46,37 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps() -> list[str]:
-    return sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+def _newer(path: str, deps: list[str]) -> bool:
+    if not os.path.exists(path):
+        return False
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def _common_deps() -> list[str]:
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB_PATH, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                  _common_deps())
+
+
+def calls_up_to_date() -> bool:
+    return _newer(CALLS_PATH, [CALLS_SRC] + _common_deps())
+
+
+def calls_wanted() -> bool:
+    """Whether there is a PyTorch whose CUDA tensors the compiled calls could take."""
+    try:
+        import torch
+    except ImportError:
+        return False
+    return torch.version.cuda is not None
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and (calls_up_to_date() or not calls_wanted())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -67,7 +89,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         fcntl.flock(lock, fcntl.LOCK_EX)
         if not force and up_to_date():
             return LIB_PATH
-        return _build_locked(verbose, extra_flags)
+        calls = calls_wanted() and (force or not calls_up_to_date())
+        with cf.ThreadPoolExecutor(max_workers=1) as ex:
+            # compiled beside the library, whose link waits for none of it
+            calls_obj = ex.submit(_compile_calls) if calls else None
+            if force or not library_up_to_date():
+                _build_library(verbose, extra_flags)
+            if calls_obj is not None:
+                _link_calls(calls_obj.result())
+        return LIB_PATH
 
 
 def _compile_calls() -> str:
@@ -102,7 +132,7 @@ def _link_calls(obj: str) -> None:
     os.replace(tmp, CALLS_PATH)
 
 
-def _build_locked(verbose: bool, extra_flags: list[str] | None) -> str:
+def _build_library(verbose: bool, extra_flags: list[str] | None) -> None:
     cc = nvcc()
     flags = NVCC_FLAGS + (extra_flags or [])
 
@@ -117,17 +147,13 @@ def _build_locked(verbose: bool, extra_flags: list[str] | None) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        calls = ex.submit(_compile_calls)
         objs = list(ex.map(compile_one, sources()))
-        calls_obj = calls.result()
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_calls(calls_obj)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from ._binding import SFLayout, _check, library
-from .build import CALLS_PATH
+from .build import CALLS_PATH, calls_match
 
 _calls = None
 
@@ -27,6 +27,9 @@ def _native():
         library()
         if not os.path.exists(CALLS_PATH):
             raise RuntimeError(f"{CALLS_PATH} is missing: build the CUDA library first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        if not calls_match():
+            raise RuntimeError(f"{CALLS_PATH} was built for another PyTorch or Python: build the CUDA library again "
                                "(python -c 'import __graft_entry__ as g; g.build()')")
         from . import _python_calls
         _calls = _python_calls

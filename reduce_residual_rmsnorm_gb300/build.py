@@ -27,6 +27,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 CALLS_SRC = os.path.join(CSRC, "python_calls.cpp")
 CALLS_PATH = os.path.join(PKG, "_python_calls.so")
 BUILD_DIR = os.path.join(PKG, "_build")
+CALLS_STAMP = "python_calls.built_for"  # in BUILD_DIR
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -62,8 +63,25 @@ def library_up_to_date() -> bool:
                   _common_deps())
 
 
+def _calls_for() -> str:
+    """What the compiled calls are bound to: the layout of PyTorch's tensors and Python's objects."""
+    import torch
+
+    return "PyTorch %s, CXX11 ABI %d, %s" % (torch.__version__, int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                                             sysconfig.get_config_var("SOABI"))
+
+
+def calls_match() -> bool:
+    """Whether the compiled calls were built for the installed PyTorch and this Python."""
+    try:
+        with open(os.path.join(BUILD_DIR, CALLS_STAMP), encoding="utf-8") as f:
+            return f.read() == _calls_for()
+    except OSError:
+        return False
+
+
 def calls_up_to_date() -> bool:
-    return _newer(CALLS_PATH, [CALLS_SRC] + _common_deps())
+    return _newer(CALLS_PATH, [CALLS_SRC] + _common_deps()) and calls_match()
 
 
 def calls_wanted() -> bool:
@@ -129,7 +147,12 @@ def _link_calls(obj: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of {CALLS_PATH} failed:\n{r.stdout}\n{r.stderr}")
+    stamp = os.path.join(BUILD_DIR, CALLS_STAMP)
+    if os.path.exists(stamp):
+        os.remove(stamp)  # (it never stands beside calls built for another PyTorch)
     os.replace(tmp, CALLS_PATH)
+    with open(stamp, "w", encoding="utf-8") as f:
+        f.write(_calls_for())
 
 
 def _build_library(verbose: bool, extra_flags: list[str] | None) -> None:

@@ -84,3 +84,39 @@ def test_each_is_made_again_alone(tree):
         tree.runs.clear()
         libbuild.build()
         assert os.path.exists(gone) and len(tree.runs) == n
+
+
+@pytest.mark.parametrize("other", ("pytorch", "python"))
+def test_calls_are_made_again_for_another_pytorch_or_python(tree, monkeypatch, other):
+    libbuild.build()
+    assert libbuild.calls_match()
+    tree.runs.clear()
+    if other == "pytorch":
+        monkeypatch.setattr(torch, "__version__", "0.0.1")
+    else:
+        real = libbuild.sysconfig.get_config_var
+        monkeypatch.setattr(libbuild.sysconfig, "get_config_var", lambda n: "cpython-0" if n == "SOABI" else real(n))
+    assert not libbuild.calls_match() and not libbuild.up_to_date()
+    libbuild.build()
+    assert [_of_calls(c) for c in tree.runs] == [True, True]
+    assert libbuild.calls_match() and libbuild.up_to_date()
+
+
+def test_calls_of_another_pytorch_are_not_loaded(monkeypatch):
+    from reduce_residual_rmsnorm_gb300 import _nvfp4_moe
+
+    libbuild.build()
+    monkeypatch.setattr(_nvfp4_moe, "_calls", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with pytest.raises(RuntimeError, match="another PyTorch"):
+        _nvfp4_moe._native()
+    monkeypatch.undo()
+    assert _nvfp4_moe._native() is not None
+
+
+def test_calls_without_a_stamp_are_made_again(tree):
+    libbuild.build()
+    os.remove(os.path.join(libbuild.BUILD_DIR, libbuild.CALLS_STAMP))
+    assert not libbuild.up_to_date()
+    libbuild.build()
+    assert libbuild.up_to_date()

@@ -13,8 +13,9 @@
  * ts_last_error_detail, TS_FLAG_PDL, no allocation and no synchronisation),
  * with these additions:
  *   - Buffers may be in device memory or in page-locked host memory, except
- *     the operands of ts_nvfp4_gemm and ts_nvfp4_grouped_gemm, which are read
- *     by the tensor copy engine and live in device memory.
+ *     the operands and the output of ts_nvfp4_gemm and ts_nvfp4_grouped_gemm,
+ *     which the tensor copy engine reads and writes and which live in device
+ *     memory (alpha and the experts' starts and counts may be in either).
  *   - NVFP4 matrices: codes uint8 [rows, K/2], element 2k in the low nibble of
  *     byte k; one E4M3 scale factor per 16 columns, in the layouts that
  *     ts_outs_t describes.  A matrix has one fp32 global scale g, and stands

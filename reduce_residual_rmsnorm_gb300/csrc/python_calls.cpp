@@ -192,6 +192,15 @@ public:
         return t;
     }
 
+    // The output of a product, which the tensor copy engine writes.
+    at::Tensor product_output(int i, int64_t rows, int64_t cols, const at::Tensor &like, int64_t *ld)
+    {
+        const at::Tensor t = matrix_output(i, "out", rows, cols, like, ld);
+        if (!t.is_cuda())
+            raise(PyExc_TypeError, "out must be a CUDA tensor");
+        return t;
+    }
+
     const float *one(int i, const char *name)
     {
         const at::Tensor &t = tensor(i, name, kF32);
@@ -369,7 +378,7 @@ PyObject *gemm(PyObject *const *args, Py_ssize_t n)
     Call::shape(bs, "b_scale", sf_dims(N, K, TS_SF_SWIZZLED_128x4));
     const float *alpha = c.one(4, "alpha");
     int64_t ldo;
-    const at::Tensor out = c.matrix_output(5, "out", M, N, a, &ldo);
+    const at::Tensor out = c.product_output(5, M, N, a, &ldo);
     c.run([&](uint32_t flags, void *stream) {
         return ts_nvfp4_gemm(ptr(a), ptr(as), ptr(b), ptr(bs), alpha, M, N, K, ptr(out), ldo, flags, stream);
     });
@@ -477,7 +486,7 @@ PyObject *grouped_gemm(PyObject *const *args, Py_ssize_t n)
     const at::Tensor &count = c.flat(6, "rows.expert_count", kI32, dims(E));
     const int64_t entries = c.integer(7);
     int64_t ldo;
-    const at::Tensor out = c.matrix_output(8, "out", rows, N, a, &ldo);
+    const at::Tensor out = c.product_output(8, rows, N, a, &ldo);
     c.run([&](uint32_t flags, void *stream) {
         return ts_nvfp4_grouped_gemm(ptr(a), ptr(as), ptr(b), ptr(bs), ptr<float>(alpha), ptr<int32_t>(start),
                                      ptr<int32_t>(count), E, rows, entries, N, K, ptr(out), ldo, flags, stream);

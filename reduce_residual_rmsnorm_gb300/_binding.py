@@ -244,6 +244,12 @@ def sf_shape(T: int, H: int, sf_layout: int = SFLayout.LINEAR) -> tuple[int, int
     return (T + tile - 1) // tile * tile, (H // 16 + 3) // 4 * 4
 
 
+def _layout_code(sf_layout: int) -> int:
+    """The layout as the library's 32-bit field; a wider number must not become another layout there."""
+    layout = int(sf_layout)
+    return layout if -2 ** 31 <= layout < 2 ** 31 else -1  # (no layout: refused where one is used)
+
+
 def sf_swizzled_shape(T: int, H: int) -> tuple[int, int]:
     """Shape of the padded SWIZZLED_128x4 scale-factor buffer for [T, H] values."""
     return sf_shape(T, H, SFLayout.SWIZZLED_128x4)
@@ -314,7 +320,7 @@ def ts_fused_reduce_norm(pattern: int, partials, residual: torch.Tensor | None =
         _dev(scale_factor, "scale_factor", torch.float32)
     outs = TsOuts(_ptr(allreduce_out), _ptr(residual_out), _ptr(norm_out), _ptr(partial_norm_out),
                   0 if partial_norm_out is None else int(partial_norm_out.shape[-1]),
-                  _ptr(quant_out), _ptr(scale_out), int(sf_layout), 0)
+                  _ptr(quant_out), _ptr(scale_out), _layout_code(sf_layout), 0)
     arr = (ctypes.c_void_p * len(ptrs))(*ptrs)
     _check(library().ts_fused_reduce_norm(int(pattern), arr, len(ptrs), _ptr(residual), _ptr(gamma),
                                           float(eps), _ptr(scale_factor), int(T), int(H),
@@ -363,7 +369,7 @@ def ts_reducescatter_fused_norm(rs_pattern: int, partials, rank: int, add_in: to
     if scale_factor is not None:
         _dev(scale_factor, "scale_factor", torch.float32)
     outs = TsOuts(_ptr(reducescatter_out), _ptr(residual_out), _ptr(norm_out), None, 0, _ptr(quant_out),
-                  _ptr(scale_out), int(sf_layout), 0)
+                  _ptr(scale_out), _layout_code(sf_layout), 0)
     arr = (ctypes.c_void_p * len(ptrs))(*ptrs)
     _check(library().ts_reducescatter_fused_norm(int(rs_pattern), arr, len(ptrs), int(rank), _ptr(add_in),
                                                  _ptr(residual), _ptr(gamma), float(eps), _ptr(scale_factor),

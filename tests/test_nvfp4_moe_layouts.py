@@ -42,6 +42,38 @@ def test_no_number():
             call(1 << 64)
 
 
+class _Library:
+    """Keeps the layout that a fused call hands over."""
+
+    def __init__(self):
+        self.layouts = []
+
+    def _call(self, outs):
+        self.layouts.append(outs._obj.sf_layout)
+        return 0
+
+    def ts_fused_reduce_norm(self, *args):
+        return self._call(args[9])
+
+    def ts_reducescatter_fused_norm(self, *args):
+        return self._call(args[11])
+
+
+def test_fused_calls_hand_over_no_other_layout(monkeypatch):
+    from reduce_residual_rmsnorm_gb300 import _binding
+
+    fake = _Library()
+    monkeypatch.setattr(_binding, "library", lambda path=None: fake)
+    monkeypatch.setattr(_binding, "_dev", lambda t, name, dtype=None: t)
+    x, g = torch.zeros(2, 32, dtype=torch.bfloat16), torch.ones(1)
+    for layout in (0, 1, 2, 3, -1, *LAYOUTS):
+        want = layout if layout in (0, 1, 2, 3) else -1
+        pkg.ts_fused_reduce_norm(3, [x], x, x[0], 1e-6, g, residual_out=x.clone(), quant_out=x, scale_out=x, sf_layout=layout, stream=0)
+        pkg.ts_reducescatter_fused_norm(3, [x], 0, residual=x, gamma=x[0], scale_factor=g, residual_out=x.clone(), quant_out=x,
+                                        scale_out=x, sf_layout=layout, stream=0)
+        assert fake.layouts[-2:] == [want, want], layout
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_refused(layout):

@@ -300,7 +300,7 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 // cycles; the partial sums travel by stores that the receiving barrier counts,
 // with no fence; the cluster's last arrival orders nothing (3.8 us below with one
 // that waits for the outputs); and a tile is found before the dependency wait.
-// 1 x 4096 x 4096 takes 3.4 us (1.4 of bytes): about 0.2 us from the wait to the
+// 1 x 4096 x 4096 takes 3.5 us (1.4 of bytes): about 0.2 us from the wait to the
 // first copy's issue, 0.9 to its arrival, 0.9 for the four steps, 0.2 to the
 // accumulator, 0.3 to the exchanged sums.
 

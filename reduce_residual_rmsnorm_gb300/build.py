@@ -94,7 +94,7 @@ def calls_wanted() -> bool:
 
 
 def up_to_date() -> bool:
-    return library_up_to_date() and (calls_up_to_date() or not calls_wanted())
+    return library_up_to_date() and (not calls_wanted() or calls_up_to_date())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:

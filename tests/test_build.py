@@ -62,8 +62,13 @@ def test_library_needs_no_cuda_in_pytorch(tree, monkeypatch):
     monkeypatch.undo()
 
 
-def test_library_needs_no_pytorch(tree, monkeypatch):
+@pytest.mark.parametrize("before", (False, True), ids=("never", "uninstalled"))
+def test_library_needs_no_pytorch(tree, monkeypatch, before):
     import builtins
+
+    if before:  # the calls of an earlier build are there
+        libbuild.build()
+        tree.runs.clear()
 
     real = builtins.__import__
 
@@ -73,6 +78,7 @@ def test_library_needs_no_pytorch(tree, monkeypatch):
         return real(name, *args, **kw)
 
     monkeypatch.setattr(builtins, "__import__", no_torch)
+    assert libbuild.up_to_date() == before
     assert libbuild.build() == tree.lib
     assert os.path.exists(tree.lib) and not any(_of_calls(c) for c in tree.runs)
 

@@ -70,6 +70,18 @@ class TsError(RuntimeError):
         self.detail = detail
 
 
+class TsKvCache(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("head_dim", ctypes.c_int64),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
 class TsOuts(ctypes.Structure):
     _fields_ = [
         ("allreduce_out", ctypes.c_void_p),
@@ -87,7 +99,8 @@ class TsOuts(ctypes.Structure):
 EXPORTS = ("ts_fused_reduce_norm", "ts_reducescatter_fused_norm", "ts_allgather_fused_norm", "ts_qk_norm_sharded",
            "ts_rms_norm_sharded", "ts_nvfp4_quantize", "ts_nvfp4_dequantize", "ts_nvfp4_gemm", "ts_moe_rows",
            "ts_moe_sort", "ts_moe_dispatch", "ts_nvfp4_grouped_gemm", "ts_moe_combine", "ts_moe_combine_grad",
-           "ts_stalled_waits", "ts_status_string", "ts_last_error_detail")
+           "ts_stalled_waits", "ts_qk_norm_rope", "ts_qk_norm_rope_grad", "ts_qk_norm_rope_grad_workspace",
+           "ts_kv_cache_read", "ts_nvfp4_attention", "ts_nvfp4_attention_workspace", "ts_status_string", "ts_last_error_detail")
 
 TS_FLAG_PDL = 1
 TS_FLAG_PDL_EARLY_READ = 2
@@ -131,7 +144,7 @@ def library(path: str | None = None):
         lib.ts_rms_norm_sharded.argtypes = [ctypes.POINTER(vp), ctypes.c_int, i64, i64, i64, vp,
                                             ctypes.c_float, vp, i64, u32, vp]
         lib.ts_rms_norm_sharded.restype = ctypes.c_int
-        i32 = ctypes.c_int
+        i32, f32, cache = ctypes.c_int, ctypes.c_float, ctypes.POINTER(TsKvCache)
         for name, types in (
                 ("ts_nvfp4_quantize", [vp, i64, i64, i64, vp, vp, vp, vp, i32, u32, vp]),
                 ("ts_nvfp4_dequantize", [vp, vp, i32, i64, i64, vp, vp, vp, i64, u32, vp]),
@@ -141,11 +154,22 @@ def library(path: str | None = None):
                 ("ts_nvfp4_grouped_gemm", [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, u32, vp]),
                 ("ts_moe_combine", [vp, i64, i64, i64, vp, vp, i64, i64, vp, i64, u32, vp]),
                 ("ts_moe_combine_grad", [vp, i64, vp, i64, i64, i64, vp, vp, i64, i64, vp, i64, vp, u32, vp]),
-                ("ts_stalled_waits", [vp])):
+                ("ts_stalled_waits", [vp]),
+                ("ts_qk_norm_rope", [vp, i64, vp, i64, i64, i64, i64, i64, vp, vp, f32, vp, vp, i64, i64, i32, vp, i64, vp,
+                                     i64, vp, i64, cache, vp, u32, vp]),
+                ("ts_qk_norm_rope_grad", [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, vp, vp, f32, vp, vp, i64,
+                                          i64, i32, vp, i64, vp, i64, vp, vp, vp, u32, vp]),
+                ("ts_kv_cache_read", [cache, vp, i64, vp, i64, vp, i64, u32, vp]),
+                ("ts_nvfp4_attention", [vp, i64, i64, i64, vp, i64, i64, cache, vp, i64, vp, f32, i32, i64, vp, i64, vp, vp,
+                                        u32, vp])):
             getattr(lib, name).argtypes = types
             getattr(lib, name).restype = ctypes.c_int
         lib.ts_moe_rows.argtypes = [i64, i64, i64, i64]
         lib.ts_moe_rows.restype = i64
+        lib.ts_qk_norm_rope_grad_workspace.argtypes = [i64]
+        lib.ts_qk_norm_rope_grad_workspace.restype = i64
+        lib.ts_nvfp4_attention_workspace.argtypes = [i64, i64, i64, i64]
+        lib.ts_nvfp4_attention_workspace.restype = i64
         lib.ts_status_string.argtypes = [ctypes.c_int]
         lib.ts_status_string.restype = ctypes.c_char_p
         lib.ts_last_error_detail.argtypes = []

@@ -1,0 +1,110 @@
+// Internal interface between the checks of the attention entry points
+// (api_attention.cu) and their launchers.  Sizes are validated; positions, slots,
+// lengths and tables are not, and the kernels check them.  As in launch_nvfp4.h, no
+// input is read through the non-coherent path.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "launch.h"
+
+namespace tsfn {
+
+// The paged cache; offsets as documented for ts_kv_cache_t.
+struct CacheArgs {
+    uint8_t *pages;
+    int64_t slots;     // num_pages * page_size
+    int num_pages;
+    int page_size;
+    DivMagic div_page;  // division by page_size
+    int heads;
+    const float *k_scale;
+    const float *v_scale;
+};
+
+struct RopeArgs {
+    const uint16_t *q, *k, *v;  // v: with a cache only
+    int64_t ldq, ldk, ldv;
+    int64_t T;
+    int hq, hk, D;
+    int lanes_log2;  // lanes of a head's row: 8 columns each
+    const uint16_t *qw, *kw;  // both or neither
+    float eps;
+    const int32_t *pos;
+    const float *table;
+    int max_pos, rot;
+    bool pairs;
+    uint16_t *q_out, *k_out;  // k_out may be null with a cache
+    int64_t ldqo, ldko;
+    bool keep;  // with a cache
+    CacheArgs cache;
+    const int32_t *slots;
+    // a run is up to U heads of one token; runs of q, k and v of a token
+    int runs_q, runs_k, runs;
+    DivMagic div_runs;
+};
+
+struct RopeGradArgs {
+    const uint16_t *dy[2], *x[2];  // q, k
+    int64_t lddy[2], ldx[2];
+    int64_t T;
+    int heads[2];
+    int D, lanes_log2;
+    const uint16_t *w[2];
+    float eps;
+    const int32_t *pos;
+    const float *table;
+    int max_pos, rot;
+    bool pairs;
+    uint16_t *dx[2];
+    int64_t lddx[2];
+    float *dw[2];
+    float *partial;  // [blocks, 2, D]
+    int runs[2];     // runs of a token
+    DivMagic div_runs[2];
+};
+
+struct CacheReadArgs {
+    CacheArgs cache;
+    int D, lanes_log2;
+    const int32_t *slots;
+    int64_t T;
+    uint16_t *out[2];
+    int64_t ld[2];
+};
+
+struct AttnArgs {
+    const uint16_t *q;
+    int64_t ldq;
+    int64_t T;
+    int hq, group;  // query heads, and those of a key head
+    const int32_t *cu;  // may be null: one query a sequence
+    int B;
+    CacheArgs cache;
+    int D;
+    const int32_t *table;
+    int64_t max_pages;
+    const int32_t *lens;
+    float scale;
+    bool causal;
+    int window;  // 0: none
+    uint16_t *out;
+    int64_t ldo;
+    float *lse;
+    float *partial;
+};
+
+// Blocks of the gradient: three for each of 152 SMs.
+constexpr int kGradBlocks = 456;
+
+cudaError_t launch_rope(const RopeArgs &a, bool pdl, cudaStream_t stream);
+cudaError_t launch_rope_grad(const RopeGradArgs &a, bool pdl, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheReadArgs &a, bool pdl, cudaStream_t stream);
+
+// Attention of few rows (queries x heads of a key head) at a time, and of many.
+cudaError_t launch_attn_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t stream);
+int64_t attn_few_workspace(int64_t D);
+
+}  // namespace tsfn

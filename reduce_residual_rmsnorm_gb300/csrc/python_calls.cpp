@@ -1,14 +1,16 @@
-// The NVFP4 and expert-routing calls on PyTorch tensors: checks of types,
-// shapes and places, new outputs, the current stream, and one call of the C ABI
-// (include/ts_nvfp4_moe.h).
+// The NVFP4, expert-routing and attention calls on PyTorch tensors: checks of
+// types, shapes and places, new outputs, the current stream, and one call of the C
+// ABI (include/ts_nvfp4_moe.h, include/ts_attention.h).
 //
 // A decoded token's operator runs for 2 to 6 us on the GPU, and the same
 // marshalling through ctypes took 6 to 18 us of the calling thread on the
 // node's CPU; here it takes 2 to 5, of which letting go of the interpreter and
 // taking it back is 0.06 to 0.2.  The documented functions are those of
-// _nvfp4_moe.py, which pass their arguments on by position.
+// _nvfp4_moe.py and _attention.py, which pass their arguments on by position.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+
+#include <cmath>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
@@ -18,7 +20,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "ts_nvfp4_moe.h"
+#include "ts_attention.h"
 
 namespace {
 
@@ -190,6 +192,74 @@ public:
         *ld = t.stride(0);
         if (t.size(0) <= 1)  // a single row has no stride that matters; torch may report any
             *ld = (t.size(1) + 7) / 8 * 8;
+        return t;
+    }
+
+    bool truth(int i) const
+    {
+        const int v = PyObject_IsTrue(args_[i]);
+        if (v < 0)
+            throw Raised{};
+        return v != 0;
+    }
+
+    double number(int i) const
+    {
+        const double v = PyFloat_AsDouble(args_[i]);
+        if (v == -1.0 && PyErr_Occurred())
+            throw Raised{};
+        return v;
+    }
+
+    // Heads [T, heads, D] whose rows are contiguous within a token; the stride of a token.
+    const at::Tensor &heads(int i, const char *name, int64_t *ld)
+    {
+        const at::Tensor &t = tensor(i, name, kBF16);
+        if (t.dim() != 3 || (t.size(2) > 1 && t.stride(2) != 1) || (t.size(1) > 1 && t.stride(1) != t.size(2)))
+            raise(PyExc_ValueError, "%s must be [T, heads, D] with contiguous heads", name);
+        *ld = t.size(0) <= 1 ? (t.size(1) * t.size(2) + 7) / 8 * 8 : t.stride(0);
+        return t;
+    }
+
+    at::Tensor heads_output(int i, const char *name, const at::Tensor &like, int64_t *ld)
+    {
+        const Dims want = dims(like.size(0), like.size(1), like.size(2));
+        if (none(i)) {
+            *ld = like.size(1) * like.size(2);
+            return fresh(want, kBF16, like);
+        }
+        const at::Tensor &t = heads(i, name, ld);
+        shape(t, name, want);
+        return t;
+    }
+
+    // The cache of three arguments (pages, k_scale, v_scale).
+    ts_kv_cache_t cache(int i)
+    {
+        const at::Tensor &p = flat(i, "cache.pages", kU8);
+        if (p.dim() != 4 || p.size(3) % 18 != 0)
+            raise(PyExc_ValueError, "cache.pages must be [pages, heads, page_size / 16, 18 * head_dim]");
+        if (p.size(2) > (1 << 20))
+            raise(PyExc_ValueError, "cache.pages: page_size out of range");
+        ts_kv_cache_t c{};
+        c.pages = p.data_ptr();
+        c.num_pages = p.size(0);
+        c.heads = p.size(1);
+        c.page_size = 16 * p.size(2);
+        c.head_dim = p.size(3) / 18;
+        c.k_scale = one(i + 1, "cache.k_scale");
+        c.v_scale = one(i + 2, "cache.v_scale");
+        return c;
+    }
+
+    // A workspace of at least `bytes`, given or new.
+    at::Tensor workspace(int i, int64_t bytes, const at::Tensor &like)
+    {
+        if (none(i))
+            return fresh(dims(bytes), kU8, like);
+        const at::Tensor &t = on_gpu(i, "workspace", kU8);
+        if (t.numel() < bytes)
+            raise(PyExc_ValueError, "workspace must hold %lld bytes, got %lld", (long long)bytes, (long long)t.numel());
         return t;
     }
 
@@ -530,6 +600,162 @@ PyObject *combine_grad(PyObject *const *args, Py_ssize_t n)
     return Py_BuildValue("(NN)", THPVariable_Wrap(dy), THPVariable_Wrap(dw));
 }
 
+// q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, v, pages, k_scale, v_scale, slots, q_out, k_out, pdl, stream
+PyObject *qk_norm_rope(PyObject *const *args, Py_ssize_t n)
+{
+    Call c(args, n, 17);
+    int64_t ldq, ldk, ldv = 0, ldqo, ldko = 0;
+    const at::Tensor &q = c.heads(0, "q", &ldq), &k = c.heads(1, "k", &ldk);
+    const int64_t T = q.size(0), hq = q.size(1), hk = k.size(1), D = q.size(2);
+    Call::shape(k, "k", dims(T, hk, D));
+    const void *qw = c.none(2) ? nullptr : ptr(c.flat(2, "q_weight", kBF16, dims(D)));
+    const void *kw = c.none(3) ? nullptr : ptr(c.flat(3, "k_weight", kBF16, dims(D)));
+    const at::Tensor &pos = c.flat(4, "positions", kI32, dims(T)), &table = c.flat(5, "cos_sin", kF32);
+    if (table.dim() != 2)
+        raise(PyExc_ValueError, "cos_sin must be [max_pos, rot]");
+    const float eps = (float)c.number(6);
+    const bool pairs = c.truth(7), kept = !c.none(9);
+    ts_kv_cache_t cache{};
+    const void *v = nullptr;
+    const int32_t *slots = nullptr;
+    if (kept) {
+        cache = c.cache(9);
+        const at::Tensor &vt = c.heads(8, "v", &ldv);
+        Call::shape(vt, "v", dims(T, hk, D));
+        v = ptr(vt);
+        slots = ptr<int32_t>(c.flat(12, "slots", kI32, dims(T)));
+    } else if (!c.none(8) || !c.none(12)) {
+        raise(PyExc_ValueError, "v and slots need a cache");
+    }
+    const at::Tensor qo = c.heads_output(13, "q_out", q, &ldqo);
+    at::Tensor ko;
+    if (!kept || !c.none(14))
+        ko = c.heads_output(14, "k_out", k, &ldko);
+    void *const qp = ptr(qo), *const kp = ko.defined() ? ptr(ko) : nullptr;
+    c.run([&](uint32_t flags, void *stream) {
+        return ts_qk_norm_rope(ptr(q), ldq, ptr(k), ldk, T, hq, hk, D, qw, kw, eps, ptr<int32_t>(pos), ptr<float>(table),
+                               table.size(0), table.size(1), pairs, qp, ldqo, kp, ldko, v, ldv, kept ? &cache : nullptr,
+                               slots, flags, stream);
+    });
+    if (!ko.defined())
+        return Py_BuildValue("(NO)", THPVariable_Wrap(qo), Py_None);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(qo), THPVariable_Wrap(ko));
+}
+
+// dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, dq, dk, dq_weight, dk_weight, workspace, pdl, stream
+PyObject *qk_norm_rope_grad(PyObject *const *args, Py_ssize_t n)
+{
+    Call c(args, n, 17);
+    int64_t ldqo, ldko, ldq, ldk, lddq, lddk;
+    const at::Tensor &dqo = c.heads(0, "dq_out", &ldqo), &dko = c.heads(1, "dk_out", &ldko);
+    const at::Tensor &q = c.heads(2, "q", &ldq), &k = c.heads(3, "k", &ldk);
+    const int64_t T = q.size(0), hq = q.size(1), hk = k.size(1), D = q.size(2);
+    Call::shape(k, "k", dims(T, hk, D));
+    Call::shape(dqo, "dq_out", dims(T, hq, D));
+    Call::shape(dko, "dk_out", dims(T, hk, D));
+    const bool norm = !c.none(4);
+    const void *qw = c.none(4) ? nullptr : ptr(c.flat(4, "q_weight", kBF16, dims(D)));
+    const void *kw = c.none(5) ? nullptr : ptr(c.flat(5, "k_weight", kBF16, dims(D)));
+    const at::Tensor &pos = c.flat(6, "positions", kI32, dims(T)), &table = c.flat(7, "cos_sin", kF32);
+    if (table.dim() != 2)
+        raise(PyExc_ValueError, "cos_sin must be [max_pos, rot]");
+    const float eps = (float)c.number(8);
+    const bool pairs = c.truth(9);
+    const at::Tensor dq = c.heads_output(10, "dq", q, &lddq), dk = c.heads_output(11, "dk", k, &lddk);
+    at::Tensor dqw, dkw, space;
+    if (norm) {
+        const int64_t bytes = ts_qk_norm_rope_grad_workspace(D);
+        if (bytes < 0)
+            raise(PyExc_ValueError, "head_dim %lld out of range", (long long)D);
+        dqw = c.output(12, "dq_weight", kF32, dims(D), q);
+        dkw = c.output(13, "dk_weight", kF32, dims(D), q);
+        space = c.workspace(14, bytes, q);
+    } else if (!c.none(12) || !c.none(13)) {
+        raise(PyExc_ValueError, "gradients of weights that are not given");
+    }
+    float *const wq = norm ? ptr<float>(dqw) : nullptr, *const wk = norm ? ptr<float>(dkw) : nullptr;
+    void *const sp = norm ? ptr(space) : nullptr;
+    c.run([&](uint32_t flags, void *stream) {
+        return ts_qk_norm_rope_grad(ptr(dqo), ldqo, ptr(dko), ldko, ptr(q), ldq, ptr(k), ldk, T, hq, hk, D, qw, kw, eps,
+                                    ptr<int32_t>(pos), ptr<float>(table), table.size(0), table.size(1), pairs, ptr(dq), lddq,
+                                    ptr(dk), lddk, wq, wk, sp, flags, stream);
+    });
+    if (!norm)
+        return Py_BuildValue("(NNOO)", THPVariable_Wrap(dq), THPVariable_Wrap(dk), Py_None, Py_None);
+    return Py_BuildValue("(NNNN)", THPVariable_Wrap(dq), THPVariable_Wrap(dk), THPVariable_Wrap(dqw), THPVariable_Wrap(dkw));
+}
+
+// pages, k_scale, v_scale, slots, k_out, v_out, pdl, stream
+PyObject *kv_cache_read(PyObject *const *args, Py_ssize_t n)
+{
+    Call c(args, n, 8);
+    const ts_kv_cache_t cache = c.cache(0);
+    const at::Tensor &slots = c.flat(3, "slots", kI32);
+    if (slots.dim() != 1)
+        raise(PyExc_ValueError, "slots must be [T]");
+    const int64_t T = slots.size(0);
+    int64_t ld[2];
+    at::Tensor out[2];
+    for (int i = 0; i < 2; ++i) {
+        if (c.none(4 + i)) {
+            out[i] = c.fresh(dims(T, cache.heads, cache.head_dim), kBF16, slots);
+            ld[i] = cache.heads * cache.head_dim;
+        } else {
+            out[i] = c.heads(4 + i, i == 0 ? "k_out" : "v_out", &ld[i]);
+            Call::shape(out[i], i == 0 ? "k_out" : "v_out", dims(T, cache.heads, cache.head_dim));
+        }
+    }
+    c.run([&](uint32_t flags, void *stream) {
+        return ts_kv_cache_read(&cache, ptr<int32_t>(slots), T, ptr(out[0]), ld[0], ptr(out[1]), ld[1], flags, stream);
+    });
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out[0]), THPVariable_Wrap(out[1]));
+}
+
+// q, pages, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, scale, causal, window, out, lse, return_lse, workspace, pdl, stream
+PyObject *attention(PyObject *const *args, Py_ssize_t n)
+{
+    Call c(args, n, 17);
+    int64_t ldq, ldo;
+    const at::Tensor &q = c.heads(0, "q", &ldq);
+    if (!q.is_cuda())
+        raise(PyExc_TypeError, "q must be a CUDA tensor");
+    const int64_t T = q.size(0), hq = q.size(1), D = q.size(2);
+    c.on_gpu(1, "cache.pages", kU8);
+    const ts_kv_cache_t cache = c.cache(1);
+    if (cache.head_dim != D)
+        raise(PyExc_ValueError, "q has head_dim %lld, the cache %lld", (long long)D, (long long)cache.head_dim);
+    const at::Tensor &table = c.flat(4, "block_table", kI32), &lens = c.flat(5, "kv_lens", kI32);
+    if (lens.dim() != 1 || table.dim() != 2 || table.size(0) != lens.size(0))
+        raise(PyExc_ValueError, "kv_lens must be [B] and block_table [B, max_pages]");
+    const int64_t B = lens.size(0);
+    const int32_t *cu = c.optional_i32(6, "cu_q", dims(B + 1));
+    if (cu == nullptr && T != B)
+        raise(PyExc_ValueError, "%lld queries of %lld sequences need cu_q", (long long)T, (long long)B);
+    const int64_t max_q = !c.none(7) ? c.integer(7) : (cu == nullptr || T == 0 ? 1 : T);
+    const float scale = c.none(8) ? (float)(1.0 / std::sqrt((double)(D > 0 ? D : 1))) : (float)c.number(8);
+    const bool causal = c.truth(9);
+    const int64_t window = c.integer(10);
+    const int64_t bytes = ts_nvfp4_attention_workspace(hq, cache.heads, D, max_q);
+    const at::Tensor out = c.heads_output(11, "out", q, &ldo);
+    if (!out.is_cuda())
+        raise(PyExc_TypeError, "out must be a CUDA tensor");
+    at::Tensor lse;
+    if (!c.none(12) || c.truth(13)) {
+        lse = c.output(12, "lse", kF32, dims(T, hq), q);
+        if (!lse.is_cuda())
+            raise(PyExc_TypeError, "lse must be a CUDA tensor");
+    }
+    const at::Tensor space = c.workspace(14, bytes < 0 ? 0 : bytes, q);  // (the call refuses the sizes)
+    float *const lp = lse.defined() ? ptr<float>(lse) : nullptr;
+    c.run([&](uint32_t flags, void *stream) {
+        return ts_nvfp4_attention(ptr(q), ldq, T, hq, cu, B, max_q, &cache, ptr<int32_t>(table), table.size(1),
+                                  ptr<int32_t>(lens), scale, causal, window, ptr(out), ldo, lp, ptr(space), flags, stream);
+    });
+    if (!c.truth(13))
+        return THPVariable_Wrap(out);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));
+}
+
 // No C++ exception leaves a call.
 template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
@@ -555,6 +781,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 #define TS_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {TS_METHOD(quantize), TS_METHOD(dequantize),   TS_METHOD(gemm),    TS_METHOD(sort),
                          TS_METHOD(dispatch), TS_METHOD(grouped_gemm), TS_METHOD(combine), TS_METHOD(combine_grad),
+                         TS_METHOD(qk_norm_rope), TS_METHOD(qk_norm_rope_grad), TS_METHOD(kv_cache_read), TS_METHOD(attention),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_python_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,448 @@
+// Per-head RMSNorm of queries and keys and rotation by position in one pass, with
+// the keys and values written to the 4-bit cache; its gradient; the cache read back.
+//
+//   n = (x rsqrt(mean x^2 + eps)) w,   y = n turned by the position's angles
+//
+// Bound by memory.  A head's row of D elements lies on D/8 neighbouring lanes, 16
+// bytes each (a power of two of lanes, those behind D/8 idle), so the sum of squares
+// is a butterfly of a few steps and a lane's partner in the rotation is at a fixed
+// distance.  The partner's raw bf16 are exchanged, not its normed fp32: half the
+// shuffles, and each lane norms both, with the same bits.  A group of lanes takes a
+// run of up to U heads of one token: their loads are issued together, and the
+// position's cosines and sines and the weights are read once for them.
+#include "device_util.cuh"
+#include "launch_attention.h"
+
+namespace tsfn {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Coherent loads of what is used again (weights, tables, positions).
+__device__ __forceinline__ uint4 ld_again(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void ld_angles(const float *p, int n4, float (&f)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (i < n4) {
+            const uint4 v = ld_again(p + 4 * i);
+            f[4 * i] = __uint_as_float(v.x);
+            f[4 * i + 1] = __uint_as_float(v.y);
+            f[4 * i + 2] = __uint_as_float(v.z);
+            f[4 * i + 3] = __uint_as_float(v.w);
+        }
+}
+
+// Sum over the lanes of a head's row, the same bits on each of them.
+__device__ __forceinline__ float group_sum(float v, int lanes)
+{
+    for (int o = lanes >> 1; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// What a lane does in the rotation: chunk c of 8 columns of a row.
+struct Turn {
+    bool in;        // the chunk is rotated
+    bool first;     // halves: the pairs' first elements
+    int partner;    // halves: lane with the pairs' other elements
+    int angle;      // index of the chunk's first cosine
+};
+
+__device__ __forceinline__ Turn turn_of(int c, int lane, int rot, bool pairs)
+{
+    const int half = rot >> 4;  // chunks of half of the rotated columns
+    Turn t;
+    t.in = c < 2 * half;
+    t.first = c < half;
+    t.partner = !t.in || pairs ? lane : (t.first ? lane + half : lane - half);
+    t.angle = pairs ? 4 * c : 8 * (t.first ? c : c - half);
+    return t;
+}
+
+// y = x turned by the angles, forwards (s = 1) or back (s = -1).  PAIRS: the chunk's
+// own neighbours; else `other` holds the partner chunk.
+template <bool PAIRS>
+__device__ __forceinline__ void rotate(float (&x)[8], const float (&other)[8], const float (&cs)[8], const float (&sn)[8],
+                                       const Turn &t, float s)
+{
+    if (!t.in)
+        return;
+    if (PAIRS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1], k = s * sn[i];
+            x[2 * i] = __fmaf_rn(a, cs[i], -__fmul_rn(b, k));
+            x[2 * i + 1] = __fmaf_rn(b, cs[i], __fmul_rn(a, k));
+        }
+    } else {
+        const float k = t.first ? -s : s;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = __fmaf_rn(x[e], cs[e], k * __fmul_rn(other[e], sn[e]));
+    }
+}
+
+__device__ __forceinline__ uint4 shuffle4(const uint4 &v, int from)
+{
+    return make_uint4(__shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from),
+                      __shfl_sync(0xffffffffu, v.z, from), __shfl_sync(0xffffffffu, v.w, from));
+}
+
+// Where the codes of K and V and the scale factors of a slot's head begin.
+__device__ __forceinline__ uint8_t *cache_tile(const CacheArgs &c, int D, int64_t slot, int h, int *in_tile)
+{
+    const uint32_t page = div_by((uint32_t)slot, c.div_page);
+    const int off = (int)((uint32_t)slot - page * (uint32_t)c.page_size);
+    *in_tile = off & 15;
+    const int64_t tile = ((int64_t)page * c.heads + h) * (c.page_size >> 4) + (off >> 4);
+    return c.pages + tile * 18 * D;
+}
+
+// A row's chunk of 8 bf16 to NVFP4 (the arithmetic of ts_nvfp4_quantize), the two lanes
+// of a block together: codes by each, the scale factor by the first.
+__device__ __forceinline__ void put_chunk(const uint4 &v, float g, bool live, uint8_t *codes, uint8_t *sf, int c)
+{
+    float n[8];
+    unpack8(v, n);
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        amax = fmaxf(amax, fabsf(n[e]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const uint32_t s = cvt_e4m3(__fmul_rn(g, div_const_rn(amax, 6.0f, kRcp6)));
+    const float d = e4m3_value(s);
+    uint32_t q = 0;
+    if (d != 0.0f) {
+        const float es = __fdiv_rn(g, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            n[e] = __fmul_rn(n[e], es);
+        q = cvt_e2m1x8(n);
+    }
+    if (live) {
+        *reinterpret_cast<uint32_t *>(codes + 4 * c) = q;
+        if ((c & 1) == 0)
+            sf[c >> 1] = (uint8_t)s;
+    }
+}
+
+// U: heads of a run.  1 where the call is short, so that it spreads over the SMs; the
+// bits do not depend on it.
+template <int U, bool PAIRS, bool CACHE>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a)
+{
+    const int lanes = 1 << a.lanes_log2;
+    const int lane = threadIdx.x & 31, c = lane & (lanes - 1);
+    const int64_t id = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> a.lanes_log2;
+    // (below 2^31: the calls' limit on T * heads)
+    const int64_t t = div_by((uint32_t)id, a.div_runs);
+    const int run = (int)(id - t * a.runs);
+    // queries, keys, values
+    const int kind = run < a.runs_q ? 0 : (run < a.runs_q + a.runs_k ? 1 : 2);
+    const int h0 = (kind == 0 ? run : (kind == 1 ? run - a.runs_q : run - a.runs_q - a.runs_k)) * U;
+    const int heads = kind == 0 ? a.hq : a.hk;
+    const bool in_row = c < (a.D >> 3);
+    pdl_wait();
+
+    bool live = t < a.T;
+    const int32_t pos = live ? a.pos[t] : -1;
+    const uint16_t *src = kind == 0 ? a.q + t * a.ldq : (kind == 1 ? a.k + t * a.ldk : a.v + t * a.ldv);
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (live && in_row && h0 + u < heads)
+            x[u] = ld_stream(src + (int64_t)(h0 + u) * a.D + c * 8);
+    }
+    live = live && pos >= 0 && pos < a.max_pos;
+    int64_t slot = -1;
+    float g = 0.0f;
+    if (CACHE && kind != 0 && live) {
+        slot = a.slots[t];
+        if (slot >= a.cache.slots)
+            slot = -1;
+        g = kind == 1 ? *a.cache.k_scale : *a.cache.v_scale;
+    }
+    const bool turned = kind != 2;
+    Turn turn = turn_of(c, lane, a.rot, PAIRS);
+    turn.in = turn.in && turned;
+    float cs[8] = {}, sn[8] = {};
+    if (live && turn.in) {
+        const float *p = a.table + (int64_t)pos * a.rot + turn.angle;
+        ld_angles(p, PAIRS ? 1 : 2, cs);
+        ld_angles(p + (a.rot >> 1), PAIRS ? 1 : 2, sn);
+    }
+    const uint16_t *w = kind == 0 ? a.qw : a.kw;
+    const bool norm = turned && w != nullptr;
+    float wf[8], wp[8];
+    if (norm && in_row) {
+        unpack8(ld_again(w + c * 8), wf);
+        unpack8(ld_again(w + (c + turn.partner - lane) * 8), wp);
+    }
+    pdl_launch_dependents();
+
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool on = live && in_row && h0 + u < heads;
+        const float r = rsqrtf(__fadd_rn(__fdiv_rn(group_sum(sumsq_bf16x8(x[u], 0.0f), lanes), (float)a.D), a.eps));
+        float f[8], o[8] = {};
+        unpack8(x[u], f);
+        if (!PAIRS)
+            unpack8(shuffle4(x[u], turn.partner), o);
+        if (norm) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[e] = __fmul_rn(__fmul_rn(f[e], r), wf[e]);
+                o[e] = __fmul_rn(__fmul_rn(o[e], r), wp[e]);
+            }
+        }
+        rotate<PAIRS>(f, o, cs, sn, turn, 1.0f);
+        const uint4 y = turned ? pack8(f) : x[u];
+        if (on && turned) {
+            uint16_t *dst = kind == 0 ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko;
+            if (kind == 0 || a.k_out != nullptr)
+                st_v4(dst + (int64_t)(h0 + u) * a.D + c * 8, y);
+        }
+        if (CACHE) {
+            int in_tile = 0;
+            const bool keep = on && slot >= 0;
+            uint8_t *tile = keep ? cache_tile(a.cache, a.D, slot, h0 + u, &in_tile) : nullptr;
+            const int second = kind == 2 ? 1 : 0;
+            put_chunk(y, g, keep, tile + second * 8 * a.D + in_tile * (a.D >> 1),
+                      tile + (16 + second) * a.D + in_tile * (a.D >> 4), c);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------
+
+// dx as above; the weights' gradient is summed by each lane over its runs, then over
+// the groups of a block in order, and over the blocks by grad_sum_kernel.
+template <int U, bool PAIRS>
+__global__ void __launch_bounds__(kThreads) rope_grad_kernel(const __grid_constant__ RopeGradArgs a)
+{
+    extern __shared__ float sums[];  // [groups of lanes][lanes * 8]
+    const int lanes = 1 << a.lanes_log2;
+    const int lane = threadIdx.x & 31, c = lane & (lanes - 1);
+    const int groups = kThreads >> a.lanes_log2, group = threadIdx.x >> a.lanes_log2;
+    const bool in_row = c < (a.D >> 3);
+    const Turn turn = turn_of(c, lane, a.rot, PAIRS);
+    pdl_wait();
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        const uint16_t *w = a.w[kind];
+        float wf[8];
+        if (w != nullptr && in_row)
+            unpack8(ld_again(w + c * 8), wf);
+        float acc[8] = {};
+        const int64_t all = a.T * a.runs[kind];
+        // (a warp's lanes stay together: the loop's bound is that of its first group)
+        const int64_t per = (int64_t)gridDim.x * groups;
+        const int first = ((threadIdx.x & ~31) >> a.lanes_log2);
+        for (int64_t base = (int64_t)blockIdx.x * groups + first; base < all; base += per) {
+            const int64_t id = base + (group - first);
+            bool live = id < all;
+            const int64_t t = live ? div_by((uint32_t)id, a.div_runs[kind]) : 0;
+            const int h0 = (int)(id - t * a.runs[kind]) * U;
+            const int32_t pos = live ? a.pos[t] : -1;
+            uint4 x[U], d[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                x[u] = d[u] = make_uint4(0, 0, 0, 0);
+                if (live && in_row && h0 + u < a.heads[kind]) {
+                    x[u] = ld_stream(a.x[kind] + t * a.ldx[kind] + (int64_t)(h0 + u) * a.D + c * 8);
+                    d[u] = ld_stream(a.dy[kind] + t * a.lddy[kind] + (int64_t)(h0 + u) * a.D + c * 8);
+                }
+            }
+            live = live && pos >= 0 && pos < a.max_pos;
+            float cs[8] = {}, sn[8] = {};
+            if (live && turn.in) {
+                const float *p = a.table + (int64_t)pos * a.rot + turn.angle;
+                ld_angles(p, PAIRS ? 1 : 2, cs);
+                ld_angles(p + (a.rot >> 1), PAIRS ? 1 : 2, sn);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool on = live && in_row && h0 + u < a.heads[kind];
+                float f[8], o[8] = {}, xf[8];
+                unpack8(d[u], f);
+                if (!PAIRS)
+                    unpack8(shuffle4(d[u], turn.partner), o);
+                rotate<PAIRS>(f, o, cs, sn, turn, -1.0f);
+                if (w != nullptr) {
+                    unpack8(x[u], xf);
+                    const float inv_d = 1.0f / (float)a.D;
+                    const float r = rsqrtf(__fadd_rn(group_sum(sumsq_bf16x8(x[u], 0.0f), lanes) * inv_d, a.eps));
+                    float dot = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float xr = xf[e] * r;
+                        if (on)
+                            acc[e] = __fmaf_rn(f[e], xr, acc[e]);
+                        f[e] = on ? f[e] * wf[e] : 0.0f;
+                        xf[e] = xr;
+                        dot = __fmaf_rn(f[e], xr, dot);
+                    }
+                    dot = group_sum(dot, lanes) * inv_d;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        f[e] = r * __fmaf_rn(-xf[e], dot, f[e]);
+                }
+                if (on)
+                    st_v4(a.dx[kind] + t * a.lddx[kind] + (int64_t)(h0 + u) * a.D + c * 8, pack8(f));
+            }
+        }
+        if (w != nullptr) {
+            if (kind == 1)
+                __syncthreads();  // the queries' sums have been read
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sums[group * lanes * 8 + c * 8 + e] = acc[e];
+            __syncthreads();
+            for (int j = threadIdx.x; j < a.D; j += kThreads) {
+                float s = 0.0f;
+                for (int i = 0; i < groups; ++i)
+                    s += sums[i * lanes * 8 + j];
+                a.partial[((int64_t)blockIdx.x * 2 + kind) * a.D + j] = s;
+            }
+        }
+    }
+    pdl_launch_dependents();
+}
+
+// dw[kind][j] = the blocks' sums in order: 8 threads a column take every eighth block.
+__global__ void __launch_bounds__(256) grad_sum_kernel(const float *partial, int blocks, int D, float *dqw, float *dkw)
+{
+    __shared__ float sums[8][33];
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
+    float s = 0.0f;
+    if (col < 2 * D) {
+#pragma unroll 8
+        for (int i = part; i < blocks; i += 8)
+            s += partial[(int64_t)i * 2 * D + col];
+    }
+    sums[part][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (part == 0 && col < 2 * D) {
+        for (int i = 1; i < 8; ++i)
+            s += sums[i][threadIdx.x];
+        (col < D ? dqw : dkw)[col < D ? col : col - D] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// read back
+// ---------------------------------------------------------------------------
+
+// A group of lanes per token and head: K, then V.
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheReadArgs a, DivMagic div_heads)
+{
+    const int lanes = 1 << a.lanes_log2;
+    const int c = threadIdx.x & (lanes - 1);
+    const int64_t id = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> a.lanes_log2;
+    const int64_t t = div_by((uint32_t)id, div_heads);
+    const int h = (int)(id - t * a.cache.heads);
+    pdl_wait();
+    if (t < a.T && c < (a.D >> 3)) {
+        const int64_t slot = a.slots[t];
+        if (slot >= 0 && slot < a.cache.slots) {
+            int in_tile;
+            const uint8_t *tile = cache_tile(a.cache, a.D, slot, h, &in_tile);
+            uint32_t codes[2], sf[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                codes[i] = *reinterpret_cast<const volatile uint32_t *>(tile + i * 8 * a.D + in_tile * (a.D >> 1) + 4 * c);
+                sf[i] = *reinterpret_cast<const volatile uint8_t *>(tile + (16 + i) * a.D + in_tile * (a.D >> 4) + (c >> 1));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (a.out[i] == nullptr)
+                    continue;
+                const float s = __fdiv_rn(e4m3_value(sf[i]), i == 0 ? *a.cache.k_scale : *a.cache.v_scale);
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t q = (codes[i] >> (4 * e)) & 15;
+                    // E2M1: 0.5 for an exponent of 0, else (2 + m) 2^(e - 2); -0 keeps its sign
+                    const uint32_t m = q & 7;
+                    const float v = m < 2 ? 0.5f * (float)m : __uint_as_float(((126 + (m >> 1)) << 23) | ((m & 1) << 22));
+                    f[e] = __fmul_rn(q & 8 ? -v : v, s);
+                }
+                st_v4(a.out[i] + t * a.ld[i] + (int64_t)h * a.D + c * 8, pack8(f));
+            }
+        }
+    }
+    pdl_launch_dependents();
+}
+
+template <int U, bool PAIRS>
+cudaError_t launch_rope_u(RopeArgs a, bool pdl, cudaStream_t stream)
+{
+    a.runs_q = (a.hq + U - 1) / U;
+    a.runs_k = (a.hk + U - 1) / U;
+    a.runs = a.runs_q + (a.keep ? 2 : 1) * a.runs_k;
+    a.div_runs = div_magic((uint32_t)a.runs);
+    const int64_t blocks = (((a.T * a.runs) << a.lanes_log2) + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    return a.keep ? launch_kernel(rope_kernel<U, PAIRS, true>, grid, block, 0, stream, pdl, a)
+                                    : launch_kernel(rope_kernel<U, PAIRS, false>, grid, block, 0, stream, pdl, a);
+}
+
+template <int U, bool PAIRS>
+cudaError_t launch_grad_u(RopeGradArgs a, bool pdl, cudaStream_t stream)
+{
+    int64_t most = 0;
+    for (int i = 0; i < 2; ++i) {
+        a.runs[i] = (a.heads[i] + U - 1) / U;
+        a.div_runs[i] = div_magic((uint32_t)a.runs[i]);
+        most = a.runs[i] > most ? a.runs[i] : most;
+    }
+    const int groups = kThreads >> a.lanes_log2;
+    const int64_t want = (a.T * most + groups - 1) / groups;
+    const int blocks = (int)(want < 1 ? 1 : (want > kGradBlocks ? kGradBlocks : want));
+    cudaError_t err = launch_kernel(rope_grad_kernel<U, PAIRS>, dim3((unsigned)blocks), dim3(kThreads), kThreads * 8 * sizeof(float),
+                                    stream, pdl, a);
+    if (err != cudaSuccess || a.w[0] == nullptr)
+        return err;
+    return launch_kernel(grad_sum_kernel, dim3((unsigned)((2 * a.D + 31) / 32)), dim3(256), 0, stream, true,
+                         (const float *)a.partial, blocks, a.D, a.dw[0], a.dw[1]);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs &a, bool pdl, cudaStream_t stream)
+{
+    const bool few = ((a.T * (a.hq + 2 * a.hk)) << a.lanes_log2) <= 152 * 1024;
+    if (a.pairs)
+        return few ? launch_rope_u<1, true>(a, pdl, stream) : launch_rope_u<4, true>(a, pdl, stream);
+    return few ? launch_rope_u<1, false>(a, pdl, stream) : launch_rope_u<4, false>(a, pdl, stream);
+}
+
+cudaError_t launch_rope_grad(const RopeGradArgs &a, bool pdl, cudaStream_t stream)
+{
+    const bool few = ((a.T * (a.heads[0] + a.heads[1])) << a.lanes_log2) <= 152 * 1024;
+    if (a.pairs)
+        return few ? launch_grad_u<1, true>(a, pdl, stream) : launch_grad_u<2, true>(a, pdl, stream);
+    return few ? launch_grad_u<1, false>(a, pdl, stream) : launch_grad_u<2, false>(a, pdl, stream);
+}
+
+cudaError_t launch_cache_read(const CacheReadArgs &a, bool pdl, cudaStream_t stream)
+{
+    const int64_t blocks = (((a.T * a.cache.heads) << a.lanes_log2) + kThreads - 1) / kThreads;
+    return launch_kernel(cache_read_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, pdl, a,
+                         div_magic((uint32_t)a.cache.heads));
+}
+
+}  // namespace tsfn

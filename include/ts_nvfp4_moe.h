@@ -203,7 +203,7 @@ TS_API int ts_moe_combine_grad(const void *dout, int64_t ldd, const void *y, int
                                int64_t H, const int32_t *row_of, const float *weights, int64_t T, int64_t k,
                                void *dy, int64_t lddy, float *dweights, uint32_t flags, void *stream);
 
-/* Number of waits inside the product kernels of the current device that ran
+/* Number of waits inside the product and attention kernels of the current device that ran
  * into their time limit since the library was loaded, written to *count (the
  * outputs of such a call are not valid).  It waits for the device. */
 TS_API int ts_stalled_waits(uint32_t *count);

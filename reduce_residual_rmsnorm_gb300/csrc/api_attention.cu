@@ -388,13 +388,22 @@ int check_attention(int64_t q_heads, int64_t heads, int64_t D, int64_t max_q)
     return check_range("max_q", max_q, 1, kMaxRows);
 }
 
+// Which kernel: rows of a sequence that share a key head.
+constexpr int64_t kFewRows = 16;
+
+int64_t attention_workspace(int64_t rows, int64_t D)
+{
+    const int64_t few = attn_few_workspace(D), prompt = rows <= kFewRows ? 0 : attn_prompt_workspace(D);
+    return few > prompt ? few : prompt;
+}
+
 }  // namespace
 
 extern "C" int64_t ts_nvfp4_attention_workspace(int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_q)
 {
     if (check_attention(q_heads, heads, head_dim, max_q) != TS_OK)
         return -1;
-    return attn_few_workspace(head_dim);
+    return attention_workspace(max_q * (q_heads / heads), head_dim);
 }
 
 extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t q_heads, const int32_t *cu_q, int64_t B,
@@ -433,7 +442,7 @@ extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t
                       flat(kv_lens, B * 4, 4, "kv_lens"),
                       matrix(out, T, q_heads * D, ldo, "out", true),
                       flat(lse, T * q_heads * 4, 4, "lse", true, true),
-                      flat(workspace, attn_few_workspace(D), 16, "workspace", true)};
+                      flat(workspace, attention_workspace(rows, D), 16, "workspace", true)};
     const bool empty = T == 0 || B == 0;
     TS_TRY(check_rows_of(b, empty));
     if (empty)
@@ -458,5 +467,7 @@ extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t
     a.ldo = ldo;
     a.lse = lse;
     a.partial = static_cast<float *>(workspace);
-    return launched(launch_attn_few(a, rows, (flags & TS_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream)));
+    const bool pdl = (flags & TS_FLAG_PDL) != 0;
+    const cudaStream_t on = static_cast<cudaStream_t>(stream);
+    return launched(rows <= kFewRows ? launch_attn_few(a, rows, pdl, on) : launch_attn_prompt(a, pdl, on));
 }

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "api_util.h"
+#include "launch_attention.h"
 #include "launch_nvfp4.h"
 #include "ts_nvfp4_moe.h"
 
@@ -448,5 +449,10 @@ extern "C" int ts_stalled_waits(uint32_t *count)
 {
     if (count == nullptr)
         return fail(TS_ERR_NULL, "count is NULL");
-    return launched(read_stalled_waits(count));
+    uint32_t products = 0, attention = 0;
+    cudaError_t err = read_stalled_waits(&products);
+    if (err == cudaSuccess)
+        err = read_attn_stalled_waits(&attention);
+    *count = products + attention;
+    return launched(err);
 }

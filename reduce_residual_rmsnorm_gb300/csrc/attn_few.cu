@@ -25,6 +25,7 @@
 // sequences of any lengths keep every block busy.  A unit inside a share is written
 // at once; of a unit over several, each block leaves its part in the workspace and
 // attn_join_kernel joins them in order.
+#include "attn_util.cuh"
 #include "device_util.cuh"
 #include "launch_attention.h"
 
@@ -39,58 +40,6 @@ constexpr int blocks_per_sm(int nt) { return nt == 1 ? 2 : 1; }
 constexpr int blocks_of(int nt) { return 152 * blocks_per_sm(nt); }
 constexpr int stages_of(int nt) { return nt == 1 ? 4 : 6; }
 constexpr int kShare = 8;     // tiles of a share, at least
-constexpr float kSlack = 8.0f;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// What a block leaves for a unit that it began and others go on with.
-struct Record {
-    int32_t last;   // the last block of the unit, or -1: nothing to join
-    int32_t q0;     // the sequence's first query
-    int32_t head;   // key head
-    int32_t rows;   // rows of the unit
-    int64_t row0;   // the unit's first row among the sequence's (query, head) pairs
-};
-
-__host__ __device__ constexpr int64_t slot_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
-
-struct Seq {
-    int64_t q0;
-    int64_t n;     // queries
-    int len;       // keys
-    int first;     // first tile
-    int tiles;     // at least 1
-    int64_t parts; // row tiles
-};
-
-template <int NR>
-__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
-{
-    Seq s;
-    if (a.cu != nullptr) {
-        int64_t lo = a.cu[b], hi = a.cu[b + 1];
-        lo = lo < 0 ? 0 : (lo > a.T ? a.T : lo);
-        hi = hi > a.T ? a.T : hi;
-        s.q0 = lo;
-        s.n = hi > lo ? hi - lo : 0;
-    } else {
-        s.q0 = b;
-        s.n = 1;
-    }
-    const int64_t room = a.max_pages * a.cache.page_size;
-    int64_t len = a.lens[b];
-    len = len < 0 ? 0 : (len > room ? room : len);
-    s.len = (int)len;
-    int64_t lo = a.window > 0 ? len - s.n + 1 - a.window : 0;  // the first query's first key
-    lo = lo < 0 ? 0 : lo;
-    s.first = (int)(lo >> 4);
-    const int last = (int)((len + 15) >> 4);
-    s.tiles = last - s.first > 1 ? last - s.first : 1;
-    s.parts = (s.n * a.group + NR - 1) / NR;
-    return s;
-}
-
-__device__ __forceinline__ int64_t weight(const AttnArgs &a, const Seq &s) { return s.parts * a.cache.heads * s.tiles; }
-
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
@@ -102,51 +51,6 @@ template <int N>
 __device__ __forceinline__ void copies_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// The codes of byte I of w as two fp16, the low nibble's in the low half.
-template <int I>
-__device__ __forceinline__ uint32_t e2m1x2(uint32_t w)
-{
-    uint32_t r;
-    if constexpr (I == 0)
-        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
-    else if constexpr (I == 1)
-        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
-    else if constexpr (I == 2)
-        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
-    else
-        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-
-// Two E4M3 in the low 16 bits as two fp16.
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t w)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t v)
@@ -178,14 +82,6 @@ __device__ __forceinline__ void join_keys(uint32_t w0, uint32_t w1, uint32_t sca
     o[2] = mul_f16x2(e2m1x2<2>(odd), scale);
     o[3] = mul_f16x2(e2m1x2<3>(odd), scale);
 }
-
-template <int D>
-struct Layout {
-    static constexpr int kTile = 18 * D;            // bytes
-    static constexpr int kRow = D / 2;              // bytes of a key's codes
-    static constexpr int kV = 8 * D, kKsf = 16 * D, kVsf = 17 * D;
-    static constexpr int kChunks = kTile / 16;
-};
 
 // Where 16-byte chunk i of a tile goes in shared memory.  Keys t and t + 4 of each 8
 // become neighbours, so that 8 lanes' reads of K fill 128 bytes; V's chunks are
@@ -286,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
         const int tile0 = (int)(pos - base - unit * s.tiles);
         const int count = (int)(s.tiles - tile0 < end - pos ? s.tiles - tile0 : end - pos);
         const int head = (int)(unit / s.parts);
-        const int64_t row0 = (unit - head * s.parts) * NR;
+        const int64_t row0 = (unit - (int64_t)head * s.parts) * NR;
         const int rows = (int)(s.n * a.group - row0 < NR ? s.n * a.group - row0 : NR);
 
         // the rows of q as fp16, each scaled by a power of two; column factors and limits
@@ -320,10 +216,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // amax into [2^7, 2^8): its smallest parts then lose below 2^-33 of it
-            int e2 = (int)(__float_as_uint(amax) >> 23) - 127;
-            e2 = e2 < -119 ? -119 : (e2 > 126 ? 126 : e2);
-            const float up = __uint_as_float((uint32_t)(127 + 7 - e2) << 23), down = __uint_as_float((uint32_t)(127 - 7 + e2 < 1 ? 1 : 127 - 7 + e2) << 23);
+            float down;
+            const float up = fp16_scale(amax, down);
 #pragma unroll
             for (int j = 0; j < KS / 2; ++j)
 #pragma unroll

@@ -483,3 +483,94 @@ def test_rope_on_pinned_host_buffers(dev):
     got = pkg.ts_qk_norm_rope(*h)
     torch.cuda.synchronize()
     assert not got[0].is_cuda and all(torch.equal(a, b.cpu()) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------------------
+# many rows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,L,hq,hk", [(17, 17, 1, 1), (20, 100, 1, 1), (32, 32, 4, 4), (130, 130, 1, 1), (129, 400, 2, 1), (300, 300, 8, 2),
+                                       (257, 1000, 5, 1), (64, 5000, 16, 2), (1000, 1111, 3, 3), (2050, 2050, 8, 1)])
+def test_prompts(dev, n, L, hq, hk, D):
+    _check_attention(dev, [n], [L], hq, hk, D, 64, seed=n, max_q=n)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 1, 100, 128, 700])
+@pytest.mark.parametrize("page", [16, 48, 256])
+def test_ragged_prompts(dev, page, window, D):
+    """Lengths of none, of fewer keys than queries, ends inside tiles and pages; rows behind the last sequence."""
+    new, lens = [100, 0, 1, 257, 33, 64, 700, 5], [100, 50, 300, 200, 0, 2000, 813, 3]
+    _check_attention(dev, new, lens, 8, 2, D, page, seed=page + window, window=window, max_q=700, gap=5)
+
+
+def test_prompts_not_causal(dev):
+    _check_attention(dev, [150, 20, 90], [600, 1000, 0], 6, 2, 128, 32, causal=False, max_q=150)
+    _check_attention(dev, [40, 300], [70, 129], 2, 2, 64, 32, causal=False, max_q=300, gap=1)
+
+
+def test_a_few_queries_far_into_a_document(dev):
+    """Few rows over many keys: one unit's keys over every block."""
+    _check_attention(dev, [9], [50000], 8, 1, 128, 128, max_q=9)
+    _check_attention(dev, [33], [20001], 10, 2, 64, 64, max_q=33)
+
+
+@pytest.mark.parametrize("B", [256, 300, 700])
+def test_prompts_of_many_sequences(dev, B):
+    r = np.random.RandomState(B)
+    new = [int(v) for v in r.randint(0, 25, B)]
+    new[0], new[B // 2] = 60, 41
+    lens = [m + int(v) for m, v in zip(new, r.randint(0, 60, B))]
+    _check_attention(dev, new, lens, 4, 2, 64, 16, seed=2, max_q=60)
+
+
+def test_prompt_scales(dev):
+    for qscale, scale in ((1e-30, None), (30.0, 0.125), (1e30, 4e-30)):
+        _check_attention(dev, [40, 130], [700, 400], 8, 2, 64, 32, qscale=qscale, scale=scale, max_q=130)
+
+
+def test_prompt_pages_outside_the_cache_are_not_seen(dev):
+    hq, hk, D, page, L, n = 8, 2, 128, 32, 500, 60
+    cache, table = _cache(dev, [L], hk, D, page, 3)
+    kv, cu = torch.tensor([L], dtype=torch.int32, device=dev), torch.tensor([0, n], dtype=torch.int32, device=dev)
+    table[0, 2], table[0, 7], table[0, 14] = -3, cache.pages.shape[0], 2 ** 31 - 1
+    q = _rand((n, hq, D), dev, 4)
+    got, lse = pkg.ts_nvfp4_attention(q, cache, table, kv, cu, return_lse=True)
+    want, want_lse, slack, slack_lse = ref.attention(q, cache.pages, cache.k_scale.double(), cache.v_scale.double(), table, [L], [0, n],
+                                                     1 / math.sqrt(D))
+    _close(got, want, slack, "out")
+    assert bool(((lse - want_lse).abs() <= slack_lse).all())
+    table[:] = -1
+    got, lse = pkg.ts_nvfp4_attention(q, cache, table, kv, cu, return_lse=True)
+    assert bool((got == 0).all() and torch.isneginf(lse).all())
+
+
+def test_prompt_not_a_number_shows(dev):
+    cache, table = _cache(dev, [300], 1, 64, 16, 3)
+    kv, cu = torch.tensor([300], dtype=torch.int32, device=dev), torch.tensor([0, 50], dtype=torch.int32, device=dev)
+    q = _rand((50, 4, 64), dev, 4)
+    good = pkg.ts_nvfp4_attention(q, cache, table, kv, cu)
+    q[10, 1, 5], q[44, 2, 9] = math.nan, math.inf
+    got, lse = pkg.ts_nvfp4_attention(q, cache, table, kv, cu, return_lse=True)
+    bad = torch.zeros(50, 4, dtype=torch.bool, device=dev)
+    bad[10, 1] = bad[44, 2] = True
+    assert bool(torch.isnan(got[bad]).all() and torch.isnan(lse[bad]).all()) and torch.equal(got[~bad], good[~bad])
+    assert pkg.ts_stalled_waits() == 0
+
+
+def test_lists_of_queries_that_do_not_fit(dev):
+    """cu_q outside the rows or descending: clamped, never followed; other rows stay."""
+    cache, table = _cache(dev, [300, 300, 300], 1, 64, 16, 3)
+    kv = torch.tensor([300] * 3, dtype=torch.int32, device=dev)
+    q = _rand((50, 4, 64), dev, 4)
+    for max_q in (2, 40):
+        for cu in ([0, 20, 10, 60], [-5, 3, 2 ** 31 - 1, 7], [40, 50, 50, 0]):
+            out = torch.full_like(q, 7.0)
+            pkg.ts_nvfp4_attention(q, cache, table, kv, torch.tensor(cu, dtype=torch.int32, device=dev), max_q=max_q, out=out)
+            torch.cuda.synchronize()
+            used = torch.zeros(50, dtype=torch.bool)
+            for lo, hi in zip(cu[:-1], cu[1:]):
+                lo, hi = max(0, min(50, lo)), min(50, hi)
+                used[lo:max(lo, hi)] = True
+            assert bool((out[~used.to(dev)] == 7.0).all()) and not bool((out[used.to(dev)] == 7.0).all(-1).any())

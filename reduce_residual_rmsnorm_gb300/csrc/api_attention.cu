@@ -453,6 +453,7 @@ extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t
     a.T = T;
     a.hq = (int)q_heads;
     a.group = (int)(q_heads / c.heads);
+    a.div_group = div_magic((uint32_t)a.group);
     a.cu = cu_q;
     a.B = (int)B;
     a.cache = cache_args(c);

@@ -7,13 +7,16 @@
 // 128, and goes over the keys 128 at a time.  K and V are exact in fp16 (6 significant
 // bits), as are rows of q scaled by a power of two; products are tcgen05.mma kind::f16
 // with fp32 sums in tensor memory, where S, p (fp16, over S) and O of both tiles take
-// all 512 columns (D = 128).  Roles of the block's 13 warps:
+// all 512 columns (D = 128).  Roles of the block's warps:
 //   - 4 for each tile: a thread has a row: its maximum and sum, exp2, p back to tensor
 //     memory, and the rescaling of O, only when a score passes the maximum by 2^8;
-//   - 4 turn codes and scale factors into fp16 tiles in shared memory, two stages
-//     deep, K and V alike with the codes of the next keys already in registers: K is
-//     read along d, V across it, so neither is transposed;
+//   - one copies the codes and scale factors of the next keys into shared memory, which
+//     lie in one piece for each 16 of them;
+//   - 4 turn them into fp16 tiles there, two stages deep, K and V alike: K is read along
+//     d, V across it, so neither is transposed;
 //   - one issues the products: while one tile's p is made, the other's run.
+// Code that runs once a unit is kept in loops: straight through, its instructions come
+// from memory for every unit anew, which took 13000 cycles of one.
 //
 // Work is split evenly as in attn_few.cu: all units' key tiles in one row, cut into
 // equal shares; what a share leaves of a unit is joined by attn_join_rows_kernel.
@@ -38,21 +41,32 @@ constexpr int kKeys = 128;          // keys of a step
 constexpr int kBlocks = 152;        // one for each SM
 constexpr int kShare = 4;           // steps of a share, at least
 constexpr int kMakers = 128;        // threads that make K and V
-constexpr int kThreads = kRows + kMakers + 32;
+constexpr int kThreads = kRows + kMakers + 128;  // four warp groups; of the last two warps work
+// Registers of a thread of each: the 128 that each is launched with, divided anew.
+constexpr int kRowRegs = 192, kMakerRegs = 72, kOtherRegs = 56;
+static_assert(kRows * kRowRegs + kMakers * kMakerRegs + 128 * kOtherRegs <= kThreads * 128, "");
+constexpr int kSwitch = 2;           // what going to a unit costs, in steps, when work is split
+constexpr int kCopies = 13;          // the warp that copies codes
+constexpr int kProducts = 12;        // the warp that issues them
 constexpr int kSeqs = 256;          // sequences whose weights are summed at a time
 
 // Shared memory: q of both tiles, two stages of K and of V, each in blocks of 64 d
-// (128 bytes) by 128 rows under the 128-byte swizzle.
+// (128 bytes) by 128 rows under the 128-byte swizzle; the codes and scale factors of
+// 128 keys of K and of V.
 template <int D>
 struct Smem {
     static constexpr int kBlock = 128 * 128;
     static constexpr int kMatrix = D / 64 * kBlock;
-    static constexpr int kQ = 0, kK = 2 * kMatrix, kV = 4 * kMatrix, kBytes = 6 * kMatrix + 1024;
+    static constexpr int kCodes = kKeys * (D / 2), kRaw = kCodes + kKeys * (D / 16);
+    static constexpr int kQ = 0, kK = 2 * kMatrix, kV = 4 * kMatrix, kRawK = 6 * kMatrix, kRawV = kRawK + kRaw,
+                         kBytes = kRawV + kRaw + 1024;
 };
 
 struct Barriers {
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];  // of each tile
+    uint64_t q_full[2], s_full[2], o_full[2];  // of each tile
+    uint64_t p_full[2][2];                     // of each half of a step's p, and tile
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // of each stage
+    uint64_t raw_full[2], raw_empty[2];                     // the codes of K, of V
     uint64_t last;
 };
 
@@ -60,6 +74,15 @@ __device__ __forceinline__ void give_up(volatile int *dead)
 {
     *dead = 1;
     atomicAdd(&g_stalled_waits, 1u);
+}
+
+// A warp arrives, by one lane after all of them got here: 32 arrivals on one barrier take
+// their turns.
+__device__ __forceinline__ void warp_arrive(uint32_t bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bar);
 }
 
 // The whole warp waits for a phase; false where the block has given up.
@@ -78,6 +101,44 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
             return false;
         }
     }
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two fp32 at a time, in 64 bits: where the pairs are kept as such, no register moves.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // The loads before it are done: the registers are used after it only.
@@ -105,7 +166,7 @@ __device__ __forceinline__ Part part_of(const AttnArgs &a, const Seq &s, int rt)
     const int all = (int)(s.n * a.group);
     p.row0 = rt * kRows;
     p.rows = all - p.row0 < kRows ? all - p.row0 : kRows;
-    const int i0 = p.row0 / a.group, i1 = (p.row0 + p.rows - 1) / a.group;
+    const int i0 = (int)div_by((uint32_t)p.row0, a.div_group), i1 = (int)div_by((uint32_t)(p.row0 + p.rows - 1), a.div_group);
     int hi = a.causal ? (int)(s.len - s.n + i1 + 1) : s.len;
     int lo = a.window > 0 ? (int)(s.len - s.n + i0 + 1) - a.window : 0;
     p.see_hi = hi < 0 ? 0 : hi;
@@ -116,38 +177,49 @@ __device__ __forceinline__ Part part_of(const AttnArgs &a, const Seq &s, int rt)
     return p;
 }
 
-// The steps of a sequence's row tiles for one key head, by a whole warp.
+// The steps of a sequence's row tiles for one key head and the ways to them, by a whole warp.
 __device__ __forceinline__ int64_t steps_of(const AttnArgs &a, const Seq &s)
 {
     int64_t sum = 0;
     for (int rt = threadIdx.x & 31; rt < s.parts; rt += 32)
-        sum += part_of(a, s, rt).steps;
+        sum += part_of(a, s, rt).steps + kSwitch;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
 
-// Where a share stands: the unit (sequence, key head, row tile) and the step in it.
+// Where a share stands: the unit (sequence, key head, row tile) and how far into its
+// kSwitch + steps.
 struct Place {
-    int64_t pos, end;  // steps of all units
-    int b, head, rt, step;
+    int64_t pos, end;  // of all units
+    int b, head, rt, at;
     Seq s;
     Part part;
 };
 
-__device__ __forceinline__ int left_of(const Place &p)
+// What a share has of the unit that it stands at.
+struct Segment {
+    int step, count;  // steps; count may be 0
+    int length;       // with the way there
+};
+
+__device__ __forceinline__ Segment segment_of(const Place &p)
 {
-    const int64_t here = p.part.steps - p.step, left = p.end - p.pos;
-    return (int)(here < left ? here : left);
+    const int64_t here = p.part.steps + kSwitch - p.at, left = p.end - p.pos;
+    Segment g;
+    g.length = (int)(here < left ? here : left);
+    g.step = max(p.at - kSwitch, 0);
+    g.count = max(p.at + g.length - kSwitch, 0) - g.step;
+    return g;
 }
 
-__device__ __forceinline__ void next_unit(const AttnArgs &a, Place &p, int count)
+__device__ __forceinline__ void next_unit(const AttnArgs &a, Place &p, int length)
 {
-    p.pos += count;
+    p.pos += length;
     if (p.pos >= p.end)
         return;
-    p.step = 0;
+    p.at = 0;
     if (++p.rt == p.s.parts) {
         p.rt = 0;
         if (++p.head == a.cache.heads) {
@@ -160,14 +232,13 @@ __device__ __forceinline__ void next_unit(const AttnArgs &a, Place &p, int count
     p.part = part_of(a, p.s, p.rt);
 }
 
-// To the next unit, whose first step comes after `count` of this one's (by one lane, for
-// its warp).
-__device__ __forceinline__ void advance(const AttnArgs &a, Place &place, int count)
+// To the next unit, `length` on (by one lane, for its warp).
+__device__ __forceinline__ void advance(const AttnArgs &a, Place &place, int length)
 {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
         Place p = place;
-        next_unit(a, p, count);
+        next_unit(a, p, length);
         place = p;
     }
     __syncwarp();
@@ -218,7 +289,7 @@ __device__ __forceinline__ Place my_share(const AttnArgs &a, int64_t *weights, i
     Place p;
     p.pos = blockIdx.x * share;
     p.end = p.pos + share < total ? p.pos + share : total;
-    p.b = p.head = p.rt = p.step = 0;
+    p.b = p.head = p.rt = p.at = 0;
     if (p.pos >= p.end)
         return p;
     int64_t base = 0;
@@ -246,11 +317,11 @@ __device__ __forceinline__ Place my_share(const AttnArgs &a, int64_t *weights, i
     r -= p.head * each;
     // the row tile, 32 at a time
     for (int rt0 = 0;; rt0 += 32) {
-        const int steps = rt0 + lane < p.s.parts ? part_of(a, p.s, rt0 + lane).steps : 0;
-        int64_t scan = steps;
+        const int steps = rt0 + lane < p.s.parts ? part_of(a, p.s, rt0 + lane).steps + kSwitch : 0;
+        int scan = steps;  // (32 of at most 2^23)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, scan, o);
+            const int up = __shfl_up_sync(0xffffffffu, scan, o);
             if (lane >= o)
                 scan += up;
         }
@@ -258,7 +329,7 @@ __device__ __forceinline__ Place my_share(const AttnArgs &a, int64_t *weights, i
         if (past != 0) {
             const int at = __ffs(past) - 1;
             p.rt = rt0 + at;
-            p.step = (int)(r - (__shfl_sync(0xffffffffu, scan, at) - __shfl_sync(0xffffffffu, steps, at)));
+            p.at = (int)(r - (__shfl_sync(0xffffffffu, scan, at) - __shfl_sync(0xffffffffu, steps, at)));
             break;
         }
         r -= __shfl_sync(0xffffffffu, scan, 31);
@@ -267,21 +338,18 @@ __device__ __forceinline__ Place my_share(const AttnArgs &a, int64_t *weights, i
     return p;
 }
 
-// 16 bytes of codes (32 d of a key) as fp16 into a row's half of a block of a swizzled
-// matrix.  `row`: the row's address, `half`: chunk 0 or 4 of it, `turn`: row % 8.  Lanes
-// with the two blocks of a row (`swap`) write their words in opposite order, so that 8
-// lanes' stores fill 128 bytes.
-__device__ __forceinline__ void put_codes(uint32_t row, uint32_t half, uint32_t turn, bool swap, uint4 w, uint32_t sf2)
+// 16 bytes of codes (32 d of a key) as fp16 into half of a row of a swizzled block: `row`
+// is the row's address, `first` the place of its first chunk.
+__device__ __forceinline__ void put_codes(uint32_t row, uint32_t first, uint4 w, uint32_t sf2)
 {
     const uint32_t sf = e4m3x2(sf2);
-    const uint32_t s0 = __byte_perm(sf, 0, swap ? 0x3232 : 0x1010), s1 = __byte_perm(sf, 0, swap ? 0x1010 : 0x3232);
-    const uint32_t word[4] = {swap ? w.z : w.x, swap ? w.w : w.y, swap ? w.x : w.z, swap ? w.y : w.w};
-    const uint32_t first = (half + (swap ? 2 : 0)) ^ turn;
+    const uint32_t s0 = __byte_perm(sf, 0, 0x1010), s1 = __byte_perm(sf, 0, 0x3232);
+    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t s = i < 2 ? s0 : s1;
-        st_shared(row + (first ^ i) * 16, make_uint4(mul_f16x2(e2m1x2<0>(word[i]), s), mul_f16x2(e2m1x2<1>(word[i]), s),
-                                                     mul_f16x2(e2m1x2<2>(word[i]), s), mul_f16x2(e2m1x2<3>(word[i]), s)));
+        st_shared(row + (first ^ (16 * i)), make_uint4(mul_f16x2(e2m1x2<0>(word[i]), s), mul_f16x2(e2m1x2<1>(word[i]), s),
+                                                       mul_f16x2(e2m1x2<2>(word[i]), s), mul_f16x2(e2m1x2<3>(word[i]), s)));
     }
 }
 
@@ -296,26 +364,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     __shared__ int64_t weights[kSeqs];
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
-    __shared__ uint8_t seen[4][8];  // whether a step's tiles of 16 keys lie in the cache
+    __shared__ int64_t out_at[kRows];
+    __shared__ int32_t lse_at[kRows];
+    // of a step: whether its tiles of 16 keys lie in the cache; the keys that some row sees,
+    // and whether there is no such step
+    __shared__ uint8_t seen[4][8];
+    __shared__ int32_t see_lo[4], see_hi[4], no_more[4];
     const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
     const int tid = threadIdx.x, warp = tid >> 5;
 
     Record *const record = reinterpret_cast<Record *>(a.partial) + blockIdx.x;
     float *const slots = a.partial + (int64_t)gridDim.x * (sizeof(Record) / 4);
 
-    if (warp == kThreads / 32 - 1)
+    if (warp == kProducts)
         tmem_alloc(smem_u32(&tmem_at), 512);
     if (tid == 0) {
         dead = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars.q_full[i]), 128);
+            mbar_init(smem_u32(&bars.q_full[i]), 4);
             mbar_init(smem_u32(&bars.s_full[i]), 1);
-            mbar_init(smem_u32(&bars.p_full[i]), 128);
+            mbar_init(smem_u32(&bars.p_full[0][i]), 4);
+            mbar_init(smem_u32(&bars.p_full[1][i]), 4);
             mbar_init(smem_u32(&bars.o_full[i]), 1);
-            mbar_init(smem_u32(&bars.k_full[i]), kMakers);
+            mbar_init(smem_u32(&bars.k_full[i]), kMakers / 32);
             mbar_init(smem_u32(&bars.k_empty[i]), 1);
-            mbar_init(smem_u32(&bars.v_full[i]), kMakers);
+            mbar_init(smem_u32(&bars.v_full[i]), kMakers / 32);
             mbar_init(smem_u32(&bars.v_empty[i]), 1);
+            mbar_init(smem_u32(&bars.raw_full[i]), 1);
+            mbar_init(smem_u32(&bars.raw_empty[i]), kMakers / 32);
         }
         mbar_init(smem_u32(&bars.last), 1);
         mbar_fence_init();
@@ -342,268 +418,368 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 
     if (warp < 8) {
         // ---- softmax: thread (tile, r) has row r of its tile
-        const int tile = warp >> 2, r = tid & 127;
+        more_registers<kRowRegs>();
+        const int tile = warp >> 2, r = tid & 127, lane = tid & 31;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 (warp % 4) of tensor memory
         const uint32_t s_at = tmem + kSCol + tile * 128 + lanes, o_at = tmem + kOCol + tile * D + lanes;
         const uint32_t q_smem = smem + S::kQ + tile * S::kMatrix;
-        const uint32_t s_full = smem_u32(&bars.s_full[tile]), p_full = smem_u32(&bars.p_full[tile]);
+        const uint32_t s_full = smem_u32(&bars.s_full[tile]);
         const float vg = *a.cache.v_scale;
         const float c0 = a.scale * kLog2e / *a.cache.k_scale;
         uint32_t step = 0, done = 0, units_done = 0;  // steps of the block and of this tile
         bool alive = true;
+        // the query and head of row `of` of the tile; whether there is one
+        auto find = [&](int of, int &i, int &qh) -> bool {
+            const int at = tile * 128 + of, row = place.part.row0 + at;
+            const bool live = at < place.part.rows;
+            i = live ? (int)div_by((uint32_t)row, a.div_group) : 0;
+            qh = place.head * a.group + (live ? row - i * a.group : 0);
+            return live;
+        };
+        // the warp's rows of q of the unit that the place is at, as they are; whole rows
+        // by neighbouring lanes
+        auto copy_q = [&]() {
+            constexpr int kLanes = D / 8, kPass = 32 / kLanes;
+            const int c = lane % kLanes;
+#pragma unroll 2
+            for (int j = 0; j < 32 / kPass; ++j) {
+                const int row = (warp & 3) * 32 + j * kPass + lane / kLanes;
+                const uint32_t dst = q_smem + (c >> 3) * S::kBlock + row * 128 + (((c & 7) ^ (row & 7)) * 16);
+                int i, qh;
+                if (find(row, i, qh))
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                                 "l"(a.q + (int64_t)(place.s.q0 + i) * a.ldq + (int64_t)qh * D + c * 8) : "memory");
+                else
+                    st_shared(dst, make_uint4(0, 0, 0, 0));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // to the next unit in which this tile has rows and steps
+        auto to_rows = [&]() {
+            while (place.pos < place.end) {
+                const Segment g = segment_of(place);
+                if (g.count > 0 && place.part.rows > tile * 128)
+                    break;
+                step += g.count;
+                advance(a, place, g.length);
+            }
+        };
+        to_rows();
+        if (place.pos < place.end)
+            copy_q();
         while (alive && place.pos < place.end) {
-            const int count = left_of(place);
-            const int rows = place.part.rows - tile * 128;  // of this tile
-            if (rows > 0) {
-                // this row of q, scaled by a power of two, as fp16
-                const int row = place.part.row0 + tile * 128 + r;
-                const bool live = r < rows;
-                const int i = live ? row / a.group : 0;
-                const int qh = place.head * a.group + (live ? row - i * a.group : 0);
-                const uint16_t *src = a.q + (int64_t)(place.s.q0 + i) * a.ldq + (int64_t)qh * D;
-                float amax = 0.0f, down;
-                auto chunk = [&](int c, float (&f)[8]) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (live)
-                        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src + c * 8) : "memory");
-                    unpack8(v, f);
-                };
-                // (read twice: 16 chunks would take 64 registers)
+            const Segment segment = segment_of(place);
+            const int count = segment.count;
+            // this row of q, scaled by a power of two, as fp16
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();
+            float amax = 0.0f, down;
+            const uint32_t q_row = q_smem + r * 128;
 #pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    float f[8];
-                    chunk(c, f);
+            for (int c = 0; c < D / 8; ++c) {
+                float f[8];
+                unpack8(ld_shared(q_row + (c >> 3) * S::kBlock + (((c & 7) ^ (r & 7)) * 16)), f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        amax = fmaxf(amax, fabsf(f[e]));
-                }
-                const float up = fp16_scale(amax, down);
+                for (int e = 0; e < 8; ++e)
+                    amax = fmaxf(amax, fabsf(f[e]));
+            }
+            const float up = fp16_scale(amax, down);
 #pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    float f[8];
-                    chunk(c, f);
-                    st_shared(q_smem + (c >> 3) * S::kBlock + r * 128 + (((c & 7) ^ (r & 7)) * 16),
-                              make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
+            for (int c = 0; c < D / 8; ++c) {
+                const uint32_t at = q_row + (c >> 3) * S::kBlock + (((c & 7) ^ (r & 7)) * 16);
+                float f[8];
+                unpack8(ld_shared(at), f);
+                st_shared(at, make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
                                          pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up)));
-                }
-                fence_async_proxy();
-                mbar_arrive(smem_u32(&bars.q_full[tile]));
-                const float cf = c0 * down;
-                int hi = a.causal ? (int)(place.s.len - place.s.n + i + 1) : place.s.len;
-                int lo = a.window > 0 ? hi - a.window : 0;
-                if (!live) {  // (its scores are zeros)
-                    hi = 0x7fffffff;
-                    lo = 0;
-                }
-                const int hi_min = min(__reduce_min_sync(0xffffffffu, hi), place.s.len);
-                const int lo_max = __reduce_max_sync(0xffffffffu, lo);
+            }
+            fence_async_proxy();
+            warp_arrive(smem_u32(&bars.q_full[tile]));
+            const float cf = c0 * down;
+            int hi, lo;  // the keys that the row sees
+            {
+                int i, qh;
+                const bool live = find(r, i, qh);
+                hi = a.causal ? place.s.len - place.s.n + i + 1 : place.s.len;
+                lo = a.window > 0 ? hi - a.window : 0;
+                hi = live ? hi : place.s.len;  // (a row that there is not scores zeros)
+                lo = live ? lo : 0;
+            }
+            const int hi_min = __reduce_min_sync(0xffffffffu, hi);
+            const int lo_max = __reduce_max_sync(0xffffffffu, lo);
+            const int key0 = (place.part.first + segment.step) * kKeys;
 
-                float m = -INFINITY, l = 0.0f;
-                for (int k = 0; k < count; ++k, ++done) {
-                    const int key = (place.part.first + place.step + k) * kKeys;
-                    alive = wait(s_full, done & 1, &dead);
-                    if (!alive)
-                        break;
-                    tmem_fence_after();
-                    const uint2 in = *reinterpret_cast<const uint2 *>(seen[(step + k) & 3]);
-                    const bool whole = key >= lo_max && key + kKeys <= hi_min && in.x == 0x01010101u && in.y == 0x01010101u;
-                    auto mask = [&](uint32_t (&v)[32], int c) {
+            float m = -INFINITY, l = 0.0f;
+            for (int k = 0; k < count; ++k, ++done) {
+                const int key = key0 + k * kKeys;
+                alive = wait(s_full, done & 1, &dead);
+                if (!alive)
+                    break;
+                tmem_fence_after();
+                const uint2 in = *reinterpret_cast<const uint2 *>(seen[(step + k) & 3]);
+                if (!(key >= lo_max && key + kKeys <= hi_min && in.x == 0x01010101u && in.y == 0x01010101u)) {
+                    // -inf for what the row does not see, a pass of its own: few steps have any
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_load32(s_at + 32 * c, v);
                         // bit j: key 32 c + j of the step is seen
-                        const int h = min(max(min(hi, place.s.len) - key - 32 * c, 0), 32), w = min(max(lo - key - 32 * c, 0), 32);
+                        const int h = min(max(hi - key - 32 * c, 0), 32), w = min(max(lo - key - 32 * c, 0), 32);
                         const uint32_t ok = (c < 2 ? in.x : in.y) >> (16 * (c & 1));
                         const uint32_t sees = (uint32_t)((1ull << h) - (1ull << min(w, h))) &
                                               ((ok & 1 ? 0xFFFFu : 0u) | (ok & 0x100 ? 0xFFFF0000u : 0u));
+                        loaded(v);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!(sees >> j & 1))
                                 v[j] = 0xFF800000u;
-                    };
-                    float top = -INFINITY;
+                        tmem_store32(s_at + 32 * c, v);
+                    }
+                    tmem_wait_stores();
+                }
+                // all of the row's scores at once: a load from tensor memory takes hundreds
+                // of cycles while products run
+                uint32_t v[4][32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_load32(s_at + 32 * c, v);
-                        loaded(v);
-                        if (!whole)
-                            mask(v, c);
+                for (int c = 0; c < 4; ++c)
+                    tmem_load32(s_at + 32 * c, v[c]);
+                float top[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    loaded(v[c]);
+                    top[c] = __uint_as_float(v[c][0]);
+                }
+#pragma unroll
+                for (int j = 1; j < 31; j += 2)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        top[c] = fmaxf(fmaxf(top[c], __uint_as_float(v[c][j])), __uint_as_float(v[c][j + 1]));
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    top[c] = fmaxf(top[c], __uint_as_float(v[c][31]));
+                const float to = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cf;
+                if (__any_sync(0xffffffffu, k == 0 || to > m + kSlack)) {  // the maximum follows
+                    const float next = fmaxf(m, to), f = m == -INFINITY ? 0.0f : exp2_approx(m - next);
+                    m = next;
+                    l *= f;
+#pragma unroll 1
+                    for (int c = 0; c < (k > 0 ? D / 32 : 0); ++c) {
+                        uint32_t o[32];
+                        tmem_load32(o_at + 32 * c, o);
+                        loaded(o);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            top = fmaxf(top, __uint_as_float(v[j]));
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_store32(o_at + 32 * c, o);
                     }
-                    top *= cf;
-                    const bool grow = top > m + kSlack;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float to = fmaxf(m, top);
-                        const float f = m == -INFINITY ? 0.0f : exp2_approx(m - to);
-                        m = to;
-                        l *= f;
-                        if (k > 0) {
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t v[32];
-                                tmem_load32(o_at + 32 * c, v);
-                                loaded(v);
+                }
+                // p, in two halves: the products with the first run beside the second
+                const float off = m == -INFINITY ? 0.0f : -m;
+                const uint64_t by = pair(cf, cf), plus = pair(off, off);
+                uint64_t part[2] = {0, 0};
 #pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-                                tmem_store32(o_at + 32 * c, v);
-                            }
-                        }
-                    }
-                    const float off = m == -INFINITY ? 0.0f : -m;
-                    float sum[2] = {0.0f, 0.0f};
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32], p[16];
-                        tmem_load32(s_at + 32 * c, v);
-                        loaded(v);
-                        if (!whole)
-                            mask(v, c);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p[32];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float e0 = exp2_approx(__fmaf_rn(__uint_as_float(v[2 * j]), cf, off));
-                            const float e1 = exp2_approx(__fmaf_rn(__uint_as_float(v[2 * j + 1]), cf, off));
-                            sum[0] += e0;
-                            sum[1] += e1;
-                            p[j] = pack_f16x2(e0, e1);
-                        }
-                        tmem_store16(s_at + 16 * c, p);
+                    for (int j = 0; j < 32; ++j) {
+                        const uint32_t *x = &v[2 * half + (j >> 4)][2 * (j & 15)];
+                        float e0, e1;
+                        unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), by, plus), e0, e1);
+                        e0 = exp2_approx(e0);
+                        e1 = exp2_approx(e1);
+                        part[j & 1] = add2(part[j & 1], pair(e0, e1));
+                        p[j] = pack_f16x2(e0, e1);
                     }
-                    l += sum[0] + sum[1];
+                    tmem_store32(s_at + 32 * half, p);
                     tmem_wait_stores();
                     tmem_fence_before();
-                    mbar_arrive(p_full);
+                    warp_arrive(smem_u32(&bars.p_full[half][tile]));
                 }
-                if (alive)
-                    alive = wait(smem_u32(&bars.o_full[tile]), units_done & 1, &dead);
-                ++units_done;
-                if (alive) {
-                    tmem_fence_after();
-                    const bool begins = place.step == 0, ends = place.step + count == place.part.steps;
-                    const bool whole_unit = begins && ends;
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
-                    float *slot = slots + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * slot_floats(kRows, D);
-                    uint16_t *dst = a.out + (int64_t)(place.s.q0 + i) * a.ldo + (int64_t)qh * D;
-                    float *part = slot + (tile * 128 + r) * D;
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_load32(o_at + 32 * c, v);
-                        loaded(v);
-                        if (live && whole_unit) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float f[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    f[e] = __uint_as_float(v[8 * j + e]) * inv;
-                                *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * j) = pack8(f);
-                            }
-                        } else if (live) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                *reinterpret_cast<uint4 *>(part + 32 * c + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                        }
-                        __syncwarp();
-                    }
-                    if (live && whole_unit && a.lse != nullptr)
-                        a.lse[(int64_t)(place.s.q0 + i) * a.hq + qh] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
-                    if (live && !whole_unit) {
-                        slot[kRows * D + tile * 128 + r] = m;
-                        slot[kRows * D + kRows + tile * 128 + r] = l;
-                    }
-                    if (tid == 0 && begins && !ends) {
-                        record->last = (int32_t)((place.pos - place.step + place.part.steps - 1) / share_of);
-                        record->q0 = (int32_t)place.s.q0;
-                        record->head = place.head;
-                        record->rows = place.part.rows;
-                        record->row0 = place.part.row0;
-                    }
-                }
-                tmem_fence_before();
+                float s0, s1;
+                unpair(add2(part[0], part[1]), s0, s1);
+                l += s0 + s1;
+            }
+            if (!alive)
+                break;
+            // where the rows go
+            const bool begins = segment.step == 0, ends = segment.step + count == place.part.steps, whole_unit = begins && ends;
+            float *const slot = slots + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * slot_floats(kRows, D);
+            {
+                int i, qh;
+                const bool live = find(r, i, qh);
+                out_at[tid] = live ? (int64_t)(place.s.q0 + i) * a.ldo + (int64_t)qh * D : -1;
+                lse_at[tid] = (place.s.q0 + i) * a.hq + qh;
+            }
+            if (tid == 0 && begins && !ends) {
+                record->last = (int32_t)((place.pos - place.at + place.part.steps + kSwitch - 1) / share_of);
+                record->q0 = place.s.q0;
+                record->head = place.head;
+                record->rows = place.part.rows;
+                record->row0 = place.part.row0;
             }
             step += count;
-            advance(a, place, count);
+            advance(a, place, segment.length);
+            to_rows();
+            alive = wait(smem_u32(&bars.o_full[tile]), units_done & 1, &dead);
+            if (!alive)
+                break;
+            ++units_done;
+            tmem_fence_after();
+            if (place.pos < place.end)
+                copy_q();  // (no product reads it now)
+            const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
+            const int64_t to = out_at[tid];
+#pragma unroll 1
+            for (int j = 0; j < D / 32; ++j) {
+                uint32_t v[32];
+                tmem_load32(o_at + 32 * j, v);
+                loaded(v);
+                if (to >= 0 && whole_unit) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = __uint_as_float(v[8 * k + e]) * inv;
+                        *reinterpret_cast<uint4 *>(a.out + to + 32 * j + 8 * k) = pack8(f);
+                    }
+                } else if (to >= 0) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4 *>(slot + tid * D + 32 * j + 4 * k) =
+                            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                }
+                __syncwarp();
+            }
+            if (out_at[tid] >= 0) {
+                if (!whole_unit) {
+                    slot[kRows * D + tid] = m;
+                    slot[kRows * D + kRows + tid] = l;
+                } else if (a.lse != nullptr) {
+                    a.lse[lse_at[tid]] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
+                }
+            }
+            tmem_fence_before();
         }
     } else if (warp < 8 + kMakers / 32) {
-        // ---- K and V in fp16: a thread has 16 bytes of the codes of every 32nd (64th) key
-        const int id = tid - kRows;
-        constexpr int kRowChunks = D / 32;                   // 16-byte chunks of a key's codes
-        constexpr int kStep = kMakers / kRowChunks;          // keys from one of a thread's chunks to the next
-        constexpr int kPer = kKeys / kStep;
-        const int key_at = id / kRowChunks, c = id % kRowChunks;
-        const uint32_t codes_at = (key_at & 15) * L::kRow + c * 16, sf_at = L::kKsf + (key_at & 15) * (D / 16) + 2 * c;
-        const uint32_t row_at = smem + (c >> 1) * S::kBlock + key_at * 128, half = (c & 1) * 4, turn = key_at & 7;
-        const bool swap = (c & 2) != 0;
-        uint32_t it = 0;
-        uint4 kw[kPer], vw[kPer];
-        uint32_t ksf[kPer], vsf[kPer];
-        uint32_t in = 0;  // whether the chunks' keys lie in the cache
-        int64_t n = place.end - place.pos;
-        int ahead = 0;
-        auto fetch = [&]() {  // the codes of the next step
-            if (place.pos >= place.end)
-                return;
-            const int key0 = (place.part.first + place.step + ahead) * kKeys;
-            const int32_t *table = a.table + (int64_t)place.b * a.max_pages;
-            in = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int key = key0 + i * kStep + key_at, tile_key = key & ~15;
-                uint32_t at = 0;
-                int32_t page = -1;
-                if (tile_key < place.s.len) {
-                    at = div_by((uint32_t)tile_key, a.cache.div_page);
-                    page = table[at];
-                }
-                kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
-                ksf[i] = vsf[i] = 0;
-                if (page >= 0 && page < a.cache.num_pages) {
-                    in |= 1u << i;
-                    const int tile = (tile_key - (int)at * a.cache.page_size) >> 4;
-                    const uint8_t *src =
-                        a.cache.pages + (((int64_t)page * a.cache.heads + place.head) * (a.cache.page_size >> 4) + tile) * L::kTile;
-                    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(kw[i].x), "=r"(kw[i].y), "=r"(kw[i].z), "=r"(kw[i].w) : "l"(src + codes_at) : "memory");
-                    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(vw[i].x), "=r"(vw[i].y), "=r"(vw[i].z), "=r"(vw[i].w) : "l"(src + L::kV + codes_at) : "memory");
-                    asm volatile("ld.global.u16 %0, [%1];" : "=r"(ksf[i]) : "l"(src + sf_at) : "memory");
-                    asm volatile("ld.global.u16 %0, [%1];" : "=r"(vsf[i]) : "l"(src + (L::kVsf - L::kKsf) + sf_at) : "memory");
-                    if (key >= place.part.see_hi || key < place.part.see_lo || key >= place.s.len)
-                        vsf[i] = 0;  // what a slot that nobody sees holds may be NaN
-                }
-            }
-            if (++ahead == left_of(place)) {
-                advance(a, place, ahead);
-                ahead = 0;
-            }
-        };
-        fetch();
-        for (; n > 0; --n, ++it) {
+        // ---- K and V in fp16: a thread has 16 bytes of the codes of every 32nd (64th) key.
+        // 8 neighbouring lanes read 128 bytes of codes and write 128 bytes without a conflict.
+        fewer_registers<kMakerRegs>();
+        const int lane = tid & 31, maker = warp - 8;
+        constexpr int kStep = D == 128 ? 32 : 64;
+        const int key_at = D == 128 ? maker * 8 + (lane & 7) : maker * 16 + (lane >> 1);
+        const int c = D == 128 ? ((lane & 7) >> 1) ^ (lane >> 3) : lane & 1;
+        const uint32_t codes_at = smem + key_at * L::kRow + c * 16, sf_at = smem + S::kCodes + key_at * (D / 16) + 2 * c;
+        const uint32_t row_at = smem + (c >> 1) * S::kBlock + key_at * 128, first = ((c & 1) * 4 ^ (key_at & 7)) * 16;
+        for (uint32_t it = 0;; ++it) {
             const int st = it & 1;
             const uint32_t phase = (it >> 1) & 1;
+            if (!wait(smem_u32(&bars.raw_full[0]), it & 1, &dead) || no_more[it & 3] != 0)
+                break;
             if (it >= 2 && !wait(smem_u32(&bars.k_empty[st]), phase ^ 1, &dead))
                 break;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                if (c == 0 && (key_at & 15) == 0)
-                    seen[it & 3][(i * kStep + key_at) >> 4] = (uint8_t)(in >> i & 1);
-                put_codes(row_at + S::kK + st * S::kMatrix + i * kStep * 128, half, turn, swap, kw[i], ksf[i]);
+#pragma unroll 2
+            for (int key = 0; key < kKeys; key += kStep)
+                put_codes(row_at + S::kK + st * S::kMatrix + key * 128, first, ld_shared(codes_at + S::kRawK + key * L::kRow),
+                          ld_shared16(sf_at + S::kRawK + key * (D / 16)));
+            fence_async_proxy();
+            warp_arrive(smem_u32(&bars.raw_empty[0]));
+            warp_arrive(smem_u32(&bars.k_full[st]));
+            if (!wait(smem_u32(&bars.raw_full[1]), it & 1, &dead) ||
+                (it >= 2 && !wait(smem_u32(&bars.v_empty[st]), phase ^ 1, &dead)))
+                break;
+            const int lo = see_lo[it & 3], hi = see_hi[it & 3];
+#pragma unroll 2
+            for (int key = 0; key < kKeys; key += kStep) {
+                const int at = key + key_at;
+                // (what a slot that nobody sees holds may be NaN)
+                const bool use = at >= lo && at < hi && seen[it & 3][at >> 4] != 0;
+                put_codes(row_at + S::kV + st * S::kMatrix + key * 128, first, ld_shared(codes_at + S::kRawV + key * L::kRow),
+                          use ? ld_shared16(sf_at + S::kRawV + key * (D / 16)) : 0);
             }
             fence_async_proxy();
-            mbar_arrive(smem_u32(&bars.k_full[st]));
-            if (it >= 2 && !wait(smem_u32(&bars.v_empty[st]), phase ^ 1, &dead))
+            warp_arrive(smem_u32(&bars.raw_empty[1]));
+            warp_arrive(smem_u32(&bars.v_full[st]));
+        }
+    } else if (warp == kCopies) {
+        // ---- codes and scale factors: lanes 0..7 have a step's tiles of 16 keys
+        fewer_registers<kOtherRegs>();
+        const int lane = tid & 31;
+        uint32_t it = 0;
+        bool alive = true;
+        auto send = [&](int which, bool in, const uint8_t *src) {  // K (0) or V (1)
+            const uint32_t bar = smem_u32(&bars.raw_full[which]), to = smem + (which == 0 ? S::kRawK : S::kRawV);
+            const int tiles = __popc(__ballot_sync(0xffffffffu, in));
+            if (lane == 0)
+                mbar_expect_tx(bar, tiles * S::kRaw / 8);
+            __syncwarp();
+            if (in) {
+                bulk_load(to + lane * 16 * L::kRow, src + which * L::kV, 16 * L::kRow, bar);
+                bulk_load(to + S::kCodes + lane * D, src + L::kKsf + which * D, D, bar);
+            }
+            __syncwarp();
+        };
+        // a step's keys and tiles, looked up while the step before is copied
+        int key0 = 0, see0 = 0, see1 = 0, ahead = 0;
+        bool in = false;
+        const uint8_t *src = nullptr;
+        auto look_up = [&]() -> bool {
+            Segment segment = segment_of(place);
+            while (ahead == segment.count) {
+                advance(a, place, segment.length);
+                if (place.pos >= place.end)
+                    return false;
+                segment = segment_of(place);
+                ahead = 0;
+            }
+            key0 = (place.part.first + segment.step + ahead++) * kKeys;
+            see0 = place.part.see_lo - key0;
+            see1 = min(place.part.see_hi, place.s.len) - key0;
+            const int key = key0 + lane * 16;
+            int32_t page = -1;
+            uint32_t at = 0;
+            if (lane < 8 && key < place.s.len) {
+                at = div_by((uint32_t)key, a.cache.div_page);
+                page = a.table[(int64_t)place.b * a.max_pages + at];
+            }
+            in = page >= 0 && page < a.cache.num_pages;
+            src = a.cache.pages + (((int64_t)(in ? page : 0) * a.cache.heads + place.head) * (a.cache.page_size >> 4) +
+                                   ((key - (int)at * a.cache.page_size) >> 4)) * L::kTile;
+            return true;
+        };
+        for (bool more = place.pos < place.end && look_up(); more; ++it) {
+            if (it >= 1 && !(alive = wait(smem_u32(&bars.raw_empty[0]), (it - 1) & 1, &dead)))
                 break;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                put_codes(row_at + S::kV + st * S::kMatrix + i * kStep * 128, half, turn, swap, vw[i], vsf[i]);
-            fence_async_proxy();
-            mbar_arrive(smem_u32(&bars.v_full[st]));
-            fetch();
+            if (lane < 8)
+                seen[it & 3][lane] = in;
+            if (lane == 0) {
+                see_lo[it & 3] = see0;
+                see_hi[it & 3] = see1;
+                no_more[it & 3] = 0;
+            }
+            send(0, in, src);
+            const bool in_v = in;
+            const uint8_t *const src_v = src;
+            more = look_up();
+            if (it >= 1 && !(alive = wait(smem_u32(&bars.raw_empty[1]), (it - 1) & 1, &dead)))
+                break;
+            send(1, in_v, src_v);
+        }
+        if (alive && (it == 0 || (alive = wait(smem_u32(&bars.raw_empty[0]), (it - 1) & 1, &dead)))) {
+            if (lane == 0)
+                no_more[it & 3] = 1;
+            warp_arrive(smem_u32(&bars.raw_full[0]));
+        }
+        if (!alive) {  // what is under way arrives before its memory goes
+            const long long t0 = clock64();
+            for (int i = 0; i < 2; ++i)
+                while (it > 0 && !mbar_try_wait(smem_u32(&bars.raw_full[i]), (it - 1) & 1) &&
+                       !mbar_try_wait(smem_u32(&bars.raw_full[i]), it & 1) && clock64() - t0 < kWaitCycles) {
+                }
         }
     } else {
-        // ---- products
+        // ---- products, by one warp
+        fewer_registers<kOtherRegs>();
+        if (warp == kProducts) {
         constexpr uint32_t kIdS = idesc_f16(128, kKeys, false), kIdO = idesc_f16(128, D, true);
         const uint32_t s_full[2] = {smem_u32(&bars.s_full[0]), smem_u32(&bars.s_full[1])};
         // (the addresses go through an asm so that descriptors are not kept in registers
@@ -622,16 +798,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             __syncwarp();
         };
-        auto values = [&](int tile, int st, bool more) {  // O (+)= p V
+        auto values = [&](int tile, int st, int half, bool more) {  // O (+)= p V, half of the keys
             uint32_t base = smem;
             asm volatile("" : "+r"(base));
             if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    mma_f16_tmem(tmem + kOCol + tile * D, tmem + kSCol + tile * 128 + k * 8,
-                                 desc_swizzled128_across(base + S::kV + st * S::kMatrix + k * 2048, S::kBlock), kIdO, more || k > 0);
+                for (int k = 0; k < kKeys / 32; ++k)
+                    mma_f16_tmem(tmem + kOCol + tile * D, tmem + kSCol + tile * 128 + (half * (kKeys / 32) + k) * 8,
+                                 desc_swizzled128_across(base + S::kV + st * S::kMatrix + (half * (kKeys / 32) + k) * 2048, S::kBlock),
+                                 kIdO, more || half > 0 || k > 0);
             }
             __syncwarp();
+        };
+        // both halves of a tile's step, as p comes
+        auto both = [&](int tile, int st, uint32_t phase, bool more) -> bool {
+            for (int half = 0; half < 2; ++half) {
+                if (!wait(smem_u32(&bars.p_full[half][tile]), phase, &dead))
+                    return false;
+                tmem_fence_after();
+                values(tile, st, half, more);
+            }
+            return true;
         };
         auto commit = [&](uint64_t *bar) {
             if (elect_one())
@@ -641,7 +828,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         uint32_t it = 0, units = 0, units1 = 0, p1 = 0;
         bool alive = true;
         while (alive && place.pos < place.end) {
-            const int count = left_of(place);
+            const Segment segment = segment_of(place);
+            const int count = segment.count;
+            if (count == 0) {
+                advance(a, place, segment.length);
+                continue;
+            }
             const bool two = place.part.rows > 128;
             const int st0 = it & 1;
             alive = wait(smem_u32(&bars.q_full[0]), units & 1, &dead) && wait(smem_u32(&bars.k_full[st0]), (it >> 1) & 1, &dead);
@@ -659,10 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             for (int k = 0; k < count; ++k, ++it) {
                 const int st = it & 1, next = st ^ 1;
                 const bool last = k + 1 == count;
-                if (!(alive = wait(smem_u32(&bars.v_full[st]), (it >> 1) & 1, &dead) && wait(smem_u32(&bars.p_full[0]), it & 1, &dead)))
+                if (!(alive = wait(smem_u32(&bars.v_full[st]), (it >> 1) & 1, &dead) && both(0, st, it & 1, k > 0)))
                     break;
-                tmem_fence_after();
-                values(0, st, k > 0);
                 if (last) {
                     commit(&bars.o_full[0]);
                 } else {
@@ -672,11 +862,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     scores(0, next);
                 }
                 if (two) {
-                    if (!(alive = wait(smem_u32(&bars.p_full[1]), p1 & 1, &dead)))
+                    if (!(alive = both(1, st, p1 & 1, k > 0)))
                         break;
                     ++p1;
-                    tmem_fence_after();
-                    values(1, st, k > 0);
                 }
                 commit(&bars.v_empty[st]);
                 if (two) {
@@ -691,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             ++units;
             units1 += two;
             if (alive)
-                advance(a, place, count);
+                advance(a, place, segment.length);
         }
         if (!alive) {  // what has been issued ends before its memory goes
             commit(&bars.last);
@@ -699,12 +887,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             while (!mbar_try_wait(smem_u32(&bars.last), 0) && clock64() - t0 < kWaitCycles) {
             }
         }
+        }
     }
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
     pdl_launch_dependents();
-    if (warp == kThreads / 32 - 1) {
+    if (warp == kProducts) {
         tmem_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -741,9 +930,17 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const __grid_consta
             const float *slot = slots + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * slot_floats(kRows, D);
             const float mi = slot[kRows * D + row], li = slot[kRows * D + kRows + row];
             float v[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[j] = slot[row * D + j * 32 + lane];
+            if constexpr (V == 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(slot + row * D + lane * V);
+                v[0] = w.x;
+                v[1] = w.y;
+                v[2] = w.z;
+                v[3] = w.w;
+            } else {
+                const float2 w = *reinterpret_cast<const float2 *>(slot + row * D + lane * V);
+                v[0] = w.x;
+                v[1] = w.y;
+            }
             const float top = fmaxf(m, mi);
             const float f0 = m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(m - top);
             const float f1 = mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - top);
@@ -758,10 +955,10 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const __grid_consta
         const int64_t r = rec.row0 + row, i = r / a.group;
         const int64_t qh = (int64_t)rec.head * a.group + (r - i * a.group);
         const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
-        uint16_t *dst = a.out + (rec.q0 + i) * a.ldo + qh * D;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (rec.q0 + i) * a.ldo + qh * D + lane * V);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            dst[j * 32 + lane] = (uint16_t)pack_bf16x2(acc[j] * inv, 0.0f);
+        for (int j = 0; j < V / 2; ++j)
+            dst[j] = pack_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
         if (a.lse != nullptr && lane == 0)
             a.lse[(rec.q0 + i) * a.hq + qh] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
     };
@@ -778,7 +975,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const __grid_consta
         gather(row, min(n, warp * per), min(n, (warp + 1) * per), m, l, acc);
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            acc_of[warp][j * 32 + lane] = acc[j];
+            acc_of[warp][lane * V + j] = acc[j];
         if (lane == 0) {
             m_of[warp] = m;
             l_of[warp] = l;
@@ -796,7 +993,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const __grid_consta
                 sum = fmaf(f, l_of[w], sum);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    acc[j] = fmaf(f, acc_of[w][j * 32 + lane], acc[j]);
+                    acc[j] = fmaf(f, acc_of[w][lane * V + j], acc[j]);
             }
             write(row, top, sum, acc);
         }
@@ -814,6 +1011,13 @@ cudaError_t launch_prompt(const AttnArgs &a, bool pdl, cudaStream_t stream)
         return err;
     const bool cached = dev >= 0 && dev < kMaxCachedDevices;
     if (!cached || !ready[dev].load(std::memory_order_relaxed)) {
+        // (a division of more registers than a block is launched with would wait for ever)
+        cudaFuncAttributes of;
+        err = cudaFuncGetAttributes(&of, attn_prompt_kernel<D>);
+        if (err == cudaSuccess && of.numRegs != 128)
+            err = cudaErrorInvalidConfiguration;
+        if (err != cudaSuccess)
+            return err;
         err = cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
         if (err != cudaSuccess)
             return err;

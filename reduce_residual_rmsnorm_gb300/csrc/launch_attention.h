@@ -80,6 +80,7 @@ struct AttnArgs {
     int64_t ldq;
     int64_t T;
     int hq, group;  // query heads, and those of a key head
+    DivMagic div_group;
     const int32_t *cu;  // may be null: one query a sequence
     int B;
     CacheArgs cache;

@@ -9,8 +9,8 @@
  * buffers, host-side checks before any launch, statuses, ts_last_error_detail,
  * TS_FLAG_PDL, no allocation and no synchronisation, strides in elements and at
  * most 2^30), with these additions:
- *   - ts_qk_norm_rope_grad and ts_nvfp4_attention enqueue two kernels: the second
- *     joins what the blocks of the first left in the caller's workspace.  A
+ *   - ts_qk_norm_rope_grad and ts_nvfp4_attention enqueue two kernels where they need
+ *     a workspace: the second joins what the blocks of the first left there.  A
  *     workspace needs no initial contents and holds nothing between calls; two
  *     calls that may run at the same time need one each.
  *   - Buffers may be in device memory or in page-locked host memory, except the
@@ -189,7 +189,8 @@ TS_API int ts_kv_cache_read(const ts_kv_cache_t *cache, const int32_t *slots, in
  *                causal only.
  *   out          bf16 [T, q_heads * D], row stride ldo.
  *   lse          fp32 [T, q_heads], natural logarithm, or NULL.
- *   workspace    ts_nvfp4_attention_workspace(...) bytes, 16-byte aligned.
+ *   workspace    ts_nvfp4_attention_workspace(...) bytes with max_keys = max_pages *
+ *                page_size, 16-byte aligned; may be NULL where that is 0.
  *   strides      >= q_heads * D, multiples of 8.  Outputs overlap no input.
  */
 TS_API int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t q_heads, const int32_t *cu_q, int64_t B,
@@ -197,8 +198,10 @@ TS_API int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t q_h
                               int64_t max_pages, const int32_t *kv_lens, float scale, int causal, int64_t window,
                               void *out, int64_t ldo, float *lse, void *workspace, uint32_t flags, void *stream);
 
-/* Bytes of the attention's workspace, whatever the lengths; -1 for sizes that it refuses. */
-TS_API int64_t ts_nvfp4_attention_workspace(int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_q);
+/* Bytes of the attention's workspace, whatever the lengths within these bounds (no fewer
+ * where a bound is larger); -1 for sizes that it refuses. */
+TS_API int64_t ts_nvfp4_attention_workspace(int64_t B, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_q,
+                                            int64_t max_keys);
 
 #ifdef __cplusplus
 }

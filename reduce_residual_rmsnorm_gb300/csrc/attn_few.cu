@@ -16,18 +16,23 @@
 // (mma.sync, not tcgen05: 8 rows would leave 15/16 of a tcgen05 tile empty, and the
 // tensor pipe is a third busy here.)
 //
-// A warp takes every 8th tile of 16 keys of its block's share, with copies of the next tiles
-// under way, with a running maximum and sum of its own.  The maximum follows only when a
-// score passes it by 2^8, so most tiles take one vote instead of a reduction and a
-// rescaling; p <= 256 is far from fp16's end.
+// A warp takes a run of tiles of 16 keys, with copies of the next ones under way, and has
+// a running maximum and sum of its own.  The maximum follows only when a score passes it
+// by 2^8, so most tiles take one vote instead of a reduction and a rescaling; p <= 256
+// is far from fp16's end.
 //
-// Work is split evenly: all units' tiles in one row, cut into equal shares, so that
-// sequences of any lengths keep every block busy.  A unit inside a share is written
-// at once; of a unit over several, each block leaves its part in the workspace and
-// attn_join_kernel joins them in order.
+// Work is split in one of two ways:
+//   - few units: a cluster of 8 blocks for each, whose parts are joined through the
+//     cluster's shared memory: one launch and no workspace;
+//   - evenly: all units' tiles in one row, cut into equal shares, so that sequences of
+//     any lengths keep every block busy.  A unit inside a share is written at once; of a
+//     unit over several, each block leaves its part in the workspace and
+//     attn_join_kernel joins them in order.
 #include "attn_util.cuh"
 #include "device_util.cuh"
 #include "launch_attention.h"
+#include "launch_nvfp4.h"
+#include "tcgen05.cuh"
 
 namespace tsfn {
 
@@ -40,6 +45,8 @@ constexpr int blocks_per_sm(int nt) { return nt == 1 ? 2 : 1; }
 constexpr int blocks_of(int nt) { return 152 * blocks_per_sm(nt); }
 constexpr int stages_of(int nt) { return nt == 1 ? 4 : 6; }
 constexpr int kShare = 8;     // tiles of a share, at least
+// Clusters take calls of few units and not too many keys.
+constexpr int64_t kClusterUnits = 76, kClusterKeys = 16384;
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
@@ -83,40 +90,391 @@ __device__ __forceinline__ void join_keys(uint32_t w0, uint32_t w1, uint32_t sca
     o[3] = mul_f16x2(e2m1x2<3>(odd), scale);
 }
 
-// Where 16-byte chunk i of a tile goes in shared memory.  Keys t and t + 4 of each 8
-// become neighbours, so that 8 lanes' reads of K fill 128 bytes; V's chunks are
-// exchanged between pairs of keys, so that half a warp's reads fill 128 bytes (D = 128).
-template <int D>
-__device__ __forceinline__ uint32_t chunk_place(int i)
-{
-    using L = Layout<D>;
-    constexpr int per = L::kRow / 16;
-    if (i < 16 * per) {
-        const int key = i / per;
-        return ((key & 8) + 2 * (key & 3) + ((key >> 2) & 1)) * L::kRow + (i % per) * 16;
-    }
-    if (i < 32 * per) {
-        const int v = i - 16 * per, key = v / per;
-        return L::kV + key * L::kRow + ((v % per) ^ (D == 128 ? key & 2 : 0)) * 16;
-    }
-    return i * 16;
-}
+// A unit's run of tiles for one block.
+struct Run {
+    int b, head, rows, first, count;  // first tile (of 16 keys) of the sequence, and how many
+    int row0;                         // first of the sequence's (query, head) pairs
+    Seq s;
+};
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(const __grid_constant__ AttnArgs a)
+struct Shared {
+    using L = Layout<D>;
+    static constexpr int NR = 8 * NT;
+    static constexpr int kRing = kWarps * stages_of(NT) * L::kTile;
+    static_assert(kWarps * NR * D * 4 <= kRing, "");
+    // the copies, [warps][stages][tile]; after them the warps' O [warps][NR][D]
+    static constexpr int kMs = kRing, kLs = kMs + kWarps * NR * 4, kBytes = kLs + kWarps * NR * 4;
+};
+
+// The parts (m, l, O) of a run's rows by the block's warps, in shared memory.
+template <int D, int NT>
+__device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float c0, uint8_t *smem)
 {
     using L = Layout<D>;
     constexpr int NR = 8 * NT, kStages = stages_of(NT);
     constexpr int KS = D / 16;  // products of S per tile and 8 rows, and of O
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const Seq &s = run.s;
+    uint8_t *const ring = smem;
+    float *const ms = reinterpret_cast<float *>(smem + Shared<D, NT>::kMs), *const ls = reinterpret_cast<float *>(smem + Shared<D, NT>::kLs);
+    const uint32_t my_ring = smem_addr(ring) + warp * kStages * L::kTile;
+
+    // this warp's tiles and their copies: 18 D contiguous bytes each
+    const int begin = (int)((int64_t)run.count * warp / kWarps), mine = (int)((int64_t)run.count * (warp + 1) / kWarps) - begin;
+    const int key0 = (run.first + begin) * 16, tiles_of_page = a.cache.page_size >> 4;
+    const int32_t *const table = a.table + (int64_t)run.b * a.max_pages;
+    const int pages = (int)((s.len + a.cache.page_size - 1) / a.cache.page_size);  // that hold keys
+    int page_at = (int)div_by((uint32_t)key0, a.cache.div_page);
+    int in_page = (key0 - page_at * a.cache.page_size) >> 4;
+    auto page_of = [&](int i) -> int32_t { return mine > 0 && i < pages ? table[i] : -1; };
+    int32_t page = page_of(page_at), next_page = page_of(page_at + 1);
+    const uint8_t *src = nullptr;
+    auto to_page = [&]() {
+        src = nullptr;
+        if (page >= 0 && page < a.cache.num_pages)
+            src = a.cache.pages + (((int64_t)page * a.cache.heads + run.head) * tiles_of_page + in_page) * L::kTile + lane * 16;
+    };
+    to_page();
+    uint32_t ok = 0;  // stages whose tile lies in the cache
+    auto issue = [&](int k) {
+        if (k < mine) {
+            if (in_page == tiles_of_page) {
+                in_page = 0;
+                page = next_page;
+                next_page = page_of(++page_at + 1);
+                to_page();
+            }
+            const int stage = k % kStages;
+            ok &= ~(1u << stage);
+            if (src != nullptr) {
+                ok |= 1u << stage;
+                const uint32_t dst = my_ring + stage * L::kTile + lane * 16;
+#pragma unroll
+                for (int i = 0; i < L::kChunks / 32; ++i)
+                    copy16(dst + i * 512, src + i * 512);
+                if (lane < L::kChunks % 32)
+                    copy16(dst + L::kChunks / 32 * 512, src + L::kChunks / 32 * 512);
+                src += L::kTile;
+            }
+            ++in_page;
+        }
+        copies_commit();
+    };
+    for (int k = 0; k < kStages - 1; ++k)
+        issue(k);
+
+    // the rows of q as fp16, each scaled by a power of two; column factors and limits
+    uint32_t qf[NT][KS][2];
+    float cf[NT][2];
+    int hi[NT][2], lo[NT][2];
+    int hi_min = 0x7fffffff, hi_max = 0, lo_min = 0x7fffffff, lo_max = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int col = nt * 8 + g;
+        const bool live = col < run.rows;
+        const int r = run.row0 + col, i = live ? (int)div_by((uint32_t)r, a.div_group) : 0, qh = live ? r - i * a.group : 0;
+        const uint16_t *q = a.q + (int64_t)(s.q0 + i) * a.ldq + ((int64_t)run.head * a.group + qh) * D + t * (D / 4);
+        uint4 v[KS / 2];
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (live)
+                asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w) : "l"(q + j * 8) : "memory");
+        }
+        float f[KS / 2][8], amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+            unpack8(v[j], f[j]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                amax = fmaxf(amax, fabsf(f[j][e]));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float down;
+        const float up = fp16_scale(amax, down);
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                qf[nt][2 * j + e / 2][e & 1] = pack_f16x2(f[j][2 * e] * up, f[j][2 * e + 1] * up);
+        // limits of this column's keys
+        int h = a.causal ? s.len - s.n + i + 1 : s.len;  // (may be <= 0)
+        int l = a.window > 0 ? h - a.window : 0;
+        if (!live) {
+            h = 0x7fffffff;
+            l = 0;
+        }
+        l = l < 0 ? 0 : l;
+        const float c = c0 * down;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int from = (2 * t + j) * 4;
+            cf[nt][j] = __shfl_sync(0xffffffffu, c, from);
+            hi[nt][j] = __shfl_sync(0xffffffffu, h, from);
+            lo[nt][j] = __shfl_sync(0xffffffffu, l, from);
+        }
+        hi_min = min(hi_min, h);
+        lo_max = max(lo_max, l);
+        if (live) {
+            hi_max = max(hi_max, h);
+            lo_min = min(lo_min, l);
+        }
+    }
+    hi_min = min(__reduce_min_sync(0xffffffffu, hi_min), s.len);
+    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+    hi_max = min(__reduce_max_sync(0xffffffffu, hi_max), s.len);
+    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+
+    float o[NT][KS][4];
+    // the maximum, what is subtracted for it (0 while there is none), how far above that a
+    // score may be, and the sum
+    float m[NT][2], off[NT][2], room[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[nt][i][j] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            m[nt][j] = room[nt][j] = -INFINITY;
+            off[nt][j] = l[nt][j] = 0.0f;
+        }
+    }
+    // rows g and g + 8 of K are keys k0 and k0 + 8: t and t + 4 then follow each other in p^T
+    const int k0 = (g >> 1) + 4 * (g & 1);
+    for (int k = 0; k < mine; ++k) {
+        __syncwarp();  // the stage that is filled next has been read
+        issue(k + kStages - 1);
+        copies_wait<kStages - 1>();
+        __syncwarp();
+        const int stage = k % kStages, key = key0 + k * 16;
+        if (!(ok >> stage & 1))
+            continue;
+        const uint8_t *tile = ring + (warp * kStages + stage) * L::kTile;
+
+        float sc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sc[nt][j] = 0.0f;
+        {
+            uint32_t w[2][KS / 2], sf[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint8_t *p = tile + (k0 + 8 * r) * L::kRow + t * (L::kRow / 4);
+                const uint8_t *ps = tile + L::kKsf + (k0 + 8 * r) * (D / 16);
+                if constexpr (D == 128) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                    w[r][0] = v.x;
+                    w[r][1] = v.y;
+                    w[r][2] = v.z;
+                    w[r][3] = v.w;
+                    sf[r] = e4m3x2(*reinterpret_cast<const uint16_t *>(ps + 2 * t));
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                    w[r][0] = v.x;
+                    w[r][1] = v.y;
+                    sf[r] = e4m3x2(ps[t]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < KS / 2; ++i) {  // a word: 8 d, two products
+                // the two words of a block of 16 share its scale
+                const uint32_t s0 = __byte_perm(sf[0], 0, i < 2 ? 0x1010 : 0x3232);
+                const uint32_t s1 = __byte_perm(sf[1], 0, i < 2 ? 0x1010 : 0x3232);
+                const uint32_t a00 = mul_f16x2(e2m1x2<0>(w[0][i]), s0), a01 = mul_f16x2(e2m1x2<1>(w[0][i]), s0);
+                const uint32_t a02 = mul_f16x2(e2m1x2<2>(w[0][i]), s0), a03 = mul_f16x2(e2m1x2<3>(w[0][i]), s0);
+                const uint32_t a10 = mul_f16x2(e2m1x2<0>(w[1][i]), s1), a11 = mul_f16x2(e2m1x2<1>(w[1][i]), s1);
+                const uint32_t a12 = mul_f16x2(e2m1x2<2>(w[1][i]), s1), a13 = mul_f16x2(e2m1x2<3>(w[1][i]), s1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma(sc[nt], a00, a10, a01, a11, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+                    mma(sc[nt], a02, a12, a03, a13, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+                }
+            }
+        }
+        uint32_t vb[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            vb[j] = tile[L::kVsf + (t + 4 * j) * (D / 16) + (D == 128 ? g : g >> 1)];
+        if (!(key >= lo_max && key + 16 <= hi_min)) {  // -inf where a row does not see the key
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = key + k0 + 8 * (j >> 1);
+                    if (!(at < hi[nt][j & 1] && at >= lo[nt][j & 1] && at < s.len))
+                        sc[nt][j] = -INFINITY;
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = key + t + 4 * j;
+                if (!(at < hi_max && at >= lo_min))
+                    vb[j] = 0;  // what a slot that nobody sees holds may be NaN
+            }
+        }
+        // x: scores in units of log2, less the maximum
+        float x[NT][4];
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[nt][j] = fmaf(sc[nt][j], cf[nt][j & 1], -off[nt][j & 1]);
+                grow = grow || x[nt][j] > room[nt][j & 1];
+            }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float f[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float top = fmaxf(x[nt][j], x[nt][j + 2]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    top = fmaxf(top + off[nt][j], m[nt][j]);
+                    f[j] = m[nt][j] == -INFINITY ? 0.0f : exp2_approx(m[nt][j] - top);
+                    m[nt][j] = top;
+                    off[nt][j] = top == -INFINITY ? 0.0f : top;
+                    room[nt][j] = top == -INFINITY ? -INFINITY : kSlack;
+                    l[nt][j] *= f[j];
+                    x[nt][j] = fmaf(sc[nt][j], cf[nt][j], -off[nt][j]);
+                    x[nt][j + 2] = fmaf(sc[nt][j + 2], cf[nt][j], -off[nt][j]);
+                }
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    o[nt][i][0] *= f[0];
+                    o[nt][i][1] *= f[1];
+                    o[nt][i][2] *= f[0];
+                    o[nt][i][3] *= f[1];
+                }
+            }
+        }
+        uint32_t pt[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                p[j] = exp2_approx(x[nt][j]);
+                l[nt][j & 1] += p[j];
+            }
+            pt[nt][0] = transpose8(pack_f16x2(p[0], p[1]));
+            pt[nt][1] = transpose8(pack_f16x2(p[2], p[3]));
+        }
+        // O^T: a lane's keys are t, t + 4, t + 8, t + 12, its d those from g D/8 on
+        const uint32_t vs[2] = {e4m3x2(vb[0] | vb[1] << 8), e4m3x2(vb[2] | vb[3] << 8)};
+        uint32_t w[4][D / 64];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint8_t *p = tile + L::kV + (t + 4 * j) * L::kRow + g * (D / 16);
+            if constexpr (D == 128) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                w[j][0] = v.x;
+                w[j][1] = v.y;
+            } else {
+                w[j][0] = *reinterpret_cast<const uint32_t *>(p);
+            }
+        }
+#pragma unroll
+        for (int h2 = 0; h2 < D / 64; ++h2) {  // words of a lane's codes
+            uint32_t e0[4], o0[4], e1[4], o1[4];
+            join_keys(w[0][h2], w[1][h2], vs[0], e0, o0);
+            join_keys(w[2][h2], w[3][h2], vs[1], e1, o1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma(o[nt][h2 * 4 + i], e0[i], o0[i], e1[i], o1[i], pt[nt][0], pt[nt][1]);
+        }
+    }
+    copies_wait<0>();
+    __syncthreads();  // the ring is free
+
+    float *parts = reinterpret_cast<float *>(ring) + warp * NR * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float v = l[nt][j];
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            const int col = nt * 8 + 2 * t + j;
+            if (g == 0) {
+                ms[warp * NR + col] = m[nt][j];
+                ls[warp * NR + col] = v;
+            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+                *reinterpret_cast<float2 *>(parts + col * D + g * (D / 8) + 2 * i) = make_float2(o[nt][i][j], o[nt][i][j + 2]);
+        }
+    }
+    __syncthreads();
+}
+
+// Parts with maxima m_i and sums l_i are joined with factors exp2(m_i - max); a part
+// without a maximum has nothing, or what is not a number.
+__device__ __forceinline__ float join_factor(float m, float l, float top)
+{
+    return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(m - top);
+}
+
+// 4 elements of a row, summed over the block's warps.
+template <int D, int NT>
+__device__ __forceinline__ float4 join_warps(const uint8_t *smem, int row, int d, float &top, float &sum)
+{
+    constexpr int NR = 8 * NT;
+    const float *ms = reinterpret_cast<const float *>(smem + Shared<D, NT>::kMs), *ls = reinterpret_cast<const float *>(smem + Shared<D, NT>::kLs);
+    top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        top = fmaxf(top, ms[w * NR + row]);
+    sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const float f = join_factor(ms[w * NR + row], ls[w * NR + row], top);
+        sum = fmaf(f, ls[w * NR + row], sum);
+        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + (w * NR + row) * D + d);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+    }
+    return acc;
+}
+
+// 4 elements of a row of the output, and its lse.
+template <int D>
+__device__ __forceinline__ void put_row(const AttnArgs &a, int q0, int head, int64_t row, int d, const float4 &acc, float top, float sum, float vg)
+{
+    const int i = (int)div_by((uint32_t)row, a.div_group);
+    const int qh = head * a.group + ((int)row - i * a.group);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum * vg);
+    *reinterpret_cast<uint2 *>(a.out + (int64_t)(q0 + i) * a.ldo + (int64_t)qh * D + d) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (a.lse != nullptr && d == 0)
+        a.lse[(int64_t)(q0 + i) * a.hq + qh] = sum == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) * kLn2 + logf(sum);
+}
+
+// Even shares.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(const __grid_constant__ AttnArgs a)
+{
+    constexpr int NR = 8 * NT;
     extern __shared__ __align__(16) uint8_t smem[];
-    uint8_t *ring = smem;  // [warps][stages][tile], and after a segment the warps' O [warps][NR][D]
-    float *ms = reinterpret_cast<float *>(smem + kWarps * kStages * L::kTile);  // [warps][NR]
-    float *ls = ms + kWarps * NR;
     __shared__ int64_t sums[kThreads];
     __shared__ int64_t warp_sums[kWarps];
-    static_assert(kWarps * NR * D * 4 <= kWarps * kStages * L::kTile, "");
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    __shared__ int64_t state[4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float *const slots = a.partial + (int64_t)gridDim.x * (sizeof(Record) / 4);
     Record *const record = reinterpret_cast<Record *>(a.partial) + blockIdx.x;
     pdl_wait();
@@ -146,15 +504,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
     __syncthreads();
     const int64_t even = (total + gridDim.x - 1) / gridDim.x, share = even > kShare ? even : kShare;
     int64_t pos = blockIdx.x * share;
-    const int64_t end = pos + share < total ? pos + share : total;
+    int64_t end = pos + share < total ? pos + share : total;
     if (tid == 0)
         record->last = -1;
     if (pos >= end) {
         pdl_launch_dependents();
         return;
     }
-    int b;
-    int64_t base;  // tiles before sequence b
+    Run run;
+    int64_t base;  // tiles before the sequence
     {
         int lo = 0, hi = kThreads - 1;  // the first thread whose sum passes pos
         while (lo < hi) {
@@ -164,344 +522,51 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
             else
                 lo = mid + 1;
         }
-        b = lo * per;
+        run.b = lo * per;
         base = lo > 0 ? sums[lo - 1] : 0;
     }
-    Seq s = sequence<NR>(a, b);
-    const float kg = *a.cache.k_scale, vg = *a.cache.v_scale;
-    const float c0 = a.scale * kLog2e / kg;
-
-    const uint32_t my_ring = smem_addr(ring) + warp * kStages * L::kTile;
+    run.s = sequence<NR>(a, run.b);
+    const float vg = *a.cache.v_scale, c0 = a.scale * kLog2e / *a.cache.k_scale;
 
     while (pos < end) {
-        while (pos >= base + weight(a, s)) {
-            base += weight(a, s);
-            s = sequence<NR>(a, ++b);
+        while (pos >= base + weight(a, run.s)) {
+            base += weight(a, run.s);
+            run.s = sequence<NR>(a, ++run.b);
         }
-        const int64_t unit = (pos - base) / s.tiles;
-        const int tile0 = (int)(pos - base - unit * s.tiles);
-        const int count = (int)(s.tiles - tile0 < end - pos ? s.tiles - tile0 : end - pos);
-        const int head = (int)(unit / s.parts);
-        const int64_t row0 = (unit - (int64_t)head * s.parts) * NR;
-        const int rows = (int)(s.n * a.group - row0 < NR ? s.n * a.group - row0 : NR);
-
-        // the rows of q as fp16, each scaled by a power of two; column factors and limits
-        uint32_t qf[NT][KS][2];
-        float cf[NT][2];
-        int hi[NT][2], lo[NT][2];
-        int hi_min = 0x7fffffff, hi_max = 0, lo_min = 0x7fffffff, lo_max = 0;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int col = nt * 8 + g;
-            const bool live = col < rows;
-            const int64_t r = row0 + col;
-            const int64_t i = live ? r / a.group : 0;
-            const int qh = live ? (int)(r - i * a.group) : 0;
-            const uint16_t *src = a.q + (s.q0 + i) * a.ldq + ((int64_t)head * a.group + qh) * D + t * (D / 4);
-            uint4 v[KS / 2];
-#pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (live)
-                    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w) : "l"(src + j * 8) : "memory");
-            }
-            float f[KS / 2][8], amax = 0.0f;
-#pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-                unpack8(v[j], f[j]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    amax = fmaxf(amax, fabsf(f[j][e]));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            float down;
-            const float up = fp16_scale(amax, down);
-#pragma unroll
-            for (int j = 0; j < KS / 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    qf[nt][2 * j + e / 2][e & 1] = pack_f16x2(f[j][2 * e] * up, f[j][2 * e + 1] * up);
-            // limits of this column's keys
-            int h = a.causal ? (int)(s.len - s.n + i + 1) : s.len;  // (may be <= 0)
-            int l = a.window > 0 ? h - a.window : 0;
-            if (!live) {
-                h = 0x7fffffff;
-                l = 0;
-            }
-            l = l < 0 ? 0 : l;
-            const float c = c0 * down;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int from = (2 * t + j) * 4;
-                cf[nt][j] = __shfl_sync(0xffffffffu, c, from);
-                hi[nt][j] = __shfl_sync(0xffffffffu, h, from);
-                lo[nt][j] = __shfl_sync(0xffffffffu, l, from);
-            }
-            hi_min = min(hi_min, h);
-            lo_max = max(lo_max, l);
-            if (live) {
-                hi_max = max(hi_max, h);
-                lo_min = min(lo_min, l);
-            }
+        const int64_t unit = (pos - base) / run.s.tiles;
+        const int skip = (int)(pos - base - unit * run.s.tiles);
+        run.count = (int)(run.s.tiles - skip < end - pos ? run.s.tiles - skip : end - pos);
+        run.first = run.s.first + skip;
+        run.head = (int)(unit / run.s.parts);
+        run.row0 = (int)(unit - (int64_t)run.head * run.s.parts) * NR;
+        run.rows = run.s.n * a.group - run.row0 < NR ? run.s.n * a.group - run.row0 : NR;
+        // (kept in shared memory over the tiles, for the registers' sake)
+        if (tid == 0) {
+            state[0] = pos;
+            state[1] = end;
+            state[2] = base;
+            state[3] = share;
         }
-        hi_min = __reduce_min_sync(0xffffffffu, hi_min);
-        lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-        hi_max = __reduce_max_sync(0xffffffffu, hi_max);
-        lo_min = __reduce_min_sync(0xffffffffu, lo_min);
-        hi_min = min(hi_min, s.len);
-
-        float o[NT][KS][4];
-        float m[NT][2], l[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < KS; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[nt][i][j] = 0.0f;
-            m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.0f;
-        }
-
-        const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;  // tiles of this warp
-        const int64_t table = (int64_t)b * a.max_pages;
-        const int key0 = (s.first + tile0 + warp) * 16;
-        uint32_t ok = 0;  // stages whose tile lies in the cache
-        auto page_of = [&](int k) -> int32_t {
-            const int key = key0 + k * kWarps * 16;
-            return k < mine && key < s.len ? a.table[table + div_by((uint32_t)key, a.cache.div_page)] : -1;
-        };
-        int32_t next_page = page_of(0);
-        auto issue = [&](int k) {
-            const int32_t page = next_page;
-            next_page = page_of(k + 1);
-            const int stage = k % kStages;
-            ok &= ~(1u << stage);
-            if (k < mine && page >= 0 && page < a.cache.num_pages) {
-                ok |= 1u << stage;
-                const int key = key0 + k * kWarps * 16;
-                const int in_page = key - (int)div_by((uint32_t)key, a.cache.div_page) * a.cache.page_size;
-                const uint8_t *src =
-                    a.cache.pages + (((int64_t)page * a.cache.heads + head) * (a.cache.page_size >> 4) + (in_page >> 4)) * L::kTile;
-                const uint32_t dst = my_ring + stage * L::kTile;
-#pragma unroll
-                for (int i = 0; i < (L::kChunks + 31) / 32; ++i)
-                    if (i * 32 + lane < L::kChunks)
-                        copy16(dst + chunk_place<D>(i * 32 + lane), src + (i * 32 + lane) * 16);
-            }
-            copies_commit();
-        };
-        for (int k = 0; k < kStages - 1; ++k)
-            issue(k);
-        for (int k = 0; k < mine; ++k) {
-            __syncwarp();  // the stage that is filled next has been read
-            issue(k + kStages - 1);
-            copies_wait<kStages - 1>();
-            __syncwarp();
-            const int stage = k % kStages;
-            const int key = key0 + k * kWarps * 16;
-            if (!(ok >> stage & 1))
-                continue;
-            const uint8_t *tile = ring + (warp * kStages + stage) * L::kTile;
-
-            // S^T: rows g and g + 8 are keys k0 and k0 + 8
-            const int k0 = (g >> 1) + 4 * (g & 1);
-            float sc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sc[nt][j] = 0.0f;
-            {
-                uint32_t w[2][KS / 2], sf[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint8_t *p = tile + (g + 8 * r) * L::kRow + t * (L::kRow / 4);
-                    const uint8_t *ps = tile + L::kKsf + (k0 + 8 * r) * (D / 16);
-                    if constexpr (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-                        w[r][0] = v.x;
-                        w[r][1] = v.y;
-                        w[r][2] = v.z;
-                        w[r][3] = v.w;
-                        sf[r] = e4m3x2(*reinterpret_cast<const uint16_t *>(ps + 2 * t));
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-                        w[r][0] = v.x;
-                        w[r][1] = v.y;
-                        sf[r] = e4m3x2(ps[t]);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < KS / 2; ++i) {  // a word: 8 d, two products
-                    // the two words of a block of 16 share its scale
-                    const uint32_t s0 = __byte_perm(sf[0], 0, i < 2 ? 0x1010 : 0x3232);
-                    const uint32_t s1 = __byte_perm(sf[1], 0, i < 2 ? 0x1010 : 0x3232);
-                    const uint32_t a00 = mul_f16x2(e2m1x2<0>(w[0][i]), s0), a01 = mul_f16x2(e2m1x2<1>(w[0][i]), s0);
-                    const uint32_t a02 = mul_f16x2(e2m1x2<2>(w[0][i]), s0), a03 = mul_f16x2(e2m1x2<3>(w[0][i]), s0);
-                    const uint32_t a10 = mul_f16x2(e2m1x2<0>(w[1][i]), s1), a11 = mul_f16x2(e2m1x2<1>(w[1][i]), s1);
-                    const uint32_t a12 = mul_f16x2(e2m1x2<2>(w[1][i]), s1), a13 = mul_f16x2(e2m1x2<3>(w[1][i]), s1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma(sc[nt], a00, a10, a01, a11, qf[nt][2 * i][0], qf[nt][2 * i][1]);
-                        mma(sc[nt], a02, a12, a03, a13, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
-                    }
-                }
-            }
-            // scores in units of log2; -inf where a row does not see the key
-            const bool whole = key >= lo_max && key + 16 <= hi_min;
-            bool grow = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float v = sc[nt][j] * cf[nt][j & 1];
-                    if (!whole) {
-                        const int at = key + k0 + 8 * (j >> 1);
-                        v = at < hi[nt][j & 1] && at >= lo[nt][j & 1] && at < s.len ? v : -INFINITY;
-                    }
-                    sc[nt][j] = v;
-                    grow = grow || v > m[nt][j & 1] + kSlack;
-                }
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float f[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float top = fmaxf(sc[nt][j], sc[nt][j + 2]);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        top = fmaxf(top, m[nt][j]);
-                        f[j] = m[nt][j] == -INFINITY ? 0.0f : exp2_approx(m[nt][j] - top);
-                        m[nt][j] = top;
-                        l[nt][j] *= f[j];
-                    }
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        o[nt][i][0] *= f[0];
-                        o[nt][i][1] *= f[1];
-                        o[nt][i][2] *= f[0];
-                        o[nt][i][3] *= f[1];
-                    }
-                }
-            }
-            uint32_t pt[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float top = m[nt][j & 1];
-                    p[j] = exp2_approx(sc[nt][j] - (top == -INFINITY ? 0.0f : top));
-                    l[nt][j & 1] += p[j];
-                }
-                pt[nt][0] = transpose8(pack_f16x2(p[0], p[1]));
-                pt[nt][1] = transpose8(pack_f16x2(p[2], p[3]));
-            }
-            // O^T: a lane's keys are t, t + 4, t + 8, t + 12, its d those from g D/8 on
-            uint32_t vs[2];
-            {
-                const uint8_t *ps = tile + L::kVsf + t * (D / 16) + (D == 128 ? g : g >> 1);
-                uint32_t b4[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    b4[j] = ps[4 * j * (D / 16)];
-                    const int at = key + t + 4 * j;
-                    if (!whole && !(at < hi_max && at >= lo_min && at < s.len))
-                        b4[j] = 0;  // what a slot that nobody sees holds may be NaN
-                }
-                vs[0] = e4m3x2(b4[0] | b4[1] << 8);
-                vs[1] = e4m3x2(b4[2] | b4[3] << 8);
-            }
-#pragma unroll
-            for (int h2 = 0; h2 < D / 64; ++h2) {  // words of a lane's codes
-                uint32_t w[4];
-                if constexpr (D == 64) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[j] = *reinterpret_cast<const uint32_t *>(tile + L::kV + (t + 4 * j) * L::kRow + g * 4);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int kk = t + 4 * j;
-                        w[j] = *reinterpret_cast<const uint32_t *>(tile + L::kV + kk * L::kRow + (((g >> 1) ^ (kk & 2)) * 16) + (g & 1) * 8 + h2 * 4);
-                    }
-                }
-                uint32_t e0[4], o0[4], e1[4], o1[4];
-                join_keys(w[0], w[1], vs[0], e0, o0);
-                join_keys(w[2], w[3], vs[1], e1, o1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma(o[nt][h2 * 4 + i], e0[i], o0[i], e1[i], o1[i], pt[nt][0], pt[nt][1]);
-            }
-        }
-        copies_wait<0>();
-        __syncthreads();  // the ring is free
-
-        // the warps' parts: (m, l, O) of each row
-        float *parts = reinterpret_cast<float *>(ring) + warp * NR * D;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float v = l[nt][j];
-                v += __shfl_xor_sync(0xffffffffu, v, 4);
-                v += __shfl_xor_sync(0xffffffffu, v, 8);
-                v += __shfl_xor_sync(0xffffffffu, v, 16);
-                const int col = nt * 8 + 2 * t + j;
-                if (g == 0) {
-                    ms[warp * NR + col] = m[nt][j];
-                    ls[warp * NR + col] = v;
-                }
-#pragma unroll
-                for (int i = 0; i < KS; ++i)
-                    *reinterpret_cast<float2 *>(parts + col * D + g * (D / 8) + 2 * i) = make_float2(o[nt][i][j], o[nt][i][j + 2]);
-            }
-        }
-        __syncthreads();
-        const bool begins = tile0 == 0, ends = tile0 + count == s.tiles;
+        attend<D, NT>(a, run, c0, smem);
+        pos = state[0];
+        end = state[1];
+        base = state[2];
+        const bool begins = run.first == run.s.first, ends = run.first + run.count == run.s.first + run.s.tiles;
+        const int tile0 = run.first - run.s.first;
         if (begins && !ends && tid == 0) {
-            record->last = (int32_t)((pos - tile0 + s.tiles - 1) / share);
-            record->q0 = (int32_t)s.q0;
-            record->head = head;
-            record->rows = rows;
-            record->row0 = row0;
+            record->last = (int32_t)((pos - tile0 + run.s.tiles - 1) / state[3]);
+            record->q0 = run.s.q0;
+            record->head = run.head;
+            record->rows = run.rows;
+            record->row0 = run.row0;
         }
         float *slot = slots + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * slot_floats(NR, D);
-        constexpr int kSets = kThreads / (D / 4);  // rows in one pass
-        for (int row = tid / (D / 4); row < rows; row += kSets) {
+        for (int row = tid / (D / 4); row < run.rows; row += kThreads / (D / 4)) {
             const int d = (tid % (D / 4)) * 4;
-            float top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                top = fmaxf(top, ms[w * NR + row]);
-            float sum_l = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float mw = ms[w * NR + row];
-                const float f = mw == -INFINITY ? (ls[w * NR + row] == 0.0f ? 0.0f : 1.0f) : exp2_approx(mw - top);
-                sum_l = fmaf(f, ls[w * NR + row], sum_l);
-                const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(ring) + (w * NR + row) * D + d);
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z);
-                acc.w = fmaf(f, v.w, acc.w);
-            }
+            float top, sum_l;
+            const float4 acc = join_warps<D, NT>(smem, row, d, top, sum_l);
             if (begins && ends) {
-                const int64_t r = row0 + row, i = r / a.group;
-                const int64_t qh = (int64_t)head * a.group + (r - i * a.group);
-                const float inv = sum_l == 0.0f ? 0.0f : 1.0f / (sum_l * vg);
-                *reinterpret_cast<uint2 *>(a.out + (s.q0 + i) * a.ldo + qh * D + d) =
-                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                if (a.lse != nullptr && d == 0)
-                    a.lse[(s.q0 + i) * a.hq + qh] = sum_l == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) * kLn2 + logf(sum_l);
+                put_row<D>(a, run.s.q0, run.head, run.row0 + row, d, acc, top, sum_l, vg);
             } else {
                 *reinterpret_cast<float4 *>(slot + row * D + d) = acc;
                 if (d == 0) {
@@ -511,60 +576,151 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
             }
         }
         __syncthreads();  // before the ring is filled again
-        pos += count;
+        pos += run.count;
     }
     pdl_launch_dependents();
 }
 
-// One block per (unit over several blocks, row): its parts in order.
+constexpr int kCluster = 8;
+
+// A cluster for each sequence and key head, and (the grid's y) row tile: the blocks have
+// an eighth of the keys each.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_cluster_kernel(const __grid_constant__ AttnArgs a)
+{
+    constexpr int NR = 8 * NT;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float part[NR][D];
+    __shared__ float part_m[NR], part_l[NR];
+    const int tid = threadIdx.x, rank = (int)cluster_rank();
+    pdl_wait();
+    const int unit = blockIdx.x / kCluster;
+    Run run;
+    run.b = unit / a.cache.heads;
+    run.head = unit - run.b * a.cache.heads;
+    run.s = sequence<NR>(a, run.b);
+    const float vg = *a.cache.v_scale, c0 = a.scale * kLog2e / *a.cache.k_scale;
+    for (int rt = blockIdx.y; rt < run.s.parts; rt += gridDim.y) {
+        run.row0 = rt * NR;
+        run.rows = run.s.n * a.group - run.row0 < NR ? run.s.n * a.group - run.row0 : NR;
+        const int begin = (int)((int64_t)run.s.tiles * rank / kCluster);
+        run.first = run.s.first + begin;
+        run.count = (int)((int64_t)run.s.tiles * (rank + 1) / kCluster) - begin;
+        attend<D, NT>(a, run, c0, smem);
+        for (int row = tid / (D / 4); row < run.rows; row += kThreads / (D / 4)) {
+            const int d = (tid % (D / 4)) * 4;
+            float top, sum_l;
+            const float4 acc = join_warps<D, NT>(smem, row, d, top, sum_l);
+            *reinterpret_cast<float4 *>(&part[row][d]) = acc;
+            if (d == 0) {
+                part_m[row] = top;
+                part_l[row] = sum_l;
+            }
+        }
+        cluster_sync();
+        // each block joins the cluster's parts of its rows
+        for (int row = rank * NT + tid / (D / 4); row < (rank + 1) * NT && row < run.rows; row += kThreads / (D / 4)) {
+            const int d = (tid % (D / 4)) * 4;
+            const uint32_t at = smem_addr(&part[row][d]), at_m = smem_addr(&part_m[row]), at_l = smem_addr(&part_l[row]);
+            float m[kCluster], l[kCluster], top = -INFINITY, sum_l = 0.0f;
+            float4 v[kCluster];
+#pragma unroll
+            for (int i = 0; i < kCluster; ++i) {
+                m[i] = __uint_as_float(ld_cluster32(map_rank(at_m, i)));
+                l[i] = __uint_as_float(ld_cluster32(map_rank(at_l, i)));
+                v[i] = ld_cluster128(map_rank(at, i));
+                top = fmaxf(top, m[i]);
+            }
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kCluster; ++i) {
+                const float f = join_factor(m[i], l[i], top);
+                sum_l = fmaf(f, l[i], sum_l);
+                acc.x = fmaf(f, v[i].x, acc.x);
+                acc.y = fmaf(f, v[i].y, acc.y);
+                acc.z = fmaf(f, v[i].z, acc.z);
+                acc.w = fmaf(f, v[i].w, acc.w);
+            }
+            put_row<D>(a, run.s.q0, run.head, run.row0 + row, d, acc, top, sum_l, vg);
+        }
+        cluster_sync();  // the parts have been read
+    }
+    pdl_launch_dependents();
+}
+
+// Units over several blocks: block (x, y) has row y of the x-th of them, a share of the
+// parts for each set of lanes, whose loads are all under way together.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a, int blocks, int NR)
 {
-    constexpr int kLanes = D / 4, kParts = 256 / kLanes;
-    __shared__ float4 acc_of[kParts][kLanes];
-    __shared__ float m_of[kParts], l_of[kParts];
-    const int first = blockIdx.x, row = blockIdx.y;
+    constexpr int kLanes = D / 4, kSets = 256 / kLanes;
+    __shared__ float4 acc_of[kSets][kLanes];
+    __shared__ float m_of[kSets], l_of[kSets];
+    __shared__ int which;
+    const int row = blockIdx.y;
     pdl_wait();
     pdl_launch_dependents();
-    const Record rec = reinterpret_cast<const Record *>(a.partial)[first];
+    const Record *records = reinterpret_cast<const Record *>(a.partial);
+    int first = blockIdx.x;
+    if ((int)gridDim.x < blocks) {  // fewer units than blocks: look for the x-th that is over several
+        if (threadIdx.x < 32) {
+            int before = 0, found = -1;
+            for (int i0 = 0; i0 < blocks; i0 += 32) {
+                const int i = i0 + (int)threadIdx.x;
+                const bool split = i < blocks && records[i].last >= 0;
+                const unsigned some = __ballot_sync(0xffffffffu, split);
+                if (split && before + __popc(some & ((1u << threadIdx.x) - 1)) == first)
+                    found = i;
+                before += __popc(some);
+            }
+            found = __reduce_max_sync(0xffffffffu, found);
+            if (threadIdx.x == 0)
+                which = found;
+        }
+        __syncthreads();
+        first = which;
+    }
+    if (first < 0)
+        return;
+    const Record rec = records[first];
     if (rec.last < 0 || row >= rec.rows)
         return;
     const float *slots = a.partial + (int64_t)blocks * (sizeof(Record) / 4);
-    const int part = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 4;
-    float m = -INFINITY, l = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int set = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 4;
     // each set of lanes takes a run of the blocks, so that the order is the keys'
-    const int n = rec.last - first + 1, per = (n + kParts - 1) / kParts;
-    const int i1 = min(n, (part + 1) * per);
-#pragma unroll 4
-    for (int i = part * per; i < i1; ++i) {
-        const float *slot = slots + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * slot_floats(NR, D);
-        const float mi = slot[NR * D + row], li = slot[NR * D + NR + row];
+    const int n = rec.last - first + 1, per = (n + kSets - 1) / kSets;
+    const int i0 = min(n, set * per), i1 = min(n, i0 + per);
+    auto slot_of = [&](int i) { return slots + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * slot_floats(NR, D); };
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 8
+    for (int i = i0; i < i1; ++i)
+        m = fmaxf(m, slot_of(i)[NR * D + row]);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int i = i0; i < i1; ++i) {
+        const float *slot = slot_of(i);
+        const float li = slot[NR * D + NR + row], f = join_factor(slot[NR * D + row], li, m);
         const float4 v = *reinterpret_cast<const float4 *>(slot + row * D + d);
-        const float top = fmaxf(m, mi);
-        const float f0 = m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(m - top);
-        const float f1 = mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - top);
-        m = top;
-        l = l * f0 + li * f1;
-        acc.x = acc.x * f0 + v.x * f1;
-        acc.y = acc.y * f0 + v.y * f1;
-        acc.z = acc.z * f0 + v.z * f1;
-        acc.w = acc.w * f0 + v.w * f1;
+        l = fmaf(f, li, l);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
     }
-    acc_of[part][threadIdx.x % kLanes] = acc;
+    acc_of[set][threadIdx.x % kLanes] = acc;
     if (d == 0) {
-        m_of[part] = m;
-        l_of[part] = l;
+        m_of[set] = m;
+        l_of[set] = l;
     }
     __syncthreads();
-    if (part != 0)
+    if (set != 0)
         return;
     float top = -INFINITY, sum = 0.0f;
-    for (int i = 0; i < kParts; ++i)
+    for (int i = 0; i < kSets; ++i)
         top = fmaxf(top, m_of[i]);
     acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < kParts; ++i) {
-        const float f = m_of[i] == -INFINITY ? (l_of[i] == 0.0f ? 0.0f : 1.0f) : exp2_approx(m_of[i] - top);
+    for (int i = 0; i < kSets; ++i) {
+        const float f = join_factor(m_of[i], l_of[i], top);
         const float4 v = acc_of[i][threadIdx.x];
         sum = fmaf(f, l_of[i], sum);
         acc.x = fmaf(f, v.x, acc.x);
@@ -572,45 +728,64 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
     }
-    const int64_t r = rec.row0 + row, i = r / a.group;
-    const int64_t qh = (int64_t)rec.head * a.group + (r - i * a.group);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum * *a.cache.v_scale);
-    *reinterpret_cast<uint2 *>(a.out + (rec.q0 + i) * a.ldo + qh * D + d) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse != nullptr && d == 0)
-        a.lse[(rec.q0 + i) * a.hq + qh] = sum == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) * kLn2 + logf(sum);
+    put_row<D>(a, rec.q0, rec.head, rec.row0 + row, d, acc, top, sum, *a.cache.v_scale);
 }
 
-template <int D, int NT>
-cudaError_t launch_few(const AttnArgs &a, bool pdl, cudaStream_t stream)
+// Dynamic shared memory above 48 KB, asked for once a device.
+template <typename K>
+cudaError_t allow_shared(K kernel, int bytes, std::atomic<bool> (&ready)[kMaxCachedDevices])
 {
-    constexpr int kBlocks = blocks_of(NT), smem = kWarps * stages_of(NT) * Layout<D>::kTile + 2 * kWarps * 8 * NT * 4;
-    static std::atomic<bool> ready[kMaxCachedDevices];
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess)
         return err;
     const bool cached = dev >= 0 && dev < kMaxCachedDevices;
-    if (!cached || !ready[dev].load(std::memory_order_relaxed)) {
-        err = cudaFuncSetAttribute(attn_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (cached && ready[dev].load(std::memory_order_relaxed))
+        return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess && cached)
+        ready[dev].store(true, std::memory_order_relaxed);
+    return err;
+}
+
+template <int D, int NT>
+cudaError_t launch_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t stream)
+{
+    constexpr int kBlocks = blocks_of(NT), smem = Shared<D, NT>::kBytes;
+    if (attn_few_clusters(a.B, a.cache.heads, rows, a.max_pages * a.cache.page_size)) {
+        static std::atomic<bool> ready[kMaxCachedDevices];
+        const cudaError_t err = allow_shared(attn_cluster_kernel<D, NT>, smem, ready);
         if (err != cudaSuccess)
             return err;
-        if (cached)
-            ready[dev].store(true, std::memory_order_relaxed);
+        return launch_clusters(attn_cluster_kernel<D, NT>, dim3((unsigned)(a.B * a.cache.heads * kCluster), (unsigned)((rows + 8 * NT - 1) / (8 * NT))),
+                               dim3(kThreads), smem, stream, pdl, kCluster, a);
     }
+    static std::atomic<bool> ready[kMaxCachedDevices];
+    cudaError_t err = allow_shared(attn_few_kernel<D, NT>, smem, ready);
+    if (err != cudaSuccess)
+        return err;
     err = launch_kernel(attn_few_kernel<D, NT>, dim3(kBlocks), dim3(kThreads), smem, stream, pdl, a);
     if (err != cudaSuccess)
         return err;
-    return launch_kernel(attn_join_kernel<D>, dim3(kBlocks, 8 * NT), dim3(256), 0, stream, true, a, kBlocks, 8 * NT);
+    // at most as many units as rows of 8 NT, and one more for each sequence and head
+    const int64_t units = a.cache.heads * (a.T * a.group / (8 * NT) + a.B);
+    return launch_kernel(attn_join_kernel<D>, dim3((unsigned)(units < kBlocks ? units : kBlocks), 8 * NT), dim3(256), 0, stream, true, a,
+                         kBlocks, 8 * NT);
 }
 
 }  // namespace
 
+bool attn_few_clusters(int64_t B, int64_t heads, int64_t rows, int64_t keys)
+{
+    const int64_t units = B * heads * (rows <= 8 ? 1 : (rows + 15) / 16);
+    return units <= kClusterUnits && keys <= kClusterKeys;
+}
+
 cudaError_t launch_attn_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t stream)
 {
     if (a.D == 64)
-        return rows <= 8 ? launch_few<64, 1>(a, pdl, stream) : launch_few<64, 2>(a, pdl, stream);
-    return rows <= 8 ? launch_few<128, 1>(a, pdl, stream) : launch_few<128, 2>(a, pdl, stream);
+        return rows <= 8 ? launch_few<64, 1>(a, rows, pdl, stream) : launch_few<64, 2>(a, rows, pdl, stream);
+    return rows <= 8 ? launch_few<128, 1>(a, rows, pdl, stream) : launch_few<128, 2>(a, rows, pdl, stream);
 }
 
 int64_t attn_few_workspace(int64_t D)

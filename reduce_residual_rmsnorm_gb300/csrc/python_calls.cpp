@@ -233,6 +233,24 @@ public:
         return t;
     }
 
+    // Outputs like two tensors of heads, given or new; small new ones share an allocation.
+    void two_heads(int i, const char *name, const at::Tensor &like, int64_t *ld, const char *name2, const at::Tensor &like2,
+                   int64_t *ld2, bool second, at::Tensor &out, at::Tensor &out2)
+    {
+        const int64_t at = (like.numel() + 127) / 128 * 128, all = at + like2.numel();
+        if (second && none(i) && none(i + 1) && all <= 32768) {
+            const at::Tensor both = fresh(dims(all), kBF16, like);
+            out = part_of(both, 0, dims(like.size(0), like.size(1), like.size(2)));
+            out2 = part_of(both, at, dims(like2.size(0), like2.size(1), like2.size(2)));
+            *ld = like.size(1) * like.size(2);
+            *ld2 = like2.size(1) * like2.size(2);
+            return;
+        }
+        out = heads_output(i, name, like, ld);
+        if (second)
+            out2 = heads_output(i + 1, name2, like2, ld2);
+    }
+
     // The cache of three arguments (pages, k_scale, v_scale).
     ts_kv_cache_t cache(int i)
     {
@@ -302,10 +320,13 @@ public:
         return at::empty(d.ref(), at::TensorOptions().dtype(type).pinned_memory(true));
     }
 
-    // A contiguous tensor on part of another's storage.
-    static at::Tensor part_of(const at::Tensor &all, int64_t offset, const Dims &d)
+    // A contiguous tensor on part of another's storage; the offset in elements of its type.
+    static at::Tensor part_of(const at::Tensor &all, int64_t offset, const Dims &d) { return part_of(all, offset, d, all.scalar_type()); }
+
+    static at::Tensor part_of(const at::Tensor &all, int64_t offset, const Dims &d, at::ScalarType type)
     {
-        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                                c10::scalarTypeToTypeMeta(type));
         t.unsafeGetTensorImpl()->set_storage_offset(offset);
         t.unsafeGetTensorImpl()->set_sizes_contiguous(d.ref());
         return t;
@@ -627,10 +648,8 @@ PyObject *qk_norm_rope(PyObject *const *args, Py_ssize_t n)
     } else if (!c.none(8) || !c.none(12)) {
         raise(PyExc_ValueError, "v and slots need a cache");
     }
-    const at::Tensor qo = c.heads_output(13, "q_out", q, &ldqo);
-    at::Tensor ko;
-    if (!kept || !c.none(14))
-        ko = c.heads_output(14, "k_out", k, &ldko);
+    at::Tensor qo, ko;
+    c.two_heads(13, "q_out", q, &ldqo, "k_out", k, &ldko, !kept || !c.none(14), qo, ko);
     void *const qp = ptr(qo), *const kp = ko.defined() ? ptr(ko) : nullptr;
     c.run([&](uint32_t flags, void *stream) {
         return ts_qk_norm_rope(ptr(q), ldq, ptr(k), ldk, T, hq, hk, D, qw, kw, eps, ptr<int32_t>(pos), ptr<float>(table),
@@ -661,14 +680,20 @@ PyObject *qk_norm_rope_grad(PyObject *const *args, Py_ssize_t n)
         raise(PyExc_ValueError, "cos_sin must be [max_pos, rot]");
     const float eps = (float)c.number(8);
     const bool pairs = c.truth(9);
-    const at::Tensor dq = c.heads_output(10, "dq", q, &lddq), dk = c.heads_output(11, "dk", k, &lddk);
-    at::Tensor dqw, dkw, space;
+    at::Tensor dq, dk, dqw, dkw, space;
+    c.two_heads(10, "dq", q, &lddq, "dk", k, &lddk, true, dq, dk);
     if (norm) {
         const int64_t bytes = ts_qk_norm_rope_grad_workspace(D);
         if (bytes < 0)
             raise(PyExc_ValueError, "head_dim %lld out of range", (long long)D);
-        dqw = c.output(12, "dq_weight", kF32, dims(D), q);
-        dkw = c.output(13, "dk_weight", kF32, dims(D), q);
+        if (c.none(12) && c.none(13)) {
+            const at::Tensor both = c.fresh(dims(2, (D + 63) / 64 * 64), kF32, q);
+            dqw = Call::part_of(both, 0, dims(D));
+            dkw = Call::part_of(both, (D + 63) / 64 * 64, dims(D));
+        } else {
+            dqw = c.output(12, "dq_weight", kF32, dims(D), q);
+            dkw = c.output(13, "dk_weight", kF32, dims(D), q);
+        }
         space = c.workspace(14, bytes, q);
     } else if (!c.none(12) || !c.none(13)) {
         raise(PyExc_ValueError, "gradients of weights that are not given");
@@ -735,21 +760,29 @@ PyObject *attention(PyObject *const *args, Py_ssize_t n)
     const float scale = c.none(8) ? (float)(1.0 / std::sqrt((double)(D > 0 ? D : 1))) : (float)c.number(8);
     const bool causal = c.truth(9);
     const int64_t window = c.integer(10);
-    const int64_t bytes = ts_nvfp4_attention_workspace(hq, cache.heads, D, max_q);
-    const at::Tensor out = c.heads_output(11, "out", q, &ldo);
-    if (!out.is_cuda())
-        raise(PyExc_TypeError, "out must be a CUDA tensor");
-    at::Tensor lse;
-    if (!c.none(12) || c.truth(13)) {
-        lse = c.output(12, "lse", kF32, dims(T, hq), q);
-        if (!lse.is_cuda())
-            raise(PyExc_TypeError, "lse must be a CUDA tensor");
+    const int64_t bytes = ts_nvfp4_attention_workspace(B, hq, cache.heads, D, max_q, table.size(1) * cache.page_size);
+    const bool with_lse = !c.none(12) || c.truth(13);
+    at::Tensor out, lse, space;
+    const int64_t lse_at = (T * hq * D * 2 + 255) / 256 * 256;
+    if (c.none(11) && c.none(12) && with_lse && lse_at <= 65536) {  // small ones share an allocation
+        const at::Tensor all = c.fresh(dims((lse_at + T * hq * 4) / 2), kBF16, q);
+        out = Call::part_of(all, 0, dims(T, hq, D));
+        lse = Call::part_of(all, lse_at / 4, dims(T, hq), kF32);
+        ldo = hq * D;
+    } else {
+        out = c.heads_output(11, "out", q, &ldo);
+        if (with_lse)
+            lse = c.output(12, "lse", kF32, dims(T, hq), q);
     }
-    const at::Tensor space = c.workspace(14, bytes < 0 ? 0 : bytes, q);  // (the call refuses the sizes)
+    if (!out.is_cuda() || (with_lse && !lse.is_cuda()))
+        raise(PyExc_TypeError, "out and lse must be CUDA tensors");
+    if (bytes > 0 || !c.none(14))  // (where the sizes are refused, by the call)
+        space = c.workspace(14, bytes < 0 ? 0 : bytes, q);
     float *const lp = lse.defined() ? ptr<float>(lse) : nullptr;
+    void *const sp = space.defined() ? ptr(space) : nullptr;
     c.run([&](uint32_t flags, void *stream) {
         return ts_nvfp4_attention(ptr(q), ldq, T, hq, cu, B, max_q, &cache, ptr<int32_t>(table), table.size(1),
-                                  ptr<int32_t>(lens), scale, causal, window, ptr(out), ldo, lp, ptr(space), flags, stream);
+                                  ptr<int32_t>(lens), scale, causal, window, ptr(out), ldo, lp, sp, flags, stream);
     });
     if (!c.truth(13))
         return THPVariable_Wrap(out);

@@ -7,10 +7,11 @@
 // bytes each (a power of two of lanes, those behind D/8 idle), so the sum of squares
 // is a butterfly of a few steps and a lane's partner in the rotation is at a fixed
 // distance.  The partner's raw bf16 are exchanged, not its normed fp32: half the
-// shuffles, and each lane norms both, with the same bits.  A group of lanes takes a
-// run of up to U heads of one token: their loads are issued together, and the
-// position's cosines and sines and the weights are read once for them.
+// shuffles, and what they are multiplied by goes into the factors.  A group of lanes
+// takes a run of up to U heads of one token: their loads are issued together, and the
+// position's cosines and sines and the weights are read, and multiplied, once for them.
 #include "device_util.cuh"
+#include "f32x2.cuh"
 #include "launch_attention.h"
 
 namespace tsfn {
@@ -67,33 +68,54 @@ __device__ __forceinline__ Turn turn_of(int c, int lane, int rot, bool pairs)
     return t;
 }
 
-// y = x turned by the angles, forwards (s = 1) or back (s = -1).  PAIRS: the chunk's
-// own neighbours; else `other` holds the partner chunk.
+// What a lane's 8 columns are multiplied by, and their partners: the rotation is
+//   y = x by + x' with,   x' the partner's columns (PAIRS: the neighbours exchanged),
+// by = cos, with = -+ sin; 1 and 0 for columns that are not rotated; s = -1 turns back.
+struct Factors {
+    uint64_t by[4], with[4];
+};
+
 template <bool PAIRS>
-__device__ __forceinline__ void rotate(float (&x)[8], const float (&other)[8], const float (&cs)[8], const float (&sn)[8],
-                                       const Turn &t, float s)
+__device__ __forceinline__ Factors factors_of(const float (&cs)[8], const float (&sn)[8], const Turn &t, float s)
 {
-    if (!t.in)
-        return;
-    if (PAIRS) {
+    Factors f;
+    const float k = t.first ? -s : s;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1], k = s * sn[i];
-            x[2 * i] = __fmaf_rn(a, cs[i], -__fmul_rn(b, k));
-            x[2 * i + 1] = __fmaf_rn(b, cs[i], __fmul_rn(a, k));
+    for (int i = 0; i < 4; ++i) {
+        if (PAIRS) {
+            f.by[i] = t.in ? twice(cs[i]) : twice(1.0f);
+            f.with[i] = t.in ? pair(-s * sn[i], s * sn[i]) : 0;
+        } else {
+            f.by[i] = t.in ? pair(cs[2 * i], cs[2 * i + 1]) : twice(1.0f);
+            f.with[i] = t.in ? pair(k * sn[2 * i], k * sn[2 * i + 1]) : 0;
         }
-    } else {
-        const float k = t.first ? -s : s;
+    }
+    return f;
+}
+
+// The lane's partner columns: another lane's, or its own neighbours exchanged; zeros where
+// nothing is rotated (0 times an infinity would not be 0).
+template <bool PAIRS>
+__device__ __forceinline__ void partners(const uint4 &x, const Turn &t, uint64_t (&o)[4])
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = __fmaf_rn(x[e], cs[e], k * __fmul_rn(other[e], sn[e]));
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t p = PAIRS ? __funnelshift_l(w[i], w[i], 16) : __shfl_sync(0xffffffffu, w[i], t.partner);
+        o[i] = widen2(t.in ? p : 0u);
     }
 }
 
-__device__ __forceinline__ uint4 shuffle4(const uint4 &v, int from)
+__device__ __forceinline__ uint4 pack2x4(const uint64_t (&v)[4])
 {
-    return make_uint4(__shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from),
-                      __shfl_sync(0xffffffffu, v.z, from), __shfl_sync(0xffffffffu, v.w, from));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpair(v[i], lo, hi);
+        w[i] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Where the codes of K and V and the scale factors of a slot's head begin.
@@ -182,38 +204,44 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
     const uint16_t *w = kind == 0 ? a.qw : a.kw;
     const bool norm = turned && w != nullptr;
-    float wf[8], wp[8];
+    // the weights go into the factors, once for the run:  y = (x r) (w cos) + (x' r) (w' sin)
+    Factors f = factors_of<PAIRS>(cs, sn, turn, 1.0f);
     if (norm && in_row) {
-        unpack8(ld_again(w + c * 8), wf);
-        unpack8(ld_again(w + (c + turn.partner - lane) * 8), wp);
+        const uint4 own = ld_again(w + c * 8);
+        uint64_t wp[4];
+        const uint4 other = PAIRS ? own : ld_again(w + (c + turn.partner - lane) * 8);
+        const uint32_t ww[4] = {own.x, own.y, own.z, own.w}, wo[4] = {other.x, other.y, other.z, other.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wp[i] = widen2(PAIRS ? __funnelshift_l(wo[i], wo[i], 16) : wo[i]);
+            f.by[i] = mul2(f.by[i], widen2(ww[i]));
+            f.with[i] = mul2(f.with[i], wp[i]);
+        }
     }
     pdl_launch_dependents();
+    const float inv_d = 1.0f / (float)a.D;
 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const bool on = live && in_row && h0 + u < heads;
-        const float r = rsqrtf(__fadd_rn(__fdiv_rn(group_sum(sumsq_bf16x8(x[u], 0.0f), lanes), (float)a.D), a.eps));
-        float f[8], o[8] = {};
-        unpack8(x[u], f);
-        if (!PAIRS)
-            unpack8(shuffle4(x[u], turn.partner), o);
-        if (norm) {
+        float r = 1.0f;
+        if (a.qw != nullptr)
+            r = rsqrtf(__fmaf_rn(group_sum(sumsq_bf16x8(x[u], 0.0f), lanes), inv_d, a.eps));
+        uint64_t o[4], y2[4];
+        partners<PAIRS>(x[u], turn, o);
+        const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[e] = __fmul_rn(__fmul_rn(f[e], r), wf[e]);
-                o[e] = __fmul_rn(__fmul_rn(o[e], r), wp[e]);
-            }
-        }
-        rotate<PAIRS>(f, o, cs, sn, turn, 1.0f);
-        const uint4 y = turned ? pack8(f) : x[u];
+        for (int i = 0; i < 4; ++i)
+            y2[i] = fma2(mul2(widen2(xw[i]), twice(r)), f.by[i], mul2(mul2(o[i], twice(r)), f.with[i]));
+        const uint4 y = turned ? pack2x4(y2) : x[u];
         if (on && turned) {
             uint16_t *dst = kind == 0 ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko;
             if (kind == 0 || a.k_out != nullptr)
                 st_v4(dst + (int64_t)(h0 + u) * a.D + c * 8, y);
         }
-        if (CACHE) {
+        const bool keep = CACHE && on && slot >= 0;
+        if (CACHE && __any_sync(0xffffffffu, keep)) {  // (most warps have queries only)
             int in_tile = 0;
-            const bool keep = on && slot >= 0;
             uint8_t *tile = keep ? cache_tile(a.cache, a.D, slot, h0 + u, &in_tile) : nullptr;
             const int second = kind == 2 ? 1 : 0;
             put_chunk(y, g, keep, tile + second * 8 * a.D + in_tile * (a.D >> 1),
@@ -229,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 // dx as above; the weights' gradient is summed by each lane over its runs, then over
 // the groups of a block in order, and over the blocks by grad_sum_kernel.
 template <int U, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) rope_grad_kernel(const __grid_constant__ RopeGradArgs a)
+__global__ void __launch_bounds__(kThreads, 3) rope_grad_kernel(const __grid_constant__ RopeGradArgs a)
 {
     extern __shared__ float sums[];  // [groups of lanes][lanes * 8]
     const int lanes = 1 << a.lanes_log2;
@@ -237,14 +265,19 @@ __global__ void __launch_bounds__(kThreads) rope_grad_kernel(const __grid_consta
     const int groups = kThreads >> a.lanes_log2, group = threadIdx.x >> a.lanes_log2;
     const bool in_row = c < (a.D >> 3);
     const Turn turn = turn_of(c, lane, a.rot, PAIRS);
+    const float inv_d = 1.0f / (float)a.D;
     pdl_wait();
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         const uint16_t *w = a.w[kind];
-        float wf[8];
-        if (w != nullptr && in_row)
-            unpack8(ld_again(w + c * 8), wf);
-        float acc[8] = {};
+        uint64_t wf[4] = {}, acc[4] = {};
+        if (w != nullptr && in_row) {
+            const uint4 v = ld_again(w + c * 8);
+            const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                wf[i] = widen2(ww[i]);
+        }
         const int64_t all = a.T * a.runs[kind];
         // (a warp's lanes stay together: the loop's bound is that of its first group)
         const int64_t per = (int64_t)gridDim.x * groups;
@@ -271,43 +304,49 @@ __global__ void __launch_bounds__(kThreads) rope_grad_kernel(const __grid_consta
                 ld_angles(p, PAIRS ? 1 : 2, cs);
                 ld_angles(p + (a.rot >> 1), PAIRS ? 1 : 2, sn);
             }
+            const Factors f = factors_of<PAIRS>(cs, sn, turn, -1.0f);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const bool on = live && in_row && h0 + u < a.heads[kind];
-                float f[8], o[8] = {}, xf[8];
-                unpack8(d[u], f);
-                if (!PAIRS)
-                    unpack8(shuffle4(d[u], turn.partner), o);
-                rotate<PAIRS>(f, o, cs, sn, turn, -1.0f);
+                const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w}, xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                uint64_t o[4], v[4];
+                partners<PAIRS>(d[u], turn, o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = fma2(widen2(dw[i]), f.by[i], mul2(o[i], f.with[i]));
                 if (w != nullptr) {
-                    unpack8(x[u], xf);
-                    const float inv_d = 1.0f / (float)a.D;
-                    const float r = rsqrtf(__fadd_rn(group_sum(sumsq_bf16x8(x[u], 0.0f), lanes) * inv_d, a.eps));
-                    float dot = 0.0f;
+                    // both sums over the row side by side: x^2, and g x with g = d w
+                    uint64_t gx = 0;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float xr = xf[e] * r;
-                        if (on)
-                            acc[e] = __fmaf_rn(f[e], xr, acc[e]);
-                        f[e] = on ? f[e] * wf[e] : 0.0f;
-                        xf[e] = xr;
-                        dot = __fmaf_rn(f[e], xr, dot);
+                    for (int i = 0; i < 4; ++i)
+                        gx = fma2(mul2(v[i], wf[i]), widen2(xw[i]), gx);
+                    float s0, s1;
+                    unpair(gx, s0, s1);
+                    float sq = sumsq_bf16x8(x[u], 0.0f), dot = s0 + s1;
+                    for (int k = lanes >> 1; k > 0; k >>= 1) {
+                        sq += __shfl_xor_sync(0xffffffffu, sq, k);
+                        dot += __shfl_xor_sync(0xffffffffu, dot, k);
                     }
-                    dot = group_sum(dot, lanes) * inv_d;
+                    const float r = rsqrtf(__fmaf_rn(sq, inv_d, a.eps));
+                    const uint64_t by = twice(r), less = twice(-(dot * inv_d) * r * r);
+                    const uint64_t sum = twice(on ? r : 0.0f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f[e] = r * __fmaf_rn(-xf[e], dot, f[e]);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t xf = widen2(xw[i]);
+                        acc[i] = fma2(mul2(v[i], xf), sum, acc[i]);
+                        v[i] = mul2(fma2(xf, less, mul2(v[i], wf[i])), by);
+                    }
                 }
                 if (on)
-                    st_v4(a.dx[kind] + t * a.lddx[kind] + (int64_t)(h0 + u) * a.D + c * 8, pack8(f));
+                    st_v4(a.dx[kind] + t * a.lddx[kind] + (int64_t)(h0 + u) * a.D + c * 8, pack2x4(v));
             }
         }
         if (w != nullptr) {
             if (kind == 1)
                 __syncthreads();  // the queries' sums have been read
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sums[group * lanes * 8 + c * 8 + e] = acc[e];
+            for (int i = 0; i < 4; ++i)
+                unpair(acc[i], sums[group * lanes * 8 + c * 8 + 2 * i], sums[group * lanes * 8 + c * 8 + 2 * i + 1]);
             __syncthreads();
             for (int j = threadIdx.x; j < a.D; j += kThreads) {
                 float s = 0.0f;
@@ -371,14 +410,18 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
                 if (a.out[i] == nullptr)
                     continue;
                 const float s = __fdiv_rn(e4m3_value(sf[i]), i == 0 ? *a.cache.k_scale : *a.cache.v_scale);
+                // (E2M1 is exact in fp16, and that in fp32)
+                uint32_t two[4];
+                asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+                    "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+                    : "=r"(two[0]), "=r"(two[1]), "=r"(two[2]), "=r"(two[3]) : "r"(codes[i]));
                 float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t q = (codes[i] >> (4 * e)) & 15;
-                    // E2M1: 0.5 for an exponent of 0, else (2 + m) 2^(e - 2); -0 keeps its sign
-                    const uint32_t m = q & 7;
-                    const float v = m < 2 ? 0.5f * (float)m : __uint_as_float(((126 + (m >> 1)) << 23) | ((m & 1) << 22));
-                    f[e] = __fmul_rn(q & 8 ? -v : v, s);
+                for (int e = 0; e < 4; ++e) {
+                    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+                        : "=f"(f[2 * e]), "=f"(f[2 * e + 1]) : "r"(two[e]));
+                    f[2 * e] = __fmul_rn(f[2 * e], s);
+                    f[2 * e + 1] = __fmul_rn(f[2 * e + 1], s);
                 }
                 st_v4(a.out[i] + t * a.ld[i] + (int64_t)h * a.D + c * 8, pack8(f));
             }

@@ -323,6 +323,14 @@ __device__ __forceinline__ uint32_t ld_cluster32(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ float4 ld_cluster128(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // 16 bytes into the shared memory of a block of the cluster, counted on a barrier
 // of that block when they are there (both addresses of map_rank).
 __device__ __forceinline__ void st_async_cluster(uint32_t addr, uint4 v, uint32_t bar)

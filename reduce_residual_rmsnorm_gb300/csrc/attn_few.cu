@@ -42,9 +42,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 // Blocks of an SM and copies of tiles in flight: 16 rows take the registers of a whole SM.
 constexpr int blocks_per_sm(int nt) { return nt == 1 ? 2 : 1; }
-constexpr int blocks_of(int nt) { return 152 * blocks_per_sm(nt); }
+constexpr int kSms = 152;
+constexpr int blocks_of(int nt) { return kSms * blocks_per_sm(nt); }
 constexpr int stages_of(int nt) { return nt == 1 ? 4 : 6; }
 constexpr int kShare = 8;     // tiles of a share, at least
+constexpr int kWay = 24;      // what going to a unit costs, in tiles of a block, when work is split
 // Clusters take calls of few units and not too many keys.
 constexpr int64_t kClusterUnits = 76, kClusterKeys = 16384;
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -473,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t sums[kThreads];
     __shared__ int64_t warp_sums[kWarps];
-    __shared__ int64_t state[4];
+    __shared__ int64_t state[6];
+    __shared__ Run kept;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float *const slots = a.partial + (int64_t)gridDim.x * (sizeof(Record) / 4);
     Record *const record = reinterpret_cast<Record *>(a.partial) + blockIdx.x;
@@ -483,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
     const int per = (a.B + kThreads - 1) / kThreads;
     int64_t sum = 0;
     for (int b = tid * per; b < a.B && b < (tid + 1) * per; ++b)
-        sum += weight(a, sequence<NR>(a, b));
+        sum += weight(a, sequence<NR>(a, b), kWay);
     int64_t scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -526,17 +529,23 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
         base = lo > 0 ? sums[lo - 1] : 0;
     }
     run.s = sequence<NR>(a, run.b);
-    const float vg = *a.cache.v_scale, c0 = a.scale * kLog2e / *a.cache.k_scale;
+    const float c0 = a.scale * kLog2e / *a.cache.k_scale;
 
     while (pos < end) {
-        while (pos >= base + weight(a, run.s)) {
-            base += weight(a, run.s);
+        while (pos >= base + weight(a, run.s, kWay)) {
+            base += weight(a, run.s, kWay);
             run.s = sequence<NR>(a, ++run.b);
         }
-        const int64_t unit = (pos - base) / run.s.tiles;
-        const int skip = (int)(pos - base - unit * run.s.tiles);
-        run.count = (int)(run.s.tiles - skip < end - pos ? run.s.tiles - skip : end - pos);
-        run.first = run.s.first + skip;
+        const int64_t unit = (pos - base) / (run.s.tiles + kWay);
+        const int skip = (int)(pos - base - unit * (run.s.tiles + kWay)), all = run.s.tiles + kWay - skip;
+        const int length = (int)(all < end - pos ? all : end - pos);
+        run.first = max(skip - kWay, 0);
+        run.count = max(skip + length - kWay, 0) - run.first;
+        if (run.count == 0) {  // the way alone
+            pos += length;
+            continue;
+        }
+        run.first += run.s.first;
         run.head = (int)(unit / run.s.parts);
         run.row0 = (int)(unit - (int64_t)run.head * run.s.parts) * NR;
         run.rows = run.s.n * a.group - run.row0 < NR ? run.s.n * a.group - run.row0 : NR;
@@ -546,15 +555,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
             state[1] = end;
             state[2] = base;
             state[3] = share;
+            state[4] = pos - skip + run.s.tiles + kWay;  // the unit's end
+            state[5] = length;
+            kept = run;
         }
-        attend<D, NT>(a, run, c0, smem);
+        __syncthreads();
+        attend<D, NT>(a, kept, c0, smem);
+        run = kept;
         pos = state[0];
         end = state[1];
         base = state[2];
         const bool begins = run.first == run.s.first, ends = run.first + run.count == run.s.first + run.s.tiles;
-        const int tile0 = run.first - run.s.first;
         if (begins && !ends && tid == 0) {
-            record->last = (int32_t)((pos - tile0 + run.s.tiles - 1) / state[3]);
+            record->last = (int32_t)((state[4] - 1) / state[3]);
             record->q0 = run.s.q0;
             record->head = run.head;
             record->rows = run.rows;
@@ -566,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
             float top, sum_l;
             const float4 acc = join_warps<D, NT>(smem, row, d, top, sum_l);
             if (begins && ends) {
-                put_row<D>(a, run.s.q0, run.head, run.row0 + row, d, acc, top, sum_l, vg);
+                put_row<D>(a, run.s.q0, run.head, run.row0 + row, d, acc, top, sum_l, *a.cache.v_scale);
             } else {
                 *reinterpret_cast<float4 *>(slot + row * D + d) = acc;
                 if (d == 0) {
@@ -575,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
                 }
             }
         }
-        __syncthreads();  // before the ring is filled again
-        pos += run.count;
+        pos += state[5];
+        __syncthreads();  // before the state and the ring are filled again
     }
     pdl_launch_dependents();
 }
@@ -648,85 +661,101 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_cluster_kern
     pdl_launch_dependents();
 }
 
-// Units over several blocks: block (x, y) has row y of the x-th of them, a share of the
-// parts for each set of lanes, whose loads are all under way together.
-template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a, int blocks, int NR)
+// Units over several blocks: block (x, y) has row y of the x-th of them, each set of
+// lanes a run of the parts in order, whose loads are all under way together.
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) attn_join_kernel(const __grid_constant__ AttnArgs a, int blocks, int NR)
 {
-    constexpr int kLanes = D / 4, kSets = 256 / kLanes;
+    constexpr int kLanes = D / 4, kSets = THREADS / kLanes, kMost = 2 * kSms;
     __shared__ float4 acc_of[kSets][kLanes];
-    __shared__ float m_of[kSets], l_of[kSets];
-    __shared__ int which;
-    const int row = blockIdx.y;
+    __shared__ float factor[kMost], l_of[kSets], top_of[THREADS / 32];
+    __shared__ int counts[kMost / 32 + 1], which;
+    const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     pdl_wait();
     pdl_launch_dependents();
     const Record *records = reinterpret_cast<const Record *>(a.partial);
     int first = blockIdx.x;
     if ((int)gridDim.x < blocks) {  // fewer units than blocks: look for the x-th that is over several
-        if (threadIdx.x < 32) {
-            int before = 0, found = -1;
-            for (int i0 = 0; i0 < blocks; i0 += 32) {
-                const int i = i0 + (int)threadIdx.x;
-                const bool split = i < blocks && records[i].last >= 0;
-                const unsigned some = __ballot_sync(0xffffffffu, split);
-                if (split && before + __popc(some & ((1u << threadIdx.x) - 1)) == first)
-                    found = i;
-                before += __popc(some);
+        if (tid == 0)
+            which = -1;
+        for (int i = tid; i < (blocks + 31) / 32 * 32; i += THREADS) {
+            const unsigned some = __ballot_sync(0xffffffffu, i < blocks && records[i].last >= 0);
+            if (lane == 0)
+                counts[i >> 5] = (int)some;
+        }
+        __syncthreads();
+        if (tid < 32) {
+            const unsigned some = lane < (blocks + 31) / 32 ? (unsigned)counts[lane] : 0u;
+            int before = __popc(some);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o)
+                    before += up;
             }
-            found = __reduce_max_sync(0xffffffffu, found);
-            if (threadIdx.x == 0)
-                which = found;
+            before -= __popc(some);
+            for (unsigned left = some; left != 0; left &= left - 1, ++before)
+                if (before == first)
+                    which = lane * 32 + __ffs(left) - 1;
         }
         __syncthreads();
         first = which;
+        if (first < 0)
+            return;
     }
-    if (first < 0)
-        return;
     const Record rec = records[first];
     if (rec.last < 0 || row >= rec.rows)
         return;
     const float *slots = a.partial + (int64_t)blocks * (sizeof(Record) / 4);
-    const int set = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 4;
-    // each set of lanes takes a run of the blocks, so that the order is the keys'
-    const int n = rec.last - first + 1, per = (n + kSets - 1) / kSets;
-    const int i0 = min(n, set * per), i1 = min(n, i0 + per);
     auto slot_of = [&](int i) { return slots + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * slot_floats(NR, D); };
-    float m = -INFINITY, l = 0.0f;
-#pragma unroll 8
-    for (int i = i0; i < i1; ++i)
-        m = fmaxf(m, slot_of(i)[NR * D + row]);
+    const int n = rec.last - first + 1;  // at most `blocks`
+    // the parts' maxima, and what each part counts for
+    float top = -INFINITY;
+    for (int i = tid; i < n; i += THREADS) {
+        factor[i] = slot_of(i)[NR * D + row];
+        top = fmaxf(top, factor[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0)
+        top_of[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i)
+        top = fmaxf(top, top_of[i]);
+    const int set = tid / kLanes, d = (tid % kLanes) * 4, per = (n + kSets - 1) / kSets;
+    const int i0 = min(n, set * per), i1 = min(n, i0 + per);
+    float l = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
     for (int i = i0; i < i1; ++i) {
         const float *slot = slot_of(i);
-        const float li = slot[NR * D + NR + row], f = join_factor(slot[NR * D + row], li, m);
+        const float li = slot[NR * D + NR + row];
         const float4 v = *reinterpret_cast<const float4 *>(slot + row * D + d);
+        const float f = join_factor(factor[i], li, top);
         l = fmaf(f, li, l);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
     }
-    acc_of[set][threadIdx.x % kLanes] = acc;
-    if (d == 0) {
-        m_of[set] = m;
+    acc_of[set][tid % kLanes] = acc;
+    if (d == 0)
         l_of[set] = l;
-    }
     __syncthreads();
     if (set != 0)
         return;
-    float top = -INFINITY, sum = 0.0f;
-    for (int i = 0; i < kSets; ++i)
-        top = fmaxf(top, m_of[i]);
+    float sum = 0.0f;
     acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
     for (int i = 0; i < kSets; ++i) {
-        const float f = join_factor(m_of[i], l_of[i], top);
-        const float4 v = acc_of[i][threadIdx.x];
-        sum = fmaf(f, l_of[i], sum);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+        const float4 v = acc_of[i][tid];
+        sum += l_of[i];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
     }
     put_row<D>(a, rec.q0, rec.head, rec.row0 + row, d, acc, top, sum, *a.cache.v_scale);
 }
@@ -769,7 +798,9 @@ cudaError_t launch_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t s
         return err;
     // at most as many units as rows of 8 NT, and one more for each sequence and head
     const int64_t units = a.cache.heads * (a.T * a.group / (8 * NT) + a.B);
-    return launch_kernel(attn_join_kernel<D>, dim3((unsigned)(units < kBlocks ? units : kBlocks), 8 * NT), dim3(256), 0, stream, true, a,
+    if (units < 32)  // few units, of many parts each
+        return launch_kernel(attn_join_kernel<D, 1024>, dim3((unsigned)units, 8 * NT), dim3(1024), 0, stream, true, a, kBlocks, 8 * NT);
+    return launch_kernel(attn_join_kernel<D, 256>, dim3((unsigned)(units < kBlocks ? units : kBlocks), 8 * NT), dim3(256), 0, stream, true, a,
                          kBlocks, 8 * NT);
 }
 

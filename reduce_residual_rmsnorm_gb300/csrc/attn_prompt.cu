@@ -46,7 +46,7 @@ constexpr int kThreads = kRows + kMakers + 128;  // four warp groups; of the las
 // Registers of a thread of each: the 128 that each is launched with, divided anew.
 constexpr int kRowRegs = 192, kMakerRegs = 72, kOtherRegs = 56;
 static_assert(kRows * kRowRegs + kMakers * kMakerRegs + 128 * kOtherRegs <= kThreads * 128, "");
-constexpr int kSwitch = 2;           // what going to a unit costs, in steps, when work is split
+constexpr int kSwitch = 4;           // what going to a unit costs, in steps, when work is split
 constexpr int kCopies = 13;          // the warp that copies codes
 constexpr int kProducts = 12;        // the warp that issues them
 constexpr int kSeqs = 256;          // sequences whose weights are summed at a time

@@ -60,7 +60,7 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
     return s;
 }
 
-__device__ __forceinline__ int64_t weight(const AttnArgs &a, const Seq &s) { return (int64_t)s.parts * a.cache.heads * s.tiles; }
+__device__ __forceinline__ int64_t weight(const AttnArgs &a, const Seq &s, int way) { return (int64_t)s.parts * a.cache.heads * (s.tiles + way); }
 
 // The power of two that takes a row of q with the largest magnitude amax into [2^7, 2^8),
 // where fp16 loses only what is below 2^-33 of amax; and its inverse.

@@ -41,8 +41,8 @@ struct RopeArgs {
     bool keep;  // with a cache
     CacheArgs cache;
     const int32_t *slots;
-    // a run is up to U heads of one token; runs of q, k and v of a token
-    int runs_q, runs_k, runs;
+    // a run: up to run_heads heads of one token; runs of q, of k, and all of a token
+    int run_heads, runs_q, runs_k, runs;
     DivMagic div_runs;
 };
 
@@ -62,7 +62,7 @@ struct RopeGradArgs {
     int64_t lddx[2];
     float *dw[2];
     float *partial;  // [blocks, 2, D]
-    int runs[2];     // runs of a token
+    int run_heads, runs[2];  // as above
     DivMagic div_runs[2];
 };
 
@@ -97,8 +97,8 @@ struct AttnArgs {
     float *partial;
 };
 
-// Blocks of the gradient: three for each of 152 SMs.
-constexpr int kGradBlocks = 456;
+// Blocks of the gradient: five for each of 152 SMs.
+constexpr int kGradBlocks = 760;
 
 cudaError_t launch_rope(const RopeArgs &a, bool pdl, cudaStream_t stream);
 cudaError_t launch_rope_grad(const RopeGradArgs &a, bool pdl, cudaStream_t stream);

@@ -8,7 +8,7 @@
 // is a butterfly of a few steps and a lane's partner in the rotation is at a fixed
 // distance.  The partner's raw bf16 are exchanged, not its normed fp32: half the
 // shuffles, and what they are multiplied by goes into the factors.  A group of lanes
-// takes a run of up to U heads of one token: their loads are issued together, and the
+// takes a run of heads of one token, the next ones' loads under way, and the
 // position's cosines and sines and the weights are read, and multiplied, once for them.
 #include "device_util.cuh"
 #include "f32x2.cuh"
@@ -156,10 +156,10 @@ __device__ __forceinline__ void put_chunk(const uint4 &v, float g, bool live, ui
     }
 }
 
-// U: heads of a run.  1 where the call is short, so that it spreads over the SMs; the
-// bits do not depend on it.
-template <int U, bool PAIRS, bool CACHE>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a)
+// A group of lanes takes a run of heads of one token, two at a time with the next two's
+// loads under way.
+template <bool PAIRS, bool CACHE>
+__global__ void __launch_bounds__(kThreads, CACHE ? 3 : 4) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     const int lanes = 1 << a.lanes_log2;
     const int lane = threadIdx.x & 31, c = lane & (lanes - 1);
@@ -169,21 +169,25 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int run = (int)(id - t * a.runs);
     // queries, keys, values
     const int kind = run < a.runs_q ? 0 : (run < a.runs_q + a.runs_k ? 1 : 2);
-    const int h0 = (kind == 0 ? run : (kind == 1 ? run - a.runs_q : run - a.runs_q - a.runs_k)) * U;
+    const int h0 = (kind == 0 ? run : (kind == 1 ? run - a.runs_q : run - a.runs_q - a.runs_k)) * a.run_heads;
     const int heads = kind == 0 ? a.hq : a.hk;
     const bool in_row = c < (a.D >> 3);
     pdl_wait();
 
     bool live = t < a.T;
     const int32_t pos = live ? a.pos[t] : -1;
-    const uint16_t *src = kind == 0 ? a.q + t * a.ldq : (kind == 1 ? a.k + t * a.ldk : a.v + t * a.ldv);
-    uint4 x[U];
+    const int n = live ? min(a.run_heads, heads - h0) : 0, most = __reduce_max_sync(0xffffffffu, n);
+    const uint16_t *src = (kind == 0 ? a.q + t * a.ldq : (kind == 1 ? a.k + t * a.ldk : a.v + t * a.ldv)) + (int64_t)h0 * a.D + c * 8;
+    uint4 x[2], next[2];
+    auto load = [&](int h, uint4 (&to)[2]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (live && in_row && h0 + u < heads)
-            x[u] = ld_stream(src + (int64_t)(h0 + u) * a.D + c * 8);
-    }
+        for (int u = 0; u < 2; ++u) {
+            to[u] = make_uint4(0, 0, 0, 0);
+            if (in_row && h + u < n)
+                to[u] = ld_stream(src + (int64_t)(h + u) * a.D);
+        }
+    };
+    load(0, next);
     live = live && pos >= 0 && pos < a.max_pos;
     int64_t slot = -1;
     float g = 0.0f;
@@ -208,44 +212,45 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     Factors f = factors_of<PAIRS>(cs, sn, turn, 1.0f);
     if (norm && in_row) {
         const uint4 own = ld_again(w + c * 8);
-        uint64_t wp[4];
         const uint4 other = PAIRS ? own : ld_again(w + (c + turn.partner - lane) * 8);
         const uint32_t ww[4] = {own.x, own.y, own.z, own.w}, wo[4] = {other.x, other.y, other.z, other.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            wp[i] = widen2(PAIRS ? __funnelshift_l(wo[i], wo[i], 16) : wo[i]);
             f.by[i] = mul2(f.by[i], widen2(ww[i]));
-            f.with[i] = mul2(f.with[i], wp[i]);
+            f.with[i] = mul2(f.with[i], widen2(PAIRS ? __funnelshift_l(wo[i], wo[i], 16) : wo[i]));
         }
     }
     pdl_launch_dependents();
     const float inv_d = 1.0f / (float)a.D;
+    uint16_t *dst = (kind == 0 ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko) + (int64_t)h0 * a.D + c * 8;
+    const bool to_rows = live && in_row && turned && (kind == 0 || a.k_out != nullptr);
 
+    for (int h = 0; h < most; h += 2) {
+        x[0] = next[0];
+        x[1] = next[1];
+        load(h + 2, next);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const bool on = live && in_row && h0 + u < heads;
-        float r = 1.0f;
-        if (a.qw != nullptr)
-            r = rsqrtf(__fmaf_rn(group_sum(sumsq_bf16x8(x[u], 0.0f), lanes), inv_d, a.eps));
-        uint64_t o[4], y2[4];
-        partners<PAIRS>(x[u], turn, o);
-        const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        for (int u = 0; u < 2; ++u) {
+            float r = 1.0f;
+            if (a.qw != nullptr)
+                r = rsqrtf(__fmaf_rn(group_sum(sumsq_bf16x8(x[u], 0.0f), lanes), inv_d, a.eps));
+            uint64_t o[4], y2[4];
+            partners<PAIRS>(x[u], turn, o);
+            const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            y2[i] = fma2(mul2(widen2(xw[i]), twice(r)), f.by[i], mul2(mul2(o[i], twice(r)), f.with[i]));
-        const uint4 y = turned ? pack2x4(y2) : x[u];
-        if (on && turned) {
-            uint16_t *dst = kind == 0 ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko;
-            if (kind == 0 || a.k_out != nullptr)
-                st_v4(dst + (int64_t)(h0 + u) * a.D + c * 8, y);
-        }
-        const bool keep = CACHE && on && slot >= 0;
-        if (CACHE && __any_sync(0xffffffffu, keep)) {  // (most warps have queries only)
-            int in_tile = 0;
-            uint8_t *tile = keep ? cache_tile(a.cache, a.D, slot, h0 + u, &in_tile) : nullptr;
-            const int second = kind == 2 ? 1 : 0;
-            put_chunk(y, g, keep, tile + second * 8 * a.D + in_tile * (a.D >> 1),
-                      tile + (16 + second) * a.D + in_tile * (a.D >> 4), c);
+            for (int i = 0; i < 4; ++i)
+                y2[i] = fma2(mul2(widen2(xw[i]), twice(r)), f.by[i], mul2(mul2(o[i], twice(r)), f.with[i]));
+            const uint4 y = turned ? pack2x4(y2) : x[u];
+            if (to_rows && h + u < n)
+                st_v4(dst + (int64_t)(h + u) * a.D, y);
+            const bool keep = CACHE && in_row && h + u < n && slot >= 0;
+            if (CACHE && __any_sync(0xffffffffu, keep)) {  // (most warps have queries only)
+                int in_tile = 0;
+                uint8_t *tile = keep ? cache_tile(a.cache, a.D, slot, h0 + h + u, &in_tile) : nullptr;
+                const int second = kind == 2 ? 1 : 0;
+                put_chunk(y, g, keep, tile + second * 8 * a.D + in_tile * (a.D >> 1),
+                          tile + (16 + second) * a.D + in_tile * (a.D >> 4), c);
+            }
         }
     }
 }
@@ -256,13 +261,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 // dx as above; the weights' gradient is summed by each lane over its runs, then over
 // the groups of a block in order, and over the blocks by grad_sum_kernel.
-template <int U, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 3) rope_grad_kernel(const __grid_constant__ RopeGradArgs a)
+// Blocks of 128 threads, five to an SM: 96 registers, with which two heads' loads are
+// under way while two others are worked on.
+constexpr int kGradThreads = 128;
+
+template <bool PAIRS>
+__global__ void __launch_bounds__(kGradThreads, 5) rope_grad_kernel(const __grid_constant__ RopeGradArgs a)
 {
     extern __shared__ float sums[];  // [groups of lanes][lanes * 8]
     const int lanes = 1 << a.lanes_log2;
     const int lane = threadIdx.x & 31, c = lane & (lanes - 1);
-    const int groups = kThreads >> a.lanes_log2, group = threadIdx.x >> a.lanes_log2;
+    const int groups = kGradThreads >> a.lanes_log2, group = threadIdx.x >> a.lanes_log2;
     const bool in_row = c < (a.D >> 3);
     const Turn turn = turn_of(c, lane, a.rot, PAIRS);
     const float inv_d = 1.0f / (float)a.D;
@@ -286,16 +295,16 @@ __global__ void __launch_bounds__(kThreads, 3) rope_grad_kernel(const __grid_con
             const int64_t id = base + (group - first);
             bool live = id < all;
             const int64_t t = live ? div_by((uint32_t)id, a.div_runs[kind]) : 0;
-            const int h0 = (int)(id - t * a.runs[kind]) * U;
+            const int h0 = (int)(id - t * a.runs[kind]) * a.run_heads;
+            const int n = live ? min(a.run_heads, a.heads[kind] - h0) : 0, most = __reduce_max_sync(0xffffffffu, n);
             const int32_t pos = live ? a.pos[t] : -1;
-            uint4 x[U], d[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                x[u] = d[u] = make_uint4(0, 0, 0, 0);
-                if (live && in_row && h0 + u < a.heads[kind]) {
-                    x[u] = ld_stream(a.x[kind] + t * a.ldx[kind] + (int64_t)(h0 + u) * a.D + c * 8);
-                    d[u] = ld_stream(a.dy[kind] + t * a.lddy[kind] + (int64_t)(h0 + u) * a.D + c * 8);
-                }
+            const int64_t at = (int64_t)h0 * a.D + c * 8;
+            const uint16_t *xs = a.x[kind] + t * a.ldx[kind] + at, *ds = a.dy[kind] + t * a.lddy[kind] + at;
+            uint16_t *to = a.dx[kind] + t * a.lddx[kind] + at;
+            uint4 next_x = make_uint4(0, 0, 0, 0), next_d = next_x;
+            if (in_row && n > 0) {
+                next_x = ld_stream(xs);
+                next_d = ld_stream(ds);
             }
             live = live && pos >= 0 && pos < a.max_pos;
             float cs[8] = {}, sn[8] = {};
@@ -305,12 +314,18 @@ __global__ void __launch_bounds__(kThreads, 3) rope_grad_kernel(const __grid_con
                 ld_angles(p + (a.rot >> 1), PAIRS ? 1 : 2, sn);
             }
             const Factors f = factors_of<PAIRS>(cs, sn, turn, -1.0f);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool on = live && in_row && h0 + u < a.heads[kind];
-                const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w}, xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            for (int h = 0; h < most; ++h) {
+                const uint4 x = next_x, d = next_d;
+                xs += a.D;
+                ds += a.D;
+                if (in_row && h + 1 < n) {
+                    next_x = ld_stream(xs);
+                    next_d = ld_stream(ds);
+                }
+                const bool on = live && in_row && h < n;
+                const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, xw[4] = {x.x, x.y, x.z, x.w};
                 uint64_t o[4], v[4];
-                partners<PAIRS>(d[u], turn, o);
+                partners<PAIRS>(d, turn, o);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     v[i] = fma2(widen2(dw[i]), f.by[i], mul2(o[i], f.with[i]));
@@ -322,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_grad_kernel(const __grid_con
                         gx = fma2(mul2(v[i], wf[i]), widen2(xw[i]), gx);
                     float s0, s1;
                     unpair(gx, s0, s1);
-                    float sq = sumsq_bf16x8(x[u], 0.0f), dot = s0 + s1;
+                    float sq = sumsq_bf16x8(x, 0.0f), dot = s0 + s1;
                     for (int k = lanes >> 1; k > 0; k >>= 1) {
                         sq += __shfl_xor_sync(0xffffffffu, sq, k);
                         dot += __shfl_xor_sync(0xffffffffu, dot, k);
@@ -338,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_grad_kernel(const __grid_con
                     }
                 }
                 if (on)
-                    st_v4(a.dx[kind] + t * a.lddx[kind] + (int64_t)(h0 + u) * a.D + c * 8, pack2x4(v));
+                    st_v4(to, pack2x4(v));
+                to += a.D;
             }
         }
         if (w != nullptr) {
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_grad_kernel(const __grid_con
             for (int i = 0; i < 4; ++i)
                 unpair(acc[i], sums[group * lanes * 8 + c * 8 + 2 * i], sums[group * lanes * 8 + c * 8 + 2 * i + 1]);
             __syncthreads();
-            for (int j = threadIdx.x; j < a.D; j += kThreads) {
+            for (int j = threadIdx.x; j < a.D; j += kGradThreads) {
                 float s = 0.0f;
                 for (int i = 0; i < groups; ++i)
                     s += sums[i * lanes * 8 + j];
@@ -430,55 +446,56 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     pdl_launch_dependents();
 }
 
-template <int U, bool PAIRS>
-cudaError_t launch_rope_u(RopeArgs a, bool pdl, cudaStream_t stream)
+// Heads of a run: as many as leave every SM 64 groups of lanes with one each, so that
+// the factors are made once for several; at most 16.  (The bits do not depend on it.)
+int run_heads(int64_t rows, int lanes_log2)
 {
-    a.runs_q = (a.hq + U - 1) / U;
-    a.runs_k = (a.hk + U - 1) / U;
-    a.runs = a.runs_q + (a.keep ? 2 : 1) * a.runs_k;
-    a.div_runs = div_magic((uint32_t)a.runs);
-    const int64_t blocks = (((a.T * a.runs) << a.lanes_log2) + kThreads - 1) / kThreads;
-    const dim3 grid((unsigned)blocks), block(kThreads);
-    return a.keep ? launch_kernel(rope_kernel<U, PAIRS, true>, grid, block, 0, stream, pdl, a)
-                                    : launch_kernel(rope_kernel<U, PAIRS, false>, grid, block, 0, stream, pdl, a);
+    const int64_t per = (rows << lanes_log2) / (152 * 1024);
+    return per < 1 ? 1 : (per > 16 ? 16 : (int)per);
 }
 
-template <int U, bool PAIRS>
-cudaError_t launch_grad_u(RopeGradArgs a, bool pdl, cudaStream_t stream)
+template <bool PAIRS>
+cudaError_t launch_rope_as(const RopeArgs &a, bool pdl, cudaStream_t stream)
 {
-    int64_t most = 0;
-    for (int i = 0; i < 2; ++i) {
-        a.runs[i] = (a.heads[i] + U - 1) / U;
-        a.div_runs[i] = div_magic((uint32_t)a.runs[i]);
-        most = a.runs[i] > most ? a.runs[i] : most;
-    }
-    const int groups = kThreads >> a.lanes_log2;
-    const int64_t want = (a.T * most + groups - 1) / groups;
-    const int blocks = (int)(want < 1 ? 1 : (want > kGradBlocks ? kGradBlocks : want));
-    cudaError_t err = launch_kernel(rope_grad_kernel<U, PAIRS>, dim3((unsigned)blocks), dim3(kThreads), kThreads * 8 * sizeof(float),
-                                    stream, pdl, a);
-    if (err != cudaSuccess || a.w[0] == nullptr)
-        return err;
-    return launch_kernel(grad_sum_kernel, dim3((unsigned)((2 * a.D + 31) / 32)), dim3(256), 0, stream, true,
-                         (const float *)a.partial, blocks, a.D, a.dw[0], a.dw[1]);
+    const int64_t blocks = (((a.T * a.runs) << a.lanes_log2) + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    return a.keep ? launch_kernel(rope_kernel<PAIRS, true>, grid, block, 0, stream, pdl, a)
+                  : launch_kernel(rope_kernel<PAIRS, false>, grid, block, 0, stream, pdl, a);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs &a, bool pdl, cudaStream_t stream)
+cudaError_t launch_rope(const RopeArgs &args, bool pdl, cudaStream_t stream)
 {
-    const bool few = ((a.T * (a.hq + 2 * a.hk)) << a.lanes_log2) <= 152 * 1024;
-    if (a.pairs)
-        return few ? launch_rope_u<1, true>(a, pdl, stream) : launch_rope_u<4, true>(a, pdl, stream);
-    return few ? launch_rope_u<1, false>(a, pdl, stream) : launch_rope_u<4, false>(a, pdl, stream);
+    RopeArgs a = args;
+    a.run_heads = run_heads(a.T * (a.hq + 2 * a.hk), a.lanes_log2);
+    a.runs_q = (a.hq + a.run_heads - 1) / a.run_heads;
+    a.runs_k = (a.hk + a.run_heads - 1) / a.run_heads;
+    a.runs = a.runs_q + (a.keep ? 2 : 1) * a.runs_k;
+    a.div_runs = div_magic((uint32_t)a.runs);
+    return a.pairs ? launch_rope_as<true>(a, pdl, stream) : launch_rope_as<false>(a, pdl, stream);
 }
 
-cudaError_t launch_rope_grad(const RopeGradArgs &a, bool pdl, cudaStream_t stream)
+cudaError_t launch_rope_grad(const RopeGradArgs &args, bool pdl, cudaStream_t stream)
 {
-    const bool few = ((a.T * (a.heads[0] + a.heads[1])) << a.lanes_log2) <= 152 * 1024;
-    if (a.pairs)
-        return few ? launch_grad_u<1, true>(a, pdl, stream) : launch_grad_u<2, true>(a, pdl, stream);
-    return few ? launch_grad_u<1, false>(a, pdl, stream) : launch_grad_u<2, false>(a, pdl, stream);
+    RopeGradArgs a = args;
+    a.run_heads = run_heads(a.T * (a.heads[0] + a.heads[1]), a.lanes_log2);
+    int64_t most = 0;
+    for (int i = 0; i < 2; ++i) {
+        a.runs[i] = (a.heads[i] + a.run_heads - 1) / a.run_heads;
+        a.div_runs[i] = div_magic((uint32_t)a.runs[i]);
+        most = a.runs[i] > most ? a.runs[i] : most;
+    }
+    const int groups = kGradThreads >> a.lanes_log2;
+    const int64_t want = (a.T * most + groups - 1) / groups;
+    const int blocks = (int)(want < 1 ? 1 : (want > kGradBlocks ? kGradBlocks : want));
+    const size_t smem = kGradThreads * 8 * sizeof(float);
+    const cudaError_t err = a.pairs ? launch_kernel(rope_grad_kernel<true>, dim3((unsigned)blocks), dim3(kGradThreads), smem, stream, pdl, a)
+                                    : launch_kernel(rope_grad_kernel<false>, dim3((unsigned)blocks), dim3(kGradThreads), smem, stream, pdl, a);
+    if (err != cudaSuccess || a.w[0] == nullptr)
+        return err;
+    return launch_kernel(grad_sum_kernel, dim3((unsigned)((2 * a.D + 31) / 32)), dim3(256), 0, stream, true,
+                         (const float *)a.partial, blocks, a.D, a.dw[0], a.dw[1]);
 }
 
 cudaError_t launch_cache_read(const CacheReadArgs &a, bool pdl, cudaStream_t stream)

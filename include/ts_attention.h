@@ -199,9 +199,9 @@ TS_API int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t q_h
                               void *out, int64_t ldo, float *lse, void *workspace, uint32_t flags, void *stream);
 
 /* Bytes of the attention's workspace, whatever the lengths within these bounds (no fewer
- * where a bound is larger); -1 for sizes that it refuses. */
+ * where a bound is larger, or a window is none); -1 for sizes that it refuses. */
 TS_API int64_t ts_nvfp4_attention_workspace(int64_t B, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_q,
-                                            int64_t max_keys);
+                                            int64_t max_keys, int64_t window);
 
 #ifdef __cplusplus
 }

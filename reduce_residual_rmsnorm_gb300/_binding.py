@@ -168,7 +168,7 @@ def library(path: str | None = None):
         lib.ts_moe_rows.restype = i64
         lib.ts_qk_norm_rope_grad_workspace.argtypes = [i64]
         lib.ts_qk_norm_rope_grad_workspace.restype = i64
-        lib.ts_nvfp4_attention_workspace.argtypes = [i64] * 6
+        lib.ts_nvfp4_attention_workspace.argtypes = [i64] * 7
         lib.ts_nvfp4_attention_workspace.restype = i64
         lib.ts_status_string.argtypes = [ctypes.c_int]
         lib.ts_status_string.restype = ctypes.c_char_p

@@ -389,11 +389,11 @@ int check_attention(int64_t q_heads, int64_t heads, int64_t D, int64_t max_q)
 }
 
 // Which kernel: rows of a sequence that share a key head.
-constexpr int64_t kFewRows = 16;
+constexpr int64_t kFewRows = 32;
 
-int64_t attention_workspace(int64_t B, int64_t heads, int64_t rows, int64_t D, int64_t keys)
+int64_t attention_workspace(int64_t B, int64_t heads, int64_t rows, int64_t D, int64_t keys, int64_t window)
 {
-    if (rows <= kFewRows && attn_few_clusters(B, heads, rows, keys))
+    if (rows <= kFewRows && attn_few_clusters(B, heads, rows, keys, window))
         return 0;
     const int64_t few = attn_few_workspace(D), prompt = rows <= kFewRows ? 0 : attn_prompt_workspace(D);
     return few > prompt ? few : prompt;  // (does not shrink where a bound grows)
@@ -402,11 +402,12 @@ int64_t attention_workspace(int64_t B, int64_t heads, int64_t rows, int64_t D, i
 }  // namespace
 
 extern "C" int64_t ts_nvfp4_attention_workspace(int64_t B, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_q,
-                                                int64_t max_keys)
+                                                int64_t max_keys, int64_t window)
 {
-    if (check_attention(q_heads, heads, head_dim, max_q) != TS_OK || B < 0 || B > 65536 || max_keys < 0 || max_keys > (1LL << 30))
+    if (check_attention(q_heads, heads, head_dim, max_q) != TS_OK || B < 0 || B > 65536 || max_keys < 0 || max_keys > (1LL << 30) ||
+        window < 0 || window > kMaxRows)
         return -1;
-    return attention_workspace(B, heads, max_q * (q_heads / heads), head_dim, max_keys);
+    return attention_workspace(B, heads, max_q * (q_heads / heads), head_dim, max_keys, window);
 }
 
 extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t q_heads, const int32_t *cu_q, int64_t B,
@@ -436,7 +437,7 @@ extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t
     if (window > 0 && causal == 0)
         return fail(TS_ERR_UNSUPPORTED, "a window needs causal");
     const int64_t rows = max_q * (q_heads / c.heads);
-    const int64_t space = attention_workspace(B, c.heads, rows, D, max_pages * c.page_size);
+    const int64_t space = attention_workspace(B, c.heads, rows, D, max_pages * c.page_size, window);
     const Rows b[] = {matrix(q, T, q_heads * D, ldq, "q"),
                       flat(cu_q, (B + 1) * 4, 4, "cu_q", false, true),
                       flat(c.pages, cache_bytes(c), 16, "pages", false, c.num_pages == 0),

@@ -4,7 +4,7 @@
 //   out = sum_j p_j V[j] / sum_j p_j,   p_j = exp2(c q.K[j] - m)      c = scale log2(e) / k_scale
 //
 // Bound by the cache's bytes, 9/8 D a key and head.  The rows of a unit are up to
-// 8 NT of the (query, head) pairs that share a key head, so a key is read once for
+// 8 NT (NT 1, 2 or 4) of the (query, head) pairs that share a key head, so a key is read once for
 // them.  E2M1 times E4M3 has at most 6 significant bits: K and V are exact in fp16, and
 // a row of q is too after scaling by a power of two, so fp16 products with fp32 sums
 // lose nothing.  The keys are the 16 rows of mma.m16n8k16 (the rows of q its 8 columns):
@@ -38,17 +38,37 @@ namespace tsfn {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-// Blocks of an SM and copies of tiles in flight: 16 rows take the registers of a whole SM.
-constexpr int blocks_per_sm(int nt) { return nt == 1 ? 2 : 1; }
+// Even shares: for 8 rows blocks of 4 warps, four to an SM (64 sequences up to 16384 keys:
+// 107.7 us; blocks of 8 warps 113.7, five blocks of 4 with 96 registers 111.7); for more
+// the registers of an SM go to one block of 8.  Clusters: blocks of 8 warps, for the
+// time of a single call.
 constexpr int kSms = 152;
+constexpr int kClusterWarps = 8;
+constexpr int share_warps(int nt) { return nt == 1 ? 4 : 8; }
+constexpr int blocks_per_sm(int nt) { return nt == 1 ? 4 : 1; }
 constexpr int blocks_of(int nt) { return kSms * blocks_per_sm(nt); }
-constexpr int stages_of(int nt) { return nt == 1 ? 4 : 6; }
+// Rows of a unit, in eights: 17 and more go 32 at a time, so that a key is turned into
+// fp16 once for them.
+int eights_of(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
+constexpr int kStages = 4;  // tiles of a warp whose copies are under way
 constexpr int kShare = 8;     // tiles of a share, at least
-constexpr int kWay = 24;      // what going to a unit costs, in tiles of a block, when work is split
-// Clusters take calls of few units and not too many keys.
-constexpr int64_t kClusterUnits = 76, kClusterKeys = 16384;
+// What going to a unit costs, in tiles of a block, when work is split.
+constexpr int way_of(int nt) { return 3 * share_warps(nt); }
+// Clusters take calls whose units are all resident at once, with at most this many keys a
+// block (16 tiles a warp: with more, sequences of different lengths leave SMs idle).
+constexpr int64_t kClusterKeys = 2048;
+// Blocks of a cluster, a power of two up to 8; 0: even shares.
+int cluster_of(int64_t B, int64_t heads, int64_t rows, int64_t keys, int64_t window)
+{
+    const int nt = eights_of(rows);
+    const int64_t units = B * heads * ((rows + 8 * nt - 1) / (8 * nt)), resident = kSms * (nt == 1 ? 2 : 1);
+    if (window > 0 && window + rows < keys)
+        keys = window + rows;  // (no more queries than rows)
+    for (int blocks = 8; blocks >= 1; blocks /= 2)
+        if (units * blocks <= resident)
+            return keys <= kClusterKeys * blocks ? blocks : 0;
+    return 0;
+}
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
@@ -71,9 +91,17 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The first product of a sum.
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Four bytes of codes of two keys, the d of each nibble alike, times the keys' scales:
@@ -99,141 +127,155 @@ struct Run {
     Seq s;
 };
 
-template <int D, int NT>
+template <int D, int NT, int WARPS>
 struct Shared {
     using L = Layout<D>;
     static constexpr int NR = 8 * NT;
-    static constexpr int kRing = kWarps * stages_of(NT) * L::kTile;
-    static_assert(kWarps * NR * D * 4 <= kRing, "");
+    static constexpr int kRing = WARPS * (kStages * L::kTile > NR * D * 4 ? kStages * L::kTile : NR * D * 4);
     // the copies, [warps][stages][tile]; after them the warps' O [warps][NR][D]
-    static constexpr int kMs = kRing, kLs = kMs + kWarps * NR * 4, kBytes = kLs + kWarps * NR * 4;
+    static constexpr int kMs = kRing, kLs = kMs + WARPS * NR * 4;  // the warps' maxima and sums
+    static constexpr int kQ = kLs + WARPS * NR * 4;                // q's fragments of the products
+    static constexpr int kFactor = kQ + NR * D * 2, kHi = kFactor + NR * 4, kLo = kHi + NR * 4;  // of each row
+    static constexpr int kLimits = kLo + NR * 4, kBytes = kLimits + 16;
 };
 
 // The parts (m, l, O) of a run's rows by the block's warps, in shared memory.
-template <int D, int NT>
+template <int D, int NT, int WARPS>
 __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float c0, uint8_t *smem)
 {
     using L = Layout<D>;
-    constexpr int NR = 8 * NT, kStages = stages_of(NT);
+    using Sh = Shared<D, NT, WARPS>;
+    constexpr int NR = 8 * NT;
     constexpr int KS = D / 16;  // products of S per tile and 8 rows, and of O
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const Seq &s = run.s;
     uint8_t *const ring = smem;
-    float *const ms = reinterpret_cast<float *>(smem + Shared<D, NT>::kMs), *const ls = reinterpret_cast<float *>(smem + Shared<D, NT>::kLs);
     const uint32_t my_ring = smem_addr(ring) + warp * kStages * L::kTile;
 
     // this warp's tiles and their copies: 18 D contiguous bytes each
-    const int begin = (int)((int64_t)run.count * warp / kWarps), mine = (int)((int64_t)run.count * (warp + 1) / kWarps) - begin;
+    const int begin = (int)((int64_t)run.count * warp / WARPS), mine = (int)((int64_t)run.count * (warp + 1) / WARPS) - begin;
     const int key0 = (run.first + begin) * 16, tiles_of_page = a.cache.page_size >> 4;
     const int32_t *const table = a.table + (int64_t)run.b * a.max_pages;
     const int pages = (int)((s.len + a.cache.page_size - 1) / a.cache.page_size);  // that hold keys
     int page_at = (int)div_by((uint32_t)key0, a.cache.div_page);
     int in_page = (key0 - page_at * a.cache.page_size) >> 4;
     auto page_of = [&](int i) -> int32_t { return mine > 0 && i < pages ? table[i] : -1; };
-    int32_t page = page_of(page_at), next_page = page_of(page_at + 1);
+    int32_t next_page = page_of(page_at);
     const uint8_t *src = nullptr;
     auto to_page = [&]() {
+        const int32_t page = next_page;
+        next_page = page_of(++page_at);
         src = nullptr;
         if (page >= 0 && page < a.cache.num_pages)
             src = a.cache.pages + (((int64_t)page * a.cache.heads + run.head) * tiles_of_page + in_page) * L::kTile + lane * 16;
     };
     to_page();
-    uint32_t ok = 0;  // stages whose tile lies in the cache
-    auto issue = [&](int k) {
-        if (k < mine) {
+    uint32_t in_cache = 0;  // bit i: of the copy i before the last one
+    uint32_t fill = my_ring + lane * 16;
+    const uint32_t ring_end = fill + kStages * L::kTile;
+    auto issue = [&](bool more) {
+        in_cache <<= 1;
+        if (more) {
             if (in_page == tiles_of_page) {
                 in_page = 0;
-                page = next_page;
-                next_page = page_of(++page_at + 1);
                 to_page();
             }
-            const int stage = k % kStages;
-            ok &= ~(1u << stage);
             if (src != nullptr) {
-                ok |= 1u << stage;
-                const uint32_t dst = my_ring + stage * L::kTile + lane * 16;
+                in_cache |= 1;
 #pragma unroll
                 for (int i = 0; i < L::kChunks / 32; ++i)
-                    copy16(dst + i * 512, src + i * 512);
+                    copy16(fill + i * 512, src + i * 512);
                 if (lane < L::kChunks % 32)
-                    copy16(dst + L::kChunks / 32 * 512, src + L::kChunks / 32 * 512);
+                    copy16(fill + L::kChunks / 32 * 512, src + L::kChunks / 32 * 512);
                 src += L::kTile;
             }
             ++in_page;
         }
+        fill += L::kTile;
+        if (fill == ring_end)
+            fill -= kStages * L::kTile;
         copies_commit();
     };
     for (int k = 0; k < kStages - 1; ++k)
-        issue(k);
+        issue(k < mine);
 
-    // the rows of q as fp16, each scaled by a power of two; column factors and limits
-    uint32_t qf[NT][KS][2];
-    float cf[NT][2];
-    int hi[NT][2], lo[NT][2];
-    int hi_min = 0x7fffffff, hi_max = 0, lo_min = 0x7fffffff, lo_max = 0;
+    // the rows of q as fp16, each scaled by a power of two; their factors and limits; by one
+    // warp for all
+    if (warp == 0) {
+        int hi_min = 0x7fffffff, hi_max = 0, lo_min = 0x7fffffff, lo_max = 0;
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = nt * 8 + g;
+            const bool live = col < run.rows;
+            const int r = run.row0 + col, i = live ? (int)div_by((uint32_t)r, a.div_group) : 0, qh = live ? r - i * a.group : 0;
+            const uint16_t *q = a.q + (int64_t)(s.q0 + i) * a.ldq + ((int64_t)run.head * a.group + qh) * D + t * (D / 4);
+            uint4 v[KS / 2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int col = nt * 8 + g;
-        const bool live = col < run.rows;
-        const int r = run.row0 + col, i = live ? (int)div_by((uint32_t)r, a.div_group) : 0, qh = live ? r - i * a.group : 0;
-        const uint16_t *q = a.q + (int64_t)(s.q0 + i) * a.ldq + ((int64_t)run.head * a.group + qh) * D + t * (D / 4);
-        uint4 v[KS / 2];
+            for (int j = 0; j < KS / 2; ++j) {
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (live)
+                    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w) : "l"(q + j * 8) : "memory");
+            }
+            float amax = 0.0f;
 #pragma unroll
-        for (int j = 0; j < KS / 2; ++j) {
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (live)
-                asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w) : "l"(q + j * 8) : "memory");
+            for (int j = 0; j < KS / 2; ++j) {
+                float f[8];
+                unpack8(v[j], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    amax = fmaxf(amax, fabsf(f[e]));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            float down;
+            const float up = fp16_scale(amax, down);
+#pragma unroll
+            for (int j = 0; j < KS / 2; ++j) {
+                float f[8];
+                unpack8(v[j], f);
+                *reinterpret_cast<uint4 *>(smem + Sh::kQ + ((nt * (KS / 2) + j) * 32 + lane) * 16) =
+                    make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up), pack_f16x2(f[4] * up, f[5] * up),
+                               pack_f16x2(f[6] * up, f[7] * up));
+            }
+            // limits of this row's keys
+            int h = a.causal ? s.len - s.n + i + 1 : s.len;  // (may be <= 0)
+            int l = a.window > 0 ? h - a.window : 0;
+            if (!live) {
+                h = 0x7fffffff;
+                l = 0;
+            }
+            l = l < 0 ? 0 : l;
+            if (t == 0) {
+                reinterpret_cast<float *>(smem + Sh::kFactor)[col] = c0 * down;
+                reinterpret_cast<int *>(smem + Sh::kHi)[col] = min(h, s.len);
+                reinterpret_cast<int *>(smem + Sh::kLo)[col] = l;
+            }
+            hi_min = min(hi_min, h);
+            lo_max = max(lo_max, l);
+            if (live) {
+                hi_max = max(hi_max, h);
+                lo_min = min(lo_min, l);
+            }
         }
-        float f[KS / 2][8], amax = 0.0f;
-#pragma unroll
-        for (int j = 0; j < KS / 2; ++j) {
-            unpack8(v[j], f[j]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                amax = fmaxf(amax, fabsf(f[j][e]));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        float down;
-        const float up = fp16_scale(amax, down);
-#pragma unroll
-        for (int j = 0; j < KS / 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                qf[nt][2 * j + e / 2][e & 1] = pack_f16x2(f[j][2 * e] * up, f[j][2 * e + 1] * up);
-        // limits of this column's keys
-        int h = a.causal ? s.len - s.n + i + 1 : s.len;  // (may be <= 0)
-        int l = a.window > 0 ? h - a.window : 0;
-        if (!live) {
-            h = 0x7fffffff;
-            l = 0;
-        }
-        l = l < 0 ? 0 : l;
-        const float c = c0 * down;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int from = (2 * t + j) * 4;
-            cf[nt][j] = __shfl_sync(0xffffffffu, c, from);
-            hi[nt][j] = __shfl_sync(0xffffffffu, h, from);
-            lo[nt][j] = __shfl_sync(0xffffffffu, l, from);
-        }
-        hi_min = min(hi_min, h);
-        lo_max = max(lo_max, l);
-        if (live) {
-            hi_max = max(hi_max, h);
-            lo_min = min(lo_min, l);
-        }
+        hi_min = min(__reduce_min_sync(0xffffffffu, hi_min), s.len);
+        lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+        hi_max = min(__reduce_max_sync(0xffffffffu, hi_max), s.len);
+        lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+        if (lane == 0)
+            *reinterpret_cast<int4 *>(smem + Sh::kLimits) = make_int4(hi_min, lo_max, hi_max, lo_min);
     }
-    hi_min = min(__reduce_min_sync(0xffffffffu, hi_min), s.len);
-    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-    hi_max = min(__reduce_max_sync(0xffffffffu, hi_max), s.len);
-    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    __syncthreads();
+    const int hi_min = reinterpret_cast<const int *>(smem + Sh::kLimits)[0], lo_max = reinterpret_cast<const int *>(smem + Sh::kLimits)[1];
+    float2 kept[NT];  // the rows' factors (32 rows leave no registers for them)
+#pragma unroll
+    for (int nt = 0; nt < NT && NT < 4; ++nt)
+        kept[nt] = *reinterpret_cast<const float2 *>(smem + Sh::kFactor + (nt * 8 + 2 * t) * 4);
 
     float o[NT][KS][4];
-    // the maximum, what is subtracted for it (0 while there is none), how far above that a
-    // score may be, and the sum
-    float m[NT][2], off[NT][2], room[NT][2], l[NT][2];
+    // the maximum (0 while there is none), how far above it a score may be (-inf while there
+    // is none), and the sum
+    float off[NT][2], room[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -243,29 +285,26 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
                 o[nt][i][j] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            m[nt][j] = room[nt][j] = -INFINITY;
+            room[nt][j] = -INFINITY;
             off[nt][j] = l[nt][j] = 0.0f;
         }
     }
     // rows g and g + 8 of K are keys k0 and k0 + 8: t and t + 4 then follow each other in p^T
     const int k0 = (g >> 1) + 4 * (g & 1);
-    for (int k = 0; k < mine; ++k) {
+    const uint8_t *tile = ring + warp * kStages * L::kTile;
+    const uint8_t *const tile_end = tile + kStages * L::kTile;
+    // tiles that every row sees: plain of them from the first plain_at on
+    const int plain_at = max((lo_max - key0 + 15) >> 4, 0), plain = max((hi_min - key0 + (hi_min < key0 ? -15 : 0)) / 16 - plain_at, 0);
+    for (int k = 0; k < mine; ++k, tile = tile + L::kTile == tile_end ? tile_end - kStages * L::kTile : tile + L::kTile) {
         __syncwarp();  // the stage that is filled next has been read
-        issue(k + kStages - 1);
+        issue(k + kStages - 1 < mine);
         copies_wait<kStages - 1>();
         __syncwarp();
-        const int stage = k % kStages, key = key0 + k * 16;
-        if (!(ok >> stage & 1))
+        if (!(in_cache >> (kStages - 1) & 1))
             continue;
-        const uint8_t *tile = ring + (warp * kStages + stage) * L::kTile;
-
         float sc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                sc[nt][j] = 0.0f;
         {
+            float s2[NT][4];
             uint32_t w[2][KS / 2], sf[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -296,24 +335,42 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
                 const uint32_t a12 = mul_f16x2(e2m1x2<2>(w[1][i]), s1), a13 = mul_f16x2(e2m1x2<3>(w[1][i]), s1);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma(sc[nt], a00, a10, a01, a11, qf[nt][2 * i][0], qf[nt][2 * i][1]);
-                    mma(sc[nt], a02, a12, a03, a13, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+                    const uint4 q = *reinterpret_cast<const uint4 *>(smem + Sh::kQ + ((nt * (KS / 2) + i) * 32 + lane) * 16);
+                    // (two sums side by side, where there are not four of them anyway: a
+                    // product waits for the one before in its sum)
+                    float(&second)[4] = NT < 4 ? s2[nt] : sc[nt];
+                    if (i == 0)
+                        mma_first(sc[nt], a00, a10, a01, a11, q.x, q.y);
+                    else
+                        mma(sc[nt], a00, a10, a01, a11, q.x, q.y);
+                    if (i == 0 && NT < 4)
+                        mma_first(second, a02, a12, a03, a13, q.z, q.w);
+                    else
+                        mma(second, a02, a12, a03, a13, q.z, q.w);
                 }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT && NT < 4; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sc[nt][j] += s2[nt][j];
         }
         uint32_t vb[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             vb[j] = tile[L::kVsf + (t + 4 * j) * (D / 16) + (D == 128 ? g : g >> 1)];
-        if (!(key >= lo_max && key + 16 <= hi_min)) {  // -inf where a row does not see the key
+        if ((unsigned)(k - plain_at) >= (unsigned)plain) {  // -inf where a row does not see the key
+            const int key = key0 + k * 16;
+            const int *hi = reinterpret_cast<const int *>(smem + Sh::kHi), *lo = reinterpret_cast<const int *>(smem + Sh::kLo);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int at = key + k0 + 8 * (j >> 1);
-                    if (!(at < hi[nt][j & 1] && at >= lo[nt][j & 1] && at < s.len))
+                    const int at = key + k0 + 8 * (j >> 1), col = nt * 8 + 2 * t + (j & 1);
+                    if (!(at < hi[col] && at >= lo[col]))
                         sc[nt][j] = -INFINITY;
                 }
+            const int hi_max = reinterpret_cast<const int *>(smem + Sh::kLimits)[2], lo_min = reinterpret_cast<const int *>(smem + Sh::kLimits)[3];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int at = key + t + 4 * j;
@@ -323,32 +380,37 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
         }
         // x: scores in units of log2, less the maximum
         float x[NT][4];
+        auto factor = [&](int nt) { return NT < 4 ? kept[nt] : *reinterpret_cast<const float2 *>(smem + Sh::kFactor + (nt * 8 + 2 * t) * 4); };
         bool grow = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            const float2 cf = factor(nt);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x[nt][j] = fmaf(sc[nt][j], cf[nt][j & 1], -off[nt][j & 1]);
+                x[nt][j] = fmaf(sc[nt][j], j & 1 ? cf.y : cf.x, -off[nt][j & 1]);
                 grow = grow || x[nt][j] > room[nt][j & 1];
             }
+        }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float f[2];
+                const float2 cf = factor(nt);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float top = fmaxf(x[nt][j], x[nt][j + 2]);
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    top = fmaxf(top + off[nt][j], m[nt][j]);
-                    f[j] = m[nt][j] == -INFINITY ? 0.0f : exp2_approx(m[nt][j] - top);
-                    m[nt][j] = top;
+                    const bool some = room[nt][j] != -INFINITY;
+                    top += off[nt][j];
+                    top = some ? fmaxf(top, off[nt][j]) : top;
+                    f[j] = some ? exp2_approx(off[nt][j] - top) : 0.0f;
                     off[nt][j] = top == -INFINITY ? 0.0f : top;
                     room[nt][j] = top == -INFINITY ? -INFINITY : kSlack;
                     l[nt][j] *= f[j];
-                    x[nt][j] = fmaf(sc[nt][j], cf[nt][j], -off[nt][j]);
-                    x[nt][j + 2] = fmaf(sc[nt][j + 2], cf[nt][j], -off[nt][j]);
+                    x[nt][j] = fmaf(sc[nt][j], j ? cf.y : cf.x, -off[nt][j]);
+                    x[nt][j + 2] = fmaf(sc[nt][j + 2], j ? cf.y : cf.x, -off[nt][j]);
                 }
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
@@ -372,7 +434,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
             pt[nt][1] = transpose8(pack_f16x2(p[2], p[3]));
         }
         // O^T: a lane's keys are t, t + 4, t + 8, t + 12, its d those from g D/8 on
-        const uint32_t vs[2] = {e4m3x2(vb[0] | vb[1] << 8), e4m3x2(vb[2] | vb[3] << 8)};
+        const uint32_t vs[2] = {e4m3x2(__byte_perm(vb[0], vb[1], 0x0040)), e4m3x2(__byte_perm(vb[2], vb[3], 0x0040))};
         uint32_t w[4][D / 64];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -401,6 +463,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
     __syncthreads();  // the ring is free
 
     float *parts = reinterpret_cast<float *>(ring) + warp * NR * D;
+    float *const ms = reinterpret_cast<float *>(smem + Sh::kMs), *const ls = reinterpret_cast<float *>(smem + Sh::kLs);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -411,7 +474,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
             v += __shfl_xor_sync(0xffffffffu, v, 16);
             const int col = nt * 8 + 2 * t + j;
             if (g == 0) {
-                ms[warp * NR + col] = m[nt][j];
+                ms[warp * NR + col] = room[nt][j] == -INFINITY ? -INFINITY : off[nt][j];
                 ls[warp * NR + col] = v;
             }
 #pragma unroll
@@ -430,19 +493,20 @@ __device__ __forceinline__ float join_factor(float m, float l, float top)
 }
 
 // 4 elements of a row, summed over the block's warps.
-template <int D, int NT>
+template <int D, int NT, int WARPS>
 __device__ __forceinline__ float4 join_warps(const uint8_t *smem, int row, int d, float &top, float &sum)
 {
     constexpr int NR = 8 * NT;
-    const float *ms = reinterpret_cast<const float *>(smem + Shared<D, NT>::kMs), *ls = reinterpret_cast<const float *>(smem + Shared<D, NT>::kLs);
+    const float *ms = reinterpret_cast<const float *>(smem + Shared<D, NT, WARPS>::kMs);
+    const float *ls = reinterpret_cast<const float *>(smem + Shared<D, NT, WARPS>::kLs);
     top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
+    for (int w = 0; w < WARPS; ++w)
         top = fmaxf(top, ms[w * NR + row]);
     sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         const float f = join_factor(ms[w * NR + row], ls[w * NR + row], top);
         sum = fmaf(f, ls[w * NR + row], sum);
         const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + (w * NR + row) * D + d);
@@ -469,9 +533,9 @@ __device__ __forceinline__ void put_row(const AttnArgs &a, int q0, int head, int
 
 // Even shares.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(const __grid_constant__ AttnArgs a)
+__global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_few_kernel(const __grid_constant__ AttnArgs a)
 {
-    constexpr int NR = 8 * NT;
+    constexpr int NR = 8 * NT, kWarps = share_warps(NT), kThreads = kWarps * 32;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t sums[kThreads];
     __shared__ int64_t warp_sums[kWarps];
@@ -486,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
     const int per = (a.B + kThreads - 1) / kThreads;
     int64_t sum = 0;
     for (int b = tid * per; b < a.B && b < (tid + 1) * per; ++b)
-        sum += weight(a, sequence<NR>(a, b), kWay);
+        sum += weight(a, sequence<NR>(a, b), way_of(NT));
     int64_t scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -532,15 +596,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
     const float c0 = a.scale * kLog2e / *a.cache.k_scale;
 
     while (pos < end) {
-        while (pos >= base + weight(a, run.s, kWay)) {
-            base += weight(a, run.s, kWay);
+        while (pos >= base + weight(a, run.s, way_of(NT))) {
+            base += weight(a, run.s, way_of(NT));
             run.s = sequence<NR>(a, ++run.b);
         }
-        const int64_t unit = (pos - base) / (run.s.tiles + kWay);
-        const int skip = (int)(pos - base - unit * (run.s.tiles + kWay)), all = run.s.tiles + kWay - skip;
+        const int64_t unit = (pos - base) / (run.s.tiles + way_of(NT));
+        const int skip = (int)(pos - base - unit * (run.s.tiles + way_of(NT))), all = run.s.tiles + way_of(NT) - skip;
         const int length = (int)(all < end - pos ? all : end - pos);
-        run.first = max(skip - kWay, 0);
-        run.count = max(skip + length - kWay, 0) - run.first;
+        run.first = max(skip - way_of(NT), 0);
+        run.count = max(skip + length - way_of(NT), 0) - run.first;
         if (run.count == 0) {  // the way alone
             pos += length;
             continue;
@@ -555,12 +619,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
             state[1] = end;
             state[2] = base;
             state[3] = share;
-            state[4] = pos - skip + run.s.tiles + kWay;  // the unit's end
+            state[4] = pos - skip + run.s.tiles + way_of(NT);  // the unit's end
             state[5] = length;
             kept = run;
         }
         __syncthreads();
-        attend<D, NT>(a, kept, c0, smem);
+        attend<D, NT, kWarps>(a, kept, c0, smem);
         run = kept;
         pos = state[0];
         end = state[1];
@@ -577,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
         for (int row = tid / (D / 4); row < run.rows; row += kThreads / (D / 4)) {
             const int d = (tid % (D / 4)) * 4;
             float top, sum_l;
-            const float4 acc = join_warps<D, NT>(smem, row, d, top, sum_l);
+            const float4 acc = join_warps<D, NT, kWarps>(smem, row, d, top, sum_l);
             if (begins && ends) {
                 put_row<D>(a, run.s.q0, run.head, run.row0 + row, d, acc, top, sum_l, *a.cache.v_scale);
             } else {
@@ -594,20 +658,20 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_few_kernel(c
     pdl_launch_dependents();
 }
 
-constexpr int kCluster = 8;
+constexpr int kMostBlocks = 8;  // of a cluster
 
-// A cluster for each sequence and key head, and (the grid's y) row tile: the blocks have
-// an eighth of the keys each.
+// A cluster for each sequence and key head, and (the grid's y) row tile: its blocks share
+// the keys.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_cluster_kernel(const __grid_constant__ AttnArgs a)
+__global__ void __launch_bounds__(kClusterWarps * 32, NT == 1 ? 2 : 1) attn_cluster_kernel(const __grid_constant__ AttnArgs a, int blocks)
 {
-    constexpr int NR = 8 * NT;
+    constexpr int NR = 8 * NT, kWarps = kClusterWarps, kThreads = kWarps * 32;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float part[NR][D];
     __shared__ float part_m[NR], part_l[NR];
     const int tid = threadIdx.x, rank = (int)cluster_rank();
     pdl_wait();
-    const int unit = blockIdx.x / kCluster;
+    const int unit = blockIdx.x / blocks;
     Run run;
     run.b = unit / a.cache.heads;
     run.head = unit - run.b * a.cache.heads;
@@ -616,14 +680,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_cluster_kern
     for (int rt = blockIdx.y; rt < run.s.parts; rt += gridDim.y) {
         run.row0 = rt * NR;
         run.rows = run.s.n * a.group - run.row0 < NR ? run.s.n * a.group - run.row0 : NR;
-        const int begin = (int)((int64_t)run.s.tiles * rank / kCluster);
+        const int begin = (int)((int64_t)run.s.tiles * rank / blocks);
         run.first = run.s.first + begin;
-        run.count = (int)((int64_t)run.s.tiles * (rank + 1) / kCluster) - begin;
-        attend<D, NT>(a, run, c0, smem);
+        run.count = (int)((int64_t)run.s.tiles * (rank + 1) / blocks) - begin;
+        attend<D, NT, kWarps>(a, run, c0, smem);
         for (int row = tid / (D / 4); row < run.rows; row += kThreads / (D / 4)) {
             const int d = (tid % (D / 4)) * 4;
             float top, sum_l;
-            const float4 acc = join_warps<D, NT>(smem, row, d, top, sum_l);
+            const float4 acc = join_warps<D, NT, kWarps>(smem, row, d, top, sum_l);
             *reinterpret_cast<float4 *>(&part[row][d]) = acc;
             if (d == 0) {
                 part_m[row] = top;
@@ -632,21 +696,24 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_cluster_kern
         }
         cluster_sync();
         // each block joins the cluster's parts of its rows
-        for (int row = rank * NT + tid / (D / 4); row < (rank + 1) * NT && row < run.rows; row += kThreads / (D / 4)) {
+        const int each = NR / blocks;
+        for (int row = rank * each + tid / (D / 4); row < (rank + 1) * each && row < run.rows; row += kThreads / (D / 4)) {
             const int d = (tid % (D / 4)) * 4;
             const uint32_t at = smem_addr(&part[row][d]), at_m = smem_addr(&part_m[row]), at_l = smem_addr(&part_l[row]);
-            float m[kCluster], l[kCluster], top = -INFINITY, sum_l = 0.0f;
-            float4 v[kCluster];
+            float m[kMostBlocks], l[kMostBlocks], top = -INFINITY, sum_l = 0.0f;
+            float4 v[kMostBlocks];
 #pragma unroll
-            for (int i = 0; i < kCluster; ++i) {
-                m[i] = __uint_as_float(ld_cluster32(map_rank(at_m, i)));
-                l[i] = __uint_as_float(ld_cluster32(map_rank(at_l, i)));
-                v[i] = ld_cluster128(map_rank(at, i));
+            for (int i = 0; i < kMostBlocks; ++i) {
+                const int from = i < blocks ? i : rank;  // (blocks that there are not count for nothing)
+                m[i] = __uint_as_float(ld_cluster32(map_rank(at_m, from)));
+                l[i] = i < blocks ? __uint_as_float(ld_cluster32(map_rank(at_l, from))) : 0.0f;
+                m[i] = i < blocks ? m[i] : -INFINITY;
+                v[i] = ld_cluster128(map_rank(at, from));
                 top = fmaxf(top, m[i]);
             }
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < kCluster; ++i) {
+            for (int i = 0; i < kMostBlocks; ++i) {
                 const float f = join_factor(m[i], l[i], top);
                 sum_l = fmaf(f, l[i], sum_l);
                 acc.x = fmaf(f, v[i].x, acc.x);
@@ -666,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT)) attn_cluster_kern
 template <int D, int THREADS>
 __global__ void __launch_bounds__(THREADS) attn_join_kernel(const __grid_constant__ AttnArgs a, int blocks, int NR)
 {
-    constexpr int kLanes = D / 4, kSets = THREADS / kLanes, kMost = 2 * kSms;
+    constexpr int kLanes = D / 4, kSets = THREADS / kLanes, kMost = blocks_of(1);
     __shared__ float4 acc_of[kSets][kLanes];
     __shared__ float factor[kMost], l_of[kSets], top_of[THREADS / 32];
     __shared__ int counts[kMost / 32 + 1], which;
@@ -780,20 +847,23 @@ cudaError_t allow_shared(K kernel, int bytes, std::atomic<bool> (&ready)[kMaxCac
 template <int D, int NT>
 cudaError_t launch_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t stream)
 {
-    constexpr int kBlocks = blocks_of(NT), smem = Shared<D, NT>::kBytes;
-    if (attn_few_clusters(a.B, a.cache.heads, rows, a.max_pages * a.cache.page_size)) {
+    constexpr int kBlocks = blocks_of(NT);
+    const int cluster = cluster_of(a.B, a.cache.heads, rows, a.max_pages * a.cache.page_size, a.window);
+    if (cluster > 0) {
+        constexpr int smem = Shared<D, NT, kClusterWarps>::kBytes;
         static std::atomic<bool> ready[kMaxCachedDevices];
         const cudaError_t err = allow_shared(attn_cluster_kernel<D, NT>, smem, ready);
         if (err != cudaSuccess)
             return err;
-        return launch_clusters(attn_cluster_kernel<D, NT>, dim3((unsigned)(a.B * a.cache.heads * kCluster), (unsigned)((rows + 8 * NT - 1) / (8 * NT))),
-                               dim3(kThreads), smem, stream, pdl, kCluster, a);
+        return launch_clusters(attn_cluster_kernel<D, NT>, dim3((unsigned)(a.B * a.cache.heads * cluster), (unsigned)((rows + 8 * NT - 1) / (8 * NT))),
+                               dim3(kClusterWarps * 32), smem, stream, pdl, (unsigned)cluster, a, cluster);
     }
+    constexpr int smem = Shared<D, NT, share_warps(NT)>::kBytes;
     static std::atomic<bool> ready[kMaxCachedDevices];
     cudaError_t err = allow_shared(attn_few_kernel<D, NT>, smem, ready);
     if (err != cudaSuccess)
         return err;
-    err = launch_kernel(attn_few_kernel<D, NT>, dim3(kBlocks), dim3(kThreads), smem, stream, pdl, a);
+    err = launch_kernel(attn_few_kernel<D, NT>, dim3(kBlocks), dim3(share_warps(NT) * 32), smem, stream, pdl, a);
     if (err != cudaSuccess)
         return err;
     // at most as many units as rows of 8 NT, and one more for each sequence and head
@@ -806,23 +876,24 @@ cudaError_t launch_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t s
 
 }  // namespace
 
-bool attn_few_clusters(int64_t B, int64_t heads, int64_t rows, int64_t keys)
+bool attn_few_clusters(int64_t B, int64_t heads, int64_t rows, int64_t keys, int64_t window)
 {
-    const int64_t units = B * heads * (rows <= 8 ? 1 : (rows + 15) / 16);
-    return units <= kClusterUnits && keys <= kClusterKeys;
+    return cluster_of(B, heads, rows, keys, window) > 0;
 }
 
 cudaError_t launch_attn_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t stream)
 {
-    if (a.D == 64)
-        return rows <= 8 ? launch_few<64, 1>(a, rows, pdl, stream) : launch_few<64, 2>(a, rows, pdl, stream);
-    return rows <= 8 ? launch_few<128, 1>(a, rows, pdl, stream) : launch_few<128, 2>(a, rows, pdl, stream);
+    switch (eights_of(rows)) {
+    case 1: return a.D == 64 ? launch_few<64, 1>(a, rows, pdl, stream) : launch_few<128, 1>(a, rows, pdl, stream);
+    case 2: return a.D == 64 ? launch_few<64, 2>(a, rows, pdl, stream) : launch_few<128, 2>(a, rows, pdl, stream);
+    default: return a.D == 64 ? launch_few<64, 4>(a, rows, pdl, stream) : launch_few<128, 4>(a, rows, pdl, stream);
+    }
 }
 
 int64_t attn_few_workspace(int64_t D)
 {
     int64_t most = 0;  // (the same for every form, so that it does not shrink where max_q grows)
-    for (int nt = 1; nt <= 2; ++nt) {
+    for (int nt = 1; nt <= 4; nt *= 2) {
         const int64_t n = blocks_of(nt) * ((int64_t)sizeof(Record) + 2 * 4 * slot_floats(8 * nt, (int)D));
         most = n > most ? n : most;
     }

@@ -108,7 +108,7 @@ cudaError_t launch_cache_read(const CacheReadArgs &a, bool pdl, cudaStream_t str
 cudaError_t launch_attn_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t stream);
 int64_t attn_few_workspace(int64_t D);
 // Whether the first needs no workspace: units by clusters.  keys: a bound of a sequence's.
-bool attn_few_clusters(int64_t B, int64_t heads, int64_t rows, int64_t keys);
+bool attn_few_clusters(int64_t B, int64_t heads, int64_t rows, int64_t keys, int64_t window);
 cudaError_t launch_attn_prompt(const AttnArgs &a, bool pdl, cudaStream_t stream);
 int64_t attn_prompt_workspace(int64_t D);
 cudaError_t read_attn_stalled_waits(uint32_t *count);

@@ -760,7 +760,7 @@ PyObject *attention(PyObject *const *args, Py_ssize_t n)
     const float scale = c.none(8) ? (float)(1.0 / std::sqrt((double)(D > 0 ? D : 1))) : (float)c.number(8);
     const bool causal = c.truth(9);
     const int64_t window = c.integer(10);
-    const int64_t bytes = ts_nvfp4_attention_workspace(B, hq, cache.heads, D, max_q, table.size(1) * cache.page_size);
+    const int64_t bytes = ts_nvfp4_attention_workspace(B, hq, cache.heads, D, max_q, table.size(1) * cache.page_size, window);
     const bool with_lse = !c.none(12) || c.truth(13);
     at::Tensor out, lse, space;
     const int64_t lse_at = (T * hq * D * 2 + 255) / 256 * 256;

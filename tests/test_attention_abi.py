@@ -37,7 +37,7 @@ CALLS = {
     "ts_kv_cache_read": dict(cache=CACHE, slots=_at(0), T=9, k_out=_at(1), ldk=128, v_out=_at(2), ldv=136, flags=0,
                              stream=None),
     "ts_nvfp4_attention": dict(q=_at(0), ldq=400, T=9, q_heads=6, cu_q=_at(1), B=4, max_q=3, cache=CACHE, block_table=_at(2),
-                               max_pages=5000, kv_lens=_at(3), scale=0.125, causal=1, window=7, out=_at(4), ldo=384,
+                               max_pages=5000, kv_lens=_at(3), scale=0.125, causal=1, window=70000, out=_at(4), ldo=384,
                                lse=_at(5), workspace=_at(6), flags=0, stream=None),
 }
 R, G, V, A = CALLS
@@ -146,15 +146,16 @@ def test_workspaces(lib):
     for bad in (0, 8, 24, 272, -16):
         assert lib.ts_qk_norm_rope_grad_workspace(bad) == -1
     size = lib.ts_nvfp4_attention_workspace
-    assert size(1, 8, 1, 128, 1, 4096) == 0 and size(0, 8, 1, 128, 1, 0) == 0  # one launch
+    assert size(1, 8, 1, 128, 1, 4096, 0) == 0 and size(0, 8, 1, 128, 1, 0, 0) == 0  # one launch
+    assert size(100, 8, 1, 128, 1, 1 << 20, 64) == 0 < size(100, 8, 1, 128, 1, 1 << 20, 0)  # a window bounds the keys
     last = 0
-    for args in ((1, 8, 1, 128, 1, 4096), (500, 8, 1, 128, 1, 4096), (500, 8, 1, 128, 2, 4096), (500, 8, 1, 128, 40, 1 << 30)):
+    for args in ((1, 8, 1, 128, 1, 4096, 0), (500, 8, 1, 128, 1, 4096, 0), (500, 8, 1, 128, 2, 4096, 0), (500, 8, 1, 128, 40, 1 << 30, 0)):
         assert size(*args) >= last and size(*args) % 16 == 0
         last = size(*args)
     assert last > 0
-    for bad in ((1, 0, 1, 128, 1, 16), (1, 6, 4, 128, 1, 16), (1, 8, 1, 96, 1, 16), (1, 8, 1, 128, 0, 16), (1, 8, 0, 128, 1, 16),
-                (1, 8, -1, 128, 1, 16), (-1, 8, 1, 128, 1, 16), (65537, 8, 1, 128, 1, 16), (1, 8, 1, 128, 1, -1),
-                (1, 8, 1, 128, 1, (1 << 30) + 1)):
+    for bad in ((1, 0, 1, 128, 1, 16, 0), (1, 6, 4, 128, 1, 16, 0), (1, 8, 1, 96, 1, 16, 0), (1, 8, 1, 128, 0, 16, 0), (1, 8, 0, 128, 1, 16, 0),
+                (1, 8, -1, 128, 1, 16, 0), (-1, 8, 1, 128, 1, 16, 0), (65537, 8, 1, 128, 1, 16, 0), (1, 8, 1, 128, 1, -1, 0),
+                (1, 8, 1, 128, 1, (1 << 30) + 1, 0), (1, 8, 1, 128, 1, 16, -1)):
         assert size(*bad) == -1
 
 

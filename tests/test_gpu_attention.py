@@ -405,7 +405,7 @@ def test_strides_streams_and_graphs(dev):
     rows, qw, kw, angles = torch.empty(B, (hq + 2 * hk) * D + 8, dtype=torch.bfloat16, device=dev), _rand((D,), dev, 1), _rand((D,), dev, 2), ref.angles(far, D).to(dev)
     pos = (lens - 1).int()
     slots = (table.gather(1, (pos // page).long().unsqueeze(1)).squeeze(1) * page + pos % page).int()
-    space = torch.full((max(16, pkg.library().ts_nvfp4_attention_workspace(B, hq, hk, D, 1, table.shape[1] * page)),), 0xA5, dtype=torch.uint8, device=dev)
+    space = torch.full((max(16, pkg.library().ts_nvfp4_attention_workspace(B, hq, hk, D, 1, table.shape[1] * page, 0)),), 0xA5, dtype=torch.uint8, device=dev)
 
     def step(out, stream=None):
         q, k, v = (rows[:, a * D:b * D].unflatten(1, (b - a, D)) for a, b in ((0, hq), (hq, hq + hk), (hq + hk, hq + 2 * hk)))

@@ -22,8 +22,8 @@
 // is far from fp16's end.
 //
 // Work is split in one of two ways:
-//   - few units: a cluster of 8 blocks for each, whose parts are joined through the
-//     cluster's shared memory: one launch and no workspace;
+//   - units that are all resident at once: a cluster of up to 8 blocks for each, whose parts
+//     are joined through the cluster's shared memory: one launch and no workspace;
 //   - evenly: all units' tiles in one row, cut into equal shares, so that sequences of
 //     any lengths keep every block busy.  A unit inside a share is written at once; of a
 //     unit over several, each block leaves its part in the workspace and
@@ -39,7 +39,8 @@ namespace tsfn {
 namespace {
 
 // Even shares: for 8 rows blocks of 4 warps, four to an SM (64 sequences up to 16384 keys:
-// 107.7 us; blocks of 8 warps 113.7, five blocks of 4 with 96 registers 111.7); for more
+// 107.7 us; blocks of 8 warps 113.7, five blocks of 4 with 96 registers 111.7, all three
+// with a way of 12 tiles); for more
 // the registers of an SM go to one block of 8.  Clusters: blocks of 8 warps, for the
 // time of a single call.
 constexpr int kSms = 152;
@@ -52,8 +53,10 @@ constexpr int blocks_of(int nt) { return kSms * blocks_per_sm(nt); }
 int eights_of(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
 constexpr int kStages = 4;  // tiles of a warp whose copies are under way
 constexpr int kShare = 8;     // tiles of a share, at least
-// What going to a unit costs, in tiles of a block, when work is split.
-constexpr int way_of(int nt) { return 3 * share_warps(nt); }
+// What going to a unit costs, in tiles of a block, when work is split (64 sequences of 0 to
+// 16384 keys: 97 us with 20 or 24 for blocks of 4 warps, 106 with 12: the blocks that had
+// many short units ended last).
+constexpr int way_of(int nt) { return nt == 1 ? 20 : 24; }
 // Clusters take calls whose units are all resident at once, with at most this many keys a
 // block (16 tiles a warp: with more, sequences of different lengths leave SMs idle).
 constexpr int64_t kClusterKeys = 2048;
@@ -136,7 +139,14 @@ struct Shared {
     static constexpr int kMs = kRing, kLs = kMs + WARPS * NR * 4;  // the warps' maxima and sums
     static constexpr int kQ = kLs + WARPS * NR * 4;                // q's fragments of the products
     static constexpr int kFactor = kQ + NR * D * 2, kHi = kFactor + NR * 4, kLo = kHi + NR * 4;  // of each row
-    static constexpr int kLimits = kLo + NR * 4, kBytes = kLimits + 16;
+    static constexpr int kLimits = kLo + NR * 4, kBytes = kLimits + NT * 16;  // of each 8 rows
+    // where 4 elements of a row of O are, in fours: lanes that write together have
+    // different rows and d, and no bank in common
+    static __device__ __forceinline__ int place(int row, int four)
+    {
+        const int r = (row >> 1) & 3;
+        return row * (D / 4) + (four ^ (D == 128 ? r : (r & 1) | (r & 2) << 1));
+    }
 };
 
 // The parts (m, l, O) of a run's rows by the block's warps, in shared memory.
@@ -199,74 +209,68 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
     for (int k = 0; k < kStages - 1; ++k)
         issue(k < mine);
 
-    // the rows of q as fp16, each scaled by a power of two; their factors and limits; by one
-    // warp for all
-    if (warp == 0) {
-        int hi_min = 0x7fffffff, hi_max = 0, lo_min = 0x7fffffff, lo_max = 0;
-#pragma unroll 1
-        for (int nt = 0; nt < NT; ++nt) {
-            const int col = nt * 8 + g;
-            const bool live = col < run.rows;
-            const int r = run.row0 + col, i = live ? (int)div_by((uint32_t)r, a.div_group) : 0, qh = live ? r - i * a.group : 0;
-            const uint16_t *q = a.q + (int64_t)(s.q0 + i) * a.ldq + ((int64_t)run.head * a.group + qh) * D + t * (D / 4);
-            uint4 v[KS / 2];
+    // the rows of q as fp16, each scaled by a power of two; their factors and limits; by a
+    // warp for 8 of them
+    if (warp < NT) {
+        const int col = warp * 8 + g;
+        const bool live = col < run.rows;
+        const int r = run.row0 + col, i = live ? (int)div_by((uint32_t)r, a.div_group) : 0, qh = live ? r - i * a.group : 0;
+        const uint16_t *q = a.q + (int64_t)(s.q0 + i) * a.ldq + ((int64_t)run.head * a.group + qh) * D + t * (D / 4);
+        uint4 v[KS / 2];
 #pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (live)
-                    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w) : "l"(q + j * 8) : "memory");
-            }
-            float amax = 0.0f;
-#pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-                float f[8];
-                unpack8(v[j], f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    amax = fmaxf(amax, fabsf(f[e]));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            float down;
-            const float up = fp16_scale(amax, down);
-#pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-                float f[8];
-                unpack8(v[j], f);
-                *reinterpret_cast<uint4 *>(smem + Sh::kQ + ((nt * (KS / 2) + j) * 32 + lane) * 16) =
-                    make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up), pack_f16x2(f[4] * up, f[5] * up),
-                               pack_f16x2(f[6] * up, f[7] * up));
-            }
-            // limits of this row's keys
-            int h = a.causal ? s.len - s.n + i + 1 : s.len;  // (may be <= 0)
-            int l = a.window > 0 ? h - a.window : 0;
-            if (!live) {
-                h = 0x7fffffff;
-                l = 0;
-            }
-            l = l < 0 ? 0 : l;
-            if (t == 0) {
-                reinterpret_cast<float *>(smem + Sh::kFactor)[col] = c0 * down;
-                reinterpret_cast<int *>(smem + Sh::kHi)[col] = min(h, s.len);
-                reinterpret_cast<int *>(smem + Sh::kLo)[col] = l;
-            }
-            hi_min = min(hi_min, h);
-            lo_max = max(lo_max, l);
-            if (live) {
-                hi_max = max(hi_max, h);
-                lo_min = min(lo_min, l);
-            }
+        for (int j = 0; j < KS / 2; ++j) {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (live)
+                asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w) : "l"(q + j * 8) : "memory");
         }
-        hi_min = min(__reduce_min_sync(0xffffffffu, hi_min), s.len);
-        lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-        hi_max = min(__reduce_max_sync(0xffffffffu, hi_max), s.len);
-        lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+        float amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+            float f[8];
+            unpack8(v[j], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                amax = fmaxf(amax, fabsf(f[e]));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float down;
+        const float up = fp16_scale(amax, down);
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+            float f[8];
+            unpack8(v[j], f);
+            *reinterpret_cast<uint4 *>(smem + Sh::kQ + ((warp * (KS / 2) + j) * 32 + lane) * 16) =
+                make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up), pack_f16x2(f[4] * up, f[5] * up),
+                           pack_f16x2(f[6] * up, f[7] * up));
+        }
+        // limits of this row's keys
+        int h = a.causal ? s.len - s.n + i + 1 : s.len;  // (may be <= 0)
+        int l = a.window > 0 ? h - a.window : 0;
+        if (!live) {
+            h = 0x7fffffff;
+            l = 0;
+        }
+        l = l < 0 ? 0 : l;
+        if (t == 0) {
+            reinterpret_cast<float *>(smem + Sh::kFactor)[col] = c0 * down;
+            reinterpret_cast<int *>(smem + Sh::kHi)[col] = min(h, s.len);
+            reinterpret_cast<int *>(smem + Sh::kLo)[col] = l;
+        }
+        const int hi_min = __reduce_min_sync(0xffffffffu, h), lo_max = __reduce_max_sync(0xffffffffu, l);
+        const int hi_max = __reduce_max_sync(0xffffffffu, live ? h : 0), lo_min = __reduce_min_sync(0xffffffffu, live ? l : 0x7fffffff);
         if (lane == 0)
-            *reinterpret_cast<int4 *>(smem + Sh::kLimits) = make_int4(hi_min, lo_max, hi_max, lo_min);
+            *reinterpret_cast<int4 *>(smem + Sh::kLimits + warp * 16) = make_int4(min(hi_min, s.len), lo_max, min(hi_max, s.len), lo_min);
     }
     __syncthreads();
-    const int hi_min = reinterpret_cast<const int *>(smem + Sh::kLimits)[0], lo_max = reinterpret_cast<const int *>(smem + Sh::kLimits)[1];
+    int hi_min = 0x7fffffff, lo_max = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int2 limits = *reinterpret_cast<const int2 *>(smem + Sh::kLimits + nt * 16);
+        hi_min = min(hi_min, limits.x);
+        lo_max = max(lo_max, limits.y);
+    }
     float2 kept[NT];  // the rows' factors (32 rows leave no registers for them)
 #pragma unroll
     for (int nt = 0; nt < NT && NT < 4; ++nt)
@@ -370,7 +374,13 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
                     if (!(at < hi[col] && at >= lo[col]))
                         sc[nt][j] = -INFINITY;
                 }
-            const int hi_max = reinterpret_cast<const int *>(smem + Sh::kLimits)[2], lo_min = reinterpret_cast<const int *>(smem + Sh::kLimits)[3];
+            int hi_max = 0, lo_min = 0x7fffffff;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int2 limits = *reinterpret_cast<const int2 *>(smem + Sh::kLimits + nt * 16 + 8);
+                hi_max = max(hi_max, limits.x);
+                lo_min = min(lo_min, limits.y);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int at = key + t + 4 * j;
@@ -462,7 +472,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
     copies_wait<0>();
     __syncthreads();  // the ring is free
 
-    float *parts = reinterpret_cast<float *>(ring) + warp * NR * D;
+    float4 *const parts = reinterpret_cast<float4 *>(ring) + warp * NR * (D / 4);
     float *const ms = reinterpret_cast<float *>(smem + Sh::kMs), *const ls = reinterpret_cast<float *>(smem + Sh::kLs);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -478,8 +488,8 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
                 ls[warp * NR + col] = v;
             }
 #pragma unroll
-            for (int i = 0; i < KS; ++i)
-                *reinterpret_cast<float2 *>(parts + col * D + g * (D / 8) + 2 * i) = make_float2(o[nt][i][j], o[nt][i][j + 2]);
+            for (int i = 0; i < KS; i += 2)
+                parts[Sh::place(col, g * (D / 32) + i / 2)] = make_float4(o[nt][i][j], o[nt][i][j + 2], o[nt][i + 1][j], o[nt][i + 1][j + 2]);
         }
     }
     __syncthreads();
@@ -492,29 +502,45 @@ __device__ __forceinline__ float join_factor(float m, float l, float top)
     return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(m - top);
 }
 
-// 4 elements of a row, summed over the block's warps.
-template <int D, int NT, int WARPS>
-__device__ __forceinline__ float4 join_warps(const uint8_t *smem, int row, int d, float &top, float &sum)
+// What lane i's part counts for, of N parts with maximum m and sum l each (lanes i, i + N, ..
+// have the same one); the parts' maximum and sum.
+template <int N>
+__device__ __forceinline__ float part_factor(float m, float l, float &top, float &sum)
 {
-    constexpr int NR = 8 * NT;
-    const float *ms = reinterpret_cast<const float *>(smem + Shared<D, NT, WARPS>::kMs);
-    const float *ls = reinterpret_cast<const float *>(smem + Shared<D, NT, WARPS>::kLs);
-    top = -INFINITY;
+    top = m;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w)
-        top = fmaxf(top, ms[w * NR + row]);
-    sum = 0.0f;
+    for (int o = 1; o < N; o <<= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = join_factor(m, l, top);
+    sum = f * l;
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return f;
+}
+
+__device__ __forceinline__ void add_scaled(float4 &acc, float f, const float4 &v)
+{
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+}
+
+// 4 elements of a row, summed over the block's warps (by whole warps, of any rows).
+template <int D, int NT, int WARPS>
+__device__ __forceinline__ float4 join_warps(const uint8_t *smem, int row, int four, float &top, float &sum)
+{
+    using Sh = Shared<D, NT, WARPS>;
+    constexpr int NR = 8 * NT;
+    const int w0 = threadIdx.x % WARPS;
+    const float f = part_factor<WARPS>(reinterpret_cast<const float *>(smem + Sh::kMs)[w0 * NR + row],
+                                       reinterpret_cast<const float *>(smem + Sh::kLs)[w0 * NR + row], top, sum);
+    const float4 *const parts = reinterpret_cast<const float4 *>(smem) + Sh::place(row, four);
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const float f = join_factor(ms[w * NR + row], ls[w * NR + row], top);
-        sum = fmaf(f, ls[w * NR + row], sum);
-        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + (w * NR + row) * D + d);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
-    }
+    for (int w = 0; w < WARPS; ++w)
+        add_scaled(acc, __shfl_sync(0xffffffffu, f, w, WARPS), parts[w * NR * (D / 4)]);
     return acc;
 }
 
@@ -535,12 +561,13 @@ __device__ __forceinline__ void put_row(const AttnArgs &a, int q0, int head, int
 template <int D, int NT>
 __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_few_kernel(const __grid_constant__ AttnArgs a)
 {
-    constexpr int NR = 8 * NT, kWarps = share_warps(NT), kThreads = kWarps * 32;
+    constexpr int NR = 8 * NT, kWarps = share_warps(NT), kThreads = kWarps * 32, kWarpRows = 128 / D;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t sums[kThreads];
     __shared__ int64_t warp_sums[kWarps];
     __shared__ int64_t state[6];
     __shared__ Run kept;
+    __shared__ float factor;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float *const slots = a.partial + (int64_t)gridDim.x * (sizeof(Record) / 4);
     Record *const record = reinterpret_cast<Record *>(a.partial) + blockIdx.x;
@@ -593,7 +620,8 @@ __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_
         base = lo > 0 ? sums[lo - 1] : 0;
     }
     run.s = sequence<NR>(a, run.b);
-    const float c0 = a.scale * kLog2e / *a.cache.k_scale;
+    if (tid == 0)
+        factor = a.scale * kLog2e / *a.cache.k_scale;
 
     while (pos < end) {
         while (pos >= base + weight(a, run.s, way_of(NT))) {
@@ -624,7 +652,7 @@ __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_
             kept = run;
         }
         __syncthreads();
-        attend<D, NT, kWarps>(a, kept, c0, smem);
+        attend<D, NT, kWarps>(a, kept, factor, smem);
         run = kept;
         pos = state[0];
         end = state[1];
@@ -638,10 +666,12 @@ __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_
             record->row0 = run.row0;
         }
         float *slot = slots + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * slot_floats(NR, D);
-        for (int row = tid / (D / 4); row < run.rows; row += kThreads / (D / 4)) {
-            const int d = (tid % (D / 4)) * 4;
+        for (int r0 = tid / 32 * kWarpRows; r0 < run.rows; r0 += kWarps * kWarpRows) {
+            const int row = r0 + lane / (D / 4), d = (tid % (D / 4)) * 4;
             float top, sum_l;
-            const float4 acc = join_warps<D, NT, kWarps>(smem, row, d, top, sum_l);
+            const float4 acc = join_warps<D, NT, kWarps>(smem, row, d / 4, top, sum_l);
+            if (row >= run.rows)
+                continue;
             if (begins && ends) {
                 put_row<D>(a, run.s.q0, run.head, run.row0 + row, d, acc, top, sum_l, *a.cache.v_scale);
             } else {
@@ -658,25 +688,30 @@ __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_
     pdl_launch_dependents();
 }
 
-constexpr int kMostBlocks = 8;  // of a cluster
-
 // A cluster for each sequence and key head, and (the grid's y) row tile: its blocks share
-// the keys.
+// the keys.  Each block joins the cluster's parts of NR / blocks rows, which the others
+// write into its shared memory.
 template <int D, int NT>
 __global__ void __launch_bounds__(kClusterWarps * 32, NT == 1 ? 2 : 1) attn_cluster_kernel(const __grid_constant__ AttnArgs a, int blocks)
 {
-    constexpr int NR = 8 * NT, kWarps = kClusterWarps, kThreads = kWarps * 32;
+    constexpr int NR = 8 * NT, kWarps = kClusterWarps, kWarpRows = 128 / D, kMostBlocks = 8;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float part[NR][D];
+    __shared__ __align__(16) float part[NR][D];  // [blocks][NR / blocks][D]
     __shared__ float part_m[NR], part_l[NR];
-    const int tid = threadIdx.x, rank = (int)cluster_rank();
-    pdl_wait();
-    const int unit = blockIdx.x / blocks;
+    const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster_rank();
+    const int each = NR / blocks, unit = blockIdx.x / blocks;
+    cluster_arrive_relaxed();  // (a block's shared memory is there once it has started)
     Run run;
     run.b = unit / a.cache.heads;
     run.head = unit - run.b * a.cache.heads;
+    // the table is read where the copies begin: have it nearer by then
+    for (int64_t i = (int64_t)tid * 32; i < a.max_pages; i += kWarps * 32 * 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + (int64_t)run.b * a.max_pages + i));
+    pdl_wait();
+    const float c0 = a.scale * kLog2e / *a.cache.k_scale;
     run.s = sequence<NR>(a, run.b);
-    const float vg = *a.cache.v_scale, c0 = a.scale * kLog2e / *a.cache.k_scale;
+    if ((int)blockIdx.y >= run.s.parts)
+        cluster_wait();
     for (int rt = blockIdx.y; rt < run.s.parts; rt += gridDim.y) {
         run.row0 = rt * NR;
         run.rows = run.s.n * a.group - run.row0 < NR ? run.s.n * a.group - run.row0 : NR;
@@ -684,58 +719,49 @@ __global__ void __launch_bounds__(kClusterWarps * 32, NT == 1 ? 2 : 1) attn_clus
         run.first = run.s.first + begin;
         run.count = (int)((int64_t)run.s.tiles * (rank + 1) / blocks) - begin;
         attend<D, NT, kWarps>(a, run, c0, smem);
-        for (int row = tid / (D / 4); row < run.rows; row += kThreads / (D / 4)) {
-            const int d = (tid % (D / 4)) * 4;
+        const float vg = *a.cache.v_scale;
+        cluster_wait();  // every block has started, and has read what it was given before
+        for (int r0 = tid / 32 * kWarpRows; r0 < run.rows; r0 += kWarps * kWarpRows) {
+            const int row = r0 + lane / (D / 4), d = (tid % (D / 4)) * 4;
             float top, sum_l;
-            const float4 acc = join_warps<D, NT, kWarps>(smem, row, d, top, sum_l);
-            *reinterpret_cast<float4 *>(&part[row][d]) = acc;
+            const float4 acc = join_warps<D, NT, kWarps>(smem, row, d / 4, top, sum_l);
+            if (row >= run.rows)
+                continue;
+            const int to = row / each, at = rank * each + row - to * each;
+            st_cluster128(map_rank(smem_addr(&part[at][d]), to), acc);
             if (d == 0) {
-                part_m[row] = top;
-                part_l[row] = sum_l;
+                st_cluster32(map_rank(smem_addr(&part_m[at]), to), __float_as_uint(top));
+                st_cluster32(map_rank(smem_addr(&part_l[at]), to), __float_as_uint(sum_l));
             }
         }
         cluster_sync();
-        // each block joins the cluster's parts of its rows
-        const int each = NR / blocks;
-        for (int row = rank * each + tid / (D / 4); row < (rank + 1) * each && row < run.rows; row += kThreads / (D / 4)) {
-            const int d = (tid % (D / 4)) * 4;
-            const uint32_t at = smem_addr(&part[row][d]), at_m = smem_addr(&part_m[row]), at_l = smem_addr(&part_l[row]);
-            float m[kMostBlocks], l[kMostBlocks], top = -INFINITY, sum_l = 0.0f;
-            float4 v[kMostBlocks];
-#pragma unroll
-            for (int i = 0; i < kMostBlocks; ++i) {
-                const int from = i < blocks ? i : rank;  // (blocks that there are not count for nothing)
-                m[i] = __uint_as_float(ld_cluster32(map_rank(at_m, from)));
-                l[i] = i < blocks ? __uint_as_float(ld_cluster32(map_rank(at_l, from))) : 0.0f;
-                m[i] = i < blocks ? m[i] : -INFINITY;
-                v[i] = ld_cluster128(map_rank(at, from));
-                top = fmaxf(top, m[i]);
-            }
+        for (int r0 = tid / 32 * kWarpRows; r0 < each; r0 += kWarps * kWarpRows) {
+            const int r = r0 + lane / (D / 4), d = (tid % (D / 4)) * 4, row = rank * each + r;
+            const int at = (lane % kMostBlocks) * each + (r < each ? r : 0);
+            const bool some = lane % kMostBlocks < blocks;
+            float top, sum_l;
+            const float f = part_factor<kMostBlocks>(some ? part_m[at] : -INFINITY, some ? part_l[at] : 0.0f, top, sum_l);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < kMostBlocks; ++i) {
-                const float f = join_factor(m[i], l[i], top);
-                sum_l = fmaf(f, l[i], sum_l);
-                acc.x = fmaf(f, v[i].x, acc.x);
-                acc.y = fmaf(f, v[i].y, acc.y);
-                acc.z = fmaf(f, v[i].z, acc.z);
-                acc.w = fmaf(f, v[i].w, acc.w);
-            }
-            put_row<D>(a, run.s.q0, run.head, run.row0 + row, d, acc, top, sum_l, vg);
+            for (int i = 0; i < blocks; ++i)
+                add_scaled(acc, __shfl_sync(0xffffffffu, f, i, kMostBlocks), *reinterpret_cast<const float4 *>(&part[i * each + (r < each ? r : 0)][d]));
+            if (r < each && row < run.rows)
+                put_row<D>(a, run.s.q0, run.head, run.row0 + row, d, acc, top, sum_l, vg);
         }
-        cluster_sync();  // the parts have been read
+        if (rt + (int)gridDim.y < run.s.parts)
+            cluster_arrive();
     }
     pdl_launch_dependents();
 }
 
-// Units over several blocks: block (x, y) has row y of the x-th of them, each set of
-// lanes a run of the parts in order, whose loads are all under way together.
-template <int D, int THREADS>
+// Units over several blocks: block (x, y, z) has row y of the x-th of them, and of that
+// the z-th LANES times 4 elements; each set of LANES lanes takes a run of the parts in
+// order, whose loads are all under way together.
+template <int D, int LANES, int THREADS>
 __global__ void __launch_bounds__(THREADS) attn_join_kernel(const __grid_constant__ AttnArgs a, int blocks, int NR)
 {
-    constexpr int kLanes = D / 4, kSets = THREADS / kLanes, kMost = blocks_of(1);
-    __shared__ float4 acc_of[kSets][kLanes];
-    __shared__ float factor[kMost], l_of[kSets], top_of[THREADS / 32];
+    constexpr int kSets = THREADS / LANES, kWarps = THREADS / 32, kMost = blocks_of(1);
+    __shared__ float4 acc_of[kWarps][LANES];
+    __shared__ float factor[kMost], l_of[kWarps], top_of[kWarps];
     __shared__ int counts[kMost / 32 + 1], which;
     const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     pdl_wait();
@@ -791,7 +817,7 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i)
         top = fmaxf(top, top_of[i]);
-    const int set = tid / kLanes, d = (tid % kLanes) * 4, per = (n + kSets - 1) / kSets;
+    const int set = tid / LANES, d = ((int)blockIdx.z * LANES + tid % LANES) * 4, per = (n + kSets - 1) / kSets;
     const int i0 = min(n, set * per), i1 = min(n, i0 + per);
     float l = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -802,29 +828,37 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const __grid_constan
         const float4 v = *reinterpret_cast<const float4 *>(slot + row * D + d);
         const float f = join_factor(factor[i], li, top);
         l = fmaf(f, li, l);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+        add_scaled(acc, f, v);
     }
-    acc_of[set][tid % kLanes] = acc;
-    if (d == 0)
-        l_of[set] = l;
-    __syncthreads();
-    if (set != 0)
-        return;
-    float sum = 0.0f;
-    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // the sets of a warp, then the warps
+    auto over_sets = [&]() {
 #pragma unroll
-    for (int i = 0; i < kSets; ++i) {
-        const float4 v = acc_of[i][tid];
-        sum += l_of[i];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+        for (int o = LANES; o < 32; o <<= 1) {
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+            acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+            acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+            acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+            acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+        }
+    };
+    over_sets();
+    if (lane < LANES)
+        acc_of[tid >> 5][lane] = acc;
+    if (lane == 0)
+        l_of[tid >> 5] = l;
+    __syncthreads();
+    if (tid >= 32)
+        return;
+    l = 0.0f;
+    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int i = lane / LANES; i < kWarps; i += 32 / LANES) {
+        l += l_of[i];
+        add_scaled(acc, 1.0f, acc_of[i][lane % LANES]);
     }
-    put_row<D>(a, rec.q0, rec.head, rec.row0 + row, d, acc, top, sum, *a.cache.v_scale);
+    over_sets();
+    if (lane < LANES)
+        put_row<D>(a, rec.q0, rec.head, rec.row0 + row, d, acc, top, l, *a.cache.v_scale);
 }
 
 // Dynamic shared memory above 48 KB, asked for once a device.
@@ -868,9 +902,9 @@ cudaError_t launch_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t s
         return err;
     // at most as many units as rows of 8 NT, and one more for each sequence and head
     const int64_t units = a.cache.heads * (a.T * a.group / (8 * NT) + a.B);
-    if (units < 32)  // few units, of many parts each
-        return launch_kernel(attn_join_kernel<D, 1024>, dim3((unsigned)units, 8 * NT), dim3(1024), 0, stream, true, a, kBlocks, 8 * NT);
-    return launch_kernel(attn_join_kernel<D, 256>, dim3((unsigned)(units < kBlocks ? units : kBlocks), 8 * NT), dim3(256), 0, stream, true, a,
+    if (units * 8 * NT * (D / 32) <= 2 * kSms)  // few units, of many parts each: all resident at once
+        return launch_kernel(attn_join_kernel<D, 8, 1024>, dim3((unsigned)units, 8 * NT, D / 32), dim3(1024), 0, stream, true, a, kBlocks, 8 * NT);
+    return launch_kernel(attn_join_kernel<D, D / 4, 256>, dim3((unsigned)(units < kBlocks ? units : kBlocks), 8 * NT), dim3(256), 0, stream, true, a,
                          kBlocks, 8 * NT);
 }
 

@@ -28,6 +28,7 @@
 //     any lengths keep every block busy.  A unit inside a share is written at once; of a
 //     unit over several, each block leaves its part in the workspace and
 //     attn_join_kernel joins them in order.
+#include "async_copy.cuh"
 #include "attn_util.cuh"
 #include "device_util.cuh"
 #include "launch_attention.h"
@@ -71,18 +72,6 @@ int cluster_of(int64_t B, int64_t heads, int64_t rows, int64_t keys, int64_t win
         if (units * blocks <= resident)
             return keys <= kClusterKeys * blocks ? blocks : 0;
     return 0;
-}
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t v)

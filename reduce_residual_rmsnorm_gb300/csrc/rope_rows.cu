@@ -10,6 +10,7 @@
 // shuffles, and what they are multiplied by goes into the factors.  A group of lanes
 // takes a run of heads of one token, the next ones' loads under way, and the
 // position's cosines and sines and the weights are read, and multiplied, once for them.
+#include "async_copy.cuh"
 #include "device_util.cuh"
 #include "f32x2.cuh"
 #include "launch_attention.h"
@@ -261,20 +262,25 @@ __global__ void __launch_bounds__(kThreads, CACHE ? 3 : 4) rope_kernel(const __g
 
 // dx as above; the weights' gradient is summed by each lane over its runs, then over
 // the groups of a block in order, and over the blocks by grad_sum_kernel.
-// Blocks of 128 threads, five to an SM: 96 registers, with which two heads' loads are
-// under way while two others are worked on.
-constexpr int kGradThreads = 128;
+// A group's heads, run after run, are one row of steps, whose copies to shared memory are
+// under way kGradAhead steps before: registers would not hold as many.
+constexpr int kGradThreads = 128, kGradAhead = 3, kGradStages = kGradAhead + 1;
+constexpr int kGradRing = kGradStages * 2 * kGradThreads * 16;  // [stages][x, dy][threads]
 
 template <bool PAIRS>
 __global__ void __launch_bounds__(kGradThreads, 5) rope_grad_kernel(const __grid_constant__ RopeGradArgs a)
 {
-    extern __shared__ float sums[];  // [groups of lanes][lanes * 8]
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *const sums = reinterpret_cast<float *>(smem + kGradRing);  // [groups of lanes][lanes * 8]
     const int lanes = 1 << a.lanes_log2;
     const int lane = threadIdx.x & 31, c = lane & (lanes - 1);
     const int groups = kGradThreads >> a.lanes_log2, group = threadIdx.x >> a.lanes_log2;
     const bool in_row = c < (a.D >> 3);
     const Turn turn = turn_of(c, lane, a.rot, PAIRS);
     const float inv_d = 1.0f / (float)a.D;
+    uint8_t *const ring = smem + threadIdx.x * 16;
+    int put = 0, take = 0;  // stages, as offsets
+    auto next = [](int at) { return at + 2 * kGradThreads * 16 == kGradRing ? 0 : at + 2 * kGradThreads * 16; };
     pdl_wait();
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
@@ -287,26 +293,61 @@ __global__ void __launch_bounds__(kGradThreads, 5) rope_grad_kernel(const __grid
             for (int i = 0; i < 4; ++i)
                 wf[i] = widen2(ww[i]);
         }
-        const int64_t all = a.T * a.runs[kind];
+        const uint32_t all = (uint32_t)(a.T * a.runs[kind]);  // (below 2^31, as T * heads)
         // (a warp's lanes stay together: the loop's bound is that of its first group)
-        const int64_t per = (int64_t)gridDim.x * groups;
+        const uint32_t per = gridDim.x * groups;
         const int first = ((threadIdx.x & ~31) >> a.lanes_log2);
-        for (int64_t base = (int64_t)blockIdx.x * groups + first; base < all; base += per) {
-            const int64_t id = base + (group - first);
-            bool live = id < all;
-            const int64_t t = live ? div_by((uint32_t)id, a.div_runs[kind]) : 0;
-            const int h0 = (int)(id - t * a.runs[kind]) * a.run_heads;
-            const int n = live ? min(a.run_heads, a.heads[kind] - h0) : 0, most = __reduce_max_sync(0xffffffffu, n);
-            const int32_t pos = live ? a.pos[t] : -1;
-            const int64_t at = (int64_t)h0 * a.D + c * 8;
-            const uint16_t *xs = a.x[kind] + t * a.ldx[kind] + at, *ds = a.dy[kind] + t * a.lddy[kind] + at;
-            uint16_t *to = a.dx[kind] + t * a.lddx[kind] + at;
-            uint4 next_x = make_uint4(0, 0, 0, 0), next_d = next_x;
-            if (in_row && n > 0) {
-                next_x = ld_stream(xs);
-                next_d = ld_stream(ds);
+        const uint32_t begin = blockIdx.x * groups + first;
+        // the run that a group has from `base` on: its token, first head and heads
+        auto run_at = [&](uint32_t base, int64_t &t, int &h0) {
+            const uint32_t id = base + (group - first), token = id < all ? div_by(id, a.div_runs[kind]) : 0;
+            t = token;
+            h0 = (int)(id - token * a.runs[kind]) * a.run_heads;
+            return id < all ? min(a.run_heads, a.heads[kind] - h0) : (h0 = 0);
+        };
+        uint32_t in_base = begin;
+        int in_n = 0, in_most = 0;  // heads left of the run that is copied
+        const uint16_t *xs = nullptr, *ds = nullptr;
+        auto issue = [&]() {
+            if (in_most == 0 && in_base < all) {
+                int64_t t;
+                int h0;
+                in_n = run_at(in_base, t, h0);
+                in_most = __reduce_max_sync(0xffffffffu, in_n);
+                xs = a.x[kind] + t * a.ldx[kind] + (int64_t)h0 * a.D + c * 8;
+                ds = a.dy[kind] + t * a.lddy[kind] + (int64_t)h0 * a.D + c * 8;
+                in_base += per;
             }
-            live = live && pos >= 0 && pos < a.max_pos;
+            if (in_most > 0) {
+                const int bytes = in_row && in_n > 0 ? 16 : 0;
+                copy16(smem_addr(ring + put), bytes ? xs : a.x[kind], bytes);
+                copy16(smem_addr(ring + put + kGradThreads * 16), bytes ? ds : a.dy[kind], bytes);
+                xs += a.D;
+                ds += a.D;
+                --in_n;
+                --in_most;
+            }
+            copies_commit();
+            put = next(put);
+        };
+        auto pos_at = [&](uint32_t base) {
+            int64_t t;
+            int h0;
+            return base < all && run_at(base, t, h0) > 0 ? a.pos[t] : -1;
+        };
+        put = take;  // (no copies are under way)
+#pragma unroll 1
+        for (int i = 0; i < kGradAhead; ++i)
+            issue();
+        int32_t next_pos = pos_at(begin);
+        for (uint32_t base = begin; base < all; base += per) {
+            int64_t t;
+            int h0;
+            const int n = run_at(base, t, h0), most = __reduce_max_sync(0xffffffffu, n);
+            const int32_t pos = next_pos;
+            next_pos = pos_at(base + per);
+            uint16_t *to = a.dx[kind] + t * a.lddx[kind] + (int64_t)h0 * a.D + c * 8;
+            const bool live = pos >= 0 && pos < a.max_pos;
             float cs[8] = {}, sn[8] = {};
             if (live && turn.in) {
                 const float *p = a.table + (int64_t)pos * a.rot + turn.angle;
@@ -315,14 +356,13 @@ __global__ void __launch_bounds__(kGradThreads, 5) rope_grad_kernel(const __grid
             }
             const Factors f = factors_of<PAIRS>(cs, sn, turn, -1.0f);
             for (int h = 0; h < most; ++h) {
-                const uint4 x = next_x, d = next_d;
-                xs += a.D;
-                ds += a.D;
-                if (in_row && h + 1 < n) {
-                    next_x = ld_stream(xs);
-                    next_d = ld_stream(ds);
-                }
+                issue();
+                copies_wait<kGradAhead>();
+                uint4 x = *reinterpret_cast<const uint4 *>(ring + take), d = *reinterpret_cast<const uint4 *>(ring + take + kGradThreads * 16);
+                take = next(take);
                 const bool on = live && in_row && h < n;
+                if (!on)  // (what a row that is left out holds may be NaN)
+                    x = d = make_uint4(0, 0, 0, 0);
                 const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, xw[4] = {x.x, x.y, x.z, x.w};
                 uint64_t o[4], v[4];
                 partners<PAIRS>(d, turn, o);
@@ -344,7 +384,7 @@ __global__ void __launch_bounds__(kGradThreads, 5) rope_grad_kernel(const __grid
                     }
                     const float r = rsqrtf(__fmaf_rn(sq, inv_d, a.eps));
                     const uint64_t by = twice(r), less = twice(-(dot * inv_d) * r * r);
-                    const uint64_t sum = twice(on ? r : 0.0f);
+                    const uint64_t sum = twice(on ? r : 0.0f);  // (no 0 times the root of 1 / 0)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint64_t xf = widen2(xw[i]);
@@ -375,26 +415,37 @@ __global__ void __launch_bounds__(kGradThreads, 5) rope_grad_kernel(const __grid
     pdl_launch_dependents();
 }
 
-// dw[kind][j] = the blocks' sums in order: 8 threads a column take every eighth block.
-__global__ void __launch_bounds__(256) grad_sum_kernel(const float *partial, int blocks, int D, float *dqw, float *dkw)
+// dw[kind][j] = the blocks' sums in order: 128 lanes for each of 8 columns take every
+// 128th block, so that all loads are under way together.
+constexpr int kSumThreads = 1024, kSumColumns = 8;
+
+__global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const float *partial, int blocks, int D, float *dqw, float *dkw)
 {
-    __shared__ float sums[8][33];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    __shared__ float sums[kSumThreads / 32][kSumColumns];
+    const int col = blockIdx.x * kSumColumns + threadIdx.x % kSumColumns, lane = threadIdx.x & 31;  // (D is a multiple of 16)
     pdl_wait();
     pdl_launch_dependents();
     float s = 0.0f;
-    if (col < 2 * D) {
-#pragma unroll 8
-        for (int i = part; i < blocks; i += 8)
-            s += partial[(int64_t)i * 2 * D + col];
-    }
-    sums[part][threadIdx.x & 31] = s;
+#pragma unroll 6
+    for (int i = threadIdx.x / kSumColumns; i < blocks; i += kSumThreads / kSumColumns)
+        s += partial[(int64_t)i * 2 * D + col];
+    auto over_lanes = [&]() {
+#pragma unroll
+        for (int o = kSumColumns; o < 32; o <<= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+    };
+    over_lanes();
+    if (lane < kSumColumns)
+        sums[threadIdx.x >> 5][lane] = s;
     __syncthreads();
-    if (part == 0 && col < 2 * D) {
-        for (int i = 1; i < 8; ++i)
-            s += sums[i][threadIdx.x];
+    if (threadIdx.x >= 32)
+        return;
+    s = 0.0f;
+    for (int i = lane / kSumColumns; i < kSumThreads / 32; i += 32 / kSumColumns)
+        s += sums[i][lane % kSumColumns];
+    over_lanes();
+    if (lane < kSumColumns)
         (col < D ? dqw : dkw)[col < D ? col : col - D] = s;
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -489,12 +540,12 @@ cudaError_t launch_rope_grad(const RopeGradArgs &args, bool pdl, cudaStream_t st
     const int groups = kGradThreads >> a.lanes_log2;
     const int64_t want = (a.T * most + groups - 1) / groups;
     const int blocks = (int)(want < 1 ? 1 : (want > kGradBlocks ? kGradBlocks : want));
-    const size_t smem = kGradThreads * 8 * sizeof(float);
+    const size_t smem = kGradRing + kGradThreads * 8 * sizeof(float);
     const cudaError_t err = a.pairs ? launch_kernel(rope_grad_kernel<true>, dim3((unsigned)blocks), dim3(kGradThreads), smem, stream, pdl, a)
                                     : launch_kernel(rope_grad_kernel<false>, dim3((unsigned)blocks), dim3(kGradThreads), smem, stream, pdl, a);
     if (err != cudaSuccess || a.w[0] == nullptr)
         return err;
-    return launch_kernel(grad_sum_kernel, dim3((unsigned)((2 * a.D + 31) / 32)), dim3(256), 0, stream, true,
+    return launch_kernel(grad_sum_kernel, dim3((unsigned)(2 * a.D / kSumColumns)), dim3(kSumThreads), 0, stream, true,
                          (const float *)a.partial, blocks, a.D, a.dw[0], a.dw[1]);
 }
 

@@ -170,6 +170,31 @@ def test_norm_rope_grad_in_place_and_empty(dev):
     assert bool((dqw == 0).all() and (dkw == 0).all())
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("T,hq,hk,D,rot", [(37, 6, 2, 64, 32), (9, 3, 1, 48, 16), (2000, 40, 5, 128, 128)])
+def test_norm_rope_grad_leaves_out_bad_positions(dev, T, hq, hk, D, rot, pairs):
+    """Rows behind a batch's end (positions below zero or past the table) may hold anything: NaN there
+    reaches neither the weights' gradient nor another row."""
+    q, k, _, qw, kw, pos, table = _rope_inputs(dev, T, hq, hk, D, rot, seed=9)
+    dq, dk = _rand((T, hq, D), dev, 1), _rand((T, hk, D), dev, 2)
+    out = torch.arange(T, device=dev) % 3 == 1
+    pos = torch.where(out, torch.where(torch.arange(T, device=dev) % 2 == 0, -1, table.shape[0]).to(pos.dtype), pos)
+    keep = ~out
+    want = pkg.ts_qk_norm_rope_grad(dq[keep], dk[keep], q[keep].contiguous(), k[keep].contiguous(), qw, kw, pos[keep].contiguous(),
+                                    table, EPS, interleaved=pairs)
+    for t in (dq, dk, q, k):
+        t[out] = float("nan")
+    to = [torch.full((T, h, D), 3.0, dtype=torch.bfloat16, device=dev) for h in (hq, hk)]
+    got = pkg.ts_qk_norm_rope_grad(dq, dk, q, k, qw, kw, pos, table, EPS, interleaved=pairs, dq=to[0], dk=to[1])
+    for i in (0, 1):
+        assert torch.equal(got[i][keep], want[i]) and bool((to[i][out] == 3.0).all())
+        # the same terms in another order: twice a sum's error, of the magnitudes' sum (at most sqrt(n) more than the sum's own)
+        x, dy = ((q, dq), (k, dk))[i]
+        r = torch.rsqrt(x[keep].double().square().mean(-1, keepdim=True) + EPS)
+        mag = (2 * dy[keep].double().abs().amax(-1, keepdim=True) * (x[keep].double() * r).abs()).sum((0, 1))
+        assert bool(((got[2 + i].double() - want[2 + i].double()).abs() <= 2 * (D + 64) * 2.0 ** -24 * mag).all())
+
+
 # ---------------------------------------------------------------------------
 # the cache
 # ---------------------------------------------------------------------------

@@ -62,8 +62,7 @@ struct RopeGradArgs {
     int64_t lddx[2];
     float *dw[2];
     float *partial;  // [blocks, 2, D]
-    int run_heads, runs[2];  // as above
-    DivMagic div_runs[2];
+    DivMagic div_heads[2];
 };
 
 struct CacheReadArgs {

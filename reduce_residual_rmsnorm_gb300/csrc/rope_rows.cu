@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, CACHE ? 3 : 4) rope_kernel(const __g
 
 // dx as above; the weights' gradient is summed by each lane over its runs, then over
 // the groups of a block in order, and over the blocks by grad_sum_kernel.
-// A group's heads, run after run, are one row of steps, whose copies to shared memory are
+// A group's share of the heads of all tokens is one row of steps, whose copies to shared memory are
 // under way kGradAhead steps before: registers would not hold as many.
 constexpr int kGradThreads = 128, kGradAhead = 3, kGradStages = kGradAhead + 1;
 constexpr int kGradRing = kGradStages * 2 * kGradThreads * 16;  // [stages][x, dy][threads]
@@ -293,109 +293,98 @@ __global__ void __launch_bounds__(kGradThreads, 5) rope_grad_kernel(const __grid
             for (int i = 0; i < 4; ++i)
                 wf[i] = widen2(ww[i]);
         }
-        const uint32_t all = (uint32_t)(a.T * a.runs[kind]);  // (below 2^31, as T * heads)
-        // (a warp's lanes stay together: the loop's bound is that of its first group)
-        const uint32_t per = gridDim.x * groups;
-        const int first = ((threadIdx.x & ~31) >> a.lanes_log2);
-        const uint32_t begin = blockIdx.x * groups + first;
-        // the run that a group has from `base` on: its token, first head and heads
-        auto run_at = [&](uint32_t base, int64_t &t, int &h0) {
-            const uint32_t id = base + (group - first), token = id < all ? div_by(id, a.div_runs[kind]) : 0;
-            t = token;
-            h0 = (int)(id - token * a.runs[kind]) * a.run_heads;
-            return id < all ? min(a.run_heads, a.heads[kind] - h0) : (h0 = 0);
-        };
-        uint32_t in_base = begin;
-        int in_n = 0, in_most = 0;  // heads left of the run that is copied
-        const uint16_t *xs = nullptr, *ds = nullptr;
+        // the group's steps: its share of all heads of all tokens, one after the other
+        const int heads = a.heads[kind];
+        const int64_t all = a.T * heads, sharers = (int64_t)gridDim.x * groups, sharer = (int64_t)blockIdx.x * groups + group;
+        const int64_t begin = all * sharer / sharers;
+        const int n = (int)(all * (sharer + 1) / sharers - begin), most = __reduce_max_sync(0xffffffffu, n);
+        int64_t t = div_by((uint32_t)begin, a.div_heads[kind]);
+        int h = (int)(begin - t * heads), in_h = h, in_step = 0;
+        const uint16_t *xs = a.x[kind] + t * a.ldx[kind] + (int64_t)h * a.D + c * 8;
+        const uint16_t *ds = a.dy[kind] + t * a.lddy[kind] + (int64_t)h * a.D + c * 8;
+        uint16_t *to = a.dx[kind] + t * a.lddx[kind] + (int64_t)h * a.D + c * 8;
         auto issue = [&]() {
-            if (in_most == 0 && in_base < all) {
-                int64_t t;
-                int h0;
-                in_n = run_at(in_base, t, h0);
-                in_most = __reduce_max_sync(0xffffffffu, in_n);
-                xs = a.x[kind] + t * a.ldx[kind] + (int64_t)h0 * a.D + c * 8;
-                ds = a.dy[kind] + t * a.lddy[kind] + (int64_t)h0 * a.D + c * 8;
-                in_base += per;
-            }
-            if (in_most > 0) {
-                const int bytes = in_row && in_n > 0 ? 16 : 0;
-                copy16(smem_addr(ring + put), bytes ? xs : a.x[kind], bytes);
-                copy16(smem_addr(ring + put + kGradThreads * 16), bytes ? ds : a.dy[kind], bytes);
-                xs += a.D;
-                ds += a.D;
-                --in_n;
-                --in_most;
+            if (in_row && in_step < n) {
+                copy16(smem_addr(ring + put), xs);
+                copy16(smem_addr(ring + put + kGradThreads * 16), ds);
             }
             copies_commit();
             put = next(put);
-        };
-        auto pos_at = [&](uint32_t base) {
-            int64_t t;
-            int h0;
-            return base < all && run_at(base, t, h0) > 0 ? a.pos[t] : -1;
+            xs += a.D;
+            ds += a.D;
+            ++in_step;
+            if (++in_h == heads) {
+                in_h = 0;
+                xs += a.ldx[kind] - (int64_t)heads * a.D;
+                ds += a.lddy[kind] - (int64_t)heads * a.D;
+            }
         };
         put = take;  // (no copies are under way)
 #pragma unroll 1
         for (int i = 0; i < kGradAhead; ++i)
             issue();
-        int32_t next_pos = pos_at(begin);
-        for (uint32_t base = begin; base < all; base += per) {
-            int64_t t;
-            int h0;
-            const int n = run_at(base, t, h0), most = __reduce_max_sync(0xffffffffu, n);
-            const int32_t pos = next_pos;
-            next_pos = pos_at(base + per);
-            uint16_t *to = a.dx[kind] + t * a.lddx[kind] + (int64_t)h0 * a.D + c * 8;
-            const bool live = pos >= 0 && pos < a.max_pos;
-            float cs[8] = {}, sn[8] = {};
-            if (live && turn.in) {
-                const float *p = a.table + (int64_t)pos * a.rot + turn.angle;
-                ld_angles(p, PAIRS ? 1 : 2, cs);
-                ld_angles(p + (a.rot >> 1), PAIRS ? 1 : 2, sn);
+        auto pos_at = [&](int64_t token) { return n > 0 && token < a.T ? a.pos[token] : -1; };
+        int32_t next_pos = pos_at(t);
+        bool live = false;
+        Factors f;
+        for (int step = 0; step < most; ++step) {
+            issue();
+            if (step == 0 || h == heads) {  // a token's first
+                if (step > 0) {
+                    h = 0;
+                    ++t;
+                    to += a.lddx[kind] - (int64_t)heads * a.D;
+                }
+                const int32_t pos = next_pos;
+                next_pos = pos_at(t + 1);
+                live = pos >= 0 && pos < a.max_pos;
+                float cs[8] = {}, sn[8] = {};
+                if (live && turn.in) {
+                    const float *p = a.table + (int64_t)pos * a.rot + turn.angle;
+                    ld_angles(p, PAIRS ? 1 : 2, cs);
+                    ld_angles(p + (a.rot >> 1), PAIRS ? 1 : 2, sn);
+                }
+                f = factors_of<PAIRS>(cs, sn, turn, -1.0f);
             }
-            const Factors f = factors_of<PAIRS>(cs, sn, turn, -1.0f);
-            for (int h = 0; h < most; ++h) {
-                issue();
-                copies_wait<kGradAhead>();
-                uint4 x = *reinterpret_cast<const uint4 *>(ring + take), d = *reinterpret_cast<const uint4 *>(ring + take + kGradThreads * 16);
-                take = next(take);
-                const bool on = live && in_row && h < n;
-                if (!on)  // (what a row that is left out holds may be NaN)
-                    x = d = make_uint4(0, 0, 0, 0);
-                const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, xw[4] = {x.x, x.y, x.z, x.w};
-                uint64_t o[4], v[4];
-                partners<PAIRS>(d, turn, o);
+            copies_wait<kGradAhead>();
+            uint4 x = *reinterpret_cast<const uint4 *>(ring + take), d = *reinterpret_cast<const uint4 *>(ring + take + kGradThreads * 16);
+            take = next(take);
+            const bool on = live && in_row && step < n;
+            if (!on)  // (what a row that is left out holds may be NaN)
+                x = d = make_uint4(0, 0, 0, 0);
+            const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, xw[4] = {x.x, x.y, x.z, x.w};
+            uint64_t o[4], v[4];
+            partners<PAIRS>(d, turn, o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = fma2(widen2(dw[i]), f.by[i], mul2(o[i], f.with[i]));
+            if (w != nullptr) {
+                // both sums over the row side by side: x^2, and g x with g = d w
+                uint64_t gx = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[i] = fma2(widen2(dw[i]), f.by[i], mul2(o[i], f.with[i]));
-                if (w != nullptr) {
-                    // both sums over the row side by side: x^2, and g x with g = d w
-                    uint64_t gx = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        gx = fma2(mul2(v[i], wf[i]), widen2(xw[i]), gx);
-                    float s0, s1;
-                    unpair(gx, s0, s1);
-                    float sq = sumsq_bf16x8(x, 0.0f), dot = s0 + s1;
-                    for (int k = lanes >> 1; k > 0; k >>= 1) {
-                        sq += __shfl_xor_sync(0xffffffffu, sq, k);
-                        dot += __shfl_xor_sync(0xffffffffu, dot, k);
-                    }
-                    const float r = rsqrtf(__fmaf_rn(sq, inv_d, a.eps));
-                    const uint64_t by = twice(r), less = twice(-(dot * inv_d) * r * r);
-                    const uint64_t sum = twice(on ? r : 0.0f);  // (no 0 times the root of 1 / 0)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint64_t xf = widen2(xw[i]);
-                        acc[i] = fma2(mul2(v[i], xf), sum, acc[i]);
-                        v[i] = mul2(fma2(xf, less, mul2(v[i], wf[i])), by);
-                    }
+                    gx = fma2(mul2(v[i], wf[i]), widen2(xw[i]), gx);
+                float s0, s1;
+                unpair(gx, s0, s1);
+                float sq = sumsq_bf16x8(x, 0.0f), dot = s0 + s1;
+                for (int k = lanes >> 1; k > 0; k >>= 1) {
+                    sq += __shfl_xor_sync(0xffffffffu, sq, k);
+                    dot += __shfl_xor_sync(0xffffffffu, dot, k);
                 }
-                if (on)
-                    st_v4(to, pack2x4(v));
-                to += a.D;
+                const float r = rsqrtf(__fmaf_rn(sq, inv_d, a.eps));
+                const uint64_t by = twice(r), less = twice(-(dot * inv_d) * r * r);
+                const uint64_t sum = twice(on ? r : 0.0f);  // (no 0 times the root of 1 / 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t xf = widen2(xw[i]);
+                    acc[i] = fma2(mul2(v[i], xf), sum, acc[i]);
+                    v[i] = mul2(fma2(xf, less, mul2(v[i], wf[i])), by);
+                }
             }
+            if (on)
+                st_v4(to, pack2x4(v));
+            to += a.D;
+            ++h;
         }
         if (w != nullptr) {
             if (kind == 1)
@@ -530,13 +519,9 @@ cudaError_t launch_rope(const RopeArgs &args, bool pdl, cudaStream_t stream)
 cudaError_t launch_rope_grad(const RopeGradArgs &args, bool pdl, cudaStream_t stream)
 {
     RopeGradArgs a = args;
-    a.run_heads = run_heads(a.T * (a.heads[0] + a.heads[1]), a.lanes_log2);
-    int64_t most = 0;
-    for (int i = 0; i < 2; ++i) {
-        a.runs[i] = (a.heads[i] + a.run_heads - 1) / a.run_heads;
-        a.div_runs[i] = div_magic((uint32_t)a.runs[i]);
-        most = a.runs[i] > most ? a.runs[i] : most;
-    }
+    for (int i = 0; i < 2; ++i)
+        a.div_heads[i] = div_magic((uint32_t)a.heads[i]);
+    const int64_t most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
     const int groups = kGradThreads >> a.lanes_log2;
     const int64_t want = (a.T * most + groups - 1) / groups;
     const int blocks = (int)(want < 1 ? 1 : (want > kGradBlocks ? kGradBlocks : want));

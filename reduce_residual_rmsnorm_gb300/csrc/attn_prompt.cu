@@ -10,8 +10,9 @@
 // all 512 columns (D = 128).  Roles of the block's warps:
 //   - 4 for each tile: a thread has a row: its maximum and sum, exp2, p back to tensor
 //     memory, and the rescaling of O, only when a score passes the maximum by 2^8;
-//   - one copies the codes and scale factors of the next keys into shared memory, which
-//     lie in one piece for each 16 of them;
+//   - two copy the codes and scale factors of the next keys into shared memory, one K's and
+//     one V's, which lie in one piece for each 16 of them (issuing the 16 copies of a step
+//     takes a warp 1300 cycles);
 //   - 4 turn them into fp16 tiles there, two stages deep, K and V alike: K is read along
 //     d, V across it, so neither is transposed;
 //   - one issues the products: while one tile's p is made, the other's run.
@@ -42,32 +43,33 @@ constexpr int kKeys = 128;          // keys of a step
 constexpr int kBlocks = 152;        // one for each SM
 constexpr int kShare = 4;           // steps of a share, at least
 constexpr int kMakers = 128;        // threads that make K and V
-constexpr int kThreads = kRows + kMakers + 128;  // four warp groups; of the last two warps work
+constexpr int kThreads = kRows + kMakers + 128;  // four warp groups; of the last three warps work
 // Registers of a thread of each: the 128 that each is launched with, divided anew.
 constexpr int kRowRegs = 192, kMakerRegs = 72, kOtherRegs = 56;
 static_assert(kRows * kRowRegs + kMakers * kMakerRegs + 128 * kOtherRegs <= kThreads * 128, "");
 constexpr int kSwitch = 4;           // what going to a unit costs, in steps, when work is split
-constexpr int kCopies = 13;          // the warp that copies codes
+constexpr int kCopies = 13;          // the warps that copy codes: of K, of V
 constexpr int kProducts = 12;        // the warp that issues them
+constexpr int kRawSlots = 3;         // places for codes
 constexpr int kSeqs = 256;          // sequences whose weights are summed at a time
 
 // Shared memory: q of both tiles, two stages of K and of V, each in blocks of 64 d
-// (128 bytes) by 128 rows under the 128-byte swizzle; the codes and scale factors of
-// 128 keys of K and of V.
+// (128 bytes) by 128 rows under the 128-byte swizzle; three times the codes and scale
+// factors of 128 keys, of K and of V in turn.  (A copy takes 2500 cycles to come: with one
+// place each for K and V, the makers waited 1200 cycles of a step's 3700 for them.)
 template <int D>
 struct Smem {
     static constexpr int kBlock = 128 * 128;
     static constexpr int kMatrix = D / 64 * kBlock;
     static constexpr int kCodes = kKeys * (D / 2), kRaw = kCodes + kKeys * (D / 16);
-    static constexpr int kQ = 0, kK = 2 * kMatrix, kV = 4 * kMatrix, kRawK = 6 * kMatrix, kRawV = kRawK + kRaw,
-                         kBytes = kRawV + kRaw + 1024;
+    static constexpr int kQ = 0, kK = 2 * kMatrix, kV = 4 * kMatrix, kRaws = 6 * kMatrix, kBytes = kRaws + kRawSlots * kRaw + 1024;
 };
 
 struct Barriers {
     uint64_t q_full[2], s_full[2], o_full[2];  // of each tile
     uint64_t p_full[2][2];                     // of each half of a step's p, and tile
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // of each stage
-    uint64_t raw_full[2], raw_empty[2];                     // the codes of K, of V
+    uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];     // the codes
     uint64_t last;
 };
 
@@ -312,6 +314,19 @@ __device__ __forceinline__ Place my_share(const AttnArgs &a, int64_t *weights, i
     return p;
 }
 
+// The places for codes in turn: which one, and the parity of its use.
+struct Turns {
+    uint32_t slot = 0, phase = 0, uses = 0;
+    __device__ __forceinline__ void next()
+    {
+        ++uses;
+        if (++slot == kRawSlots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 // 16 bytes of codes (32 d of a key) as fp16 into half of a row of a swizzled block: `row`
 // is the row's address, `first` the place of its first chunk.
 __device__ __forceinline__ void put_codes(uint32_t row, uint32_t first, uint4 w, uint32_t sf2)
@@ -364,6 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             mbar_init(smem_u32(&bars.k_empty[i]), 1);
             mbar_init(smem_u32(&bars.v_full[i]), kMakers / 32);
             mbar_init(smem_u32(&bars.v_empty[i]), 1);
+        }
+        for (int i = 0; i < kRawSlots; ++i) {
             mbar_init(smem_u32(&bars.raw_full[i]), 1);
             mbar_init(smem_u32(&bars.raw_empty[i]), kMakers / 32);
         }
@@ -642,23 +659,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         constexpr int kStep = D == 128 ? 32 : 64;
         const int key_at = D == 128 ? maker * 8 + (lane & 7) : maker * 16 + (lane >> 1);
         const int c = D == 128 ? ((lane & 7) >> 1) ^ (lane >> 3) : lane & 1;
-        const uint32_t codes_at = smem + key_at * L::kRow + c * 16, sf_at = smem + S::kCodes + key_at * (D / 16) + 2 * c;
+        const uint32_t codes_at = smem + S::kRaws + key_at * L::kRow + c * 16, sf_at = smem + S::kRaws + S::kCodes + key_at * (D / 16) + 2 * c;
         const uint32_t row_at = smem + (c >> 1) * S::kBlock + key_at * 128, first = ((c & 1) * 4 ^ (key_at & 7)) * 16;
+        Turns raw;
         for (uint32_t it = 0;; ++it) {
             const int st = it & 1;
             const uint32_t phase = (it >> 1) & 1;
-            if (!wait(smem_u32(&bars.raw_full[0]), it & 1, &dead) || no_more[it & 3] != 0)
+            if (!wait(smem_u32(&bars.raw_full[raw.slot]), raw.phase, &dead) || no_more[it & 3] != 0)
                 break;
             if (it >= 2 && !wait(smem_u32(&bars.k_empty[st]), phase ^ 1, &dead))
                 break;
 #pragma unroll 2
             for (int key = 0; key < kKeys; key += kStep)
-                put_codes(row_at + S::kK + st * S::kMatrix + key * 128, first, ld_shared(codes_at + S::kRawK + key * L::kRow),
-                          ld_shared16(sf_at + S::kRawK + key * (D / 16)));
+                put_codes(row_at + S::kK + st * S::kMatrix + key * 128, first, ld_shared(codes_at + raw.slot * S::kRaw + key * L::kRow),
+                          ld_shared16(sf_at + raw.slot * S::kRaw + key * (D / 16)));
             fence_async_proxy();
-            warp_arrive(smem_u32(&bars.raw_empty[0]));
+            warp_arrive(smem_u32(&bars.raw_empty[raw.slot]));
             warp_arrive(smem_u32(&bars.k_full[st]));
-            if (!wait(smem_u32(&bars.raw_full[1]), it & 1, &dead) ||
+            raw.next();
+            if (!wait(smem_u32(&bars.raw_full[raw.slot]), raw.phase, &dead) ||
                 (it >= 2 && !wait(smem_u32(&bars.v_empty[st]), phase ^ 1, &dead)))
                 break;
             const int lo = see_lo[it & 3], hi = see_hi[it & 3];
@@ -667,31 +686,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 const int at = key + key_at;
                 // (what a slot that nobody sees holds may be NaN)
                 const bool use = at >= lo && at < hi && seen[it & 3][at >> 4] != 0;
-                put_codes(row_at + S::kV + st * S::kMatrix + key * 128, first, ld_shared(codes_at + S::kRawV + key * L::kRow),
-                          use ? ld_shared16(sf_at + S::kRawV + key * (D / 16)) : 0);
+                put_codes(row_at + S::kV + st * S::kMatrix + key * 128, first, ld_shared(codes_at + raw.slot * S::kRaw + key * L::kRow),
+                          use ? ld_shared16(sf_at + raw.slot * S::kRaw + key * (D / 16)) : 0);
             }
             fence_async_proxy();
-            warp_arrive(smem_u32(&bars.raw_empty[1]));
+            warp_arrive(smem_u32(&bars.raw_empty[raw.slot]));
             warp_arrive(smem_u32(&bars.v_full[st]));
+            raw.next();
         }
-    } else if (warp == kCopies) {
+    } else if (warp == kCopies || warp == kCopies + 1) {
         // ---- codes and scale factors: lanes 0..7 have a step's tiles of 16 keys
         fewer_registers<kOtherRegs>();
-        const int lane = tid & 31;
+        const int lane = tid & 31, which = warp - kCopies;  // K (0) or V (1)
         uint32_t it = 0;
         bool alive = true;
-        auto send = [&](int which, bool in, const uint8_t *src) {  // K (0) or V (1)
-            const uint32_t bar = smem_u32(&bars.raw_full[which]), to = smem + (which == 0 ? S::kRawK : S::kRawV);
-            const int tiles = __popc(__ballot_sync(0xffffffffu, in));
-            if (lane == 0)
-                mbar_expect_tx(bar, tiles * S::kRaw / 8);
-            __syncwarp();
-            if (in) {
-                bulk_load(to + lane * 16 * L::kRow, src + which * L::kV, 16 * L::kRow, bar);
-                bulk_load(to + S::kCodes + lane * D, src + L::kKsf + which * D, D, bar);
-            }
-            __syncwarp();
-        };
+        Turns raw;
+        if (which == 1)
+            raw.next();
+        auto room = [&]() -> bool { return raw.uses < kRawSlots || wait(smem_u32(&bars.raw_empty[raw.slot]), raw.phase ^ 1, &dead); };
         // a step's keys and tiles, looked up while the step before is copied
         int key0 = 0, see0 = 0, see1 = 0, ahead = 0;
         bool in = false;
@@ -721,34 +733,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             return true;
         };
         for (bool more = place.pos < place.end && look_up(); more; ++it) {
-            if (it >= 1 && !(alive = wait(smem_u32(&bars.raw_empty[0]), (it - 1) & 1, &dead)))
+            if (!(alive = room()))
                 break;
-            if (lane < 8)
-                seen[it & 3][lane] = in;
-            if (lane == 0) {
-                see_lo[it & 3] = see0;
-                see_hi[it & 3] = see1;
-                no_more[it & 3] = 0;
+            if (which == 0) {
+                // (the products with the V four steps before have run, or V two before would not
+                // have been made: nobody reads what is overwritten)
+                if (lane < 8)
+                    seen[it & 3][lane] = in;
+                if (lane == 0) {
+                    see_lo[it & 3] = see0;
+                    see_hi[it & 3] = see1;
+                    no_more[it & 3] = 0;
+                }
             }
-            send(0, in, src);
-            const bool in_v = in;
-            const uint8_t *const src_v = src;
+            const uint32_t bar = smem_u32(&bars.raw_full[raw.slot]), to = smem + S::kRaws + raw.slot * S::kRaw;
+            const int tiles = __popc(__ballot_sync(0xffffffffu, in));
+            if (lane == 0)
+                mbar_expect_tx(bar, tiles * S::kRaw / 8);
+            __syncwarp();
+            if (in) {
+                bulk_load(to + lane * 16 * L::kRow, src + which * L::kV, 16 * L::kRow, bar);
+                bulk_load(to + S::kCodes + lane * D, src + L::kKsf + which * D, D, bar);
+            }
+            __syncwarp();
+            raw.next();
+            raw.next();
             more = look_up();
-            if (it >= 1 && !(alive = wait(smem_u32(&bars.raw_empty[1]), (it - 1) & 1, &dead)))
-                break;
-            send(1, in_v, src_v);
         }
-        if (alive && (it == 0 || (alive = wait(smem_u32(&bars.raw_empty[0]), (it - 1) & 1, &dead)))) {
+        if (which == 0 && alive && (alive = room())) {
             if (lane == 0)
                 no_more[it & 3] = 1;
-            warp_arrive(smem_u32(&bars.raw_full[0]));
+            warp_arrive(smem_u32(&bars.raw_full[raw.slot]));
         }
-        if (!alive) {  // what is under way arrives before its memory goes
+        if (!alive) {  // what is under way (of two uses at most) arrives before its memory goes
             const long long t0 = clock64();
-            for (int i = 0; i < 2; ++i)
-                while (it > 0 && !mbar_try_wait(smem_u32(&bars.raw_full[i]), (it - 1) & 1) &&
-                       !mbar_try_wait(smem_u32(&bars.raw_full[i]), it & 1) && clock64() - t0 < kWaitCycles) {
+            for (uint32_t i = 1; i <= 2 && i <= it; ++i) {
+                const uint32_t use = raw.uses - 2 * i;
+                while (!mbar_try_wait(smem_u32(&bars.raw_full[use % kRawSlots]), use / kRawSlots & 1) && clock64() - t0 < kWaitCycles) {
                 }
+            }
         }
     } else {
         // ---- products, by one warp

@@ -777,35 +777,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // ---- products, by one warp
         fewer_registers<kOtherRegs>();
         if (warp == kProducts) {
+        const bool lead = elect_one();
         constexpr uint32_t kIdS = idesc_f16(128, kKeys, false), kIdO = idesc_f16(128, D, true);
         const uint32_t s_full[2] = {smem_u32(&bars.s_full[0]), smem_u32(&bars.s_full[1])};
         // (the addresses go through an asm so that descriptors are not kept in registers
-        // over the whole loop)
+        // over the whole loop; a product takes one lane chosen once and additions to low
+        // words: choosing it and making descriptors anew for each took 886 us where this
+        // takes 787)
         auto scores = [&](int tile, int st) {  // S = q K^T
             uint32_t base = smem;
             asm volatile("" : "+r"(base));
-            if (elect_one()) {
+            const uint64_t q = desc_swizzled128(base + S::kQ + tile * S::kMatrix), k_at = desc_swizzled128(base + S::kK + st * S::kMatrix);
+            if (lead) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = (k >> 2) * S::kBlock + (k & 3) * 32;
-                    mma_f16(tmem + kSCol + tile * 128, desc_swizzled128(base + S::kQ + tile * S::kMatrix + off),
-                            desc_swizzled128(base + S::kK + st * S::kMatrix + off), kIdS, k > 0);
+                    mma_f16(tmem + kSCol + tile * 128, desc_plus(q, off), desc_plus(k_at, off), kIdS, k > 0);
                 }
                 mma_commit(s_full[tile]);
             }
-            __syncwarp();
         };
         auto values = [&](int tile, int st, int half, bool more) {  // O (+)= p V, half of the keys
             uint32_t base = smem;
             asm volatile("" : "+r"(base));
-            if (elect_one()) {
+            const uint64_t v = desc_swizzled128_across(base + S::kV + st * S::kMatrix + half * (kKeys / 32) * 2048, S::kBlock);
+            const uint32_t p_at = tmem + kSCol + tile * 128 + half * (kKeys / 32) * 8;
+            if (lead) {
 #pragma unroll
                 for (int k = 0; k < kKeys / 32; ++k)
-                    mma_f16_tmem(tmem + kOCol + tile * D, tmem + kSCol + tile * 128 + (half * (kKeys / 32) + k) * 8,
-                                 desc_swizzled128_across(base + S::kV + st * S::kMatrix + (half * (kKeys / 32) + k) * 2048, S::kBlock),
-                                 kIdO, more || half > 0 || k > 0);
+                    mma_f16_tmem(tmem + kOCol + tile * D, p_at + k * 8, desc_plus(v, k * 2048), kIdO, k > 0 || more || half > 0);
             }
-            __syncwarp();
         };
         // both halves of a tile's step, as p comes
         auto both = [&](int tile, int st, uint32_t phase, bool more) -> bool {
@@ -818,9 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             return true;
         };
         auto commit = [&](uint64_t *bar) {
-            if (elect_one())
+            if (lead)
                 mma_commit(smem_u32(bar));
-            __syncwarp();
         };
         uint32_t it = 0, units = 0, units1 = 0, p1 = 0;
         bool alive = true;

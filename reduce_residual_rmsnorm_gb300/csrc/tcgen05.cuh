@@ -223,6 +223,14 @@ __device__ __forceinline__ uint64_t desc_swizzled128_across(uint32_t addr, uint3
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// A descriptor's operand `off` bytes on, within shared memory.
+__device__ __forceinline__ uint64_t desc_plus(uint64_t desc, uint32_t off)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"((uint32_t)desc + (off >> 4)), "r"((uint32_t)(desc >> 32)));
+    return d;
+}
+
 // Instruction descriptor of kind::f16: fp16 times fp16 into fp32, A along K, B along K or
 // (b_across) across it, M rows, N columns, K = 16.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n, bool b_across)

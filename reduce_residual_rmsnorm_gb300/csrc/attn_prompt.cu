@@ -327,6 +327,13 @@ struct Turns {
     }
 };
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // 16 bytes of codes (32 d of a key) as fp16 into half of a row of a swizzled block: `row`
 // is the row's address, `first` the place of its first chunk.
 __device__ __forceinline__ void put_codes(uint32_t row, uint32_t first, uint4 w, uint32_t sf2)
@@ -427,19 +434,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             qh = place.head * a.group + (live ? row - i * a.group : 0);
             return live;
         };
-        // the warp's rows of q of the unit that the place is at, as they are; whole rows
-        // by neighbouring lanes
-        auto copy_q = [&]() {
-            constexpr int kLanes = D / 8, kPass = 32 / kLanes;
-            const int c = lane % kLanes;
+        // where the row is in q, in the unit that the place is at (in the weights' memory,
+        // which is not used any more)
+        static_assert(kRows <= kSeqs, "");
+        int64_t *const q_from = weights;
+        auto find_q = [&]() {
+            int i, qh;
+            const bool live = find(r, i, qh);
+            q_from[tid] = live ? (int64_t)(place.s.q0 + i) * a.ldq + (int64_t)qh * D : -1;
+            __syncwarp();
+        };
+        // 64 columns of the warp's rows of q, as they are: 8 neighbouring lanes a row
+        auto copy_q = [&](int block) {
 #pragma unroll 2
-            for (int j = 0; j < 32 / kPass; ++j) {
-                const int row = (warp & 3) * 32 + j * kPass + lane / kLanes;
-                const uint32_t dst = q_smem + (c >> 3) * S::kBlock + row * 128 + (((c & 7) ^ (row & 7)) * 16);
-                int i, qh;
-                if (find(row, i, qh))
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                                 "l"(a.q + (int64_t)(place.s.q0 + i) * a.ldq + (int64_t)qh * D + c * 8) : "memory");
+            for (int j = 0; j < 8; ++j) {
+                const int row = (warp & 3) * 32 + j * 4 + lane / 8, c = lane & 7;
+                const uint32_t dst = q_smem + block * S::kBlock + row * 128 + ((c ^ (row & 7)) * 16);
+                const int64_t from = q_from[tile * 128 + row];
+                if (from >= 0)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(a.q + from + block * 64 + c * 8) : "memory");
                 else
                     st_shared(dst, make_uint4(0, 0, 0, 0));
             }
@@ -455,26 +468,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 advance(a, place, g.length);
             }
         };
+        constexpr int kLast = D / 64 - 1;  // block of columns
         to_rows();
-        if (place.pos < place.end)
-            copy_q();
+        if (place.pos < place.end) {
+            find_q();
+#pragma unroll 1
+            for (int block = 0; block <= kLast; ++block)
+                copy_q(block);
+        }
         while (alive && place.pos < place.end) {
             const Segment segment = segment_of(place);
             const int count = segment.count;
             // this row of q, scaled by a power of two, as fp16
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncwarp();
-            float amax = 0.0f, down;
+            float down;
             const uint32_t q_row = q_smem + r * 128;
+            uint32_t top2[2] = {0, 0};  // pairs of bf16
 #pragma unroll 4
             for (int c = 0; c < D / 8; ++c) {
-                float f[8];
-                unpack8(ld_shared(q_row + (c >> 3) * S::kBlock + (((c & 7) ^ (r & 7)) * 16)), f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    amax = fmaxf(amax, fabsf(f[e]));
+                const uint4 v = ld_shared(q_row + (c >> 3) * S::kBlock + (((c & 7) ^ (r & 7)) * 16));
+                top2[0] = max_bf16x2(max_bf16x2(top2[0], v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+                top2[1] = max_bf16x2(max_bf16x2(top2[1], v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
             }
-            const float up = fp16_scale(amax, down);
+            top2[0] = max_bf16x2(top2[0], top2[1]);
+            const float up = fp16_scale(fmaxf(__uint_as_float(top2[0] << 16), __uint_as_float(top2[0] & 0xFFFF0000u)), down);
 #pragma unroll 4
             for (int c = 0; c < D / 8; ++c) {
                 const uint32_t at = q_row + (c >> 3) * S::kBlock + (((c & 7) ^ (r & 7)) * 16);
@@ -610,37 +628,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             step += count;
             advance(a, place, segment.length);
             to_rows();
+            if (place.pos < place.end)
+                find_q();
             alive = wait(smem_u32(&bars.o_full[tile]), units_done & 1, &dead);
             if (!alive)
                 break;
             ++units_done;
             tmem_fence_after();
+            // (no product reads q now: the next unit's takes its place, but for the last block,
+            // which the rows go through on their way out)
             if (place.pos < place.end)
-                copy_q();  // (no product reads it now)
-            const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
-            const int64_t to = out_at[tid];
 #pragma unroll 1
-            for (int j = 0; j < D / 32; ++j) {
-                uint32_t v[32];
-                tmem_load32(o_at + 32 * j, v);
-                loaded(v);
-                if (to >= 0 && whole_unit) {
+                for (int block = 0; block < kLast; ++block)
+                    copy_q(block);
+            // 128 bytes of a row at a time, written by 8 neighbouring lanes (lanes that write
+            // their own rows took 4000 cycles)
+            const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
+            const uint32_t way_out = q_smem + kLast * S::kBlock + (warp & 3) * 32 * 128;
+#pragma unroll 1
+            for (int at = 0; at < D; at += whole_unit ? 64 : 32) {
+#pragma unroll 1
+                for (int half = 0; half < (whole_unit ? 2 : 1); ++half) {
+                    uint32_t v[32];
+                    tmem_load32(o_at + at + 32 * half, v);
+                    loaded(v);
+                    if (whole_unit) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float f[8];
+                        for (int k = 0; k < 4; ++k) {
+                            float f[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            f[e] = __uint_as_float(v[8 * k + e]) * inv;
-                        *reinterpret_cast<uint4 *>(a.out + to + 32 * j + 8 * k) = pack8(f);
+                            for (int e = 0; e < 8; ++e)
+                                f[e] = __uint_as_float(v[8 * k + e]) * inv;
+                            st_shared(way_out + lane * 128 + (((half * 4 + k) ^ (lane & 7)) * 16), pack8(f));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            st_shared(way_out + lane * 128 + ((k ^ (lane & 7)) * 16),
+                                      make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
                     }
-                } else if (to >= 0) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4 *>(slot + tid * D + 32 * j + 4 * k) =
-                            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                }
+                __syncwarp();
+#pragma unroll 2
+                for (int j = 0; j < 8; ++j) {
+                    const int row = j * 4 + lane / 8, c = lane & 7, of = (warp * 32) + row;
+                    const uint4 v = ld_shared(way_out + row * 128 + ((c ^ (row & 7)) * 16));
+                    const int64_t to = out_at[of];
+                    if (to >= 0) {
+                        if (whole_unit)
+                            *reinterpret_cast<uint4 *>(a.out + to + at + 8 * c) = v;
+                        else
+                            *reinterpret_cast<uint4 *>(slot + of * D + at + 4 * c) = v;
+                    }
                 }
                 __syncwarp();
             }
+            if (place.pos < place.end)
+                copy_q(kLast);
             if (out_at[tid] >= 0) {
                 if (!whole_unit) {
                     slot[kRows * D + tid] = m;

@@ -361,6 +361,75 @@ def test_a_few_queries(dev, hq, hk, window, D):
     _check_attention(dev, new, lens, hq, hk, D, 16, seed=hq + window, window=window, max_q=7, gap=3)
 
 
+# (sequences, key heads, query heads of each, queries, keys at most): units of up to 8, 16 and 32 rows, as
+# many as take clusters of 8, 4, 2 and 1 blocks, and one more than take any; then keys that are too many for a
+# cluster, with few units (joined by large blocks) and with many
+SPLITS = [(19, 2, 8, 1, 700), (39, 1, 5, 1, 700), (77, 1, 8, 1, 300), (51, 3, 4, 1, 300), (61, 5, 8, 1, 300),
+          (19, 1, 8, 2, 700), (20, 1, 4, 4, 300), (39, 1, 8, 2, 300), (77, 1, 6, 2, 300), (51, 3, 8, 2, 200),
+          (19, 1, 5, 5, 700), (20, 1, 8, 3, 300), (13, 3, 16, 2, 300), (77, 1, 4, 8, 300), (51, 3, 5, 4, 200),
+          (2, 1, 8, 1, 17000), (2, 2, 8, 2, 17000), (3, 2, 5, 5, 17000), (12, 2, 8, 1, 17000), (6, 3, 8, 3, 17000)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,hk,group,n,most", SPLITS)
+def test_every_split_of_few_rows(dev, B, hk, group, n, most, D):
+    r = np.random.RandomState(B + n)
+    lens = [int(v) for v in r.randint(0, min(most, 600), B)]
+    lens[B // 2], lens[-1] = most, 1
+    new = [n] * B
+    if n > 1:
+        new[0], new[B // 3] = 0, 1
+    _check_attention(dev, new, lens, hk * group, hk, D, 16, seed=B, max_q=n, gap=1 if n > 1 else 0, window=150 if most == 200 else 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [31, 32, 33, 34])
+def test_rows_at_the_change_of_kernels(dev, rows, D):
+    """Up to 32 (query, head) pairs of a key head go one way, more another."""
+    _check_attention(dev, [rows, 1, rows - 1], [300, 40, 2100], 2, 2, D, 48, seed=rows, max_q=rows)
+
+
+def test_two_calls_at_once(dev):
+    """Calls on two streams, each with a workspace of its own, and captured ones that share one in turn, give the bits of
+    calls on their own: each way to split the work."""
+    D, hk, page = 128, 2, 16
+    lens = [17000, 300, 0, 2500]
+    cache, table = _cache(dev, lens, hk, D, page, 3)
+    kv = torch.tensor(lens, dtype=torch.int32, device=dev)
+    side, calls = torch.cuda.Stream(), []
+    for new in ([1, 1, 1, 1], [4, 0, 1, 2], [200, 30, 5, 300]):
+        q = _rand((sum(new), 8, D), dev, len(calls))
+        cu = torch.tensor([0, *np.cumsum(new)], dtype=torch.int32, device=dev)
+        bytes_ = pkg.library().ts_nvfp4_attention_workspace(4, 8, hk, D, max(new), table.shape[1] * page, 0)
+        assert bytes_ > 0
+        args = dict(cu_q=cu, max_q=max(new), return_lse=True)
+        calls.append((q, args, [torch.full((bytes_,), 0xA5, dtype=torch.uint8, device=dev) for _ in range(2)]))
+    want = [pkg.ts_nvfp4_attention(q, cache, table, kv, **args) for q, args, _ in calls]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for q, args, spaces in calls:
+            got.append([pkg.ts_nvfp4_attention(q, cache, table, kv, workspace=spaces[0], launch_with_pdl=True, **args),
+                        pkg.ts_nvfp4_attention(q, cache, table, kv, workspace=spaces[1], stream=side, **args)])
+    torch.cuda.synchronize()
+    for i, pair in enumerate(got):
+        for out, lse in pair:
+            assert torch.equal(out, want[i % 3][0]) and torch.equal(lse, want[i % 3][1])
+    shared = max((spaces[0] for _, _, spaces in calls), key=lambda t: t.numel())
+    graph, outs = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        for q, args, _ in calls + calls:
+            outs.append(pkg.ts_nvfp4_attention(q, cache, table, kv, workspace=shared, launch_with_pdl=True, **args))
+    for _ in range(2):
+        for out, lse in outs:
+            out.fill_(3.0)
+            lse.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (out, lse) in enumerate(outs):
+            assert torch.equal(out, want[i % 3][0]) and torch.equal(lse, want[i % 3][1])
+
+
 def test_not_causal(dev):
     _check_attention(dev, [4, 1, 3, 2], [100, 9, 2, 0], 6, 2, 128, 32, causal=False, max_q=4)
 

@@ -388,14 +388,17 @@ int check_attention(int64_t q_heads, int64_t heads, int64_t D, int64_t max_q)
     return check_range("max_q", max_q, 1, kMaxRows);
 }
 
-// Which kernel: rows of a sequence that share a key head.
-constexpr int64_t kFewRows = 32;
+// Which kernel: rows of a sequence that share a key head, for the kernel of few rows at most.
+// Few against many rows, us, 1 sequence of 1024 keys, 8 up to 2048, 32 up to 8192, 8 key heads:
+//   D = 128   32 rows 8.6 / 20.8, 17.2 / 24.5, 121.6 / 117.1    40 rows 13.8 / 20.8, 24.6 / 22.7, 127 / 117
+//   D = 64    32 rows 7.0 / 18.0, 12.8 / 21.7,  87.7 /  99.8    48 rows 12.4 / 18.0, 16.9 / 20.1, 80.5 / 81.1
+constexpr int64_t few_rows(int64_t D) { return D == 64 ? 48 : 32; }
 
 int64_t attention_workspace(int64_t B, int64_t heads, int64_t rows, int64_t D, int64_t keys, int64_t window)
 {
-    if (rows <= kFewRows && attn_few_clusters(B, heads, rows, keys, window))
+    if (rows <= few_rows(D) && attn_few_clusters(B, heads, rows, keys, window))
         return 0;
-    const int64_t few = attn_few_workspace(D), prompt = rows <= kFewRows ? 0 : attn_prompt_workspace(D);
+    const int64_t few = attn_few_workspace(D), prompt = rows <= few_rows(D) ? 0 : attn_prompt_workspace(D);
     return few > prompt ? few : prompt;  // (does not shrink where a bound grows)
 }
 
@@ -475,5 +478,5 @@ extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t
     a.partial = static_cast<float *>(workspace);
     const bool pdl = (flags & TS_FLAG_PDL) != 0;
     const cudaStream_t on = static_cast<cudaStream_t>(stream);
-    return launched(rows <= kFewRows ? launch_attn_few(a, rows, pdl, on) : launch_attn_prompt(a, pdl, on));
+    return launched(rows <= few_rows(D) ? launch_attn_few(a, rows, pdl, on) : launch_attn_prompt(a, pdl, on));
 }

@@ -41,9 +41,8 @@ namespace {
 
 // Even shares: for 8 rows blocks of 4 warps, four to an SM (64 sequences up to 16384 keys:
 // 107.7 us; blocks of 8 warps 113.7, five blocks of 4 with 96 registers 111.7, all three
-// with a way of 12 tiles); for more
-// the registers of an SM go to one block of 8.  Clusters: blocks of 8 warps, for the
-// time of a single call.
+// with a way of 12 tiles); for more rows the registers of an SM go to one block of 8.
+// Clusters: blocks of 8 warps, for the time of a single call.
 constexpr int kSms = 152;
 constexpr int kClusterWarps = 8;
 constexpr int share_warps(int nt) { return nt == 1 ? 4 : 8; }
@@ -59,18 +58,24 @@ constexpr int kShare = 8;     // tiles of a share, at least
 // many short units ended last).
 constexpr int way_of(int nt) { return nt == 1 ? 20 : 24; }
 // Clusters take calls whose units are all resident at once, with at most this many keys a
-// block (16 tiles a warp: with more, sequences of different lengths leave SMs idle).
+// block (16 tiles a warp: with more, sequences of different lengths leave SMs idle), or half
+// as many where the clusters leave most of the SMs idle.  Clusters against even shares, us,
+// 8 rows, D = 128:
+//   1 unit        1024 keys 4.9 / 9.0    8192 keys 9.4 / 9.4     16384 keys 15.0 / 10.5
+//   8 units       1024 keys 5.3 / 11.5   16384 keys 15.3 / 16.0  32768 keys 26.0 / 19.5
+//   128 units     lengths up to 1024 8.8 / 14.8, to 4096 18.5 / 19.2, to 8192 31.1 / 24.0
 constexpr int64_t kClusterKeys = 2048;
-// Blocks of a cluster, a power of two up to 8; 0: even shares.
+constexpr int kMostBlocks = 8;  // of a cluster
+// Blocks of a cluster, a power of two; 0: even shares.
 int cluster_of(int64_t B, int64_t heads, int64_t rows, int64_t keys, int64_t window)
 {
     const int nt = eights_of(rows);
     const int64_t units = B * heads * ((rows + 8 * nt - 1) / (8 * nt)), resident = kSms * (nt == 1 ? 2 : 1);
     if (window > 0 && window + rows < keys)
         keys = window + rows;  // (no more queries than rows)
-    for (int blocks = 8; blocks >= 1; blocks /= 2)
+    for (int blocks = kMostBlocks; blocks >= 1; blocks /= 2)
         if (units * blocks <= resident)
-            return keys <= kClusterKeys * blocks ? blocks : 0;
+            return keys <= (units * blocks < resident / 8 ? kClusterKeys / 2 : kClusterKeys) * blocks ? blocks : 0;
     return 0;
 }
 
@@ -683,7 +688,7 @@ __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_
 template <int D, int NT>
 __global__ void __launch_bounds__(kClusterWarps * 32, NT == 1 ? 2 : 1) attn_cluster_kernel(const __grid_constant__ AttnArgs a, int blocks)
 {
-    constexpr int NR = 8 * NT, kWarps = kClusterWarps, kWarpRows = 128 / D, kMostBlocks = 8;
+    constexpr int NR = 8 * NT, kWarps = kClusterWarps, kWarpRows = 128 / D;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float part[NR][D];  // [blocks][NR / blocks][D]
     __shared__ float part_m[NR], part_l[NR];
@@ -901,7 +906,10 @@ cudaError_t launch_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t s
 
 bool attn_few_clusters(int64_t B, int64_t heads, int64_t rows, int64_t keys, int64_t window)
 {
-    return cluster_of(B, heads, rows, keys, window) > 0;
+    // (and no smaller call of as many keys takes shares)
+    if (window > 0 && window + rows < keys)
+        keys = window + rows;
+    return cluster_of(B, heads, rows, keys, 0) > 0 && keys <= kClusterKeys / 2 * kMostBlocks;
 }
 
 cudaError_t launch_attn_few(const AttnArgs &a, int64_t rows, bool pdl, cudaStream_t stream)

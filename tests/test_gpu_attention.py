@@ -367,6 +367,7 @@ def test_a_few_queries(dev, hq, hk, window, D):
 SPLITS = [(19, 2, 8, 1, 700), (39, 1, 5, 1, 700), (77, 1, 8, 1, 300), (51, 3, 4, 1, 300), (61, 5, 8, 1, 300),
           (19, 1, 8, 2, 700), (20, 1, 4, 4, 300), (39, 1, 8, 2, 300), (77, 1, 6, 2, 300), (51, 3, 8, 2, 200),
           (19, 1, 5, 5, 700), (20, 1, 8, 3, 300), (13, 3, 16, 2, 300), (77, 1, 4, 8, 300), (51, 3, 5, 4, 200),
+          (1, 1, 8, 1, 8192), (4, 1, 8, 1, 8193), (5, 1, 8, 1, 16384),
           (2, 1, 8, 1, 17000), (2, 2, 8, 2, 17000), (3, 2, 5, 5, 17000), (12, 2, 8, 1, 17000), (6, 3, 8, 3, 17000)]
 
 
@@ -383,9 +384,9 @@ def test_every_split_of_few_rows(dev, B, hk, group, n, most, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("rows", [31, 32, 33, 34])
+@pytest.mark.parametrize("rows", [31, 32, 33, 34, 47, 48, 49, 50])
 def test_rows_at_the_change_of_kernels(dev, rows, D):
-    """Up to 32 (query, head) pairs of a key head go one way, more another."""
+    """Up to 32 (D = 64: 48) (query, head) pairs of a key head go one way, more another."""
     _check_attention(dev, [rows, 1, rows - 1], [300, 40, 2100], 2, 2, D, 48, seed=rows, max_q=rows)
 
 

@@ -19,7 +19,11 @@ namespace tsfn {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Blocks to an SM by their registers (16384 tokens, 64 + 8 heads of 128, with the cache
+// written and read back: 144.5 us; blocks of 256 threads, three to an SM, 149; without the
+// cache, 64 columns turned: 100.5, and 104 with four of 256).
+constexpr int kThreads = 128;
+constexpr int rope_blocks_per_sm(bool pairs, bool cache) { return cache ? (pairs ? 6 : 7) : (pairs ? 8 : 9); }
 
 // Coherent loads of what is used again (weights, tables, positions).
 __device__ __forceinline__ uint4 ld_again(const void *p)
@@ -160,7 +164,7 @@ __device__ __forceinline__ void put_chunk(const uint4 &v, float g, bool live, ui
 // A group of lanes takes a run of heads of one token, two at a time with the next two's
 // loads under way.
 template <bool PAIRS, bool CACHE>
-__global__ void __launch_bounds__(kThreads, CACHE ? 3 : 4) rope_kernel(const __grid_constant__ RopeArgs a)
+__global__ void __launch_bounds__(kThreads, rope_blocks_per_sm(PAIRS, CACHE)) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     const int lanes = 1 << a.lanes_log2;
     const int lane = threadIdx.x & 31, c = lane & (lanes - 1);

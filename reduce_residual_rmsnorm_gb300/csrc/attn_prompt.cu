@@ -940,35 +940,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     }
 }
 
-// Units over several blocks: a block has 8 rows of one, a warp each where the parts are
-// few; else the warps share a row's parts.
-template <int D>
-__global__ void __launch_bounds__(256) attn_join_rows_kernel(const __grid_constant__ AttnArgs a, int blocks)
+// R neighbouring rows of a unit over n blocks, by a warp: their parts in order, UNROLL of
+// them under way together.
+template <int D, int R, int UNROLL>
+__device__ __forceinline__ void join_rows(const AttnArgs &a, const Record &rec, const float *slots, int first, int n, int row0)
 {
     constexpr int V = D / 32;  // floats of a lane
-    __shared__ float acc_of[8][D];
-    __shared__ float m_of[8], l_of[8];
-    const int first = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait();
-    pdl_launch_dependents();
-    const Record rec = reinterpret_cast<const Record *>(a.partial)[first];
-    const int row0 = blockIdx.y * 8;
-    if (rec.last < 0 || row0 >= rec.rows)
-        return;
-    const float *slots = a.partial + (int64_t)blocks * (sizeof(Record) / 4);
-    const int n = rec.last - first + 1;
-    const float vg = *a.cache.v_scale;
-
-    // parts i0 .. i1 of a row in order
-    auto gather = [&](int row, int i0, int i1, float &m, float &l, float (&acc)[V]) {
-        m = -INFINITY;
-        l = 0.0f;
+    const int lane = threadIdx.x & 31;
+    float m[R], l[R], acc[R][V];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        m[u] = -INFINITY;
+        l[u] = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            acc[j] = 0.0f;
-#pragma unroll 4
-        for (int i = i0; i < i1; ++i) {
-            const float *slot = slots + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * slot_floats(kRows, D);
+            acc[u][j] = 0.0f;
+    }
+#pragma unroll UNROLL
+    for (int i = 0; i < n; ++i) {
+        const float *slot = slots + ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * slot_floats(kRows, D);
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const int row = min(row0 + u, rec.rows - 1);
             const float mi = slot[kRows * D + row], li = slot[kRows * D + kRows + row];
             float v[V];
             if constexpr (V == 4) {
@@ -982,64 +975,50 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const __grid_consta
                 v[0] = w.x;
                 v[1] = w.y;
             }
-            const float top = fmaxf(m, mi);
-            const float f0 = m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : exp2_approx(m - top);
+            const float top = fmaxf(m[u], mi);
+            const float f0 = m[u] == -INFINITY ? (l[u] == 0.0f ? 0.0f : 1.0f) : exp2_approx(m[u] - top);
             const float f1 = mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - top);
-            m = top;
-            l = l * f0 + li * f1;
+            m[u] = top;
+            l[u] = l[u] * f0 + li * f1;
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                acc[j] = acc[j] * f0 + v[j] * f1;
+                acc[u][j] = acc[u][j] * f0 + v[j] * f1;
         }
-    };
-    auto write = [&](int row, float m, float l, const float (&acc)[V]) {
-        const int64_t r = rec.row0 + row, i = r / a.group;
-        const int64_t qh = (int64_t)rec.head * a.group + (r - i * a.group);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
-        uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (rec.q0 + i) * a.ldo + qh * D + lane * V);
+    }
+    const float vg = *a.cache.v_scale;
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        if (row0 + u >= rec.rows)
+            break;
+        const uint32_t r = (uint32_t)rec.row0 + row0 + u, i = div_by(r, a.div_group);
+        const int64_t qh = (int64_t)rec.head * a.group + (r - i * a.group), q = (int64_t)rec.q0 + i;
+        const float inv = l[u] == 0.0f ? 0.0f : 1.0f / (l[u] * vg);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + q * a.ldo + qh * D + lane * V);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j)
-            dst[j] = pack_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+            dst[j] = pack_bf16x2(acc[u][2 * j] * inv, acc[u][2 * j + 1] * inv);
         if (a.lse != nullptr && lane == 0)
-            a.lse[(rec.q0 + i) * a.hq + qh] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
-    };
-    float m, l, acc[V];
-    if (n <= 8) {
-        if (row0 + warp < rec.rows) {
-            gather(row0 + warp, 0, n, m, l, acc);
-            write(row0 + warp, m, l, acc);
-        }
+            a.lse[q * a.hq + qh] = l[u] == 0.0f ? -INFINITY : (m[u] == -INFINITY ? 0.0f : m[u]) * kLn2 + logf(l[u]);
+    }
+}
+
+// Units over several blocks: where the parts are few, a warp has 4 rows of one (and the last
+// blocks of a unit nothing); else a row.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_rows_kernel(const __grid_constant__ AttnArgs a, int blocks)
+{
+    const int first = blockIdx.x, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
+    const Record rec = reinterpret_cast<const Record *>(a.partial)[first];
+    const int n = rec.last - first + 1, each = n <= 8 ? 4 : 1, row0 = ((int)blockIdx.y * 8 + warp) * each;
+    if (rec.last < 0 || row0 >= rec.rows)
         return;
-    }
-    const int per = (n + 7) / 8;
-    for (int row = row0; row < row0 + 8 && row < rec.rows; ++row) {
-        gather(row, min(n, warp * per), min(n, (warp + 1) * per), m, l, acc);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            acc_of[warp][lane * V + j] = acc[j];
-        if (lane == 0) {
-            m_of[warp] = m;
-            l_of[warp] = l;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            float top = -INFINITY, sum = 0.0f;
-            for (int w = 0; w < 8; ++w)
-                top = fmaxf(top, m_of[w]);
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                acc[j] = 0.0f;
-            for (int w = 0; w < 8; ++w) {
-                const float f = m_of[w] == -INFINITY ? (l_of[w] == 0.0f ? 0.0f : 1.0f) : exp2_approx(m_of[w] - top);
-                sum = fmaf(f, l_of[w], sum);
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    acc[j] = fmaf(f, acc_of[w][lane * V + j], acc[j]);
-            }
-            write(row, top, sum, acc);
-        }
-        __syncthreads();
-    }
+    const float *slots = a.partial + (int64_t)blocks * (sizeof(Record) / 4);
+    if (each == 4)
+        join_rows<D, 4, 2>(a, rec, slots, first, n, row0);
+    else
+        join_rows<D, 1, 8>(a, rec, slots, first, n, row0);
 }
 
 template <int D>

@@ -3,11 +3,12 @@
 //
 //   out = sum_j p_j V[j] / sum_j p_j,   p_j = exp2(c q.K[j] - m)      c = scale log2(e) / k_scale
 //
-// Bound by the cache's bytes, 9/8 D a key and head.  The rows of a unit are up to
-// 8 NT (NT 1, 2 or 4) of the (query, head) pairs that share a key head, so a key is read once for
-// them.  E2M1 times E4M3 has at most 6 significant bits: K and V are exact in fp16, and
+// Bound by the cache's bytes, 9/8 D a key and head.  The rows of a unit are up to 8 NT
+// (NT 1, 2 or 4) of the (query, head) pairs that share a key head, so a key is read once
+// for them.  E2M1 times E4M3 has at most 6 significant bits: K and V are exact in fp16, and
 // a row of q is too after scaling by a power of two, so fp16 products with fp32 sums
-// lose nothing.  The keys are the 16 rows of mma.m16n8k16 (the rows of q its 8 columns):
+// lose nothing; p is rounded to fp16, by an eighth of the output's own rounding to bf16 at
+// most.  The keys are the 16 rows of mma.m16n8k16 (the rows of q its 8 columns):
 //   S^T = K q^T     a lane's part of a row of K is 16 contiguous bytes of codes: which
 //                   d a product's k stands for is free as long as q follows
 //   O^T = V^T p^T   a lane holds D/8 contiguous d of 4 keys; two keys' nibbles are
@@ -28,6 +29,11 @@
 //     any lengths keep every block busy.  A unit inside a share is written at once; of a
 //     unit over several, each block leaves its part in the workspace and
 //     attn_join_kernel joins them in order.
+// 64 sequences of 0 to 16384 keys, 64 heads over 8 of 128: 97 us, 4.5 TB/s.  The tiles run at
+// the memory's rate (435 MB in 64 us; 340 instructions a tile and warp, nine tenths of what
+// four blocks can issue); beside them 8 us pass until the first tiles are there, 10 to 20
+// between most blocks' end and the last one's, 5 for the join.  One sequence of 131072
+// keys and 8 heads over one: 16 us; of 1024 keys 4.9, a chain of latencies.
 #include "async_copy.cuh"
 #include "attn_util.cuh"
 #include "device_util.cuh"

@@ -580,6 +580,18 @@ def test_rope_on_pinned_host_buffers(dev):
     assert not got[0].is_cuda and all(torch.equal(a, b.cpu()) for a, b in zip(got, want))
 
 
+def test_norm_rope_grad_on_pinned_host_buffers(dev):
+    """So does the gradient, whose rows are copied to shared memory ahead."""
+    T, hq, hk, D, rot = 300, 4, 2, 64, 32
+    q, k, _, qw, kw, pos, table = _rope_inputs(dev, T, hq, hk, D, rot, strided=False)
+    dq, dk = _rand((T, hq, D), dev, 1), _rand((T, hk, D), dev, 2)
+    want = pkg.ts_qk_norm_rope_grad(dq, dk, q, k, qw, kw, pos, table)
+    h = [t.cpu().pin_memory() for t in (dq, dk, q, k, qw, kw, pos, table)]
+    got = pkg.ts_qk_norm_rope_grad(*h)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.cpu(), b.cpu()) for a, b in zip(got, want))
+
+
 # ---------------------------------------------------------------------------
 # many rows
 # ---------------------------------------------------------------------------

@@ -270,11 +270,12 @@ public:
         return c;
     }
 
-    // A workspace of at least `bytes`, given or new.
+    // A workspace of at least `bytes`, given or new; a new one is in device memory, of the
+    // call's stream, since it is given back while the call's kernels run.
     at::Tensor workspace(int i, int64_t bytes, const at::Tensor &like)
     {
         if (none(i))
-            return fresh(dims(bytes), kU8, like);
+            return fresh_on(like.is_cuda() ? like.device() : c10::Device(c10::kCUDA, c10::cuda::current_device()), dims(bytes), kU8);
         const at::Tensor &t = on_gpu(i, "workspace", kU8);
         if (t.numel() < bytes)
             raise(PyExc_ValueError, "workspace must hold %lld bytes, got %lld", (long long)bytes, (long long)t.numel());
@@ -303,20 +304,23 @@ public:
         return none(i) ? nullptr : static_cast<const int32_t *>(flat(i, name, kI32, want).data_ptr());
     }
 
+    at::Tensor fresh_on(c10::Device on, const Dims &d, at::ScalarType type) const
+    {
+        const Unlocked unlocked;
+        if (!given_)
+            return at::detail::empty_cuda(d.ref(), type, on, std::nullopt);
+        const c10::cuda::CUDAStreamGuard guard(stream_ == nullptr ? c10::cuda::getDefaultCUDAStream(on.index())
+                                                                  : c10::cuda::getStreamFromExternal(stream_, on.index()));
+        return at::detail::empty_cuda(d.ref(), type, on, std::nullopt);
+    }
+
     // A new contiguous tensor where `like` lives, from the memory of the stream
     // that writes it: another stream's free memory may still be in use there.
     at::Tensor fresh(const Dims &d, at::ScalarType type, const at::Tensor &like) const
     {
+        if (like.is_cuda())
+            return fresh_on(like.device(), d, type);
         const Unlocked unlocked;
-        if (like.is_cuda()) {
-            if (!given_)
-                return at::detail::empty_cuda(d.ref(), type, like.device(), std::nullopt);
-            const c10::DeviceIndex device = like.device().index();
-            const c10::cuda::CUDAStreamGuard guard(stream_ == nullptr
-                                                       ? c10::cuda::getDefaultCUDAStream(device)
-                                                       : c10::cuda::getStreamFromExternal(stream_, device));
-            return at::detail::empty_cuda(d.ref(), type, like.device(), std::nullopt);
-        }
         return at::empty(d.ref(), at::TensorOptions().dtype(type).pinned_memory(true));
     }
 

@@ -390,6 +390,33 @@ def test_rows_at_the_change_of_kernels(dev, rows, D):
     _check_attention(dev, [rows, 1, rows - 1], [300, 40, 2100], 2, 2, D, 48, seed=rows, max_q=rows)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(49, 1), (64, 1), (130, 2), (1024, 1)])
+def test_single_tokens_of_many_heads(dev, hq, hk, D):
+    """More heads to a key head than the kernel of few rows takes."""
+    _check_attention(dev, [1] * 5, [1, 0, 129, 700, 33], hq, hk, D, 16, seed=hq)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_lengths_beyond_the_table(dev, rows):
+    """A length counts as far as its table goes, which may be nowhere."""
+    D, page = 64, 32
+    lens = [64, 90, 5]
+    cache, table = _cache(dev, lens, 2, D, page, 4)
+    table = table[:, :2].contiguous()
+    cu = torch.tensor([0, rows, 2 * rows, 3 * rows], dtype=torch.int32, device=dev)
+    q = _rand((3 * rows, 4, D), dev, 1)
+
+    def call(table, lens):
+        return pkg.ts_nvfp4_attention(q, cache, table, torch.tensor(lens, dtype=torch.int32, device=dev), cu, max_q=rows, return_lse=True)
+
+    want, got = call(table, [64, 64, 5]), call(table, [65, 2 ** 31 - 1, 5])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for t, n in ((table[:, :0].contiguous(), [3, 2 ** 31 - 1, 0]), (table, [0, -1, -2 ** 31])):
+        out, lse = call(t, n)
+        assert bool((out == 0).all() and torch.isneginf(lse).all())
+
+
 def test_two_calls_at_once(dev):
     """Calls on two streams, each with a workspace of its own, and captured ones that share one in turn, give the bits of
     calls on their own: each way to split the work."""
@@ -587,7 +614,10 @@ def test_norm_rope_grad_on_pinned_host_buffers(dev):
     dq, dk = _rand((T, hq, D), dev, 1), _rand((T, hk, D), dev, 2)
     want = pkg.ts_qk_norm_rope_grad(dq, dk, q, k, qw, kw, pos, table)
     h = [t.cpu().pin_memory() for t in (dq, dk, q, k, qw, kw, pos, table)]
+    before = torch.cuda.memory_stats()["allocated_bytes.all.allocated"]
     got = pkg.ts_qk_norm_rope_grad(*h)
+    # (the workspace is on the GPU: host memory given back early could be another tensor's while the kernels run)
+    assert torch.cuda.memory_stats()["allocated_bytes.all.allocated"] - before >= pkg.library().ts_qk_norm_rope_grad_workspace(D)
     torch.cuda.synchronize()
     assert all(torch.equal(a.cpu(), b.cpu()) for a, b in zip(got, want))
 

@@ -33,7 +33,8 @@
 // Measured and not kept: p in one piece (the same) or in quarters (20 % slower, an arrival costs
 // more than it hides), a warp for each tile's products (30 % slower, the tiles fall into
 // step), polling waits (2 to 9 % slower), the code that goes to the next rows unrolled (2 %
-// slower).
+// slower), a warp of its own that copies the next rows of q as soon as their place is free
+// (25 % slower: its 64 passes a tile take longer than the rows' own warps do).
 #include "attn_util.cuh"
 #include "device_util.cuh"
 #include "f32x2.cuh"

@@ -265,6 +265,30 @@ def test_cache_beyond_4_gib(dev):
 # attention
 # ---------------------------------------------------------------------------
 
+def test_one_slot_for_many_tokens(dev):
+    """Tokens with the same slot leave the bytes of one or another of them there, and nothing elsewhere."""
+    T, hk, D, page = 300, 2, 64, 16
+    _, k, v, _, kw, pos, table = _rope_inputs(dev, T, hk, hk, D, D, seed=12)
+    g = torch.tensor([300.0], device=dev)
+    apart = pkg.ts_kv_cache(-(-T // page), hk, D, g, g, page_size=page, device=dev)
+    one = pkg.ts_kv_cache(2, hk, D, g, g, page_size=page, device=dev)
+    one.pages.fill_(0xA5)
+    for cache, slots in ((apart, torch.arange(T, device=dev).int()), (one, torch.full((T,), 21, dtype=torch.int32, device=dev))):
+        pkg.ts_qk_norm_rope(k, k, kw, kw, pos, table, EPS, v=v, cache=cache, slots=slots)
+
+    def token(pages, slot):  # [heads, bytes of the slot]
+        tile = pages[slot // page, :, slot % page // 16]
+        i = slot % 16
+        return torch.cat([tile[:, o + i * n:o + (i + 1) * n] for o, n in ((0, D // 2), (8 * D, D // 2), (16 * D, D // 16), (17 * D, D // 16))], 1)
+
+    theirs, got = torch.stack([token(apart.pages, t) for t in range(T)]), token(one.pages, 21)
+    assert bool((theirs == got).any(0).all())
+    rest = one.pages.clone()
+    rest[1, :, 0] = 0xA5
+    others = [token(one.pages, s) for s in range(16, 32) if s != 21]
+    assert bool((rest == 0xA5).all()) and all(bool((o == 0xA5).all()) for o in others)
+
+
 def _cache(dev, lens, hk, D, page, seed, spread=1.0):
     """A cache whose unused slots hold NaN scale factors, pages in random order; table [B, most + 1], ids of no page
     behind the used ones."""
@@ -415,6 +439,22 @@ def test_lengths_beyond_the_table(dev, rows):
     for t, n in ((table[:, :0].contiguous(), [3, 2 ** 31 - 1, 0]), (table, [0, -1, -2 ** 31])):
         out, lse = call(t, n)
         assert bool((out == 0).all() and torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("rows", [1, 5, 70])
+def test_pages_shared_by_sequences(dev, rows):
+    """Sequences with a common beginning may have its pages in common."""
+    D, page, L = 128, 32, 500
+    cache, table = _cache(dev, [L], 2, D, page, 8)
+    table = table.expand(3, -1).contiguous()
+    lens = torch.tensor([L, 300, L], dtype=torch.int32, device=dev)
+    q = _rand((3 * rows, 8, D), dev, 2)
+    cu = torch.arange(4, device=dev).int() * rows
+    out, lse = pkg.ts_nvfp4_attention(q, cache, table, lens, cu, max_q=rows, return_lse=True)
+    want, want_lse, slack, slack_lse = ref.attention(q, cache.pages, cache.k_scale.double(), cache.v_scale.double(), table, lens.tolist(),
+                                                     cu.tolist(), 1 / math.sqrt(D), True, 0)
+    _close(out, want, slack, "out")
+    assert bool(((lse.double() - want_lse).abs() <= slack_lse).all())
 
 
 def test_two_calls_at_once(dev):

@@ -38,6 +38,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
+// a + b of products, each rounded on its own: the compiler fuses mul2 into an add2 after it, but
+// not into this.  one: 1, of which it must not know.
+__device__ __forceinline__ uint64_t add_products2(uint64_t a, uint64_t b, uint64_t one) { return fma2(a, one, b); }
+
 // The two bf16 of a word.
 __device__ __forceinline__ uint64_t widen2(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 

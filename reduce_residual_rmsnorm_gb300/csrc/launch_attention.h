@@ -41,9 +41,11 @@ struct RopeArgs {
     bool keep;  // with a cache
     CacheArgs cache;
     const int32_t *slots;
-    // a run: up to run_heads heads of one token; runs of q, of k, and all of a token
-    int run_heads, runs_q, runs_k, runs;
-    DivMagic div_runs;
+    // a run: up to run_heads heads of one token; runs of a token's q, of its k, of k and v
+    int run_heads, runs_q, runs_k, runs_kv;
+    int q_blocks, kv_blocks, kv_every;  // blocks of runs of each; every kv_every-th is of the latter
+    float one;  // 1, for add_products2
+    DivMagic div_q, div_kv, div_every;  // division by runs_q, runs_kv, kv_every
 };
 
 struct RopeGradArgs {

@@ -6,29 +6,32 @@
 // Bound by memory.  A head's row of D elements lies on D/8 neighbouring lanes, 16
 // bytes each (a power of two of lanes, those behind D/8 idle), so the sum of squares
 // is a butterfly of a few steps and a lane's partner in the rotation is at a fixed
-// distance.  The partner's raw bf16 are exchanged, not its normed fp32: half the
-// shuffles, and what they are multiplied by goes into the factors.  A group of lanes
-// takes a run of heads of one token, the next ones' loads under way, and the
-// position's cosines and sines and the weights are read, and multiplied, once for them.
-// 16383 tokens of 64 + 8 heads of 128, half of each turned: 100.5 us, 6.05 TB/s, four fifths of
-// what the SMs can issue; with 8 heads of keys and values kept and read back, 16384 tokens:
-// 144.5 us (the calls take 118 and 19).  Equal shares of all heads to each warp with copies to
-// shared memory, as the gradient has them, took 105 and 168: half as many instructions again
-// a head.
+// distance.  Products and sums are rounded one by one, in the formula's order, and a key's
+// squares are summed in an order that the header states: a key one step of bf16 away may be
+// another code in the cache, or another scale factor of a block, so its bits are to be
+// the same wherever it is computed.  (Weights multiplied into the cosines and sines, bf16
+// partners exchanged and one fused addition took as long, with 3 in 100000 elements a step
+// away.)  A group of lanes takes a run of heads of one token, the next ones' loads under way,
+// and the position's cosines and sines and the weights are read once for them.
+// 16383 tokens of 64 + 8 heads of 128, half of each turned: 100.7 us, 6.04 TB/s; with 8 heads of
+// keys and values kept and read back, 16384 tokens: 141.7 us (the calls take 116 and 19).
+// Equal shares of all heads to each warp with copies to shared memory, as the gradient has
+// them, took 105 and 168: half as many instructions again a head.
 #include "async_copy.cuh"
 #include "device_util.cuh"
 #include "f32x2.cuh"
 #include "launch_attention.h"
+#include "tcgen05.cuh"
 
 namespace tsfn {
 
 namespace {
 
 // Blocks to an SM by their registers (16384 tokens, 64 + 8 heads of 128, with the cache
-// written and read back: 144.5 us; blocks of 256 threads, three to an SM, 149; without the
-// cache, 64 columns turned: 100.5, and 104 with four of 256).
+// written and read back: 142 us, and 150 with six blocks; without the cache, 64 columns
+// turned: 100.7, and 101.8 with nine, which spill).
 constexpr int kThreads = 128;
-constexpr int rope_blocks_per_sm(bool pairs, bool cache) { return cache ? (pairs ? 6 : 7) : (pairs ? 8 : 9); }
+constexpr int rope_blocks_per_sm(bool pairs, bool cache) { return cache ? (pairs ? 6 : 7) : 8; }
 
 // Coherent loads of what is used again (weights, tables, positions).
 __device__ __forceinline__ uint4 ld_again(const void *p)
@@ -51,12 +54,60 @@ __device__ __forceinline__ void ld_angles(const float *p, int n4, float (&f)[8])
         }
 }
 
-// Sum over the lanes of a head's row, the same bits on each of them.
+// Sum over the lanes of a head's row, neighbours first, the same bits on each of them.
 __device__ __forceinline__ float group_sum(float v, int lanes)
 {
-    for (int o = lanes >> 1; o > 0; o >>= 1)
+    for (int o = 1; o < lanes; o <<= 1)
         v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// A key's squares, from its row in shared memory, are summed in an order of their own: column j
+// to sum j mod 32, then neighbouring sums together.  This lane's N of the 32 sums, from `row` on.
+template <int N>
+__device__ __forceinline__ float key_squares(uint32_t row, int columns)
+{
+    if constexpr (N > 2) {
+        const float a = key_squares<N / 2>(row, columns);
+        return a + key_squares<N / 2>(row + N, columns - N / 2);
+    } else {
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 1
+        for (; columns > 0; columns -= 128, row += 256) {
+            uint32_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = 0;
+                if (columns > 32 * j) {
+                    if constexpr (N == 2)
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[j]) : "r"(row + 64 * j) : "memory");
+                    else
+                        v[j] = ld_shared16(row + 64 * j);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float lo = __uint_as_float(v[j] << 16), hi = __uint_as_float(v[j] & 0xFFFF0000u);
+                s0 = __fmaf_rn(lo, lo, s0);
+                if constexpr (N == 2)
+                    s1 = __fmaf_rn(hi, hi, s1);
+            }
+        }
+        return s0 + s1;
+    }
+}
+
+__device__ __forceinline__ float key_squares_of(uint32_t row, int c, int lanes, int D)
+{
+    const int at = c * (32 / lanes);
+    row += 2 * at;
+    switch (lanes) {
+    case 2: return key_squares<16>(row, D - at);
+    case 4: return key_squares<8>(row, D - at);
+    case 8: return key_squares<4>(row, D - at);
+    case 16: return key_squares<2>(row, D - at);
+    default: return key_squares<1>(row, D - at);
+    }
 }
 
 // What a lane does in the rotation: chunk c of 8 columns of a row.
@@ -80,7 +131,8 @@ __device__ __forceinline__ Turn turn_of(int c, int lane, int rot, bool pairs)
 
 // What a lane's 8 columns are multiplied by, and their partners: the rotation is
 //   y = x by + x' with,   x' the partner's columns (PAIRS: the neighbours exchanged),
-// by = cos, with = -+ sin; 1 and 0 for columns that are not rotated; s = -1 turns back.
+// by = cos, with = -+ sin; 1 and -0 for columns that are not rotated, which with a partner of 0
+// leave every x as it is; s = -1 turns back.
 struct Factors {
     uint64_t by[4], with[4];
 };
@@ -94,17 +146,26 @@ __device__ __forceinline__ Factors factors_of(const float (&cs)[8], const float 
     for (int i = 0; i < 4; ++i) {
         if (PAIRS) {
             f.by[i] = t.in ? twice(cs[i]) : twice(1.0f);
-            f.with[i] = t.in ? pair(-s * sn[i], s * sn[i]) : 0;
+            f.with[i] = t.in ? pair(-s * sn[i], s * sn[i]) : twice(-0.0f);
         } else {
             f.by[i] = t.in ? pair(cs[2 * i], cs[2 * i + 1]) : twice(1.0f);
-            f.with[i] = t.in ? pair(k * sn[2 * i], k * sn[2 * i + 1]) : 0;
+            f.with[i] = t.in ? pair(k * sn[2 * i], k * sn[2 * i + 1]) : twice(-0.0f);
         }
     }
     return f;
 }
 
-// The lane's partner columns: another lane's, or its own neighbours exchanged; zeros where
-// nothing is rotated (0 times an infinity would not be 0).
+// The partner's fp32 columns, where the rotation comes after the norm.
+template <bool PAIRS>
+__device__ __forceinline__ uint64_t partner2(uint64_t v, const Turn &t)
+{
+    float lo, hi;
+    unpair(v, lo, hi);
+    return PAIRS ? pair(hi, lo) : pair(__shfl_sync(0xffffffffu, lo, t.partner), __shfl_sync(0xffffffffu, hi, t.partner));
+}
+
+// The lane's partner columns in bf16: another lane's, or its own neighbours exchanged; zeros
+// where nothing is rotated (0 times an infinity would not be 0).
 template <bool PAIRS>
 __device__ __forceinline__ void partners(const uint4 &x, const Turn &t, uint64_t (&o)[4])
 {
@@ -167,102 +228,124 @@ __device__ __forceinline__ void put_chunk(const uint4 &v, float g, bool live, ui
 }
 
 // A group of lanes takes a run of heads of one token, two at a time with the next two's
-// loads under way.
-template <bool PAIRS, bool CACHE>
-__global__ void __launch_bounds__(kThreads, rope_blocks_per_sm(PAIRS, CACHE)) rope_kernel(const __grid_constant__ RopeArgs a)
+// loads under way.  KEYS: of keys, and with a CACHE of values; else of queries.
+template <bool PAIRS, bool KEYS, bool CACHE>
+__device__ __forceinline__ void rope_run(const RopeArgs &a, uint32_t id, uint4 (&rows)[2][kThreads])
 {
     const int lanes = 1 << a.lanes_log2;
     const int lane = threadIdx.x & 31, c = lane & (lanes - 1);
-    const int64_t id = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> a.lanes_log2;
-    // (below 2^31: the calls' limit on T * heads)
-    const int64_t t = div_by((uint32_t)id, a.div_runs);
-    const int run = (int)(id - t * a.runs);
-    // queries, keys, values
-    const int kind = run < a.runs_q ? 0 : (run < a.runs_q + a.runs_k ? 1 : 2);
-    const int h0 = (kind == 0 ? run : (kind == 1 ? run - a.runs_q : run - a.runs_q - a.runs_k)) * a.run_heads;
-    const int heads = kind == 0 ? a.hq : a.hk;
+    const int64_t t = div_by(id, KEYS ? a.div_kv : a.div_q);
+    const int run = (int)(id - t * (KEYS ? a.runs_kv : a.runs_q));
+    const bool values = CACHE && run >= a.runs_k;
+    const int h0 = (values ? run - a.runs_k : run) * a.run_heads;
+    const int heads = KEYS ? a.hk : a.hq;
     const bool in_row = c < (a.D >> 3);
-    pdl_wait();
 
     bool live = t < a.T;
     const int32_t pos = live ? a.pos[t] : -1;
     const int n = live ? min(a.run_heads, heads - h0) : 0, most = __reduce_max_sync(0xffffffffu, n);
-    const uint16_t *src = (kind == 0 ? a.q + t * a.ldq : (kind == 1 ? a.k + t * a.ldk : a.v + t * a.ldv)) + (int64_t)h0 * a.D + c * 8;
+    const uint16_t *src = (values ? a.v + t * a.ldv : (KEYS ? a.k + t * a.ldk : a.q + t * a.ldq)) + (int64_t)h0 * a.D + c * 8;
     uint4 x[2], next[2];
     auto load = [&](int h, uint4 (&to)[2]) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             to[u] = make_uint4(0, 0, 0, 0);
             if (in_row && h + u < n)
-                to[u] = ld_stream(src + (int64_t)(h + u) * a.D);
+                to[u] = ld_stream(src + (h + u) * a.D);
         }
     };
     load(0, next);
     live = live && pos >= 0 && pos < a.max_pos;
-    int64_t slot = -1;
+    uint8_t *codes = nullptr;  // of the head in the token's slot; how far on its scale factors are, 0: not kept
+    int to_sf = 0;
     float g = 0.0f;
-    if (CACHE && kind != 0 && live) {
-        slot = a.slots[t];
-        if (slot >= a.cache.slots)
-            slot = -1;
-        g = kind == 1 ? *a.cache.k_scale : *a.cache.v_scale;
+    if (CACHE && live) {
+        const int64_t slot = a.slots[t];
+        g = values ? *a.cache.v_scale : *a.cache.k_scale;
+        if (slot >= 0 && slot < a.cache.slots) {
+            int in_tile = 0;
+            codes = cache_tile(a.cache, a.D, slot, h0, &in_tile) + (values ? 8 * a.D : 0) + in_tile * (a.D >> 1);
+            to_sf = (values ? 9 : 16) * a.D - in_tile * (a.D >> 4) * 7;
+        }
     }
-    const bool turned = kind != 2;
     Turn turn = turn_of(c, lane, a.rot, PAIRS);
-    turn.in = turn.in && turned;
+    turn.in = turn.in && !values;
     float cs[8] = {}, sn[8] = {};
     if (live && turn.in) {
         const float *p = a.table + (int64_t)pos * a.rot + turn.angle;
         ld_angles(p, PAIRS ? 1 : 2, cs);
         ld_angles(p + (a.rot >> 1), PAIRS ? 1 : 2, sn);
     }
-    const uint16_t *w = kind == 0 ? a.qw : a.kw;
-    const bool norm = turned && w != nullptr;
-    // the weights go into the factors, once for the run:  y = (x r) (w cos) + (x' r) (w' sin)
-    Factors f = factors_of<PAIRS>(cs, sn, turn, 1.0f);
-    if (norm && in_row) {
-        const uint4 own = ld_again(w + c * 8);
-        const uint4 other = PAIRS ? own : ld_again(w + (c + turn.partner - lane) * 8);
-        const uint32_t ww[4] = {own.x, own.y, own.z, own.w}, wo[4] = {other.x, other.y, other.z, other.w};
+    const uint16_t *w = KEYS ? a.kw : a.qw;
+    const Factors f = factors_of<PAIRS>(cs, sn, turn, 1.0f);
+    uint64_t wf[4] = {twice(1.0f), twice(1.0f), twice(1.0f), twice(1.0f)};
+    if (w != nullptr && in_row && !values) {
+        const uint4 v = ld_again(w + c * 8);
+        const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f.by[i] = mul2(f.by[i], widen2(ww[i]));
-            f.with[i] = mul2(f.with[i], widen2(PAIRS ? __funnelshift_l(wo[i], wo[i], 16) : wo[i]));
-        }
+        for (int i = 0; i < 4; ++i)
+            wf[i] = widen2(ww[i]);
     }
     pdl_launch_dependents();
     const float inv_d = 1.0f / (float)a.D;
-    uint16_t *dst = (kind == 0 ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko) + (int64_t)h0 * a.D + c * 8;
-    const bool to_rows = live && in_row && turned && (kind == 0 || a.k_out != nullptr);
+    uint16_t *dst = (KEYS ? a.k_out + t * a.ldko : a.q_out + t * a.ldqo) + (int64_t)h0 * a.D + c * 8;
+    const bool to_rows = live && in_row && !values && (!KEYS || a.k_out != nullptr);
+    const uint32_t mine = smem_addr(&rows[0][threadIdx.x]);
 
     for (int h = 0; h < most; h += 2) {
         x[0] = next[0];
         x[1] = next[1];
         load(h + 2, next);
+        float sq[2] = {};
+        if (KEYS && w != nullptr) {
+            st_shared(mine, x[0]);
+            st_shared(mine + kThreads * 16, x[1]);
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                sq[u] = key_squares_of(mine - c * 16 + u * kThreads * 16, c, lanes, a.D);
+            __syncwarp();
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             float r = 1.0f;
-            if (a.qw != nullptr)
-                r = rsqrtf(__fmaf_rn(group_sum(sumsq_bf16x8(x[u], 0.0f), lanes), inv_d, a.eps));
-            uint64_t o[4], y2[4];
-            partners<PAIRS>(x[u], turn, o);
+            if (w != nullptr)
+                r = rsqrtf(__fmaf_rn(group_sum(KEYS ? sq[u] : sumsq_bf16x8(x[u], 0.0f), lanes), inv_d, a.eps));
+            uint64_t n2[4];
             const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y2[i] = fma2(mul2(widen2(xw[i]), twice(r)), f.by[i], mul2(mul2(o[i], twice(r)), f.with[i]));
-            const uint4 y = turned ? pack2x4(y2) : x[u];
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t v = mul2(mul2(widen2(xw[i]), twice(r)), wf[i]);
+                const uint64_t other = partner2<PAIRS>(v, turn), o = turn.in ? other : 0;  // (0 times an infinity would not be 0)
+                n2[i] = add_products2(mul2(v, f.by[i]), mul2(o, f.with[i]), twice(a.one));
+            }
+            const uint4 y = values ? x[u] : pack2x4(n2);
             if (to_rows && h + u < n)
-                st_v4(dst + (int64_t)(h + u) * a.D, y);
-            const bool keep = CACHE && in_row && h + u < n && slot >= 0;
-            if (CACHE && __any_sync(0xffffffffu, keep)) {  // (most warps have queries only)
-                int in_tile = 0;
-                uint8_t *tile = keep ? cache_tile(a.cache, a.D, slot, h0 + h + u, &in_tile) : nullptr;
-                const int second = kind == 2 ? 1 : 0;
-                put_chunk(y, g, keep, tile + second * 8 * a.D + in_tile * (a.D >> 1),
-                          tile + (16 + second) * a.D + in_tile * (a.D >> 4), c);
+                st_v4(dst + (h + u) * a.D, y);
+            if (CACHE) {
+                put_chunk(y, g, in_row && h + u < n && to_sf != 0, codes, codes + to_sf, c);
+                codes += (a.cache.page_size >> 4) * 18 * a.D;
             }
         }
     }
+}
+
+template <bool PAIRS, bool CACHE>
+__global__ void __launch_bounds__(kThreads, rope_blocks_per_sm(PAIRS, CACHE)) rope_kernel(const __grid_constant__ RopeArgs a)
+{
+    __shared__ __align__(16) uint4 rows[2][kThreads];
+    // every kv_every-th block has runs of keys (and values), up to kv_blocks of them, the others
+    // runs of queries (100.7 and 141.7 us; every block with runs of both 116.8 and 149.5, keys and
+    // values of all tokens first 102.6 and 156.9)
+    const uint32_t turn = div_by(blockIdx.x, a.div_every);
+    const bool keys = turn < (uint32_t)a.kv_blocks && turn * a.kv_every == blockIdx.x;
+    const int64_t block = keys ? turn : blockIdx.x - min(turn + 1, (uint32_t)a.kv_blocks);
+    const uint32_t id = (uint32_t)((block * kThreads + threadIdx.x) >> a.lanes_log2);  // (below 2^31: the calls' limit on T * heads)
+    pdl_wait();
+    if (keys)
+        rope_run<PAIRS, true, CACHE>(a, id, rows);
+    else
+        rope_run<PAIRS, false, false>(a, id, rows);
 }
 
 // ---------------------------------------------------------------------------
@@ -510,8 +593,7 @@ int run_heads(int64_t rows, int lanes_log2)
 template <bool PAIRS>
 cudaError_t launch_rope_as(const RopeArgs &a, bool pdl, cudaStream_t stream)
 {
-    const int64_t blocks = (((a.T * a.runs) << a.lanes_log2) + kThreads - 1) / kThreads;
-    const dim3 grid((unsigned)blocks), block(kThreads);
+    const dim3 grid((unsigned)(a.kv_blocks + a.q_blocks)), block(kThreads);
     return a.keep ? launch_kernel(rope_kernel<PAIRS, true>, grid, block, 0, stream, pdl, a)
                   : launch_kernel(rope_kernel<PAIRS, false>, grid, block, 0, stream, pdl, a);
 }
@@ -524,8 +606,15 @@ cudaError_t launch_rope(const RopeArgs &args, bool pdl, cudaStream_t stream)
     a.run_heads = run_heads(a.T * (a.hq + 2 * a.hk), a.lanes_log2);
     a.runs_q = (a.hq + a.run_heads - 1) / a.run_heads;
     a.runs_k = (a.hk + a.run_heads - 1) / a.run_heads;
-    a.runs = a.runs_q + (a.keep ? 2 : 1) * a.runs_k;
-    a.div_runs = div_magic((uint32_t)a.runs);
+    a.runs_kv = (a.keep ? 2 : 1) * a.runs_k;
+    const auto blocks = [&](int64_t runs) { return (int)(((a.T * runs << a.lanes_log2) + kThreads - 1) / kThreads); };
+    a.kv_blocks = blocks(a.runs_kv);
+    a.q_blocks = blocks(a.runs_q);
+    a.kv_every = (a.kv_blocks + a.q_blocks) / a.kv_blocks;
+    a.div_every = div_magic((uint32_t)a.kv_every);
+    a.div_q = div_magic((uint32_t)a.runs_q);
+    a.div_kv = div_magic((uint32_t)a.runs_kv);
+    a.one = 1.0f;
     return a.pairs ? launch_rope_as<true>(a, pdl, stream) : launch_rope_as<false>(a, pdl, stream);
 }
 

@@ -151,7 +151,7 @@ struct Shared {
 
 // The parts (m, l, O) of a run's rows by the block's warps, in shared memory.
 template <int D, int NT, int WARPS>
-__device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float c0, uint8_t *smem)
+__device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float k_scale, uint8_t *smem)
 {
     using L = Layout<D>;
     using Sh = Shared<D, NT, WARPS>;
@@ -254,7 +254,7 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
         }
         l = l < 0 ? 0 : l;
         if (t == 0) {
-            reinterpret_cast<float *>(smem + Sh::kFactor)[col] = c0 * down;
+            reinterpret_cast<float *>(smem + Sh::kFactor)[col] = score_factor(a, down, k_scale);
             reinterpret_cast<int *>(smem + Sh::kHi)[col] = min(h, s.len);
             reinterpret_cast<int *>(smem + Sh::kLo)[col] = l;
         }
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_
     __shared__ int64_t warp_sums[kWarps];
     __shared__ int64_t state[6];
     __shared__ Run kept;
-    __shared__ float factor;
+    __shared__ float k_scale;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float *const slots = a.partial + (int64_t)gridDim.x * (sizeof(Record) / 4);
     Record *const record = reinterpret_cast<Record *>(a.partial) + blockIdx.x;
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_
     }
     run.s = sequence<NR>(a, run.b);
     if (tid == 0)
-        factor = a.scale * kLog2e / *a.cache.k_scale;
+        k_scale = *a.cache.k_scale;
 
     while (pos < end) {
         while (pos >= base + weight(a, run.s, way_of(NT))) {
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(share_warps(NT) * 32, blocks_per_sm(NT)) attn_
             kept = run;
         }
         __syncthreads();
-        attend<D, NT, kWarps>(a, kept, factor, smem);
+        attend<D, NT, kWarps>(a, kept, k_scale, smem);
         run = kept;
         pos = state[0];
         end = state[1];
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kClusterWarps * 32, NT == 1 ? 2 : 1) attn_clus
     for (int64_t i = (int64_t)tid * 32; i < a.max_pages; i += kWarps * 32 * 32)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + (int64_t)run.b * a.max_pages + i));
     pdl_wait();
-    const float c0 = a.scale * kLog2e / *a.cache.k_scale;
+    const float k_scale = *a.cache.k_scale;
     run.s = sequence<NR>(a, run.b);
     if ((int)blockIdx.y >= run.s.parts)
         cluster_wait();
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(kClusterWarps * 32, NT == 1 ? 2 : 1) attn_clus
         const int begin = (int)((int64_t)run.s.tiles * rank / blocks);
         run.first = run.s.first + begin;
         run.count = (int)((int64_t)run.s.tiles * (rank + 1) / blocks) - begin;
-        attend<D, NT, kWarps>(a, run, c0, smem);
+        attend<D, NT, kWarps>(a, run, k_scale, smem);
         const float vg = *a.cache.v_scale;
         cluster_wait();  // every block has started, and has read what it was given before
         for (int r0 = tid / 32 * kWarpRows; r0 < run.rows; r0 += kWarps * kWarpRows) {

@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const uint32_t q_smem = smem + S::kQ + tile * S::kMatrix;
         const uint32_t s_full = smem_u32(&bars.s_full[tile]);
         const float vg = *a.cache.v_scale;
-        const float c0 = a.scale * kLog2e / *a.cache.k_scale;
+        const float k_scale = *a.cache.k_scale;
         uint32_t step = 0, done = 0, units_done = 0;  // steps of the block and of this tile
         bool alive = true;
         // the query and head of row `of` of the tile; whether there is one
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             fence_async_proxy();
             warp_arrive(smem_u32(&bars.q_full[tile]));
-            const float cf = c0 * down;
+            const float cf = score_factor(a, down, k_scale);
             int hi, lo;  // the keys that the row sees
             {
                 int i, qh;

@@ -72,6 +72,15 @@ __device__ __forceinline__ float fp16_scale(float amax, float &down)
     return __uint_as_float((uint32_t)(134 - e) << 23);
 }
 
+// What the scores of a row, scaled by 1 / down, are multiplied by to be in units of log2.  Not
+// below the smallest normal number (a row of zeros, or tiny scales: the scores are zeros
+// then): -inf, where a key is not seen, times 0 would not be -inf.
+__device__ __forceinline__ float score_factor(const AttnArgs &a, float down, float k_scale)
+{
+    const float f = a.scale * kLog2e * down / k_scale;
+    return f < 0x1p-126f ? 0x1p-126f : f;
+}
+
 __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;

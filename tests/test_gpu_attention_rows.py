@@ -1,0 +1,67 @@
+"""Rows of queries and bounds that attention may meet at the ends of their ranges, in each way to split the work."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import reduce_residual_rmsnorm_gb300 as pkg
+from tests import attention_ref as ref
+from tests.test_gpu_attention import _cache, _close, _rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import __graft_entry__
+
+    __graft_entry__.build()
+    return torch.device("cuda:0")
+
+
+# queries and lengths of the sequences: units by clusters (of 8, 16 and 32 rows), by even shares, on the fifth-generation
+# tensor cores in one piece and in shares
+FORMS = {"cluster": ([1, 1, 1, 1], [300, 17, 0, 1]), "cluster16": ([3, 2, 0, 4], [150, 40, 9, 2]), "cluster32": ([7, 8, 5], [90, 200, 3]),
+         "shares": ([1, 1, 1], [17000, 33, 700]), "shares32": ([6, 8, 3], [17001, 40, 1]), "prompt": ([70, 130, 20], [200, 150, 10]),
+         "prompt_shares": ([40, 33], [20001, 300])}
+
+
+def _call(dev, q, cache, table, lens, new, scale=None, **args):
+    """(out, lse) and the reference's four."""
+    cu = np.concatenate(([0], np.cumsum(new)))
+    got = pkg.ts_nvfp4_attention(q, cache, table, torch.tensor(lens, dtype=torch.int32, device=dev), torch.from_numpy(cu).int().to(dev),
+                                 max_q=max(new), scale=scale, return_lse=True, **args)
+    real = 1 / math.sqrt(q.shape[2]) if scale is None else float(torch.tensor(scale, dtype=torch.float32))
+    return got, ref.attention(q, cache.pages, cache.k_scale.double(), cache.v_scale.double(), table, lens, cu, real,
+                              args.get("causal", True), args.get("window", 0))
+
+
+def _check(got, want):
+    out, lse, slack, slack_lse = want
+    _close(got[0], out, slack, "out")
+    none = torch.isinf(lse)
+    assert torch.equal(torch.isneginf(got[1]), none)
+    assert bool(((got[1].double() - lse).abs()[~none] <= slack_lse[~none]).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("k_scale,scale,spread", [(1e7, None, 4e4), (300.0, 1e-30, 1.0), (300.0, 1e-45, 1.0), (1e7, 1e-37, 3e37),
+                                                  (1e30, None, 1e25), (300.0, 1e-38, 1e36)])
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_of_zeros_and_tiny_factors(dev, form, k_scale, scale, spread, window, D):
+    """A row of zeros (padding) sees the mean of V, whatever the other rows, the scales and the mask are; so does any row
+    whose scores all come out at zero."""
+    new, lens = FORMS[form]
+    cache, table = _cache(dev, lens, 2, D, 32, 5)
+    cache = pkg.KVCache(cache.pages, torch.tensor([k_scale], device=dev), cache.v_scale)
+    if len(lens) > 1 and lens[1] > 32:
+        table[1, 1] = -1  # a page that is not there
+    q = _rand((sum(new), 8, D), dev, 3, spread)
+    q[::2, 1::3] = 0.0
+    q[1::2, ::5] = 0.0
+    got, want = _call(dev, q, cache, table, lens, new, scale, window=window)
+    _check(got, want)
+    assert bool(torch.isfinite(got[0]).all()) and not bool(torch.isnan(got[1]).any())

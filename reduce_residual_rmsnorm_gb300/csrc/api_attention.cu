@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxHeadRows = 1LL << 30;  // tokens x heads: 32-bit indexes of rows
+constexpr int64_t kMaxKeys = 1LL << 30;      // of a sequence
 
 // Rows of `width` bytes, `ld` bytes apart; flat buffers are one row.
 struct Rows {
@@ -407,7 +408,7 @@ int64_t attention_workspace(int64_t B, int64_t heads, int64_t rows, int64_t D, i
 extern "C" int64_t ts_nvfp4_attention_workspace(int64_t B, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_q,
                                                 int64_t max_keys, int64_t window)
 {
-    if (check_attention(q_heads, heads, head_dim, max_q) != TS_OK || B < 0 || B > 65536 || max_keys < 0 || max_keys > (1LL << 30) ||
+    if (check_attention(q_heads, heads, head_dim, max_q) != TS_OK || B < 0 || B > 65536 || max_keys < 0 || max_keys > kMaxKeys ||
         window < 0 || window > kMaxRows)
         return -1;
     return attention_workspace(B, heads, max_q * (q_heads / heads), head_dim, max_keys, window);
@@ -430,7 +431,7 @@ extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t
     TS_TRY(check_range("B", B, 0, 65536));
     if (cu_q == nullptr && T != B)
         return fail(TS_ERR_SHAPE, "T = %lld queries of B = %lld sequences need cu_q", (long long)T, (long long)B);
-    TS_TRY(check_range("max_pages", max_pages, 0, (1LL << 30) / c.page_size));
+    TS_TRY(check_range("max_pages", max_pages, 0, kMaxKeys / c.page_size));
     TS_TRY(check_ld("ldq", ldq, q_heads * D));
     TS_TRY(check_ld("ldo", ldo, q_heads * D));
     if (!(scale > 0.0f) || std::isinf(scale))
@@ -471,7 +472,7 @@ extern "C" int ts_nvfp4_attention(const void *q, int64_t ldq, int64_t T, int64_t
     a.lens = kv_lens;
     a.scale = scale;
     a.causal = causal != 0;
-    a.window = (int)window;
+    a.window = (int)(window < kMaxKeys ? window : kMaxKeys);  // (a row's position less it stays within 32 bits)
     a.out = static_cast<uint16_t *>(out);
     a.ldo = ldo;
     a.lse = lse;

@@ -65,3 +65,16 @@ def test_rows_of_zeros_and_tiny_factors(dev, form, k_scale, scale, spread, windo
     got, want = _call(dev, q, cache, table, lens, new, scale, window=window)
     _check(got, want)
     assert bool(torch.isfinite(got[0]).all()) and not bool(torch.isnan(got[1]).any())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30 + 1, 2 ** 30])
+def test_windows_that_bound_nothing(dev, window, D):
+    """Windows beyond every length give the bits of none, also where queries stand in front of the first key."""
+    for new, lens in (([20, 150, 3], [10, 100, 2]), ([600, 40], [300, 20]), ([5, 3, 7], [3, 1, 50]), ([2, 4], [1, 2])):
+        cache, table = _cache(dev, lens, 2, D, 32, 5)
+        q = _rand((sum(new), 8, D), dev, 3)
+        args = dict(cu_q=torch.tensor([0, *np.cumsum(new)], dtype=torch.int32, device=dev), max_q=max(new), return_lse=True)
+        kv = torch.tensor(lens, dtype=torch.int32, device=dev)
+        want, got = (pkg.ts_nvfp4_attention(q, cache, table, kv, window=w, **args) for w in (0, window))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -550,9 +550,9 @@ __device__ __forceinline__ void put_row(const AttnArgs &a, int q0, int head, int
 {
     const int i = (int)div_by((uint32_t)row, a.div_group);
     const int qh = head * a.group + ((int)row - i * a.group);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum * vg);
+    const float by = sum == 0.0f ? 0.0f : 1.0f / sum, of = 1.0f / vg;  // (their product may be out of range)
     *reinterpret_cast<uint2 *>(a.out + (int64_t)(q0 + i) * a.ldo + (int64_t)qh * D + d) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        make_uint2(pack_bf16x2(acc.x * by * of, acc.y * by * of), pack_bf16x2(acc.z * by * of, acc.w * by * of));
     if (a.lse != nullptr && d == 0)
         a.lse[(int64_t)(q0 + i) * a.hq + qh] = sum == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) * kLn2 + logf(sum);
 }

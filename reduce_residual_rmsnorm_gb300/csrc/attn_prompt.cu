@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     copy_q(block);
             // 128 bytes of a row at a time, written by 8 neighbouring lanes (lanes that write
             // their own rows took 4000 cycles)
-            const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
+            const float by = l == 0.0f ? 0.0f : 1.0f / l, of = 1.0f / vg;  // (their product may be out of range)
             const uint32_t way_out = q_smem + kLast * S::kBlock + (warp & 3) * 32 * 128;
 #pragma unroll 1
             for (int at = 0; at < D; at += whole_unit ? 64 : 32) {
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                             float f[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                f[e] = __uint_as_float(v[8 * k + e]) * inv;
+                                f[e] = __uint_as_float(v[8 * k + e]) * by * of;
                             st_shared(way_out + lane * 128 + (((half * 4 + k) ^ (lane & 7)) * 16), pack8(f));
                         }
                     } else {
@@ -1006,11 +1006,11 @@ __device__ __forceinline__ void join_rows(const AttnArgs &a, const Record &rec, 
             break;
         const uint32_t r = (uint32_t)rec.row0 + row0 + u, i = div_by(r, a.div_group);
         const int64_t qh = (int64_t)rec.head * a.group + (r - i * a.group), q = (int64_t)rec.q0 + i;
-        const float inv = l[u] == 0.0f ? 0.0f : 1.0f / (l[u] * vg);
+        const float by = l[u] == 0.0f ? 0.0f : 1.0f / l[u], of = 1.0f / vg;
         uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + q * a.ldo + qh * D + lane * V);
 #pragma unroll
         for (int j = 0; j < V / 2; ++j)
-            dst[j] = pack_bf16x2(acc[u][2 * j] * inv, acc[u][2 * j + 1] * inv);
+            dst[j] = pack_bf16x2(acc[u][2 * j] * by * of, acc[u][2 * j + 1] * by * of);
         if (a.lse != nullptr && lane == 0)
             a.lse[q * a.hq + qh] = l[u] == 0.0f ? -INFINITY : (m[u] == -INFINITY ? 0.0f : m[u]) * kLn2 + logf(l[u]);
     }

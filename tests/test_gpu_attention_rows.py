@@ -78,3 +78,15 @@ def test_windows_that_bound_nothing(dev, window, D):
         kv = torch.tensor(lens, dtype=torch.int32, device=dev)
         want, got = (pkg.ts_nvfp4_attention(q, cache, table, kv, window=w, **args) for w in (0, window))
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("v_scale", [1e36, 1e30, 1e-30])
+@pytest.mark.parametrize("form", FORMS)
+def test_scales_of_values(dev, form, v_scale, D):
+    """Values of any magnitude that their scale gives come out, however large the sum of a row is."""
+    new, lens = FORMS[form]
+    cache, table = _cache(dev, lens, 2, D, 32, 5)
+    cache = pkg.KVCache(cache.pages, cache.k_scale, torch.tensor([v_scale], device=dev))
+    q = _rand((sum(new), 8, D), dev, 3, 0.01)  # (nearly equal weights: a sum as large as the length)
+    _check(*_call(dev, q, cache, table, lens, new))

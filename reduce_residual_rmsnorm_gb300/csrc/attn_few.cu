@@ -7,8 +7,9 @@
 // (NT 1, 2 or 4) of the (query, head) pairs that share a key head, so a key is read once
 // for them.  E2M1 times E4M3 has at most 6 significant bits: K and V are exact in fp16, and
 // a row of q is too after scaling by a power of two, so fp16 products with fp32 sums
-// lose nothing; p is rounded to fp16, by an eighth of the output's own rounding to bf16 at
-// most.  The keys are the 16 rows of mma.m16n8k16 (the rows of q its 8 columns):
+// lose nothing; p is rounded to fp16, by an eighth of the output's own rounding to bf16 for
+// weights above 2^-21 of the row's largest, by 2^-32 of that for smaller ones.  The keys are
+// the 16 rows of mma.m16n8k16 (the rows of q its 8 columns):
 //   S^T = K q^T     a lane's part of a row of K is 16 contiguous bytes of codes: which
 //                   d a product's k stands for is free as long as q follows
 //   O^T = V^T p^T   a lane holds D/8 contiguous d of 4 keys; two keys' nibbles are
@@ -19,8 +20,7 @@
 //
 // A warp takes a run of tiles of 16 keys, with copies of the next ones under way, and has
 // a running maximum and sum of its own.  The maximum follows only when a score passes it
-// by 2^8, so most tiles take one vote instead of a reduction and a rescaling; p <= 256
-// is far from fp16's end.
+// by 2^8, so most tiles take one vote instead of a reduction and a rescaling.
 //
 // Work is split in one of two ways:
 //   - units that are all resident at once: a cluster of up to 8 blocks for each, whose parts
@@ -277,8 +277,8 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
         kept[nt] = *reinterpret_cast<const float2 *>(smem + Sh::kFactor + (nt * 8 + 2 * t) * 4);
 
     float o[NT][KS][4];
-    // the maximum (0 while there is none), how far above it a score may be (-inf while there
-    // is none), and the sum
+    // the maximum less kLift (0 while there is none), how far above that a score may be (-inf
+    // while there is none), and the sum
     float off[NT][2], room[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -413,11 +413,11 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     const bool some = room[nt][j] != -INFINITY;
-                    top += off[nt][j];
+                    top += off[nt][j] - kLift;
                     top = some ? fmaxf(top, off[nt][j]) : top;
                     f[j] = some ? exp2_approx(off[nt][j] - top) : 0.0f;
                     off[nt][j] = top == -INFINITY ? 0.0f : top;
-                    room[nt][j] = top == -INFINITY ? -INFINITY : kSlack;
+                    room[nt][j] = top == -INFINITY ? -INFINITY : kLift + kSlack;
                     l[nt][j] *= f[j];
                     x[nt][j] = fmaf(sc[nt][j], j ? cf.y : cf.x, -off[nt][j]);
                     x[nt][j + 2] = fmaf(sc[nt][j + 2], j ? cf.y : cf.x, -off[nt][j]);

@@ -1,7 +1,7 @@
 // Attention of many rows over the paged NVFP4 cache, on the fifth-generation tensor
 // cores: prompts, and pieces of them after what the cache holds.
 //
-//   S = q K^T,   p_j = exp2(c S_j - m),   O = p V,   out = O / (sum_j p_j v_scale)
+//   S = q K^T,   p_j = exp2(c S_j - m),   O = p V,   out = O / sum_j p_j / v_scale
 //
 // A block works on 256 rows, (query, head) pairs that share a key head, as two tiles of
 // 128, and goes over the keys 128 at a time.  K and V are exact in fp16 (6 significant
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const int lo_max = __reduce_max_sync(0xffffffffu, lo);
             const int key0 = (place.part.first + segment.step) * kKeys;
 
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f;  // the maximum less kLift, and the sum
             for (int k = 0; k < count; ++k, ++done) {
                 const int key = key0 + k * kKeys;
                 alive = wait(s_full, done & 1, &dead);
@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 for (int c = 0; c < 4; ++c)
                     top[c] = fmaxf(top[c], __uint_as_float(v[c][31]));
                 const float to = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cf;
-                if (__any_sync(0xffffffffu, k == 0 || to > m + kSlack)) {  // the maximum follows
-                    const float next = fmaxf(m, to), f = m == -INFINITY ? 0.0f : exp2_approx(m - next);
+                if (__any_sync(0xffffffffu, k == 0 || to > m + (kLift + kSlack))) {  // the maximum follows
+                    const float next = fmaxf(m, to - kLift), f = m == -INFINITY ? 0.0f : exp2_approx(m - next);
                     m = next;
                     l *= f;
 #pragma unroll 1

@@ -8,8 +8,11 @@
 
 namespace tsfn {
 
-// A running maximum follows a score only when that passes it by 2^kSlack.
-constexpr float kSlack = 8.0f;
+// p is exp2(score - top) 2^kLift, so that fp16 keeps what is far below the largest: 11 bits
+// down to 2^-21 of it, and something down to 2^-32.  The top follows a score only when that
+// passes it by 2^kSlack; p stays below 2^(kLift + kSlack), fp16's end at 2^16.  What is kept
+// of a row as its maximum is top - kLift: sums and outputs of parts go with that.
+constexpr float kLift = 7.0f, kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What a block leaves for a unit that it began and others go on with.

@@ -90,3 +90,45 @@ def test_scales_of_values(dev, form, v_scale, D):
     cache = pkg.KVCache(cache.pages, cache.k_scale, torch.tensor([v_scale], device=dev))
     q = _rand((sum(new), 8, D), dev, 3, 0.01)  # (nearly equal weights: a sum as large as the length)
     _check(*_call(dev, q, cache, table, lens, new))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [18.62, 21.62, 22.62, 24.62, 26.62])
+@pytest.mark.parametrize("new,lens", [([1] * 20, [3000] * 20), ([4] * 20, [2500] * 20), ([200], [20000]), ([40], [33000])],
+                         ids=["single", "few", "prompt", "prompt_far"])
+def test_one_key_that_outweighs_the_others(dev, new, lens, far, D):
+    """A key with the weight of 2^far others and no value of its own: the output is made of the small weights.
+
+    A weight is rounded to fp16 as 2^7 times its part of the largest: 2^-11 of it, or 2^-25 / 2^7 of the largest where it
+    is subnormal.  The scores' error and the fp32 sums' as in the reference's bounds."""
+    hk, G, page = 2, 4, 64
+    g = torch.Generator(device=dev).manual_seed(1)
+    one = torch.ones(1, device=dev)
+    used = [-(-n // page) for n in lens]
+    cache = pkg.ts_kv_cache(sum(used), hk, D, one, 1700 * one, page_size=page, device=dev)
+    table = torch.arange(sum(used), device=dev).int().view(len(lens), -1)
+    slots = (table.long().repeat_interleave(page, 1) * page + torch.arange(page, device=dev).repeat(used[0]))[:, :lens[0]].int().flatten()
+    k = torch.zeros(len(lens), lens[0], hk, D, dtype=torch.bfloat16, device=dev)
+    v = (0.5 + torch.rand(k.shape, generator=g, device=dev)).bfloat16()
+    k[:, 0, :, 0], v[:, 0] = 6.0, 0.0  # (6 is exact in the cache)
+    flat = torch.zeros(1, 16, device=dev)
+    flat[:, :8] = 1.0
+    k, v = k.flatten(0, 1), v.flatten(0, 1)
+    pkg.ts_qk_norm_rope(k, k, None, None, torch.zeros(len(k), dtype=torch.int32, device=dev), flat, v=v, cache=cache, slots=slots)
+    q = torch.randn(sum(new), hk * G, D, generator=g, device=dev).bfloat16()
+    q[..., 0] = 1.0
+    scale = far * math.log(2.0) / 6.0
+    got, (out, lse, _, slack_lse) = _call(dev, q, cache, table, lens, new, scale)
+    values = ref.cached(cache.pages, 1) / 1700.0
+    at = 0
+    for b, n in enumerate(new):
+        all_v = values[table[b].long()].transpose(0, 1).flatten(1, 2)[:, :lens[b]].abs().cumsum(1)  # [hk, keys, D]
+        seen = all_v[:, lens[b] - n:lens[b]].transpose(0, 1).repeat_interleave(G, 1)                # of each query
+        rows = slice(at, at + n)
+        top = torch.exp(scale * 6.0 - lse[rows]).unsqueeze(-1)
+        es = (D + 4) * 2.0 ** -23 * scale * 6.0 + 2.0 ** -20
+        slack = (2.0 ** -11 + 2.0 ** -18 + 2 * es) * out[rows].abs() + 2.0 ** -32 * top * seen
+        _close(got[0][rows], out[rows], slack, "out")
+        at += n
+    assert bool(((got[1].double() - lse).abs() <= slack_lse).all())
+    assert float(out.abs().min()) > 0

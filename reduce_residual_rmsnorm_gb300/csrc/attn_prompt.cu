@@ -670,8 +670,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         for (int k = 0; k < 4; ++k) {
                             float f[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                f[e] = __uint_as_float(v[8 * k + e]) * by * of;
+                            for (int e = 0; e < 8; e += 2)
+                                unpair(mul2(mul2(pair(__uint_as_float(v[8 * k + e]), __uint_as_float(v[8 * k + e + 1])), twice(by)), twice(of)),
+                                       f[e], f[e + 1]);
                             st_shared(way_out + lane * 128 + (((half * 4 + k) ^ (lane & 7)) * 16), pack8(f));
                         }
                     } else {

@@ -122,6 +122,7 @@ TS_API int ts_qk_norm_rope(const void *q, int64_t ldq, const void *k, int64_t ld
  *   dw[j] = sum over tokens and heads of d[j] * x[j] * r                      fp32
  *
  *   dq_out, dk_out  bf16, row strides lddqo, lddko.
+ *   q, k            the forward call's inputs (which it must not have written in place).
  *   dq, dk          bf16, row strides lddq, lddk; may be dq_out, dk_out in place.
  *   dq_weight, dk_weight  fp32 [D]; NULL exactly where the weights are.  Written
  *                   for T == 0 too (zeros).

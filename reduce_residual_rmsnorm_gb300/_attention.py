@@ -74,7 +74,8 @@ def ts_qk_norm_rope_grad(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Te
                          workspace: torch.Tensor | None = None, launch_with_pdl: bool = False, stream=None):
     """The gradient of ``ts_qk_norm_rope``: (dq, dk bf16, dq_weight, dk_weight fp32 [D] or None without weights).
 
-    ``dq``, ``dk`` may be ``dq_out``, ``dk_out``.
+    ``q``, ``k`` are the forward call's inputs, which it must not have written in place; ``dq``, ``dk`` may be ``dq_out``,
+    ``dk_out``.
     """
     return _native().qk_norm_rope_grad(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, dq, dk,
                                        dq_weight, dk_weight, workspace, launch_with_pdl, stream)

@@ -807,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             const uint32_t bar = smem_u32(&bars.raw_full[raw.slot]), to = smem + S::kRaws + raw.slot * S::kRaw;
             const int tiles = __popc(__ballot_sync(0xffffffffu, in));
+            __syncwarp();  // (the arrival hands on what the lanes wrote; a vote orders no memory)
             if (lane == 0)
                 mbar_expect_tx(bar, tiles * S::kRaw / 8);
             __syncwarp();

@@ -85,7 +85,8 @@ def ts_kv_cache_read(cache: KVCache, slots: torch.Tensor, *, k_out: torch.Tensor
                      v_out: torch.Tensor | None = None, launch_with_pdl: bool = False, stream=None):
     """The bf16 keys and values [T, heads, D] that the cache's ``slots`` (int32 [T]) hold.
 
-    Tokens with a slot outside the cache are left as they were.
+    New outputs are where the cache is.  Tokens with a slot outside the cache are left as they were (in a new output:
+    undefined).
     """
     return _native().kv_cache_read(*cache, slots, k_out, v_out, launch_with_pdl, stream)
 

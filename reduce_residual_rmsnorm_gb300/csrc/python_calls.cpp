@@ -719,6 +719,7 @@ PyObject *kv_cache_read(PyObject *const *args, Py_ssize_t n)
 {
     Call c(args, n, 8);
     const ts_kv_cache_t cache = c.cache(0);
+    const at::Tensor &pages = c.tensor(0, "cache.pages", kU8);  // (new outputs are where it is)
     const at::Tensor &slots = c.flat(3, "slots", kI32);
     if (slots.dim() != 1)
         raise(PyExc_ValueError, "slots must be [T]");
@@ -727,7 +728,7 @@ PyObject *kv_cache_read(PyObject *const *args, Py_ssize_t n)
     at::Tensor out[2];
     for (int i = 0; i < 2; ++i) {
         if (c.none(4 + i)) {
-            out[i] = c.fresh(dims(T, cache.heads, cache.head_dim), kBF16, slots);
+            out[i] = c.fresh(dims(T, cache.heads, cache.head_dim), kBF16, pages);
             ld[i] = cache.heads * cache.head_dim;
         } else {
             out[i] = c.heads(4 + i, i == 0 ? "k_out" : "v_out", &ld[i]);

@@ -270,12 +270,13 @@ public:
         return c;
     }
 
-    // A workspace of at least `bytes`, given or new; a new one is in device memory, of the
+    // A workspace of at least `bytes`, given or new; a new one is in the memory of the device
+    // that the call runs on (its tensors', the current one where all are in host memory), of the
     // call's stream, since it is given back while the call's kernels run.
-    at::Tensor workspace(int i, int64_t bytes, const at::Tensor &like)
+    at::Tensor workspace(int i, int64_t bytes)
     {
         if (none(i))
-            return fresh_on(like.is_cuda() ? like.device() : c10::Device(c10::kCUDA, c10::cuda::current_device()), dims(bytes), kU8);
+            return fresh_on(c10::Device(c10::kCUDA, device_ >= 0 ? (c10::DeviceIndex)device_ : c10::cuda::current_device()), dims(bytes), kU8);
         const at::Tensor &t = on_gpu(i, "workspace", kU8);
         if (t.numel() < bytes)
             raise(PyExc_ValueError, "workspace must hold %lld bytes, got %lld", (long long)bytes, (long long)t.numel());
@@ -698,7 +699,7 @@ PyObject *qk_norm_rope_grad(PyObject *const *args, Py_ssize_t n)
             dqw = c.output(12, "dq_weight", kF32, dims(D), q);
             dkw = c.output(13, "dk_weight", kF32, dims(D), q);
         }
-        space = c.workspace(14, bytes, q);
+        space = c.workspace(14, bytes);
     } else if (!c.none(12) || !c.none(13)) {
         raise(PyExc_ValueError, "gradients of weights that are not given");
     }
@@ -782,7 +783,7 @@ PyObject *attention(PyObject *const *args, Py_ssize_t n)
     if (!out.is_cuda() || (with_lse && !lse.is_cuda()))
         raise(PyExc_TypeError, "out and lse must be CUDA tensors");
     if (bytes > 0 || !c.none(14))  // (where the sizes are refused, by the call)
-        space = c.workspace(14, bytes < 0 ? 0 : bytes, q);
+        space = c.workspace(14, bytes < 0 ? 0 : bytes);
     float *const lp = lse.defined() ? ptr<float>(lse) : nullptr;
     void *const sp = space.defined() ? ptr(space) : nullptr;
     c.run([&](uint32_t flags, void *stream) {

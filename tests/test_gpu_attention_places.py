@@ -33,3 +33,18 @@ def test_the_cache_read_back_is_where_the_cache_is(dev):
         for a, b in zip(got, want):
             assert a.is_cuda == on_gpu and (on_gpu or a.is_pinned())
             assert torch.equal(a.cpu(), b.cpu())
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="one device: the current one and the tensors' are the same")
+def test_a_new_workspace_is_on_the_device_that_the_call_runs_on(dev):
+    """Rows in host memory with lists on a device that is not the current one: the call runs there."""
+    T, h, D = 30, 2, 64
+    other = torch.device("cuda:1")
+    g = torch.Generator().manual_seed(0)
+    dq, dk, q, k = (torch.randn(T, h, D, generator=g).bfloat16().pin_memory() for _ in range(4))
+    w, pos, table = torch.ones(D).bfloat16().to(other), torch.arange(T).int().to(other), ref.angles(T, D).to(other)
+    with torch.cuda.device(0):
+        before = torch.cuda.memory_stats(other)["allocation.all.allocated"]
+        pkg.ts_qk_norm_rope_grad(dq, dk, q, k, w, w, pos, table)
+        torch.cuda.synchronize(other)
+        assert torch.cuda.memory_stats(other)["allocation.all.allocated"] > before

@@ -21,7 +21,8 @@
 //
 // Work is split evenly as in attn_few.cu: all units' key tiles in one row, cut into
 // equal shares; what a share leaves of a unit is joined by attn_join_rows_kernel.
-// Every wait has a limit, after which the block records it and ends.
+// Every wait has a limit, after which the block records it, waits (with the limit again) for
+// its copies and products in flight, and ends: what it has not written is not defined.
 //
 // A prompt of 8191 tokens, 64 heads over 8 of 128: 790 us, 1.39 PFLOP/s, 73 % of a large
 // library product's rate, the tensor pipe 61 % busy.  A step of 128 keys takes 3000 cycles
@@ -86,6 +87,18 @@ struct Barriers {
     uint64_t last;
 };
 
+#ifdef TSFN_RUN_OUT
+// For the tests of the give-up path, which are built with it: the waits that begin
+// this many cycles after their block's start run out at once.
+__device__ long long g_run_out = 1LL << 62;
+
+__device__ __forceinline__ long long &block_start()
+{
+    __shared__ long long start;
+    return start;
+}
+#endif
+
 __device__ __forceinline__ void give_up(volatile int *dead)
 {
     *dead = 1;
@@ -104,6 +117,14 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar)
 // The whole warp waits for a phase; false where the block has given up.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *dead)
 {
+#ifdef TSFN_RUN_OUT
+    if (__shfl_sync(0xffffffffu, (int)(clock64() - block_start() >= g_run_out), 0) != 0) {
+        if ((threadIdx.x & 31) == 0)
+            give_up(dead);
+        __syncwarp();
+        return false;
+    }
+#endif
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
         return true;
     const long long t0 = clock64();
@@ -373,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     __shared__ int64_t weights[kSeqs];
     __shared__ uint32_t tmem_at;
     __shared__ volatile int dead;
+    __shared__ uint32_t next_use[2];  // of the places for codes, that K's and V's copies did not get to
     __shared__ int64_t out_at[kRows];
     __shared__ int32_t lse_at[kRows];
     // of a step: whether its tiles of 16 keys lie in the cache; the keys that some row sees,
@@ -389,6 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         tmem_alloc(smem_u32(&tmem_at), 512);
     if (tid == 0) {
         dead = 0;
+#ifdef TSFN_RUN_OUT
+        block_start() = clock64();
+#endif
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars.q_full[i]), 4);
             mbar_init(smem_u32(&bars.s_full[i]), 1);
@@ -820,19 +845,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             raw.next();
             more = look_up();
         }
-        if (which == 0 && alive && (alive = room())) {
+        if (which == 0 && alive && room()) {
             if (lane == 0)
                 no_more[it & 3] = 1;
             warp_arrive(smem_u32(&bars.raw_full[raw.slot]));
+            raw.uses += 2;
         }
-        if (!alive) {  // what is under way (of two uses at most) arrives before its memory goes
-            const long long t0 = clock64();
-            for (uint32_t i = 1; i <= 2 && i <= it; ++i) {
-                const uint32_t use = raw.uses - 2 * i;
-                while (!mbar_try_wait(smem_u32(&bars.raw_full[use % kRawSlots]), use / kRawSlots & 1) && clock64() - t0 < kWaitCycles) {
-                }
-            }
-        }
+        if (lane == 0)
+            next_use[which] = raw.uses;
     } else {
         // ---- products, by one warp
         fewer_registers<kOtherRegs>();
@@ -938,17 +958,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (alive)
                 advance(a, place, segment.length);
         }
-        if (!alive) {  // what has been issued ends before its memory goes
-            commit(&bars.last);
-            const long long t0 = clock64();
-            while (!mbar_try_wait(smem_u32(&bars.last), 0) && clock64() - t0 < kWaitCycles) {
-            }
+        // what has been issued ends before its memory goes, whichever warp gave up
+        commit(&bars.last);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(smem_u32(&bars.last), 0) && clock64() - t0 < kWaitCycles) {
         }
         }
     }
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
+    if (dead != 0) {  // the block gave up: copies in flight arrive before their memory goes
+        const long long t0 = clock64();
+        if (warp == kCopies) {  // the last use of each place
+            for (int slot = 0; slot < kRawSlots; ++slot) {
+                int last = -1;
+                for (int back = 2; back <= 2 * kRawSlots; back += 2)
+                    for (int which = 0; which < 2; ++which) {
+                        const int use = (int)next_use[which] - back;
+                        if (use > last && use % kRawSlots == slot)
+                            last = use;
+                    }
+                while (last >= 0 && !mbar_try_wait(smem_u32(&bars.raw_full[slot]), last / kRawSlots & 1) && clock64() - t0 < kWaitCycles) {
+                }
+            }
+        }
+        __syncwarp();
+    }
     pdl_launch_dependents();
     if (warp == kProducts) {
         tmem_fence_after();

@@ -15,8 +15,9 @@
 //   O^T = V^T p^T   a lane holds D/8 contiguous d of 4 keys; two keys' nibbles are
 //                   joined in one byte before the conversion, which then gives pairs
 //                   along the keys, as the product wants them; p^T by movmatrix
-// (mma.sync, not tcgen05: 8 rows would leave 15/16 of a tcgen05 tile empty, and the
-// tensor pipe is a third busy here.)
+// (mma.sync, not tcgen05: that takes its operands from shared or tensor memory, where K and V
+// would have to be written as fp16 first, four times the bytes of their codes; mma.sync takes
+// them from the registers in which they are made.  The tensor pipe is a quarter busy.)
 //
 // A warp takes a run of tiles of 16 keys, with copies of the next ones under way, and has
 // a running maximum and sum of its own.  The maximum follows only when a score passes it
@@ -29,7 +30,7 @@
 //     any lengths keep every block busy.  A unit inside a share is written at once; of a
 //     unit over several, each block leaves its part in the workspace and
 //     attn_join_kernel joins them in order.
-// 64 sequences of 0 to 16384 keys, 64 heads over 8 of 128: 97 us, 4.5 TB/s.  The tiles run at
+// 64 sequences of 0 to 16384 keys, 64 heads over 8 of 128: 98 us, 4.4 TB/s.  The tiles run at
 // the memory's rate (435 MB in 64 us; 340 instructions a tile and warp, nine tenths of what
 // four blocks can issue); beside them 8 us pass until the first tiles are there, 10 to 20
 // between most blocks' end and the last one's, 5 for the join.  One sequence of 131072
@@ -47,7 +48,7 @@ namespace {
 
 // Even shares: for 8 rows blocks of 4 warps, four to an SM (64 sequences up to 16384 keys:
 // 107.7 us; blocks of 8 warps 113.7, five blocks of 4 with 96 registers 111.7, all three
-// with a way of 12 tiles); for more rows the registers of an SM go to one block of 8.
+// measured with a way of 12 tiles, see below); for more rows the registers of an SM go to one block of 8.
 // Clusters: blocks of 8 warps, for the time of a single call.
 constexpr int kSms = 152;
 constexpr int kClusterWarps = 8;
@@ -59,9 +60,16 @@ constexpr int blocks_of(int nt) { return kSms * blocks_per_sm(nt); }
 int eights_of(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
 constexpr int kStages = 4;  // tiles of a warp whose copies are under way
 constexpr int kShare = 8;     // tiles of a share, at least
-// What going to a unit costs, in tiles of a block, when work is split (64 sequences of 0 to
-// 16384 keys: 97 us with 20 or 24 for blocks of 4 warps, 106 with 12: the blocks that had
-// many short units ended last).
+// What going to a unit costs, in tiles of a block, when work is split (more makes short units
+// longer, so that blocks with many of them do not end last).  us, 8 key heads of 128, by way:
+//                               12     16     20     24     32
+//   8 rows, 64 of 0-16384 keys  131.3  126.8  127.0  127.4  129.4
+//           300 of 0-4096       169.7  164.1  160.3  161.1  164.0
+//  16 rows, 64 of 0-16384       229.9  226.0  222.2  216.1  210.7
+//  32 rows, 64 of 0-16384       328.7  324.1  314.7  308.6  301.6
+//           300 of 0-4096       487.0  472.8  464.7  457.9  440.0
+// Sequences of equal lengths do not depend on it (64 of 8192: 130 us, with 32 rows 280).  For
+// 16 and more rows the best lies beyond 24.
 constexpr int way_of(int nt) { return nt == 1 ? 20 : 24; }
 // Clusters take calls whose units are all resident at once, with at most this many keys a
 // block (16 tiles a warp: with more, sequences of different lengths leave SMs idle), or half

@@ -24,8 +24,9 @@
 // Every wait has a limit, after which the block records it, waits (with the limit again) for
 // its copies and products in flight, and ends: what it has not written is not defined.
 //
-// A prompt of 8191 tokens, 64 heads over 8 of 128: 790 us, 1.39 PFLOP/s, 73 % of a large
-// library product's rate, the tensor pipe 61 % busy.  A step of 128 keys takes 3000 cycles
+// A prompt of 8191 tokens, 64 heads over 8 of 128: 788 us, 1.39 PFLOP/s, 73 % of a large
+// library product's rate, the tensor pipe 61 % busy; of 64 columns 675 us, where the products
+// take 288 and the exponentials 226 (9.5 T/s measured).  A step of 128 keys takes 3000 cycles
 // for 2048 of products.  Most of the rest is a tile's own chain: its scores' way to the
 // registers and the maximum 450 cycles, p in two halves 1300, the second half's products and
 // the next scores 850, and 400 until waits end and products are issued, with the other
@@ -61,7 +62,11 @@ constexpr int kThreads = kRows + kMakers + 128;  // four warp groups; of the las
 // Registers of a thread of each: the 128 that each is launched with, divided anew.
 constexpr int kRowRegs = 192, kMakerRegs = 72, kOtherRegs = 56;
 static_assert(kRows * kRowRegs + kMakers * kMakerRegs + 128 * kOtherRegs <= kThreads * 128, "");
-constexpr int kSwitch = 4;           // what going to a unit costs, in steps, when work is split
+// What going to a unit costs, in steps, when work is split.  us for 2, 3, 4, 5, 6:
+//   D = 128, 8191 queries              868  808  773  782  792;  D = 64  700  666  675  681  691
+//            5 x 1024 of 1024-6144     403  367  351  352  357           316  292  298  301  306
+//            40 x 64 of 64-4096        181  161  150  151  150           129  119  122  126  127
+constexpr int kSwitch = 4;
 constexpr int kCopies = 13;          // the warps that copy codes: of K, of V
 constexpr int kProducts = 12;        // the warp that issues them
 constexpr int kRawSlots = 3;         // places for codes

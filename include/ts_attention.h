@@ -76,10 +76,10 @@ typedef struct {
  *
  * where pair i is (i, i + rot/2), or (2i, 2i + 1) with `interleaved`, and c, s are
  * cos_sin[positions[t]][i], cos_sin[positions[t]][rot/2 + i].  Products and sums are
- * rounded to fp32 one by one in this order.  The squares of a key's row are summed in 32
- * sums, column j in sum j mod 32 in ascending order, which are then added in pairs,
- * neighbours first, so that its bits (and those in the cache) can be computed elsewhere; those of a
- * query in an order that depends on D alone.
+ * rounded to fp32 one by one in this order (sum / D as sum * (1 / D)).  The squares of
+ * a key's row are summed in 32 sums, column j in sum j mod 32 in ascending order, which
+ * are then added in pairs, neighbours first, so that its bits (and those in the cache)
+ * can be computed elsewhere; those of a query in an order that depends on D alone.
  *
  *   q             bf16 [T, q_heads * D], row stride ldq.
  *   k             bf16 [T, k_heads * D], row stride ldk.

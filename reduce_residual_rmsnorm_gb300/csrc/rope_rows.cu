@@ -310,7 +310,7 @@ __device__ __forceinline__ void rope_run(const RopeArgs &a, uint32_t id, uint4 (
         for (int u = 0; u < 2; ++u) {
             float r = 1.0f;
             if (w != nullptr)
-                r = rsqrtf(__fmaf_rn(group_sum(KEYS ? sq[u] : sumsq_bf16x8(x[u], 0.0f), lanes), inv_d, a.eps));
+                r = rsqrtf(__fadd_rn(__fmul_rn(group_sum(KEYS ? sq[u] : sumsq_bf16x8(x[u], 0.0f), lanes), inv_d), a.eps));
             uint64_t n2[4];
             const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll

@@ -43,10 +43,10 @@ def _formula(x, w, pos, table, pairs):
 
 @pytest.mark.parametrize("pairs", [False, True])
 @pytest.mark.parametrize("norm", [True, False])
-@pytest.mark.parametrize("D,rot", [(256, 256), (128, 128), (128, 64), (64, 64), (32, 16), (16, 16)])
+@pytest.mark.parametrize("D,rot", [(256, 256), (128, 128), (128, 64), (64, 64), (32, 16), (16, 16), (48, 32), (80, 80), (144, 64), (208, 208)])
 def test_bits_of_the_documented_order(dev, D, rot, norm, pairs):
-    """Keys and the cache bit for bit (D a power of two, so that the mean is the sum's exact part).  The queries hold whole
-    numbers up to 7: their squares' sum, at most 49 * 256, is exact in fp32 in any order."""
+    """Keys and the cache bit for bit.  The queries hold whole numbers up to 7: their squares' sum, at most 49 * 256, is exact
+    in fp32 in any order."""
     T, hq, hk, page, far = 2000, 8, 8, 64, 700
     g = torch.Generator(device=dev).manual_seed(D + rot)
     q = torch.randint(-7, 8, (T, hq, D), generator=g, device=dev).bfloat16()

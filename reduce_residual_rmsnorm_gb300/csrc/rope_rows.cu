@@ -308,6 +308,8 @@ __device__ __forceinline__ void rope_run(const RopeArgs &a, uint32_t id, uint4 (
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+            if (u > 0 && h + u >= most)  // (few tokens: one head each)
+                break;
             float r = 1.0f;
             if (w != nullptr)
                 r = rsqrtf(__fadd_rn(__fmul_rn(group_sum(KEYS ? sq[u] : sumsq_bf16x8(x[u], 0.0f), lanes), inv_d), a.eps));

@@ -171,8 +171,7 @@ TS_API int ts_kv_cache_read(const ts_kv_cache_t *cache, const int32_t *slots, in
  * A query that sees no key gets zeros and lse = -inf.  Products are exact (a query's
  * row is first scaled by a power of two into fp16, where K and V are exact), sums
  * are in fp32, and exp(s - max) is rounded for the product with V, to 11 bits down to 2^-21 and
- * to multiples of 2^-31 below.  A row with a score beyond 10^8 in magnitude, where neighbouring
- * fp32 are further apart than exp can tell, has no defined output.  Scale factors of keys that a query of the call sees must not
+ * to multiples of 2^-31 below.  Scale factors of keys that a query of the call sees must not
  * be NaN; those of other slots are not used.
  *
  *   q            bf16 [T, q_heads * D], row stride ldq.

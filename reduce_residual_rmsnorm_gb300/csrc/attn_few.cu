@@ -416,19 +416,22 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Run &run, float 
                 const float2 cf = factor(nt);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float top = fmaxf(x[nt][j], x[nt][j + 2]);
+                    const float c = j ? cf.y : cf.x;
+                    const float s0 = __fmul_rn(sc[nt][j], c), s1 = __fmul_rn(sc[nt][j + 2], c);
+                    float top = fmaxf(s0, s1);
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     const bool some = room[nt][j] != -INFINITY;
-                    top += off[nt][j] - kLift;
+                    top -= kLift;
                     top = some ? fmaxf(top, off[nt][j]) : top;
                     f[j] = some ? exp2_approx(off[nt][j] - top) : 0.0f;
                     off[nt][j] = top == -INFINITY ? 0.0f : top;
-                    room[nt][j] = top == -INFINITY ? -INFINITY : kLift + kSlack;
+                    const bool far = fabsf(off[nt][j]) >= kFar;  // (comes here for every tile)
+                    room[nt][j] = top == -INFINITY ? -INFINITY : (far ? -0x1p127f : kLift + kSlack);
                     l[nt][j] *= f[j];
-                    x[nt][j] = fmaf(sc[nt][j], j ? cf.y : cf.x, -off[nt][j]);
-                    x[nt][j + 2] = fmaf(sc[nt][j + 2], j ? cf.y : cf.x, -off[nt][j]);
+                    x[nt][j] = far ? s0 - off[nt][j] : fmaf(sc[nt][j], c, -off[nt][j]);
+                    x[nt][j + 2] = far ? s1 - off[nt][j] : fmaf(sc[nt][j + 2], c, -off[nt][j]);
                 }
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {

@@ -546,7 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             fence_async_proxy();
             warp_arrive(smem_u32(&bars.q_full[tile]));
-            const float cf = score_factor(a, down, k_scale);
+            // (a score is at most 2^8 times K's largest times D times its factor; where that may be
+            // far, it is rounded on its own, in the pass that few steps have)
+            const float all_of = score_factor(a, down, k_scale);
+            const bool far = all_of >= kFar / (256.0f * 2688.0f * D), some_far = __any_sync(0xffffffffu, far);
+            const float cf = far ? 1.0f : all_of, before = far ? all_of : 1.0f;
             int hi, lo;  // the keys that the row sees
             {
                 int i, qh;
@@ -568,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     break;
                 tmem_fence_after();
                 const uint2 in = *reinterpret_cast<const uint2 *>(seen[(step + k) & 3]);
-                if (!(key >= lo_max && key + kKeys <= hi_min && in.x == 0x01010101u && in.y == 0x01010101u)) {
+                if (some_far || !(key >= lo_max && key + kKeys <= hi_min && in.x == 0x01010101u && in.y == 0x01010101u)) {
                     // -inf for what the row does not see, a pass of its own: few steps have any
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
@@ -580,6 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         const uint32_t sees = (uint32_t)((1ull << h) - (1ull << min(w, h))) &
                                               ((ok & 1 ? 0xFFFFu : 0u) | (ok & 0x100 ? 0xFFFF0000u : 0u));
                         loaded(v);
+                        if (some_far) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), before));
+                        }
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!(sees >> j & 1))

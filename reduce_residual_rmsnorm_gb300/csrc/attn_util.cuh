@@ -13,6 +13,10 @@ namespace tsfn {
 // passes it by 2^kSlack; p stays below 2^(kLift + kSlack), fp16's end at 2^16.  What is kept
 // of a row as its maximum is top - kLift: sums and outputs of parts go with that.
 constexpr float kLift = 7.0f, kSlack = 8.0f;
+// Scores from here on are rounded before the top is taken off them: their neighbouring fp32
+// are 2 and more apart, and one operation for both would leave what the top's own rounding
+// lost, up to any power of two.
+constexpr float kFar = 0x1p24f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What a block leaves for a unit that it began and others go on with.

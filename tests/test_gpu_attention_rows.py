@@ -132,3 +132,55 @@ def test_one_key_that_outweighs_the_others(dev, new, lens, far, D):
         at += n
     assert bool(((got[1].double() - lse).abs() <= slack_lse).all())
     assert float(out.abs().min()) > 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [1e6, -1e6, 1e8, 4e8, -4e8, 1e9, 3e12, -3e12, 1e30])
+@pytest.mark.parametrize("form", FORMS)
+def test_scores_of_any_size(dev, form, size, D):
+    """Scores whose neighbouring fp32 are far apart: alike they weigh alike, and where one key has twice the others', it
+    (or, below zero, the others) has all the weight.  Weights are then equal or zero, so that fp16 and the sums cost
+    2^-11 and 2^-16 of the output at most."""
+    hk, G, page = 2, 4, 32
+    new, lens = FORMS[form]
+    g = torch.Generator(device=dev).manual_seed(3)
+    one = torch.ones(1, device=dev)
+    used = [-(-n // page) for n in lens]
+    cache = pkg.ts_kv_cache(max(1, sum(used)), hk, D, one, 1700 * one, page_size=page, device=dev)
+    table = torch.full((len(lens), max(used)), -1, dtype=torch.int32, device=dev)
+    flat = torch.zeros(1, 16, device=dev)
+    flat[:, :8] = 1.0
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        table[b, :used[b]] = sum(used[:b]) + torch.arange(used[b], device=dev).int()
+        k = torch.zeros(n, hk, D, dtype=torch.bfloat16, device=dev)
+        k[..., 0] = 3.0
+        k[n // 3, 1, 0] = 6.0  # (the first head's keys are all alike)
+        v = (0.5 + torch.rand(n, hk, D, generator=g, device=dev)).bfloat16()
+        at = torch.arange(n, device=dev)
+        slots = (table[b].long()[at // page] * page + at % page).int()
+        pkg.ts_qk_norm_rope(k, k, None, None, torch.zeros(n, dtype=torch.int32, device=dev), flat, v=v, cache=cache, slots=slots)
+    q = torch.zeros(sum(new), hk * G, D, dtype=torch.bfloat16, device=dev)
+    q[..., 0] = size / (3 * 0.125)
+    got, _ = _call(dev, q, cache, table, lens, new, 0.125)
+    # the scores less their largest, which 64 bits hold whatever their size (lse would lose the logarithm of the sum)
+    values, at = ref.cached(cache.pages, 1) / 1700.0, 0
+    s0 = float(q[0, 0, 0]) * 0.125 * 3.0 if len(q) else 0.0
+    for n, m, ids in zip(lens, new, table):
+        for i in range(m):
+            seen = max(n - m + i + 1, 0)
+            out, lse = got[0][at + i].unflatten(0, (hk, G)), got[1][at + i].view(hk, G)
+            if seen == 0:
+                assert bool((out == 0).all() and torch.isneginf(lse).all())
+                continue
+            s = torch.full((hk, seen), s0, dtype=torch.float64, device=dev)
+            if n // 3 < seen:
+                s[1, n // 3] *= 2
+            v = values[ids[:-(-seen // page)].long()].transpose(0, 1).flatten(1, 2)[:, :seen]
+            want = torch.einsum("hj,hjd->hd", torch.softmax(s, 1), v).unsqueeze(1)
+            _close(out, want.expand(out.shape), (2.0 ** -11 + 2.0 ** -16) * want, "out")
+            # (scale, log2 e and the products: a few roundings of the score)
+            total = torch.logsumexp(s, 1, keepdim=True)
+            assert bool(((lse.double() - total).abs() <= 2.0 ** -21 * total.abs() + 2.0 ** -16).all())
+        at += m
